@@ -49,8 +49,10 @@ extern "C" {
 
 typedef struct spmv_handle_s *spmv_handle_t;
 
-/* value type of the matrix, x and y */
-typedef enum { SPMV_F64 = 0, SPMV_F32 = 1 } spmv_dtype;
+/* value type of the matrix, x and y: SPMV_F64 or SPMV_F32.  The 16-bit types (IEEE half and
+ * bfloat16) are for the dense rows of the sparse-row operators at the end of this file, which
+ * take them or SPMV_F32. */
+typedef enum { SPMV_F64 = 0, SPMV_F32 = 1, SPMV_F16 = 2, SPMV_BF16 = 3 } spmv_dtype;
 
 /*
  * Storage formats.
@@ -555,6 +557,140 @@ SPMV_API int spmv_probe_gather(const void *x, int64_t n, int dtype, int sectors_
  */
 SPMV_API int spmv_csr_apply_noalloc(int64_t n, int64_t nnz, const int32_t *row_ptr, const int32_t *col_idx,
                                     const void *vals, int dtype, const void *x, void *y, void *stream);
+
+/* ========================================================================================
+ * Sparse rows: at most k entries in every row of a matrix that is made anew at each step,
+ * beside dense matrices of rows.  None of the pages has a counterpart.  The router of a
+ * layer of sparse experts makes such a matrix (tokens x experts, k entries a row), and so
+ * does a teacher whose k largest logits of each row are kept (tokens x vocabulary).
+ *
+ * Shared by these entry points, besides the conventions at the top of this file:
+ *  - Nothing is allocated, nothing is synchronised and no state is kept: every call only
+ *    enqueues kernels on `stream` (so it may be captured into a graph), with its outputs
+ *    and any workspace in the caller's memory.
+ *  - Dense matrices are row-major with a leading dimension (in values) >= the row length, of
+ *    type SPMV_F32, SPMV_F16 or SPMV_BF16, at any address that is a multiple of the value
+ *    size (16-byte aligned rows run fastest).  int32 and float arrays are contiguous.
+ *  - Sums, softmax statistics and products are in 32 bits; 16-bit outputs are rounded once.
+ *  - Results do not depend on timing: no floating-point atomics; the same call gives the
+ *    same bits.
+ *  - Arrays must be memory of the current device; an output may not overlap another array
+ *    of the call (SPMV_ERR_INVALID_ARG), except where a call says that it works in place.
+ *  - An entry whose column is outside the matrix (-1 by convention) is no entry.
+ */
+
+/* weights of spmv_topk_rows: none; softmax over the chosen entries; softmax over the whole
+ * row, of which the chosen entries' are returned */
+typedef enum { SPMV_WEIGHTS_NONE = 0, SPMV_WEIGHTS_SELECTED = 1, SPMV_WEIGHTS_ROW = 2 } spmv_weighting;
+
+/*
+ * The k largest entries of every row of x (rows x n).
+ *   k         1 <= k <= min(n, 256).
+ *   ids       int32[rows][k]: their columns, values descending, ties to the lowest column.
+ *             An entry of -inf is never taken (a masked column): where a row has fewer than
+ *             k others, the remaining ids are -1.  The type's lowest finite value is a value
+ *             like any other.  A NaN counts as larger than +inf.
+ *   vals      float[rows][k]: their values (-inf beside an id of -1).
+ *   weights   float[rows][k] (weighting not NONE): exp(v / temperature) over the sum of the
+ *             chosen entries' (SELECTED) or of the whole row's (ROW); 0 beside an id of -1.
+ *   lse       float[rows], or NULL: log of the sum of exp(x / temperature) over the row
+ *             (-inf for a row without an entry above -inf).
+ *   temperature  in [1e-6, 1e6].
+ */
+SPMV_API int spmv_topk_rows(int64_t rows, int64_t n, int32_t k, const void *x, int64_t ldx, int dtype,
+                            double temperature, int weighting, int32_t *ids, float *vals, float *weights,
+                            float *lse, void *stream);
+
+/*
+ * The gradient of spmv_topk_rows' weights (the choice itself has none): with dweights the
+ * loss's gradient in the weights, dx (rows x n, of type `dtype`, overwritten) is its gradient
+ * in x.  ids and weights are the forward call's.  weighting ROW also reads x and the forward
+ * call's lse; with SELECTED they may be NULL.
+ */
+SPMV_API int spmv_topk_rows_grad(int64_t rows, int64_t n, int32_t k, const int32_t *ids, const float *weights,
+                                 const float *dweights, int weighting, double temperature, const void *x,
+                                 int64_t ldx, const float *lse, void *dx, int64_t lddx, int dtype, void *stream);
+
+/*
+ * Rows sorted by expert.  ids (int32[tokens][k]) names up to k experts for every token; an
+ * entry outside [0, experts) is dropped.  The plan gives each expert a segment of rows of a
+ * sorted matrix, its entries in the order of (token, position), every segment's length
+ * rounded up to a multiple of `align` (so that a tile of `align` rows has one expert):
+ *   offsets   int32[experts + 1]: the segments' starts; offsets[experts] = rows in use.
+ *   slots     int32[tokens][k]: the sorted row of every entry, -1 for a dropped one.
+ *   sources   int32[spmv_route_rows(...)]: the entry (token * k + position) at every sorted
+ *             row, -1 for padding and for the rows behind the last segment.
+ * spmv_route_rows gives the sorted matrix's number of rows: enough for any ids (a bound known
+ * without reading them), so nothing has to come back to the host.  spmv_route_workspace
+ * gives the bytes of workspace (0: it may be NULL).  Both return a negative status for
+ * arguments out of range: tokens * k < 2^31, k >= 1, 1 <= experts <= 4096,
+ * 1 <= align <= 65536.  The workspace is free for other use when the call's kernels have run.
+ */
+SPMV_API int64_t spmv_route_rows(int64_t tokens, int32_t k, int32_t experts, int32_t align);
+SPMV_API int64_t spmv_route_workspace(int64_t tokens, int32_t k, int32_t experts);
+SPMV_API int spmv_route_plan(int64_t tokens, int32_t k, int32_t experts, int32_t align, const int32_t *ids,
+                             int32_t *offsets, int32_t *slots, int32_t *sources, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
+/* xs[slots[t][j]] = x[t] for every entry (x: tokens x d, xs: rows x d); rows without a source
+ * become 0.  The product of the routing's transposed pattern with x. */
+SPMV_API int spmv_route_dispatch(int64_t tokens, int32_t k, int64_t rows, int64_t d, const int32_t *slots,
+                                 const int32_t *sources, const void *x, int64_t ldx, void *xs, int64_t ldxs,
+                                 int dtype, void *stream);
+
+/* y[t] = sum over j of weights[t][j] * ys[slots[t][j]] (ys: rows x d, y: tokens x d; weights
+ * float[tokens][k], NULL = all 1); a token without entries gets 0, and the row and the weight
+ * of a dropped entry are not read.  With weights NULL this is also the gradient of dispatch: it
+ * takes the gradient in xs to the gradient in x. */
+SPMV_API int spmv_route_combine(int64_t tokens, int32_t k, int64_t rows, int64_t d, const int32_t *slots,
+                                const float *weights, const void *ys, int64_t ldys, void *y, int64_t ldy,
+                                int dtype, void *stream);
+
+/* The gradients of combine: dys[slots[t][j]] = weights[t][j] * dy[t], 0 in rows without a source
+ * (dys: rows x d), and dweights[t][j] = <dy[t], ys[slots[t][j]]>, 0 for a dropped entry. */
+SPMV_API int spmv_route_combine_grad(int64_t tokens, int32_t k, int64_t rows, int64_t d, const int32_t *slots,
+                                     const int32_t *sources, const float *weights, const void *dy, int64_t lddy,
+                                     const void *ys, int64_t ldys, void *dys, int64_t lddys, float *dweights,
+                                     int dtype, void *stream);
+
+/*
+ * Distillation from a teacher's top logits.  z (rows x vocab) are the student's logits; row t
+ * of the target has the columns ids[t][0..k) (each column at most once) with the teacher's
+ * logits teacher[t][0..k), of type `teacher_dtype`.  With q = softmax(z / temperature):
+ *   teacher_lse NULL   p = softmax(teacher / temperature) over the row's entries, and
+ *       loss[t] = sum p_j (log p_j - log q_j).
+ *   teacher_lse given  (float[rows], the log of the sum of exp(teacher / temperature) over the
+ *       whole vocabulary, as spmv_topk_rows' lse) p_j = exp(teacher_j / temperature - lse), and
+ *       the other columns count as one class, of probability r = max(0, 1 - sum p_j) for the
+ *       teacher and 1 - sum q_j for the student (summed over those columns, not subtracted):
+ *       loss[t] = sum p_j (log p_j - log q_j) + r (log r - log(1 - sum q_j)).
+ *       An r below 1e-5 is rounding where the student has no mass on the other columns at
+ *       all, and counts as 0 there.
+ * A row without entries (padding, say) has loss 0 and gradient 0, whatever z holds.  A teacher
+ * logit of -inf has p = 0.  The loss is not scaled: neither by temperature^2 nor to a mean.
+ *   k 1..512 (k may exceed vocab only by absent entries), vocab 1..2^22, temperature in
+ *   [1e-6, 1e6].
+ *   stats    float[rows][4], 16-byte aligned, or NULL: what the gradient needs of the row
+ *            (z's maximum and its sum of exponentials, of all and of the other columns).
+ *   dz       rows x vocab, z's type, overwritten:
+ *            scale * row_scale[t] * d loss[t] / d z[t] (row_scale float[rows], NULL = all 1).
+ *            It may be z itself (same address and leading dimension): the gradient then
+ *            replaces the logits.
+ * spmv_distill_loss is the loss; spmv_distill_grad the gradient from that call's arguments and
+ * stats; spmv_distill_loss_grad both at once, reading z once.
+ */
+SPMV_API int spmv_distill_loss(int64_t rows, int64_t vocab, int32_t k, const void *z, int64_t ldz, int dtype,
+                               const int32_t *ids, const void *teacher, int teacher_dtype,
+                               const float *teacher_lse, double temperature, float *loss, float *stats,
+                               void *stream);
+SPMV_API int spmv_distill_grad(int64_t rows, int64_t vocab, int32_t k, const void *z, int64_t ldz, int dtype,
+                               const int32_t *ids, const void *teacher, int teacher_dtype,
+                               const float *teacher_lse, double temperature, const float *stats, double scale,
+                               const float *row_scale, void *dz, int64_t lddz, void *stream);
+SPMV_API int spmv_distill_loss_grad(int64_t rows, int64_t vocab, int32_t k, const void *z, int64_t ldz, int dtype,
+                                    const int32_t *ids, const void *teacher, int teacher_dtype,
+                                    const float *teacher_lse, double temperature, float *loss, double scale,
+                                    const float *row_scale, void *dz, int64_t lddz, void *stream);
 
 #ifdef __cplusplus
 }

@@ -7,6 +7,10 @@ entry points one to one; :class:`SpmvMatrix` wraps a handle for torch tensors.
     import torch, sparse_matrix_vector_csr_gb300 as spmv
     A = spmv.SpmvMatrix.from_csr(row_ptr, col_idx, vals)        # CUDA tensors
     y = A @ x                                                   # or A.apply(x, y)
+
+``sparse_rows`` has the operators of matrices with at most k entries a row that are made
+anew at each step: a router's choice and the rows sorted by it (:func:`topk_rows`,
+:class:`RoutePlan`), and distillation from a teacher's top logits (:func:`distill_loss`).
 """
 from __future__ import annotations
 
@@ -42,9 +46,33 @@ from ._abi import (  # noqa: F401
     spmv_last_error,
     spmv_last_error_message,
     spmv_to_csr,
+    spmv_topk_rows,
+    spmv_topk_rows_grad,
+    spmv_route_rows,
+    spmv_route_workspace,
+    spmv_route_plan,
+    spmv_route_dispatch,
+    spmv_route_combine,
+    spmv_route_combine_grad,
+    spmv_distill_loss,
+    spmv_distill_grad,
+    spmv_distill_loss_grad,
 )
 
-__all__ = ["SpmvMatrix", "SpmvError", "FORMATS", "ORDERINGS"] + [n for n in _abi.EXPORTS]
+#: names of ``sparse_rows``, which needs torch and is imported with the first of them
+_SPARSE_ROWS = ("TopRows", "RoutePlan", "DistillLoss", "topk_rows", "distill_loss", "distill_loss_grad")
+
+__all__ = ["SpmvMatrix", "SpmvError", "FORMATS", "ORDERINGS"] + list(_SPARSE_ROWS) + [n for n in _abi.EXPORTS]
+
+
+def __getattr__(name):
+    if name not in _SPARSE_ROWS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import sparse_rows
+
+    for n in _SPARSE_ROWS:
+        globals()[n] = getattr(sparse_rows, n)
+    return globals()[name]
 
 
 class SpmvMatrix:

@@ -14,7 +14,7 @@ import os
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspmv_gb300.so")
 
-SPMV_F64, SPMV_F32 = 0, 1
+SPMV_F64, SPMV_F32, SPMV_F16, SPMV_BF16 = 0, 1, 2, 3
 FORMATS = {"auto": 0, "csr_vector": 1, "ell_r": 2, "sell": 3, "hyb": 4, "merge": 5}
 STATUS = {
     0: "SPMV_OK", -1: "SPMV_ERR_INVALID_ARG", -2: "SPMV_ERR_BAD_CSR", -3: "SPMV_ERR_CUDA",
@@ -29,7 +29,13 @@ EXPORTS = (
     "spmv_csr_apply_noalloc", "spmv_apply_ex", "spmv_apply_multi", "spmv_cg", "spmv_get_slots",
     "spmv_build_permuted", "spmv_get_permutation", "spmv_permute_vector", "spmv_apply_mapped", "spmv_bicgstab",
     "spmv_gmres", "spmv_probe_gather", "spmv_device_status", "spmv_device_memory",
+    "spmv_topk_rows", "spmv_topk_rows_grad", "spmv_route_rows", "spmv_route_workspace", "spmv_route_plan",
+    "spmv_route_dispatch", "spmv_route_combine", "spmv_route_combine_grad", "spmv_distill_loss",
+    "spmv_distill_grad", "spmv_distill_loss_grad",
 )
+
+#: spmv_weighting codes
+WEIGHTINGS = {None: 0, "none": 0, "selected": 1, "row": 2}
 
 #: spmv_ordering codes
 ORDERINGS = {"natural": 0, "row_length": 1, "rcm": 2, "user": 3}
@@ -121,6 +127,29 @@ def _load():
     lib.spmv_get_permutation.restype = c_int
     lib.spmv_permute_vector.argtypes = [vp, vp, vp, c_int, vp]
     lib.spmv_permute_vector.restype = c_int
+    lib.spmv_topk_rows.argtypes = [i64, i64, i32, vp, i64, c_int, f64, c_int, vp, vp, vp, vp, vp]
+    lib.spmv_topk_rows.restype = c_int
+    lib.spmv_topk_rows_grad.argtypes = [i64, i64, i32, vp, vp, vp, c_int, f64, vp, i64, vp, vp, i64, c_int, vp]
+    lib.spmv_topk_rows_grad.restype = c_int
+    lib.spmv_route_rows.argtypes = [i64, i32, i32, i32]
+    lib.spmv_route_rows.restype = i64
+    lib.spmv_route_workspace.argtypes = [i64, i32, i32]
+    lib.spmv_route_workspace.restype = i64
+    lib.spmv_route_plan.argtypes = [i64, i32, i32, i32, vp, vp, vp, vp, vp, i64, vp]
+    lib.spmv_route_plan.restype = c_int
+    lib.spmv_route_dispatch.argtypes = [i64, i32, i64, i64, vp, vp, vp, i64, vp, i64, c_int, vp]
+    lib.spmv_route_dispatch.restype = c_int
+    lib.spmv_route_combine.argtypes = [i64, i32, i64, i64, vp, vp, vp, i64, vp, i64, c_int, vp]
+    lib.spmv_route_combine.restype = c_int
+    lib.spmv_route_combine_grad.argtypes = [i64, i32, i64, i64, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, c_int, vp]
+    lib.spmv_route_combine_grad.restype = c_int
+    lib.spmv_distill_loss.argtypes = [i64, i64, i32, vp, i64, c_int, vp, vp, c_int, vp, f64, vp, vp, vp]
+    lib.spmv_distill_loss.restype = c_int
+    lib.spmv_distill_grad.argtypes = [i64, i64, i32, vp, i64, c_int, vp, vp, c_int, vp, f64, vp, f64, vp, vp, i64, vp]
+    lib.spmv_distill_grad.restype = c_int
+    lib.spmv_distill_loss_grad.argtypes = [i64, i64, i32, vp, i64, c_int, vp, vp, c_int, vp, f64, vp, f64, vp, vp, i64,
+                                           vp]
+    lib.spmv_distill_loss_grad.restype = c_int
     del i32
     return lib
 
@@ -357,3 +386,75 @@ def spmv_gmres(h, b, x, restart, rtol, max_iter, stream=None):
     _check(lib.spmv_gmres(h, _ptr(b), _ptr(x), int(restart), float(rtol), int(max_iter), _stream(stream),
                           ctypes.byref(it), ctypes.byref(res)))
     return int(it.value), float(res.value)
+
+
+def spmv_topk_rows(rows, n, k, x, ldx, dtype, temperature, weighting, ids, vals, weights=None, lse=None,
+                   stream=None) -> None:
+    """The k largest entries of every row (see spmv.h)."""
+    _check(lib.spmv_topk_rows(int(rows), int(n), int(k), _ptr(x), int(ldx), int(dtype), float(temperature),
+                              int(WEIGHTINGS.get(weighting, weighting)), _ptr(ids), _ptr(vals), _ptr(weights),
+                              _ptr(lse), _stream(stream)))
+
+
+def spmv_topk_rows_grad(rows, n, k, ids, weights, dweights, weighting, temperature, x, ldx, lse, dx, lddx, dtype,
+                        stream=None) -> None:
+    """The gradient of spmv_topk_rows' weights (see spmv.h)."""
+    _check(lib.spmv_topk_rows_grad(int(rows), int(n), int(k), _ptr(ids), _ptr(weights), _ptr(dweights),
+                                   int(WEIGHTINGS.get(weighting, weighting)), float(temperature), _ptr(x), int(ldx),
+                                   _ptr(lse), _ptr(dx), int(lddx), int(dtype), _stream(stream)))
+
+
+def spmv_route_rows(tokens, k, experts, align=1) -> int:
+    """Rows of the matrix sorted by expert: enough for any choice."""
+    return int(_check(lib.spmv_route_rows(int(tokens), int(k), int(experts), int(align))))
+
+
+def spmv_route_workspace(tokens, k, experts) -> int:
+    """Bytes of workspace that spmv_route_plan needs (0: none)."""
+    return int(_check(lib.spmv_route_workspace(int(tokens), int(k), int(experts))))
+
+
+def spmv_route_plan(tokens, k, experts, align, ids, offsets, slots, sources, workspace=None, workspace_bytes=0,
+                    stream=None) -> None:
+    _check(lib.spmv_route_plan(int(tokens), int(k), int(experts), int(align), _ptr(ids), _ptr(offsets), _ptr(slots),
+                               _ptr(sources), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def spmv_route_dispatch(tokens, k, rows, d, slots, sources, x, ldx, xs, ldxs, dtype, stream=None) -> None:
+    _check(lib.spmv_route_dispatch(int(tokens), int(k), int(rows), int(d), _ptr(slots), _ptr(sources), _ptr(x),
+                                   int(ldx), _ptr(xs), int(ldxs), int(dtype), _stream(stream)))
+
+
+def spmv_route_combine(tokens, k, rows, d, slots, weights, ys, ldys, y, ldy, dtype, stream=None) -> None:
+    _check(lib.spmv_route_combine(int(tokens), int(k), int(rows), int(d), _ptr(slots), _ptr(weights), _ptr(ys),
+                                  int(ldys), _ptr(y), int(ldy), int(dtype), _stream(stream)))
+
+
+def spmv_route_combine_grad(tokens, k, rows, d, slots, sources, weights, dy, lddy, ys, ldys, dys, lddys, dweights,
+                            dtype, stream=None) -> None:
+    _check(lib.spmv_route_combine_grad(int(tokens), int(k), int(rows), int(d), _ptr(slots), _ptr(sources),
+                                       _ptr(weights), _ptr(dy), int(lddy), _ptr(ys), int(ldys), _ptr(dys), int(lddys),
+                                       _ptr(dweights), int(dtype), _stream(stream)))
+
+
+def spmv_distill_loss(rows, vocab, k, z, ldz, dtype, ids, teacher, teacher_dtype, teacher_lse, temperature, loss,
+                      stats=None, stream=None) -> None:
+    """Distillation loss against a teacher's top logits (see spmv.h)."""
+    _check(lib.spmv_distill_loss(int(rows), int(vocab), int(k), _ptr(z), int(ldz), int(dtype), _ptr(ids),
+                                 _ptr(teacher), int(teacher_dtype), _ptr(teacher_lse), float(temperature), _ptr(loss),
+                                 _ptr(stats), _stream(stream)))
+
+
+def spmv_distill_grad(rows, vocab, k, z, ldz, dtype, ids, teacher, teacher_dtype, teacher_lse, temperature, stats,
+                      scale, row_scale, dz, lddz, stream=None) -> None:
+    _check(lib.spmv_distill_grad(int(rows), int(vocab), int(k), _ptr(z), int(ldz), int(dtype), _ptr(ids),
+                                 _ptr(teacher), int(teacher_dtype), _ptr(teacher_lse), float(temperature), _ptr(stats),
+                                 float(scale), _ptr(row_scale), _ptr(dz), int(lddz), _stream(stream)))
+
+
+def spmv_distill_loss_grad(rows, vocab, k, z, ldz, dtype, ids, teacher, teacher_dtype, teacher_lse, temperature,
+                           loss, scale, row_scale, dz, lddz, stream=None) -> None:
+    _check(lib.spmv_distill_loss_grad(int(rows), int(vocab), int(k), _ptr(z), int(ldz), int(dtype), _ptr(ids),
+                                      _ptr(teacher), int(teacher_dtype), _ptr(teacher_lse), float(temperature),
+                                      _ptr(loss), float(scale), _ptr(row_scale), _ptr(dz), int(lddz),
+                                      _stream(stream)))

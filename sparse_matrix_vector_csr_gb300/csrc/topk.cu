@@ -1,0 +1,483 @@
+// The k largest entries of every row of a dense matrix: dense rows to sparse rows.  Values
+// descend, ties go to the lowest column, -inf is never taken.  With them the row's
+// log-sum-exp (the same pass over the row) and softmax weights, and the weights' gradient.
+#include "rows_common.cuh"
+
+namespace spmv {
+namespace {
+
+using namespace rows;
+
+constexpr int kMaxTop = 256;
+constexpr int kGateMaxN = 512;    // rows up to this length are taken by one warp each
+constexpr int kGateMaxK = 32;     // ... with one lane per chosen entry
+constexpr int kMaxCand = 1024;    // candidates that one CTA sorts
+constexpr int kMaxGroups = 1024;  // maxima that set the first threshold
+
+// (key of the value, column) as one number: unique within a row, larger = taken earlier.
+__device__ __forceinline__ unsigned long long composite(float v, int64_t col) {
+    return (static_cast<unsigned long long>(order_key(v)) << 32) | (0xffffffffu - static_cast<uint32_t>(col));
+}
+__device__ __forceinline__ int32_t composite_col(unsigned long long c) {
+    return static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
+}
+
+struct TopArgs {
+    int64_t rows, n, ldx;
+    int k, weighting;
+    float scale, inv_temperature;  // scale = log2(e) / temperature
+    const void *x;
+    int32_t *ids;
+    float *vals, *weights, *lse;
+};
+
+// ----------------------------------------------------------------------------
+// short rows: one warp per row
+// ----------------------------------------------------------------------------
+// The row sits in registers, value i * 32 + lane in register i.  k rounds: the warp's
+// largest key (redux), the lowest column that has it (redux), the owner drops it.
+template <typename T, int kR>
+__global__ void __launch_bounds__(256) k_topk_warp(TopArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= a.rows) return;
+    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+    const int n = static_cast<int>(a.n);
+    uint32_t key[kR];  // 0 = taken, or not there, or -inf
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+        const int c = i * 32 + lane;
+        const float v = c < n ? to_f32(x[c]) : kNegInf;
+        key[i] = v == kNegInf ? 0u : order_key(v);
+    }
+    float sum = 0.0f, m = 0.0f;
+    if (a.lse || a.weighting == SPMV_WEIGHTS_ROW) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kR; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        m = best ? key_value(best) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kR; ++i)
+            if (key[i]) sum += ex2((key_value(key[i]) - m) * a.scale);
+        sum = warp_sum(sum);
+    }
+    int32_t my_id = -1;
+    uint32_t my_key = 0;
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < kR; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top == 0) break;
+        const uint32_t mine = best == top ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu;
+        const uint32_t col = __reduce_min_sync(0xffffffffu, mine);
+        if (mine == col) {
+#pragma unroll
+            for (int i = 0; i < kR; ++i)
+                if (i == at) key[i] = 0;
+        }
+        if (lane == j) {
+            my_id = static_cast<int32_t>(col);
+            my_key = top;
+        }
+    }
+    const float v = my_key ? key_value(my_key) : kNegInf;
+    if (a.weighting == SPMV_WEIGHTS_SELECTED) {
+        const float m0 = reference_of(__shfl_sync(0xffffffffu, v, 0));
+        const float e = my_key ? ex2((v - m0) * a.scale) : 0.0f;
+        const float s = warp_sum(e);
+        if (lane < a.k) a.weights[row * a.k + lane] = my_key ? e / s : 0.0f;
+    } else if (a.weighting == SPMV_WEIGHTS_ROW) {
+        if (lane < a.k) a.weights[row * a.k + lane] = my_key ? ex2((v - m) * a.scale) / sum : 0.0f;
+    }
+    if (lane < a.k) {
+        a.ids[row * a.k + lane] = my_id;
+        a.vals[row * a.k + lane] = v;
+    }
+    if (a.lse && lane == 0) a.lse[row] = fmaf(m, a.inv_temperature, logf(sum));
+}
+
+// ----------------------------------------------------------------------------
+// long rows: a CTA, or a cluster of CTAs, per row
+// ----------------------------------------------------------------------------
+// 1. Every thread takes its share's maximum; the k-th largest of the maxima of groups of
+//    threads is a lower bound of the row's k-th largest entry that passes few others.
+// 2. Entries at or above it go to the first CTA's candidate list.
+// 3. If the list overflows (values bunched in one group, or many ties), the threshold is
+//    bisected on (value, column) numbers, which are unique, until between k and kMaxCand
+//    pass: at most 64 counting passes, whatever the row holds.
+// 4. The first CTA ranks the candidates by counting and writes the k largest.
+// kR > 0: a thread's share is kR vectors in registers, read once.  kR = 0: any length, read
+// again by each pass (from L2).
+struct TopShared {
+    unsigned long long cand[kMaxCand];
+    float group_max[kMaxGroups];
+    float2 sums[kMaxCluster * 16];  // per warp of the cluster: maximum, sum of exponentials
+    float top_vals[kMaxTop];
+    uint32_t count[4];  // [0] candidates (first CTA's), [1..3] the bisection's counts
+    float thr, lse_m, lse_sum;
+};
+
+template <typename T, int kR, typename F>
+__device__ __forceinline__ void each_value(const RowView<T> &row, const uint4 *reg, int64_t v0, int64_t v1, F f) {
+    constexpr int kN = Vec<T>::kN;
+    if constexpr (kR > 0) {
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            float x[kN];
+            unpack<T>(reg[i], x);
+            const int64_t e = row.first(v0 + static_cast<int64_t>(i) * blockDim.x + threadIdx.x);
+#pragma unroll
+            for (int q = 0; q < kN; ++q) f(x[q], e + q);
+        }
+    } else {
+        for (int64_t v = v0 + threadIdx.x; v < v1; v += blockDim.x) {
+            float x[kN];
+            unpack<T>(row.load(v), x);
+            const int64_t e = row.first(v);
+#pragma unroll
+            for (int q = 0; q < kN; ++q) f(x[q], e + q);
+        }
+    }
+}
+
+template <typename T, int kR>
+__global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group) {
+    __shared__ TopShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
+    const int64_t r = blockIdx.x / ctas;
+    const uint32_t rank = blockIdx.x % ctas;
+    const RowView<T> row(static_cast<const T *>(a.x) + r * a.ldx, a.n);
+    const int64_t nv = row.vectors(), share = (nv + ctas - 1) / ctas;
+    const int64_t v0 = rank * share, v1 = v0 + share < nv ? v0 + share : nv;
+    uint4 reg[kR > 0 ? kR : 1];
+    if constexpr (kR > 0) {
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            const int64_t v = v0 + static_cast<int64_t>(i) * blockDim.x + tid;
+            float pad[Vec<T>::kN];
+#pragma unroll
+            for (int q = 0; q < Vec<T>::kN; ++q) pad[q] = kNegInf;
+            reg[i] = v < v1 ? row.load(v) : pack<T>(pad);
+        }
+    }
+    if (ctas > 1) cluster_arrive();  // the peers' shared memory may be written from here on ...
+    if (tid < 4) sh.count[tid] = 0;
+    float m = kNegInf;
+    each_value<T, kR>(row, reg, v0, v1, [&](float x, int64_t) { m = fmaxf(m, x); });
+    float g = m;
+    for (int o = 1; o < group; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    const bool want_lse = a.lse || a.weighting == SPMV_WEIGHTS_ROW;
+    float sum = 0.0f;
+    m = warp_max(m);
+    if (want_lse) {
+        const float m0 = reference_of(m);
+        each_value<T, kR>(row, reg, v0, v1, [&](float x, int64_t) { sum += ex2((x - m0) * a.scale); });
+        sum = warp_sum(sum);
+    }
+    if (ctas > 1) cluster_wait();  // ... once they have all started
+    const int per_cta = blockDim.x / group, n_groups = per_cta * ctas;
+    if (tid % group == 0)
+        for (int c = 0; c < ctas; ++c) {
+            float *slot = &sh.group_max[rank * per_cta + tid / group];
+            if (ctas > 1) peer_store(peer_addr(slot, c), g);
+            else *slot = g;
+        }
+    if (lane < ctas) {
+        float2 *slot = &sh.sums[rank * n_warps + warp];
+        if (ctas > 1) peer_store2(peer_addr(slot, lane), m, sum);
+        else *slot = make_float2(m, sum);
+    }
+    cluster_sync(ctas);
+
+    if (tid == 0) sh.thr = kNegInf;
+    __syncthreads();
+    for (int i = tid; i < n_groups; i += blockDim.x) {
+        const float v = sh.group_max[i];
+        int above = 0;
+        for (int j = 0; j < n_groups; ++j) {
+            const float w = sh.group_max[j];
+            above += w > v || (w == v && j < i);
+        }
+        if (above == a.k - 1) sh.thr = v;
+    }
+    __syncthreads();
+    const float thr = fmaxf(sh.thr, -FLT_MAX);  // above -inf: masked entries are never candidates
+
+    const auto collect = [&](auto taken) {
+        int mine = 0;
+        each_value<T, kR>(row, reg, v0, v1, [&](float x, int64_t e) { mine += taken(x, e); });
+        if (mine) {
+            const uint32_t counter = peer_addr(&sh.count[0], 0);
+            uint32_t at = ctas > 1 ? peer_add(counter, mine) : atomicAdd(&sh.count[0], mine);
+            each_value<T, kR>(row, reg, v0, v1, [&](float x, int64_t e) {
+                if (taken(x, e)) {
+                    if (at < kMaxCand) {
+                        if (ctas > 1) peer_store64(peer_addr(&sh.cand[at], 0), composite(x, e));
+                        else sh.cand[at] = composite(x, e);
+                    }
+                    ++at;
+                }
+            });
+        }
+    };
+    collect([&](float x, int64_t) { return !(x < thr); });
+    cluster_sync(ctas);
+    uint32_t found = ctas > 1 ? peer_load(peer_addr(&sh.count[0], 0)) : sh.count[0];
+    if (found > kMaxCand) {
+        unsigned long long lo = static_cast<unsigned long long>(order_key(thr)) << 32, hi = ~0ull, cut = lo;
+        for (int step = 0; step < 64 && found > kMaxCand; ++step) {
+            cut = lo + (hi - lo) / 2;
+            int mine = 0;
+            each_value<T, kR>(row, reg, v0, v1,
+                              [&](float x, int64_t e) { mine += x != kNegInf && composite(x, e) >= cut; });
+            mine = warp_sum(mine);
+            const int slot = 1 + step % 3;
+            if (lane < ctas && mine) {
+                if (ctas > 1) peer_add(peer_addr(&sh.count[slot], lane), mine);
+                else atomicAdd(&sh.count[slot], mine);
+            }
+            cluster_sync(ctas);
+            found = sh.count[slot];
+            if (tid == 0) sh.count[1 + (step + 2) % 3] = 0;  // last read before the previous barrier
+            if (found > kMaxCand) lo = cut;
+            else if (found < static_cast<uint32_t>(a.k)) {
+                hi = cut;
+                found = kMaxCand + 1;
+            }
+        }
+        if (tid == 0) sh.count[0] = 0;
+        cluster_sync(ctas);
+        collect([&](float x, int64_t e) { return x != kNegInf && composite(x, e) >= cut; });
+        cluster_sync(ctas);
+        found = ctas > 1 ? peer_load(peer_addr(&sh.count[0], 0)) : sh.count[0];
+    }
+    // the first CTA stays until the others have read its count; they have nothing left to do
+    if (ctas > 1) {
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) return;
+    }
+
+    // rank 0: the candidates in order, the row's sum
+    if (warp == 0 && want_lse) {
+        float mm = kNegInf;
+        for (int i = lane; i < n_warps * ctas; i += 32) mm = fmaxf(mm, sh.sums[i].x);
+        mm = reference_of(warp_max(mm));
+        float s = 0.0f;
+        for (int i = lane; i < n_warps * ctas; i += 32) {
+            const float2 w = sh.sums[i];  // a warp without a value above -inf adds its 0 (or a NaN)
+            s += w.x == kNegInf ? w.y : w.y * ex2((w.x - mm) * a.scale);
+        }
+        s = warp_sum(s);
+        if (lane == 0) {
+            sh.lse_m = mm;
+            sh.lse_sum = s;
+            if (a.lse) a.lse[r] = fmaf(mm, a.inv_temperature, logf(s));
+        }
+    }
+    const int n_cand = static_cast<int>(found < kMaxCand ? found : kMaxCand);
+    for (int i = tid; i < n_cand; i += blockDim.x) {
+        const unsigned long long c = sh.cand[i];
+        int above = 0;
+        for (int j = 0; j < n_cand; ++j) above += sh.cand[j] > c;
+        if (above < a.k) {
+            const float v = key_value(static_cast<uint32_t>(c >> 32));
+            sh.top_vals[above] = v;
+            a.ids[r * a.k + above] = composite_col(c);
+            a.vals[r * a.k + above] = v;
+        }
+    }
+    for (int j = n_cand + tid; j < a.k; j += blockDim.x) {
+        sh.top_vals[j] = kNegInf;
+        a.ids[r * a.k + j] = -1;
+        a.vals[r * a.k + j] = kNegInf;
+    }
+    if (a.weighting == SPMV_WEIGHTS_NONE) return;
+    __syncthreads();
+    if (warp == 0) {
+        float mm = sh.lse_m, s = sh.lse_sum;
+        if (a.weighting == SPMV_WEIGHTS_SELECTED) {
+            mm = reference_of(sh.top_vals[0]);
+            s = 0.0f;
+            for (int j = lane; j < a.k; j += 32) s += ex2((sh.top_vals[j] - mm) * a.scale);
+            s = warp_sum(s);
+        }
+        for (int j = lane; j < a.k; j += 32) {
+            const float v = sh.top_vals[j];
+            a.weights[r * a.k + j] = v == kNegInf ? 0.0f : ex2((v - mm) * a.scale) / s;
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------
+// gradient of the weights
+// ----------------------------------------------------------------------------
+// With s = sum over j of w_j dw_j, both weightings give dx[id_j] = w_j (dw_j - s) / temperature;
+// elsewhere dx is 0 (weights over the chosen entries) or -q s / temperature with
+// q = exp(x / temperature - lse) (weights over the whole row).  A warp writes a piece of a
+// row; __syncwarp orders its plain stores before the stores to the chosen columns.
+constexpr int kGradPiece = 1024;  // values per warp
+
+struct TopGradArgs {
+    int64_t rows, n, ldx, lddx, pieces;
+    int k, weighting;
+    float inv_temperature;
+    const int32_t *ids;
+    const float *weights, *dweights, *lse;
+    const void *x;
+    void *dx;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_topk_grad(TopGradArgs a) {
+    constexpr int kN = Vec<T>::kN;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t r = item / a.pieces;
+    if (r >= a.rows) return;
+    T *out = static_cast<T *>(a.dx) + r * a.lddx;
+    const RowView<T> view(out, a.n);
+    const int64_t per = kGradPiece / kN, nv = view.vectors();
+    const int64_t v0 = (item - r * a.pieces) * per, v1 = v0 + per < nv ? v0 + per : nv;
+    const int32_t *ids = a.ids + r * a.k;
+    const float *w = a.weights + r * a.k, *dw = a.dweights + r * a.k;
+    float s = 0.0f;
+    for (int j = lane; j < a.k; j += 32)
+        if (ids[j] >= 0) s = fmaf(w[j], dw[j], s);
+    s = warp_sum(s);
+    const bool whole_row = a.weighting == SPMV_WEIGHTS_ROW;
+    const T *x = static_cast<const T *>(a.x) + (whole_row ? r * a.ldx : 0);
+    const float lse = whole_row ? a.lse[r] : 0.0f;
+    const float factor = -s * a.inv_temperature;
+    for (int64_t v = v0 + lane; v < v1; v += 32) {
+        float f[kN] = {};
+        if (whole_row) {
+            const int64_t e = view.first(v);
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (e + i >= 0 && e + i < a.n) {
+                    const float xi = to_f32(x[e + i]);
+                    f[i] = xi == kNegInf ? 0.0f : factor * ex2(fmaf(xi, a.inv_temperature, -lse) * kLog2e);
+                }
+        }
+        store_vec<T>(out, view, v, f, true);
+    }
+    __syncwarp();
+    const int64_t e0 = view.first(v0), e1 = view.first(v1);
+    for (int j = lane; j < a.k; j += 32) {
+        const int32_t id = ids[j];
+        if (id >= e0 && id < e1 && id >= 0 && id < a.n) out[id] = from_f32<T>(w[j] * (dw[j] - s) * a.inv_temperature);
+    }
+}
+
+template <typename T>
+cudaError_t launch_topk_warp(const TopArgs &a, cudaStream_t s) {
+    const unsigned grid = static_cast<unsigned>(ceil_div(a.rows, 8));
+    if (a.n <= 64) k_topk_warp<T, 2><<<grid, 256, 0, s>>>(a);
+    else if (a.n <= 128) k_topk_warp<T, 4><<<grid, 256, 0, s>>>(a);
+    else if (a.n <= 256) k_topk_warp<T, 8><<<grid, 256, 0, s>>>(a);
+    else k_topk_warp<T, 16><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_topk_row(const TopArgs &a, cudaStream_t s) {
+    const int threads = 512, ctas = 1, group = 1;
+    return launch_rows(k_topk_row<T, 0>, a.rows * ctas, threads, ctas, 0, s, a, ctas, group);
+}
+
+template <typename T>
+cudaError_t launch_topk(const TopArgs &a, cudaStream_t s) {
+    return a.n <= kGateMaxN && a.k <= kGateMaxK ? launch_topk_warp<T>(a, s) : launch_topk_row<T>(a, s);
+}
+
+int check_top(int64_t rows, int64_t n, int32_t k, int dtype, double temperature) {
+    if (!row_dtype_ok(dtype)) return refuse("dtype must be SPMV_F32, SPMV_F16 or SPMV_BF16");
+    if (k < 1 || k > kMaxTop || k > n)
+        return refuse("k must lie in [1, min(n, " + std::to_string(kMaxTop) + ")]");
+    if (!(temperature > 0.0) || !(temperature <= 1e6) || temperature < 1e-6)
+        return refuse("temperature must lie in [1e-6, 1e6]");
+    if (rows * static_cast<int64_t>(k) >= (int64_t(1) << 40)) return set_error(SPMV_ERR_TOO_LARGE, "rows * k is too large");
+    return SPMV_OK;
+}
+
+}  // namespace
+}  // namespace spmv
+
+using namespace spmv;
+
+extern "C" SPMV_API int spmv_topk_rows(int64_t rows, int64_t n, int32_t k, const void *x, int64_t ldx, int dtype,
+                                       double temperature, int weighting, int32_t *ids, float *vals, float *weights,
+                                       float *lse, void *stream) {
+    SPMV_TRY(check_shape(rows, n, ldx, "x"));
+    SPMV_TRY(check_top(rows, n, k, dtype, temperature));
+    if (weighting < SPMV_WEIGHTS_NONE || weighting > SPMV_WEIGHTS_ROW) return refuse("no such weighting");
+    if (rows == 0) return SPMV_OK;
+    const int vb = row_value_bytes(dtype);
+    SPMV_TRY(check_array(x, "x", vb));
+    SPMV_TRY(check_array(ids, "ids", 4));
+    SPMV_TRY(check_array(vals, "vals", 4));
+    if (weighting != SPMV_WEIGHTS_NONE) SPMV_TRY(check_array(weights, "weights", 4));
+    if (lse) SPMV_TRY(check_array(lse, "lse", 4));
+    const size_t xb = span_bytes(rows, n, ldx, vb), m = static_cast<size_t>(rows) * k * 4;
+    const struct { const void *p; size_t bytes; const char *name; } out[] = {
+        {ids, m, "ids"}, {vals, m, "vals"}, {weighting ? weights : nullptr, m, "weights"}, {lse, static_cast<size_t>(rows) * 4, "lse"}};
+    for (int i = 0; i < 4; ++i) {
+        if (out[i].p && spans_overlap(out[i].p, out[i].bytes, x, xb)) return refuse(std::string(out[i].name) + " overlaps x");
+        for (int j = 0; j < i; ++j)
+            if (out[i].p && out[j].p && spans_overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                return refuse(std::string(out[i].name) + " overlaps " + out[j].name);
+    }
+    const TopArgs a{rows, n, ldx, k, weighting, static_cast<float>(1.4426950408889634 / temperature),
+                    static_cast<float>(1.0 / temperature), x, ids, vals, weights, lse};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    SPMV_TRY_CUDA(dtype == SPMV_F32   ? launch_topk<float>(a, s)
+                  : dtype == SPMV_F16 ? launch_topk<__half>(a, s)
+                                      : launch_topk<__nv_bfloat16>(a, s));
+    return SPMV_OK;
+}
+
+extern "C" SPMV_API int spmv_topk_rows_grad(int64_t rows, int64_t n, int32_t k, const int32_t *ids,
+                                            const float *weights, const float *dweights, int weighting,
+                                            double temperature, const void *x, int64_t ldx, const float *lse, void *dx,
+                                            int64_t lddx, int dtype, void *stream) {
+    SPMV_TRY(check_shape(rows, n, lddx, "dx"));
+    SPMV_TRY(check_top(rows, n, k, dtype, temperature));
+    if (weighting != SPMV_WEIGHTS_SELECTED && weighting != SPMV_WEIGHTS_ROW) return refuse("no such weighting, or none");
+    const bool whole_row = weighting == SPMV_WEIGHTS_ROW;
+    if (whole_row) SPMV_TRY(check_shape(rows, n, ldx, "x"));
+    if (rows == 0) return SPMV_OK;
+    const int vb = row_value_bytes(dtype);
+    SPMV_TRY(check_array(ids, "ids", 4));
+    SPMV_TRY(check_array(weights, "weights", 4));
+    SPMV_TRY(check_array(dweights, "dweights", 4));
+    SPMV_TRY(check_array(dx, "dx", vb));
+    if (whole_row) {
+        SPMV_TRY(check_array(x, "x", vb));
+        SPMV_TRY(check_array(lse, "lse", 4));
+    }
+    const size_t out = span_bytes(rows, n, lddx, vb), m = static_cast<size_t>(rows) * k * 4;
+    const struct { const void *p; size_t bytes; const char *name; } in[] = {
+        {ids, m, "ids"}, {weights, m, "weights"}, {dweights, m, "dweights"},
+        {whole_row ? x : nullptr, span_bytes(rows, n, ldx, vb), "x"}, {whole_row ? lse : nullptr, static_cast<size_t>(rows) * 4, "lse"}};
+    for (const auto &i : in)
+        if (i.p && spans_overlap(dx, out, i.p, i.bytes)) return refuse(std::string("dx overlaps ") + i.name);
+    // a row may start up to 15 bytes behind a 16-byte boundary: one vector more
+    const int64_t pieces = ceil_div(n + 16 / vb - 1, kGradPiece);
+    const TopGradArgs a{rows, n, ldx, lddx, pieces, k, weighting,
+                        static_cast<float>(1.0 / temperature), ids, weights, dweights, lse, x, dx};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = static_cast<unsigned>(ceil_div(rows * pieces, 8));
+    if (dtype == SPMV_F32) k_topk_grad<float><<<grid, 256, 0, s>>>(a);
+    else if (dtype == SPMV_F16) k_topk_grad<__half><<<grid, 256, 0, s>>>(a);
+    else k_topk_grad<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    SPMV_TRY_CUDA(cudaGetLastError());
+    return SPMV_OK;
+}

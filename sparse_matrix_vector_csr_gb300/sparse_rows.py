@@ -1,0 +1,283 @@
+"""Sparse rows: at most k entries in every row of a matrix that is made anew at each step.
+
+    top = spmv.topk_rows(router_logits, k, weights="selected")     # a router's choice
+    plan = spmv.RoutePlan(top.ids, experts, align=128)              # rows sorted by expert
+    xs = plan.dispatch(x)                                           # tokens out ...
+    y = plan.combine(ys, top.weights)                               # ... and back, weighted
+    dys, dw = plan.combine_grad(dy, ys, top.weights)
+    dx, dlogits = plan.dispatch_grad(dxs), top.grad(dw)
+
+    t = spmv.topk_rows(teacher_logits, 64, lse=True)                # a teacher's top logits
+    loss, dz = spmv.distill_loss_grad(z, t.ids, t.vals, teacher_lse=t.lse, scale=1 / len(z))
+
+Every function takes CUDA tensors, enqueues on the current (or given) stream and returns
+without waiting.  Results are allocated on that stream.  Gradients are functions of their
+own; nothing is recorded by autograd.  The semantics are those of ``include/spmv.h``.
+"""
+from __future__ import annotations
+
+import torch
+
+from ._abi import SPMV_BF16, SPMV_F16, SPMV_F32, WEIGHTINGS, _check, lib
+
+_DTYPES = {torch.float32: SPMV_F32, torch.float16: SPMV_F16, torch.bfloat16: SPMV_BF16}
+
+
+class _On:
+    """The stream of a call: ``handle`` for the library; on a stream other than the current
+    one, allocations are made for it and the inputs are kept until it has read them."""
+
+    __slots__ = ("handle", "_ctx")
+
+    def __init__(self, stream, inputs):
+        self._ctx = None
+        if stream is None:
+            self.handle = torch.cuda.current_stream().cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        self.handle = stream.cuda_stream
+        if self.handle != torch.cuda.current_stream().cuda_stream:
+            self._ctx = torch.cuda.stream(stream)
+            for t in inputs:
+                if t is not None and t.is_cuda:
+                    t.record_stream(stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _matrix(t, name, rows=None, cols=None, dtype=None):
+    """(type code, leading dimension) of a row-major matrix of one of the row types."""
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must be {rows if rows is not None else r} x {cols if cols is not None else c}, "
+                         f"not {r} x {c}")
+    s0, s1 = t.stride()
+    if c > 1 and s1 != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if r > 1 and s0 < c:
+        raise ValueError(f"{name} has overlapping rows")
+    return code, (s0 if r > 1 else c)
+
+
+def _plain(t, name, shape, dtype):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or None
+
+
+def _out(t, name, like, rows, cols):
+    """A new matrix of `like`'s type, or the checked one given, with its leading dimension."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=like.dtype, device=like.device), cols
+    return t, _matrix(t, name, rows, cols, like.dtype)[1]
+
+
+class TopRows:
+    """The k largest entries of every row of ``x``: ``ids`` (int32, -1 = none), ``vals``, and,
+    where asked for, ``weights`` and ``lse`` (float32)."""
+
+    __slots__ = ("ids", "vals", "weights", "lse", "_x", "_weighting", "_temperature")
+
+    def grad(self, dweights, out=None, stream=None):
+        """The gradient in x of a loss whose gradient in the weights is ``dweights``."""
+        if not self._weighting:
+            raise ValueError("topk_rows was called without weights")
+        x, (rows, k) = self._x, self.ids.shape
+        code, ldx = _matrix(x, "x")
+        dw = _plain(dweights, "dweights", self.ids.shape, torch.float32)
+        with _On(stream, (x, self.ids, self.weights, self.lse, dweights, out)) as s:
+            dx, lddx = _out(out, "out", x, rows, x.shape[1])
+            _check(lib.spmv_topk_rows_grad(rows, x.shape[1], k, self.ids.data_ptr(), self.weights.data_ptr(), dw,
+                                           self._weighting, self._temperature, x.data_ptr(), ldx,
+                                           self.lse.data_ptr() if self.lse is not None else None, dx.data_ptr(), lddx,
+                                           code, s))
+        return dx
+
+
+def topk_rows(x, k, temperature=1.0, weights=None, lse=False, stream=None) -> TopRows:
+    """The k largest entries of every row of x, values descending, ties to the lowest column;
+    -inf is never taken (its id is -1).  ``weights``: None, "selected" (softmax over the
+    chosen) or "row" (softmax over the row); ``lse``: also the row's log-sum-exp.  Both at
+    ``temperature``.  1 <= k <= min(n, 256)."""
+    code, ldx = _matrix(x, "x")
+    rows, n = x.shape
+    top = TopRows()
+    top._x, top._weighting, top._temperature = x, WEIGHTINGS[weights], float(temperature)
+    if not 1 <= k <= min(n, 256):
+        raise ValueError("k must lie in [1, min(n, 256)]")
+    with _On(stream, (x,)) as s:
+        top.ids = torch.empty((rows, k), dtype=torch.int32, device=x.device)
+        top.vals = torch.empty((rows, k), dtype=torch.float32, device=x.device)
+        top.weights = torch.empty_like(top.vals) if top._weighting else None
+        # the gradient of weights over the row needs lse too
+        top.lse = (torch.empty((rows,), dtype=torch.float32, device=x.device)
+                   if lse or top._weighting == WEIGHTINGS["row"] else None)
+        _check(lib.spmv_topk_rows(rows, n, k, x.data_ptr(), ldx, code, top._temperature, top._weighting,
+                                  top.ids.data_ptr(), top.vals.data_ptr(),
+                                  top.weights.data_ptr() if top._weighting else None,
+                                  top.lse.data_ptr() if top.lse is not None else None, s))
+    return top
+
+
+class RoutePlan:
+    """Rows sorted by expert: the plan of one choice ``ids`` (int32, tokens x k; an entry
+    outside [0, experts) is dropped).  ``rows`` is the sorted matrix's number of rows;
+    ``offsets`` (experts + 1), ``slots`` (tokens x k) and ``sources`` (rows) as in spmv.h."""
+
+    def __init__(self, ids, experts, align=1, stream=None):
+        if ids.dim() != 2:
+            raise ValueError("ids must be a matrix")
+        ptr = _plain(ids, "ids", ids.shape, torch.int32)
+        self.tokens, self.k = ids.shape
+        self.experts, self.align = int(experts), int(align)
+        self.rows = _check(lib.spmv_route_rows(self.tokens, self.k, self.experts, self.align))
+        work = _check(lib.spmv_route_workspace(self.tokens, self.k, self.experts))
+        m, dev = self.tokens * self.k, ids.device
+        with _On(stream, (ids,)) as s:
+            # one allocation: slots, sources, offsets, workspace
+            self._buf = torch.empty((m + self.rows + self.experts + 1 + work // 4,), dtype=torch.int32, device=dev)
+            base = self._buf.data_ptr()
+            self._slots, self._sources = base, base + 4 * m
+            self._offsets = self._sources + 4 * self.rows
+            _check(lib.spmv_route_plan(self.tokens, self.k, self.experts, self.align, ptr, self._offsets, self._slots,
+                                       self._sources, self._offsets + 4 * (self.experts + 1), work, s))
+
+    @property
+    def slots(self):
+        return self._buf[:self.tokens * self.k].view(self.tokens, self.k)
+
+    @property
+    def sources(self):
+        a = self.tokens * self.k
+        return self._buf[a:a + self.rows]
+
+    @property
+    def offsets(self):
+        a = self.tokens * self.k + self.rows
+        return self._buf[a:a + self.experts + 1]
+
+    def dispatch(self, x, out=None, stream=None):
+        """The tokens' rows sorted by expert (rows x d); rows without a source are 0."""
+        code, ldx = _matrix(x, "x", self.tokens)
+        d = x.shape[1]
+        with _On(stream, (x, out, self._buf)) as s:
+            xs, ldxs = _out(out, "out", x, self.rows, d)
+            _check(lib.spmv_route_dispatch(self.tokens, self.k, self.rows, d, self._slots, self._sources, x.data_ptr(),
+                                           ldx, xs.data_ptr(), ldxs, code, s))
+        return xs
+
+    def combine(self, ys, weights=None, out=None, stream=None):
+        """y[t] = sum over j of weights[t, j] ys[slots[t, j]] (weights None: all 1)."""
+        code, ldys = _matrix(ys, "ys", self.rows)
+        d = ys.shape[1]
+        w = None if weights is None else _plain(weights, "weights", (self.tokens, self.k), torch.float32)
+        with _On(stream, (ys, weights, out, self._buf)) as s:
+            y, ldy = _out(out, "out", ys, self.tokens, d)
+            _check(lib.spmv_route_combine(self.tokens, self.k, self.rows, d, self._slots, w, ys.data_ptr(), ldys,
+                                          y.data_ptr(), ldy, code, s))
+        return y
+
+    def combine_grad(self, dy, ys, weights, out=None, stream=None):
+        """(dys, dweights): the gradients of combine in ys and in the weights."""
+        code, lddy = _matrix(dy, "dy", self.tokens)
+        d = dy.shape[1]
+        ldys = _matrix(ys, "ys", self.rows, d, dy.dtype)[1]
+        w = _plain(weights, "weights", (self.tokens, self.k), torch.float32)
+        with _On(stream, (dy, ys, weights, out, self._buf)) as s:
+            dys, lddys = _out(out, "out", dy, self.rows, d)
+            dw = torch.empty((self.tokens, self.k), dtype=torch.float32, device=dy.device)
+            _check(lib.spmv_route_combine_grad(self.tokens, self.k, self.rows, d, self._slots, self._sources, w,
+                                               dy.data_ptr(), lddy, ys.data_ptr(), ldys, dys.data_ptr(), lddys,
+                                               dw.data_ptr(), code, s))
+        return dys, dw
+
+    def dispatch_grad(self, dxs, out=None, stream=None):
+        """The gradient of dispatch: dx[t] = sum over j of dxs[slots[t, j]]."""
+        return self.combine(dxs, None, out, stream)
+
+
+class DistillLoss:
+    """``loss`` (float32, one a row, neither averaged nor scaled) and what its gradient needs."""
+
+    __slots__ = ("loss", "stats", "_args")
+
+    def grad(self, dloss=None, scale=1.0, out=None, stream=None):
+        """scale * dloss[t] * d loss[t] / d z[t] (dloss float32, None = all 1).  ``out`` may be
+        the logits themselves, which the gradient then replaces."""
+        z, ids, teacher, lse, temperature = self._args
+        code, ldz = _matrix(z, "z")
+        rows, vocab = z.shape
+        g = None if dloss is None else _plain(dloss, "dloss", (rows,), torch.float32)
+        with _On(stream, (z, ids, teacher, lse, self.stats, dloss, out)) as s:
+            dz, lddz = _out(out, "out", z, rows, vocab)
+            _check(lib.spmv_distill_grad(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, ids.data_ptr(),
+                                         teacher.data_ptr(), _DTYPES[teacher.dtype],
+                                         None if lse is None else lse.data_ptr(), temperature, self.stats.data_ptr(),
+                                         scale, g, dz.data_ptr(), lddz, s))
+        return dz
+
+
+def _distill_args(z, ids, teacher, teacher_lse):
+    code, ldz = _matrix(z, "z")
+    rows = z.shape[0]
+    if ids.dim() != 2 or ids.shape[0] != rows:
+        raise ValueError(f"ids must be a matrix of {rows} rows")
+    i = _plain(ids, "ids", ids.shape, torch.int32)
+    tcode = _DTYPES.get(teacher.dtype)
+    if tcode is None:
+        raise TypeError(f"teacher must be float32, float16 or bfloat16, not {teacher.dtype}")
+    t = _plain(teacher, "teacher", ids.shape, teacher.dtype)
+    lse = None if teacher_lse is None else _plain(teacher_lse, "teacher_lse", (rows,), torch.float32)
+    return code, ldz, i, t, tcode, lse
+
+
+def distill_loss(z, ids, teacher, teacher_lse=None, temperature=1.0, stream=None) -> DistillLoss:
+    """The loss of logits z (rows x vocab) against a teacher's top logits: columns ``ids``
+    (int32, rows x k, -1 = none, a column at most once) with logits ``teacher``.  With
+    ``teacher_lse`` (the teacher's log-sum-exp over the whole vocabulary at the same
+    temperature) the other columns count as one more class; without it the teacher's
+    distribution is the softmax over the given entries."""
+    code, ldz, i, t, tcode, lse = _distill_args(z, ids, teacher, teacher_lse)
+    rows, vocab = z.shape
+    res = DistillLoss()
+    res._args = (z, ids, teacher, teacher_lse, float(temperature))
+    with _On(stream, (z, ids, teacher, teacher_lse)) as s:
+        res.loss = torch.empty((rows,), dtype=torch.float32, device=z.device)
+        res.stats = torch.empty((rows, 4), dtype=torch.float32, device=z.device)
+        _check(lib.spmv_distill_loss(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, i, t, tcode, lse,
+                                     res._args[4], res.loss.data_ptr(), res.stats.data_ptr(), s))
+    return res
+
+
+def distill_loss_grad(z, ids, teacher, teacher_lse=None, temperature=1.0, scale=1.0, row_scale=None, out=None,
+                      stream=None):
+    """(loss, dz): :func:`distill_loss` and its gradient scale * row_scale[t] * d loss[t] / d z[t],
+    reading z once.  ``out`` may be z itself, which the gradient then replaces."""
+    code, ldz, i, t, tcode, lse = _distill_args(z, ids, teacher, teacher_lse)
+    rows, vocab = z.shape
+    g = None if row_scale is None else _plain(row_scale, "row_scale", (rows,), torch.float32)
+    with _On(stream, (z, ids, teacher, teacher_lse, row_scale, out)) as s:
+        loss = torch.empty((rows,), dtype=torch.float32, device=z.device)
+        dz, lddz = _out(out, "out", z, rows, vocab)
+        _check(lib.spmv_distill_loss_grad(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, i, t, tcode, lse,
+                                          float(temperature), loss.data_ptr(), scale, g, dz.data_ptr(), lddz, s))
+    return loss, dz
