@@ -12,13 +12,12 @@
 // (the student may put nearly everything on the entries): a bit per value of the row marks the
 // entries' columns, which the row's sums then leave out; the entries' own sum joins at the end.
 //
-// The row is what costs: V values read, V written.  One pass takes each thread's share into
-// registers, a warp's maximum and sum (relative to its own maximum), one exchange joins the
-// warps of the CTA or of the cluster that share the row, and the gradient leaves from the same
-// registers, so z is read once and dz written once.  Rows that do not fit the registers of a
-// cluster are read again (from L2) by each step.
-//
-// The entries (at most kMaxEntries) are warp 0's business while the row's loads are in flight.
+// The row is what costs: V values read, V written.  Long rows pass through the registers twice,
+// once for the sums (maximum and sum together, rescaled when a thread's maximum grows) and once for
+// the gradient, the second time from L2; rows that fit the registers of a CTA stay there.  Few
+// rows are shared by a cluster of CTAs each, which exchange their warps' sums through
+// distributed shared memory.  The entries (at most kMaxEntries) are the business of each CTA's
+// last warp while the others read the row.
 #pragma once
 
 #include "rows_common.cuh"
@@ -50,7 +49,7 @@ struct DistillArgs {
 
 struct DistillShared {
     // per warp of the cluster: maximum and sum of its columns (with lse: of those that are no
-    // entries, and in z, w of its CTA's entries, from warp 0)
+    // entries, and in z, w of its CTA's entries, from its last warp)
     float4 warp_part[kMaxCluster * 16];
     int32_t id[kMaxEntries];             // column, or -1
     float p[kMaxEntries], z[kMaxEntries];  // z: see load_entries
@@ -58,7 +57,7 @@ struct DistillShared {
     int valid;
 };
 
-// Warp 0: the entries' probabilities, and z at those of columns [e0, e1) (the CTA's own, or all
+// One warp: the entries' probabilities, and z at those of columns [e0, e1) (the CTA's own, or all
 // for the CTA that sums the loss).
 template <typename T>
 __device__ __forceinline__ void load_entries(const DistillArgs &a, DistillShared &sh, int64_t r, const T *z, int64_t e0,
@@ -112,89 +111,124 @@ __device__ __forceinline__ void load_entries(const DistillArgs &a, DistillShared
     }
 }
 
-// f(values[kN], vector) over this thread's vectors of [v0, v1)
-template <typename T, int kR, typename F>
-__device__ __forceinline__ void each_vector(const RowView<T> &row, const uint4 *reg, int64_t v0, int64_t v1, F f) {
-    if constexpr (kR > 0) {
+// -inf in the places of the marked values
+template <typename T>
+__device__ __forceinline__ void mask_vec(uint4 &v, uint32_t marked) {
+    if (marked) {
+        float x[Vec<T>::kN];
+        unpack<T>(v, x);
 #pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            const int64_t v = v0 + static_cast<int64_t>(i) * blockDim.x + threadIdx.x;
-            float x[Vec<T>::kN];
-            unpack<T>(reg[i], x);
-            if (v < v1) f(x, v);
-        }
-    } else {
-        for (int64_t v = v0 + threadIdx.x; v < v1; v += blockDim.x) {
-            float x[Vec<T>::kN];
-            unpack<T>(row.load(v), x);
-            f(x, v);
-        }
+        for (int i = 0; i < Vec<T>::kN; ++i)
+            if (marked >> i & 1) x[i] = kNegInf;
+        v = pack<T>(x);
     }
 }
 
+// scale_signed * exp2((x - ref) scale2) of a vector.  16-bit results take the factor's logarithm
+// into the exponent (one operation less a value, its rounding far below theirs).
+template <typename T>
+struct GradOf {
+    float ref, scale2, factor, log_factor;
+    uint32_t flip;  // the factor's sign, for both values of a word
+    __device__ __forceinline__ GradOf(float ref_, float scale2_, float factor_)
+        : ref(ref_), scale2(scale2_), factor(factor_), log_factor(log2f(fabsf(factor_))), flip(factor_ < 0.0f ? 0x80008000u : 0u) {}
+    __device__ __forceinline__ uint4 operator()(const uint4 &v) const {
+        float x[Vec<T>::kN];
+        unpack<T>(v, x);
+#pragma unroll
+        for (int i = 0; i < Vec<T>::kN; i += 2) {
+            float2 d = add2(make_float2(x[i], x[i + 1]), both(-ref));
+            if constexpr (sizeof(T) == 2) {
+                d = fma2(d, both(scale2), both(log_factor));
+                x[i] = ex2(d.x);
+                x[i + 1] = ex2(d.y);
+            } else {
+                d = mul2(d, both(scale2));
+                d = mul2(make_float2(ex2(d.x), ex2(d.y)), both(factor));
+                x[i] = d.x;
+                x[i + 1] = d.y;
+            }
+        }
+        uint4 o = pack<T>(x);
+        if constexpr (sizeof(T) == 2) o = make_uint4(o.x ^ flip, o.y ^ flip, o.z ^ flip, o.w ^ flip);
+        return o;
+    }
+};
+
 template <typename T, int kR, int kMode>
-__global__ void __launch_bounds__(512) k_distill(DistillArgs a, int ctas) {
+__global__ void __launch_bounds__(512, 2) k_distill(DistillArgs a, int ctas) {
     constexpr int kN = Vec<T>::kN;
+    constexpr int kU = 4;  // vectors in flight per thread where the row is read twice
     __shared__ DistillShared sh;
     extern __shared__ uint32_t marks_mem[];  // with lse: a byte per vector of the CTA's share, a bit per value
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
+    const int workers = blockDim.x - 32;
+    const bool entry_warp = tid >= workers;
     const int64_t r = blockIdx.x / ctas;
     const uint32_t rank = blockIdx.x % ctas;
     const T *z = static_cast<const T *>(a.z) + r * a.ldz;
     const RowView<T> row(z, a.n);
-    const int64_t nv = row.vectors(), share = (nv + ctas - 1) / ctas;
-    const int64_t v0 = rank * share < nv ? rank * share : nv, v1 = v0 + share < nv ? v0 + share : nv;
-    const int64_t e0 = row.first(v0), e1 = row.first(v1);
+    const Share<T> share(row, rank, ctas);
     const bool tail = a.teacher_lse != nullptr;
-    const auto own = [&](int32_t id) { return id >= 0 && id >= e0 && id < e1; };
+    const auto own = [&](int32_t id) { return id >= 0 && share.owns(id); };
     uint4 reg[kR > 0 ? kR : 1];
-    if constexpr (kR > 0) {
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            const int64_t v = v0 + static_cast<int64_t>(i) * blockDim.x + tid;
-            if (v < v1) reg[i] = row.load(v);
-        }
-    }
+    if constexpr (kR > 0)
+        if (!entry_warp) load_share<T, kR>(share, tid, workers, reg);
     if (kMode != kGrad && ctas > 1) cluster_arrive();  // the peers' shared memory may be written ...
     const uint8_t *marks = reinterpret_cast<const uint8_t *>(marks_mem);
-    if (kMode != kGrad && tail)
-        for (int64_t i = tid; i < (share + 3) / 4; i += blockDim.x) marks_mem[i] = 0;
-    if (warp == 0) {
+    if (kMode != kGrad && tail) {
+        // marked from the ids alone: the row waits for nothing else of its entries
+        int32_t id = tid < a.k ? a.ids[r * a.k + tid] : -1;
+        for (int i = tid; i < (share.count + 3) / 4; i += blockDim.x) marks_mem[i] = 0;
+        __syncthreads();
+        for (int j = tid; j < a.k; j += blockDim.x) {
+            if (j != tid) id = a.ids[r * a.k + j];
+            if (id < a.n && own(id)) {
+                const uint32_t at = static_cast<uint32_t>(id - share.e0), byte = at / kN;
+                atomicOr(&marks_mem[byte / 4], 1u << (byte % 4 * 8 + at % kN));
+            }
+        }
+        __syncthreads();
+    }
+    if (entry_warp) {
         const bool sums_loss = kMode != kGrad && rank == 0;
-        load_entries<T>(a, sh, r, z, sums_loss ? 0 : e0, sums_loss ? a.n : e1);
+        load_entries<T>(a, sh, r, z, sums_loss ? 0 : share.e0, sums_loss ? a.n : share.first(share.count));
     }
 
     // of all columns; of the others (with lse)
     float m, sum, m_rest = 0.0f, rest_sum = 0.0f;
     if constexpr (kMode != kGrad) {
-        if (tail) {
-            __syncthreads();
-            for (int j = tid; j < a.k; j += blockDim.x) {
-                const int32_t id = sh.id[j];
-                if (own(id)) {
-                    const uint32_t at = static_cast<uint32_t>(id - e0), byte = at / kN;
-                    atomicOr(&marks_mem[byte / 4], 1u << (byte % 4 * 8 + at % kN));
-                }
-            }
-            __syncthreads();
-        }
-        const auto others = [&](const float *x, int64_t v, auto f) {
-            const uint32_t skip = tail ? marks[v - v0] : 0;
+        float wm = kNegInf, ws = 0.0f, em = kNegInf, es = 0.0f;
+        if (!entry_warp) {
+            if constexpr (kR > 0) {
+                if (tail) {
 #pragma unroll
-            for (int i = 0; i < kN; ++i) f(skip >> i & 1 ? kNegInf : x[i]);
-        };
-        float wm = kNegInf, ws = 0.0f;
-        each_vector<T, kR>(row, reg, v0, v1, [&](const float *x, int64_t v) {
-            others(x, v, [&](float xi) { wm = fmaxf(wm, xi); });
-        });
-        wm = warp_max(wm);
-        const float w0 = reference_of(wm);
-        each_vector<T, kR>(row, reg, v0, v1, [&](const float *x, int64_t v) {
-            others(x, v, [&](float xi) { ws += ex2((xi - w0) * a.scale2); });
-        });
-        ws = warp_sum(ws);
-        float em = kNegInf, es = 0.0f;
-        if (tail && warp == 0) {
+                    for (int i = 0; i < kR; ++i)
+                        if (i * workers + tid < share.count) mask_vec<T>(reg[i], marks[i * workers + tid]);
+                }
+#pragma unroll
+                for (int i = 0; i < kR; ++i) wm = fmaxf(wm, vec_max(reg[i], T()));
+                wm = warp_max(wm);
+                const float w0 = reference_of(wm);
+                float2 s2 = both(0.0f);
+#pragma unroll
+                for (int i = 0; i < kR; ++i) s2 = exp_sum<T>(reg[i], w0, a.scale2, s2);
+                ws = s2.x + s2.y;
+            } else {
+                Running run;
+                stream_share<T, kU, kMode == kLoss>(share, tid, workers, [&](uint4 *x, int v, int have) {
+                    if (tail) {
+#pragma unroll
+                        for (int i = 0; i < kU; ++i)
+                            if (i < have) mask_vec<T>(x[i], marks[v + i * workers]);
+                    }
+                    run.add<T, kU>(x, a.scale2);
+                });
+                wm = warp_max(run.m);
+                ws = run.sum();
+                if (run.m != kNegInf) ws *= ex2((run.m - wm) * a.scale2);
+            }
+        } else if (tail) {
             for (int j = lane; j < a.k; j += 32)
                 if (own(sh.id[j])) em = fmaxf(em, sh.z[j]);
             em = warp_max(em);
@@ -203,6 +237,7 @@ __global__ void __launch_bounds__(512) k_distill(DistillArgs a, int ctas) {
                 if (own(sh.id[j])) es += ex2((sh.z[j] - m0) * a.scale2);
             es = warp_sum(es);
         }
+        ws = warp_sum(ws);
         if (ctas > 1) cluster_wait();  // ... once they have started
         if (lane < ctas) {
             float4 *slot = &sh.warp_part[rank * n_warps + warp];
@@ -232,7 +267,7 @@ __global__ void __launch_bounds__(512) k_distill(DistillArgs a, int ctas) {
         rest_sum = warp_sum(rest_sum);
         sum = rest_sum;
         if (tail) sum = warp_sum(es) + (rest_sum != 0.0f ? scaled(rest_sum, m_rest, m) : 0.0f);
-        if (rank == 0 && warp == 0) {
+        if (rank == 0 && entry_warp) {
             float cross = 0.0f;  // sum p (z - m)
             for (int j = lane; j < a.k; j += 32)
                 if (sh.id[j] >= 0 && sh.p[j] != 0.0f) cross = fmaf(sh.p[j], sh.z[j] - m, cross);
@@ -268,12 +303,25 @@ __global__ void __launch_bounds__(512) k_distill(DistillArgs a, int ctas) {
         }
         T *dz = static_cast<T *>(a.dz) + r * a.lddz;
         const bool congruent = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-        each_vector<T, kR>(row, reg, v0, v1, [&](const float *x, int64_t v) {
-            float o[kN];
+        if (!entry_warp) {
+            if (!live) {
+                const uint4 zero = splat<T>(0.0f);
+                for (int v = tid; v < share.count; v += workers) share.store(dz, v, zero, congruent);
+            } else {
+                const GradOf<T> grad(ref, a.scale2, o_scale);
+                if constexpr (kR > 0) {
 #pragma unroll
-            for (int i = 0; i < kN; ++i) o[i] = live ? ex2((x[i] - ref) * a.scale2) * o_scale : 0.0f;
-            store_vec<T>(dz, row, v, o, congruent);
-        });
+                    for (int i = 0; i < kR; ++i)
+                        if (i * workers + tid < share.count) share.store(dz, i * workers + tid, grad(reg[i]), congruent);
+                } else {
+                    stream_share<T, kU, true>(share, tid, workers, [&](uint4 *x, int v, int have) {
+#pragma unroll
+                        for (int i = 0; i < kU; ++i)
+                            if (i < have) share.store(dz, v + i * workers, grad(x[i]), congruent);
+                    });
+                }
+            }
+        }
         __syncthreads();  // the entries' columns are written after the plain stores
         if (live)
             for (int j = tid; j < a.k; j += blockDim.x) {
@@ -283,17 +331,29 @@ __global__ void __launch_bounds__(512) k_distill(DistillArgs a, int ctas) {
     }
 }
 
-template <typename T, int kMode>
-cudaError_t launch_distill_mode(const DistillArgs &a, cudaStream_t s) {
-    const int ctas = 1, threads = 512;
-    const int64_t share = ceil_div(ceil_div(a.n + Vec<T>::kN - 1, Vec<T>::kN), ctas);
-    const size_t smem = kMode != kGrad && a.teacher_lse ? static_cast<size_t>((share + 3) / 4 * 4) : 0;
-    auto *kernel = k_distill<T, 0, kMode>;
-    if (smem > 16 * 1024) {
+template <typename T, int kR, int kMode>
+cudaError_t launch_distill_shape(const RowShape &shape, int64_t vectors, const DistillArgs &a, cudaStream_t s) {
+    auto *kernel = k_distill<T, kR, kMode>;
+    size_t smem = 0;
+    if (kMode != kGrad && a.teacher_lse) smem = static_cast<size_t>(ceil_div(ceil_div(vectors, shape.ctas), 4) * 4);
+    if (smem + sizeof(DistillShared) > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    return launch_rows(kernel, a.rows * ctas, threads, ctas, smem, s, a, ctas);
+    // the gradient alone needs no exchange: its CTAs are no cluster
+    return launch_rows(kernel, a.rows * shape.ctas, shape.threads, kMode == kGrad ? 1 : shape.ctas, smem, s, a, shape.ctas);
+}
+
+template <typename T, int kMode>
+cudaError_t launch_distill_mode(const DistillArgs &a, cudaStream_t s) {
+    const int64_t vectors = row_vectors<T>(a.n, a.z, a.ldz);
+    const RowShape shape = row_shape(a.rows, vectors);
+    switch (shape.regs) {
+        case 2: return launch_distill_shape<T, 2, kMode>(shape, vectors, a, s);
+        case 4: return launch_distill_shape<T, 4, kMode>(shape, vectors, a, s);
+        case 8: return launch_distill_shape<T, 8, kMode>(shape, vectors, a, s);
+        default: return launch_distill_shape<T, 0, kMode>(shape, vectors, a, s);
+    }
 }
 
 template <typename T>

@@ -79,6 +79,49 @@ __device__ __forceinline__ uint4 pack(const float *in) {
                       pack_word(in + 3 * kW, T()));
 }
 
+template <typename T>
+__device__ __forceinline__ uint4 splat(float v) {
+    float f[Vec<T>::kN];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kN; ++i) f[i] = v;
+    return pack<T>(f);
+}
+// The largest of a vector's values: a NaN is passed over, or (nan_max) is the result.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+template <typename H2>
+__device__ __forceinline__ H2 as_pair(uint32_t w) { return *reinterpret_cast<const H2 *>(&w); }
+__device__ __forceinline__ float vec_max(const uint4 &v, float) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+__device__ __forceinline__ float vec_max_nan(const uint4 &v, float) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+__device__ __forceinline__ float vec_max(const uint4 &v, __half) {
+    const float2 f = __half22float2(__hmax2(__hmax2(as_pair<__half2>(v.x), as_pair<__half2>(v.y)),
+                                            __hmax2(as_pair<__half2>(v.z), as_pair<__half2>(v.w))));
+    return fmaxf(f.x, f.y);
+}
+__device__ __forceinline__ float vec_max_nan(const uint4 &v, __half) {
+    const float2 f = __half22float2(__hmax2_nan(__hmax2_nan(as_pair<__half2>(v.x), as_pair<__half2>(v.y)),
+                                                __hmax2_nan(as_pair<__half2>(v.z), as_pair<__half2>(v.w))));
+    return max_nan(f.x, f.y);
+}
+__device__ __forceinline__ float vec_max(const uint4 &v, __nv_bfloat16) {
+    const float2 f = __bfloat1622float2(__hmax2(__hmax2(as_pair<__nv_bfloat162>(v.x), as_pair<__nv_bfloat162>(v.y)),
+                                                __hmax2(as_pair<__nv_bfloat162>(v.z), as_pair<__nv_bfloat162>(v.w))));
+    return fmaxf(f.x, f.y);
+}
+__device__ __forceinline__ float vec_max_nan(const uint4 &v, __nv_bfloat16) {
+    const float2 f =
+        __bfloat1622float2(__hmax2_nan(__hmax2_nan(as_pair<__nv_bfloat162>(v.x), as_pair<__nv_bfloat162>(v.y)),
+                                       __hmax2_nan(as_pair<__nv_bfloat162>(v.z), as_pair<__nv_bfloat162>(v.w))));
+    return max_nan(f.x, f.y);
+}
+
 // The value a teacher array of any of the three types holds at i.
 __device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
     if (dtype == SPMV_F32) return static_cast<const float *>(p)[i];
@@ -104,28 +147,102 @@ struct RowView {
         : p(row), n(n_values), head(static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T))) {}
     __device__ __forceinline__ int64_t vectors() const { return (head + n + kN - 1) / kN; }
     __device__ __forceinline__ int64_t first(int64_t v) const { return v * kN - head; }
-    __device__ __forceinline__ bool whole(int64_t e) const { return e >= 0 && e + kN <= n; }
-    // values outside the row read as -inf
-    __device__ __forceinline__ uint4 load(int64_t v) const {
+};
+// The consecutive vectors of a row that one CTA has: `count` of them, of which [lo, hi) lie
+// inside the row; only the row's own first and last vector can be others.
+template <typename T>
+struct Share {
+    static constexpr int kN = Vec<T>::kN;
+    const T *p;        // the row
+    int64_t n, e0;     // its length; the first value of vector 0 (negative in front of the row)
+    int count, lo, hi;
+    __device__ __forceinline__ Share(const RowView<T> &row, uint32_t rank, int ctas) : p(row.p), n(row.n) {
+        const int64_t nv = row.vectors(), per = (nv + ctas - 1) / ctas;
+        const int64_t v0 = rank * per < nv ? rank * per : nv, v1 = v0 + per < nv ? v0 + per : nv;
+        e0 = row.first(v0);
+        count = static_cast<int>(v1 - v0);
+        lo = e0 < 0 ? 1 : 0;
+        hi = e0 + static_cast<int64_t>(count) * kN > n ? count - 1 : count;
+        if (lo > count) lo = count;
+    }
+    __device__ __forceinline__ bool whole(int v) const { return v >= lo && v < hi; }
+    __device__ __forceinline__ int64_t first(int v) const { return e0 + static_cast<int64_t>(v) * kN; }
+    __device__ __forceinline__ bool owns(int64_t e) const { return e >= e0 && e < first(count); }
+    __device__ __forceinline__ uint4 load_whole(int v) const { return *reinterpret_cast<const uint4 *>(p + first(v)); }
+    __device__ __forceinline__ uint4 load_last(int v) const { return __ldcs(reinterpret_cast<const uint4 *>(p + first(v))); }
+    // any vector of the share; values outside the row read as -inf
+    __device__ __forceinline__ uint4 load(int v) const {
+        if (whole(v)) return load_whole(v);
         const int64_t e = first(v);
-        if (whole(e)) return *reinterpret_cast<const uint4 *>(p + e);
         float f[kN];
 #pragma unroll
         for (int i = 0; i < kN; ++i) f[i] = (e + i >= 0 && e + i < n) ? to_f32(p[e + i]) : kNegInf;
         return pack<T>(f);
     }
-};
-// Store one vector of a row whose geometry is that of `at` (same head) or not (`congruent`
-// false: the row starts at another offset from a 16-byte boundary, values go one by one).
-template <typename T>
-__device__ __forceinline__ void store_vec(T *row, const RowView<T> &at, int64_t v, const float *f, bool congruent) {
-    const int64_t e = at.first(v);
-    if (congruent && at.whole(e)) {
-        *reinterpret_cast<uint4 *>(row + e) = pack<T>(f);
-    } else {
+    // one vector of a row of the same length; `congruent`: it starts at the same offset from
+    // a 16-byte boundary as this one (otherwise values go one by one)
+    __device__ __forceinline__ void store(T *row, int v, const uint4 &x, bool congruent) const {
+        const int64_t e = first(v);
+        if (congruent && whole(v)) {
+            __stcs(reinterpret_cast<uint4 *>(row + e), x);
+        } else {
+            float f[kN];
+            unpack<T>(x, f);
 #pragma unroll
-        for (int i = 0; i < Vec<T>::kN; ++i)
-            if (e + i >= 0 && e + i < at.n) row[e + i] = from_f32<T>(f[i]);
+            for (int i = 0; i < kN; ++i)
+                if (e + i >= 0 && e + i < n) row[e + i] = from_f32<T>(f[i]);
+        }
+    }
+};
+
+// Vectors t, t + workers, t + 2 workers, ... of the share, thread t's of `workers`, in
+// registers: all loads are issued before the few threads with a vector at the row's ends look
+// at theirs.  What is not there is -inf.
+template <typename T, int kR>
+__device__ __forceinline__ void load_share(const Share<T> &sh, int t, int workers, uint4 *reg) {
+    const uint4 none = splat<T>(kNegInf);
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+        const int v = i * workers + t;
+        reg[i] = none;
+        if (sh.whole(v)) reg[i] = sh.load_whole(v);
+    }
+    if (sh.lo != 0 || sh.hi != sh.count) {
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            const int v = i * workers + t;
+            if (v < sh.count && !sh.whole(v)) reg[i] = sh.load(v);
+        }
+    }
+}
+// f(vectors[kU], index of the first, how many) over thread t's vectors, `workers` apart, read
+// from memory kU at a time (those past the count are -inf), the vectors inside the row first.
+template <typename T, int kU, bool kLast, typename F>
+__device__ __forceinline__ void stream_share(const Share<T> &sh, int t, int workers, F f) {
+    uint4 x[kU];
+    int v = sh.lo + t;
+    for (; v + (kU - 1) * workers < sh.hi; v += kU * workers) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) x[i] = kLast ? sh.load_last(v + i * workers) : sh.load_whole(v + i * workers);
+        f(x, v, kU);
+    }
+    const uint4 none = splat<T>(kNegInf);
+    if (v < sh.hi) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+            x[i] = none;
+            if (v + i * workers < sh.hi) x[i] = sh.load_whole(v + i * workers);
+        }
+        f(x, v, (sh.hi - v + workers - 1) / workers);
+    }
+    // the vectors at the row's ends (one vector may be both)
+    const bool first = t == 0 && sh.lo == 1 && sh.count > 0, last = t == 1 && sh.hi < sh.count && sh.hi >= sh.lo;
+    if (first || last) {
+        const int edge = first ? 0 : sh.hi;
+#pragma unroll
+        for (int i = 1; i < kU; ++i) x[i] = none;
+        x[0] = sh.load(edge);
+        f(x, edge, 1);
     }
 }
 
@@ -139,6 +256,63 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two floats at a time: one instruction for both.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+          "l"(reinterpret_cast<unsigned long long &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// acc + the vector's exp2((x - m) scale): the difference first, so that values and maxima near
+// the type's limits (masks) neither overflow nor meet an infinity of their own
+template <typename T>
+__device__ __forceinline__ float2 exp_sum(const uint4 &v, float m, float scale, float2 acc) {
+    float x[Vec<T>::kN];
+    unpack<T>(v, x);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kN; i += 2) {
+        const float2 d = mul2(add2(make_float2(x[i], x[i + 1]), both(-m)), both(scale));
+        acc = add2(acc, make_float2(ex2(d.x), ex2(d.y)));
+    }
+    return acc;
+}
+// Maximum and sum of exponentials of a thread's values, as they come.
+struct Running {
+    float m = kNegInf;
+    float2 s = {0.0f, 0.0f};
+    // kU vectors more
+    template <typename T, int kU>
+    __device__ __forceinline__ void add(const uint4 *x, float scale) {
+        float top = vec_max(x[0], T());
+#pragma unroll
+        for (int i = 1; i < kU; ++i) top = fmaxf(top, vec_max(x[i], T()));
+        if (top > m) {
+            if (m != kNegInf) s = mul2(s, both(ex2((m - top) * scale)));
+            m = top;
+        }
+        const float m0 = m == kNegInf ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < kU; ++i) s = exp_sum<T>(x[i], m0, scale, s);
+    }
+    __device__ __forceinline__ float sum() const { return s.x + s.y; }
+};
 // The reference point of a sum of exponentials: the maximum, or 0 if nothing is above -inf
 // (so that -inf - m is -inf and never NaN).
 __device__ __forceinline__ float reference_of(float m) { return m == kNegInf ? 0.0f : m; }
@@ -238,6 +412,40 @@ cudaError_t launch_rows(void (*kernel)(Params...), int64_t grid, int threads, in
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// 16-byte vectors that a row of n values reaches into, wherever the matrix's rows start.
+template <typename T>
+int64_t row_vectors(int64_t n, const void *p, int64_t ld) {
+    const bool aligned = (reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld) * sizeof(T)) % 16 == 0;
+    return ceil_div(n + (aligned ? 0 : Vec<T>::kN - 1), Vec<T>::kN);
+}
+// How a row of `vectors` 16-byte vectors is shared out: `ctas` CTAs (a cluster) of `threads`
+// threads with `regs` vectors in registers each, or regs = 0 where the largest cluster's
+// registers do not hold it.
+struct RowShape {
+    int ctas, threads, regs;
+};
+constexpr int kRowRegs = 8;  // 32 registers of data: two CTAs of 512 threads fit an SM
+// One warp of each CTA does not take part in the row itself (`threads` counts it).
+inline RowShape row_shape(int64_t rows, int64_t vectors) {
+    constexpr int64_t kFull = 480 * kRowRegs;
+    constexpr int kSms = 152;
+    RowShape s{1, 512, 0};
+    // few rows: more CTAs a row while SMs would be idle and each thread still has a vector
+    while (s.ctas < kMaxCluster && rows * s.ctas < kSms && vectors > s.ctas * 480) s.ctas *= 2;
+    if (vectors > s.ctas * kFull) {
+        // read twice: small CTAs hide each other's barriers, but the rows in flight have to stay
+        // in L2 (65536 fp16 values, loss: 61 us with 256 threads, 76 with 512; 131072 bf16
+        // values, loss and gradient: 944 and 808)
+        if (ceil_div(vectors, s.ctas) <= 8192) s.threads = 256;
+        return s;
+    }
+    const int64_t share = ceil_div(vectors, s.ctas);
+    s.threads = share <= 192 ? 128 : share <= 896 ? 256 : 512;
+    s.regs = 2;
+    while (static_cast<int64_t>(s.regs) * (s.threads - 32) < share) s.regs *= 2;
+    return s;
 }
 
 inline int refuse(const std::string &what) { return set_error(SPMV_ERR_INVALID_ARG, what); }

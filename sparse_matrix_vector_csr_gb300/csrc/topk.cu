@@ -125,25 +125,19 @@ struct TopShared {
 };
 
 template <typename T, int kR, typename F>
-__device__ __forceinline__ void each_value(const RowView<T> &row, const uint4 *reg, int64_t v0, int64_t v1, F f) {
-    constexpr int kN = Vec<T>::kN;
+__device__ __forceinline__ void each_value(const Share<T> &share, const uint4 *reg, F f) {
+    const auto one = [&](const uint4 &vec, int v) {
+        float x[Vec<T>::kN];
+        unpack<T>(vec, x);
+        const int64_t e = share.first(v);
+#pragma unroll
+        for (int q = 0; q < Vec<T>::kN; ++q) f(x[q], e + q);
+    };
     if constexpr (kR > 0) {
 #pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            float x[kN];
-            unpack<T>(reg[i], x);
-            const int64_t e = row.first(v0 + static_cast<int64_t>(i) * blockDim.x + threadIdx.x);
-#pragma unroll
-            for (int q = 0; q < kN; ++q) f(x[q], e + q);
-        }
+        for (int i = 0; i < kR; ++i) one(reg[i], i * blockDim.x + threadIdx.x);
     } else {
-        for (int64_t v = v0 + threadIdx.x; v < v1; v += blockDim.x) {
-            float x[kN];
-            unpack<T>(row.load(v), x);
-            const int64_t e = row.first(v);
-#pragma unroll
-            for (int q = 0; q < kN; ++q) f(x[q], e + q);
-        }
+        for (int v = threadIdx.x; v < share.count; v += blockDim.x) one(share.load(v), v);
     }
 }
 
@@ -154,23 +148,13 @@ __global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group
     const int64_t r = blockIdx.x / ctas;
     const uint32_t rank = blockIdx.x % ctas;
     const RowView<T> row(static_cast<const T *>(a.x) + r * a.ldx, a.n);
-    const int64_t nv = row.vectors(), share = (nv + ctas - 1) / ctas;
-    const int64_t v0 = rank * share, v1 = v0 + share < nv ? v0 + share : nv;
+    const Share<T> share(row, rank, ctas);
     uint4 reg[kR > 0 ? kR : 1];
-    if constexpr (kR > 0) {
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            const int64_t v = v0 + static_cast<int64_t>(i) * blockDim.x + tid;
-            float pad[Vec<T>::kN];
-#pragma unroll
-            for (int q = 0; q < Vec<T>::kN; ++q) pad[q] = kNegInf;
-            reg[i] = v < v1 ? row.load(v) : pack<T>(pad);
-        }
-    }
+    if constexpr (kR > 0) load_share<T, kR>(share, tid, blockDim.x, reg);
     if (ctas > 1) cluster_arrive();  // the peers' shared memory may be written from here on ...
     if (tid < 4) sh.count[tid] = 0;
     float m = kNegInf;
-    each_value<T, kR>(row, reg, v0, v1, [&](float x, int64_t) { m = fmaxf(m, x); });
+    each_value<T, kR>(share, reg, [&](float x, int64_t) { m = fmaxf(m, x); });
     float g = m;
     for (int o = 1; o < group; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
     const bool want_lse = a.lse || a.weighting == SPMV_WEIGHTS_ROW;
@@ -178,7 +162,7 @@ __global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group
     m = warp_max(m);
     if (want_lse) {
         const float m0 = reference_of(m);
-        each_value<T, kR>(row, reg, v0, v1, [&](float x, int64_t) { sum += ex2((x - m0) * a.scale); });
+        each_value<T, kR>(share, reg, [&](float x, int64_t) { sum += ex2((x - m0) * a.scale); });
         sum = warp_sum(sum);
     }
     if (ctas > 1) cluster_wait();  // ... once they have all started
@@ -212,11 +196,11 @@ __global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group
 
     const auto collect = [&](auto taken) {
         int mine = 0;
-        each_value<T, kR>(row, reg, v0, v1, [&](float x, int64_t e) { mine += taken(x, e); });
+        each_value<T, kR>(share, reg, [&](float x, int64_t e) { mine += taken(x, e); });
         if (mine) {
             const uint32_t counter = peer_addr(&sh.count[0], 0);
             uint32_t at = ctas > 1 ? peer_add(counter, mine) : atomicAdd(&sh.count[0], mine);
-            each_value<T, kR>(row, reg, v0, v1, [&](float x, int64_t e) {
+            each_value<T, kR>(share, reg, [&](float x, int64_t e) {
                 if (taken(x, e)) {
                     if (at < kMaxCand) {
                         if (ctas > 1) peer_store64(peer_addr(&sh.cand[at], 0), composite(x, e));
@@ -235,7 +219,7 @@ __global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group
         for (int step = 0; step < 64 && found > kMaxCand; ++step) {
             cut = lo + (hi - lo) / 2;
             int mine = 0;
-            each_value<T, kR>(row, reg, v0, v1,
+            each_value<T, kR>(share, reg,
                               [&](float x, int64_t e) { mine += x != kNegInf && composite(x, e) >= cut; });
             mine = warp_sum(mine);
             const int slot = 1 + step % 3;
@@ -344,8 +328,7 @@ __global__ void __launch_bounds__(256) k_topk_grad(TopGradArgs a) {
     if (r >= a.rows) return;
     T *out = static_cast<T *>(a.dx) + r * a.lddx;
     const RowView<T> view(out, a.n);
-    const int64_t per = kGradPiece / kN, nv = view.vectors();
-    const int64_t v0 = (item - r * a.pieces) * per, v1 = v0 + per < nv ? v0 + per : nv;
+    const Share<T> piece(view, static_cast<uint32_t>(item - r * a.pieces), static_cast<int>(a.pieces));
     const int32_t *ids = a.ids + r * a.k;
     const float *w = a.weights + r * a.k, *dw = a.dweights + r * a.k;
     float s = 0.0f;
@@ -356,10 +339,10 @@ __global__ void __launch_bounds__(256) k_topk_grad(TopGradArgs a) {
     const T *x = static_cast<const T *>(a.x) + (whole_row ? r * a.ldx : 0);
     const float lse = whole_row ? a.lse[r] : 0.0f;
     const float factor = -s * a.inv_temperature;
-    for (int64_t v = v0 + lane; v < v1; v += 32) {
+    for (int v = lane; v < piece.count; v += 32) {
         float f[kN] = {};
         if (whole_row) {
-            const int64_t e = view.first(v);
+            const int64_t e = piece.first(v);
 #pragma unroll
             for (int i = 0; i < kN; ++i)
                 if (e + i >= 0 && e + i < a.n) {
@@ -367,13 +350,12 @@ __global__ void __launch_bounds__(256) k_topk_grad(TopGradArgs a) {
                     f[i] = xi == kNegInf ? 0.0f : factor * ex2(fmaf(xi, a.inv_temperature, -lse) * kLog2e);
                 }
         }
-        store_vec<T>(out, view, v, f, true);
+        piece.store(out, v, pack<T>(f), true);
     }
     __syncwarp();
-    const int64_t e0 = view.first(v0), e1 = view.first(v1);
     for (int j = lane; j < a.k; j += 32) {
         const int32_t id = ids[j];
-        if (id >= e0 && id < e1 && id >= 0 && id < a.n) out[id] = from_f32<T>(w[j] * (dw[j] - s) * a.inv_temperature);
+        if (id >= 0 && id < a.n && piece.owns(id)) out[id] = from_f32<T>(w[j] * (dw[j] - s) * a.inv_temperature);
     }
 }
 
