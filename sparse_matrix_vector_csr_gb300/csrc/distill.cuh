@@ -156,7 +156,7 @@ struct GradOf {
 };
 
 template <typename T, int kR, int kMode>
-__global__ void __launch_bounds__(512, 2) k_distill(DistillArgs a, int ctas) {
+__global__ void __launch_bounds__(512, 2) k_distill(DistillArgs a, int log2_ctas) {
     constexpr int kN = Vec<T>::kN;
     constexpr int kU = 4;  // vectors in flight per thread where the row is read twice
     __shared__ DistillShared sh;
@@ -164,11 +164,12 @@ __global__ void __launch_bounds__(512, 2) k_distill(DistillArgs a, int ctas) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
     const int workers = blockDim.x - 32;
     const bool entry_warp = tid >= workers;
-    const int64_t r = blockIdx.x / ctas;
-    const uint32_t rank = blockIdx.x % ctas;
+    const int ctas = 1 << log2_ctas;
+    const int64_t r = blockIdx.x >> log2_ctas;
+    const uint32_t rank = blockIdx.x & (ctas - 1);
     const T *z = static_cast<const T *>(a.z) + r * a.ldz;
     const RowView<T> row(z, a.n);
-    const Share<T> share(row, rank, ctas);
+    const Share<T> share(row, rank, log2_ctas);
     const bool tail = a.teacher_lse != nullptr;
     const auto own = [&](int32_t id) { return id >= 0 && share.owns(id); };
     uint4 reg[kR > 0 ? kR : 1];
@@ -341,7 +342,7 @@ cudaError_t launch_distill_shape(const RowShape &shape, int64_t vectors, const D
         if (e != cudaSuccess) return e;
     }
     // the gradient alone needs no exchange: its CTAs are no cluster
-    return launch_rows(kernel, a.rows * shape.ctas, shape.threads, kMode == kGrad ? 1 : shape.ctas, smem, s, a, shape.ctas);
+    return launch_rows(kernel, a.rows * shape.ctas, shape.threads, kMode == kGrad ? 1 : shape.ctas, smem, s, a, shape.log2_ctas());
 }
 
 template <typename T, int kMode>

@@ -156,9 +156,14 @@ struct Share {
     const T *p;        // the row
     int64_t n, e0;     // its length; the first value of vector 0 (negative in front of the row)
     int count, lo, hi;
-    __device__ __forceinline__ Share(const RowView<T> &row, uint32_t rank, int ctas) : p(row.p), n(row.n) {
-        const int64_t nv = row.vectors(), per = (nv + ctas - 1) / ctas;
-        const int64_t v0 = rank * per < nv ? rank * per : nv, v1 = v0 + per < nv ? v0 + per : nv;
+    // the rank-th of 2^log2_ctas equal shares (the last may be shorter)
+    __device__ __forceinline__ Share(const RowView<T> &row, uint32_t rank, int log2_ctas)
+        : Share(row, static_cast<int64_t>(rank) * ((row.vectors() + (1 << log2_ctas) - 1) >> log2_ctas), (row.vectors() + (1 << log2_ctas) - 1) >> log2_ctas) {}
+    // up to `per` vectors from v0 on
+    __device__ __forceinline__ Share(const RowView<T> &row, int64_t v0, int64_t per) : p(row.p), n(row.n) {
+        const int64_t nv = row.vectors();
+        if (v0 > nv) v0 = nv;
+        const int64_t v1 = v0 + per < nv ? v0 + per : nv;
         e0 = row.first(v0);
         count = static_cast<int>(v1 - v0);
         lo = e0 < 0 ? 1 : 0;
@@ -303,6 +308,11 @@ struct Running {
         float top = vec_max(x[0], T());
 #pragma unroll
         for (int i = 1; i < kU; ++i) top = fmaxf(top, vec_max(x[i], T()));
+        add<T, kU>(x, top, scale);
+    }
+    // with their maximum at hand (a NaN where they have one: the sum becomes NaN whatever m is)
+    template <typename T, int kU>
+    __device__ __forceinline__ void add(const uint4 *x, float top, float scale) {
         if (top > m) {
             if (m != kNegInf) s = mul2(s, both(ex2((m - top) * scale)));
             m = top;
@@ -425,6 +435,7 @@ int64_t row_vectors(int64_t n, const void *p, int64_t ld) {
 // registers do not hold it.
 struct RowShape {
     int ctas, threads, regs;
+    int log2_ctas() const { return ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3; }
 };
 constexpr int kRowRegs = 8;  // 32 registers of data: two CTAs of 512 threads fit an SM
 // One warp of each CTA does not take part in the row itself (`threads` counts it).

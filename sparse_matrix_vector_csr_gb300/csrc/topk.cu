@@ -106,15 +106,18 @@ __global__ void __launch_bounds__(256) k_topk_warp(TopArgs a) {
 // ----------------------------------------------------------------------------
 // long rows: a CTA, or a cluster of CTAs, per row
 // ----------------------------------------------------------------------------
-// 1. Every thread takes its share's maximum; the k-th largest of the maxima of groups of
+// 1. Every thread reads its share once, a few vectors (a batch) at a time, and keeps its maximum
+//    and its batches' maxima (in shared memory).  The k-th largest of the maxima of groups of
 //    threads is a lower bound of the row's k-th largest entry that passes few others.
-// 2. Entries at or above it go to the first CTA's candidate list.
+// 2. The few batches that reach it are read again (from L2), a warp at a time, and their entries
+//    at or above it go to the first CTA's candidate list.
 // 3. If the list overflows (values bunched in one group, or many ties), the threshold is
 //    bisected on (value, column) numbers, which are unique, until between k and kMaxCand
 //    pass: at most 64 counting passes, whatever the row holds.
 // 4. The first CTA ranks the candidates by counting and writes the k largest.
-// kR > 0: a thread's share is kR vectors in registers, read once.  kR = 0: any length, read
-// again by each pass (from L2).
+constexpr int kBatch = 4;        // vectors a thread loads at a time
+constexpr int kBatchMaxima = 15; // a thread's batches share this many maxima (and one for the row's ends)
+
 struct TopShared {
     unsigned long long cand[kMaxCand];
     float group_max[kMaxGroups];
@@ -124,124 +127,220 @@ struct TopShared {
     float thr, lse_m, lse_sum;
 };
 
-template <typename T, int kR, typename F>
-__device__ __forceinline__ void each_value(const Share<T> &share, const uint4 *reg, F f) {
-    const auto one = [&](const uint4 &vec, int v) {
-        float x[Vec<T>::kN];
-        unpack<T>(vec, x);
-        const int64_t e = share.first(v);
-#pragma unroll
-        for (int q = 0; q < Vec<T>::kN; ++q) f(x[q], e + q);
-    };
-    if constexpr (kR > 0) {
-#pragma unroll
-        for (int i = 0; i < kR; ++i) one(reg[i], i * blockDim.x + threadIdx.x);
-    } else {
-        for (int v = threadIdx.x; v < share.count; v += blockDim.x) one(share.load(v), v);
+// Thread t's batches of a share: batch q < whole covers the vectors lo + t + (q kBatch + i) W inside
+// the row; batch `whole` is, for threads 0 and 1, the vector at the row's start and end.
+template <typename T>
+struct Batches {
+    const Share<T> &share;
+    int t, w, whole;
+    __device__ __forceinline__ Batches(const Share<T> &s, int t_, int w_)
+        : share(s), t(t_), w(w_), whole(s.hi > s.lo ? (s.hi - s.lo + kBatch * w_ - 1) / (kBatch * w_) : 0) {}
+    __device__ __forceinline__ int edge() const {
+        if (t == 0 && share.lo == 1 && share.count > 0) return 0;
+        if (t == 1 && share.hi < share.count && share.hi >= share.lo) return share.hi;
+        return -1;
     }
+    __device__ __forceinline__ int vector(int q, int i) const { return share.lo + t + (q * kBatch + i) * w; }
+    // absent vectors are -inf
+    __device__ __forceinline__ void load(int q, uint4 *x) const {
+        const int v = vector(q, 0);
+        if (v + (kBatch - 1) * w < share.hi) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) x[i] = share.load_whole(v + i * w);
+        } else {
+            const uint4 none = splat<T>(kNegInf);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                x[i] = none;
+                if (v + i * w < share.hi) x[i] = share.load_whole(v + i * w);
+            }
+        }
+    }
+    // f(vector, its index) over all of the thread's vectors
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll 1
+        for (int v = share.lo + t; v < share.hi; v += w) f(share.load_whole(v), v);
+        if (edge() >= 0) f(share.load(edge()), edge());
+    }
+};
+// f(value, column) over the values of a vector
+template <typename T, typename F>
+__device__ __forceinline__ void each_value(const Share<T> &share, const uint4 &vec, int v, F f) {
+    float x[Vec<T>::kN];
+    unpack<T>(vec, x);
+    const int64_t e = share.first(v);
+#pragma unroll
+    for (int q = 0; q < Vec<T>::kN; ++q) f(x[q], e + q);
 }
 
-template <typename T, int kR>
-__global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group) {
-    __shared__ TopShared sh;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
-    const int64_t r = blockIdx.x / ctas;
-    const uint32_t rank = blockIdx.x % ctas;
+// The list overflowed: candidates by bisection on (value, column); returns how many.
+template <typename T>
+__device__ __noinline__ uint32_t collect_by_bisection(const TopArgs &a, TopShared &sh, const Batches<T> &batches, int ctas,
+                                                      float thr) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    unsigned long long lo = static_cast<unsigned long long>(order_key(thr)) << 32, hi = ~0ull, cut = lo;
+    uint32_t found = kMaxCand + 1;
+    for (int step = 0; step < 64 && found > kMaxCand; ++step) {
+        cut = lo + (hi - lo) / 2;
+        int mine = 0;
+        batches.each([&](const uint4 &x, int v) {
+            each_value<T>(batches.share, x, v, [&](float f, int64_t e) { mine += f != kNegInf && composite(f, e) >= cut; });
+        });
+        __syncwarp();
+        mine = warp_sum(mine);
+        const int slot = 1 + step % 3;
+        if (lane < ctas && mine) {
+            if (ctas > 1) peer_add(peer_addr(&sh.count[slot], lane), mine);
+            else atomicAdd(&sh.count[slot], mine);
+        }
+        cluster_sync(ctas);
+        found = sh.count[slot];
+        if (tid == 0) sh.count[1 + (step + 2) % 3] = 0;  // last read before the previous barrier
+        if (found > kMaxCand) lo = cut;
+        else if (found < static_cast<uint32_t>(a.k)) {
+            hi = cut;
+            found = kMaxCand + 1;
+        }
+    }
+    if (tid == 0) sh.count[0] = 0;
+    cluster_sync(ctas);
+    batches.each([&](const uint4 &x, int v) {
+        each_value<T>(batches.share, x, v, [&](float f, int64_t e) {
+            if (f == kNegInf || composite(f, e) < cut) return;
+            if (ctas > 1) {
+                const uint32_t at = peer_add(peer_addr(&sh.count[0], 0), 1);
+                if (at < kMaxCand) peer_store64(peer_addr(&sh.cand[at], 0), composite(f, e));
+            } else {
+                const uint32_t at = atomicAdd(&sh.count[0], 1u);
+                if (at < kMaxCand) sh.cand[at] = composite(f, e);
+            }
+        });
+    });
+    __syncwarp();
+    cluster_sync(ctas);
+    return ctas > 1 ? peer_load(peer_addr(&sh.count[0], 0)) : sh.count[0];
+}
+
+// per: batches that share a maximum; slots: maxima a thread has for its whole batches.
+template <typename T>
+__global__ void __launch_bounds__(512, 2) k_topk_row(TopArgs a, int log2_ctas, int log2_group, int per, int slots) {
+    __shared__ __align__(16) TopShared sh;
+    extern __shared__ float batch_max[];  // [slots + 1][threads]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_threads = blockDim.x, n_warps = n_threads >> 5;
+    const int ctas = 1 << log2_ctas, group = 1 << log2_group;
+    const int64_t r = blockIdx.x >> log2_ctas;
+    const uint32_t rank = blockIdx.x & (ctas - 1);
     const RowView<T> row(static_cast<const T *>(a.x) + r * a.ldx, a.n);
-    const Share<T> share(row, rank, ctas);
-    uint4 reg[kR > 0 ? kR : 1];
-    if constexpr (kR > 0) load_share<T, kR>(share, tid, blockDim.x, reg);
+    const Share<T> share(row, rank, log2_ctas);
+    const Batches<T> batches(share, tid, n_threads);
+    const bool want_lse = a.lse || a.weighting == SPMV_WEIGHTS_ROW;
     if (ctas > 1) cluster_arrive();  // the peers' shared memory may be written from here on ...
     if (tid < 4) sh.count[tid] = 0;
-    float m = kNegInf;
-    each_value<T, kR>(share, reg, [&](float x, int64_t) { m = fmaxf(m, x); });
-    float g = m;
+
+    Running run;  // its maximum passes over NaNs; the batches' maxima hand them on
+    const auto take = [&](const uint4 *x, int n) {
+        float top = vec_max_nan(x[0], T());
+#pragma unroll
+        for (int i = 1; i < kBatch; ++i)
+            if (i < n) top = max_nan(top, vec_max_nan(x[i], T()));
+        if (want_lse) {
+            if (n == kBatch) run.add<T, kBatch>(x, top, a.scale);
+            else run.add<T, 1>(x, top, a.scale);
+        } else if (top > run.m) {
+            run.m = top;
+        }
+        return top;
+    };
+    for (int s = 0; s < slots; ++s) {
+        float top = kNegInf;
+        for (int q = s * per; q < (s + 1) * per && q < batches.whole; ++q) {
+            uint4 x[kBatch];
+            batches.load(q, x);
+            top = max_nan(top, take(x, kBatch));
+        }
+        batch_max[s * n_threads + tid] = top;
+    }
+    {
+        float top = kNegInf;
+        if (batches.edge() >= 0) {
+            const uint4 x = share.load(batches.edge());
+            top = take(&x, 1);
+        }
+        batch_max[slots * n_threads + tid] = top;
+    }
+    float g = run.m;
     for (int o = 1; o < group; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-    const bool want_lse = a.lse || a.weighting == SPMV_WEIGHTS_ROW;
+    const float m = warp_max(run.m);
     float sum = 0.0f;
-    m = warp_max(m);
     if (want_lse) {
-        const float m0 = reference_of(m);
-        each_value<T, kR>(share, reg, [&](float x, int64_t) { sum += ex2((x - m0) * a.scale); });
+        sum = run.sum();
+        if (run.m != kNegInf) sum *= ex2((run.m - m) * a.scale);
         sum = warp_sum(sum);
     }
     if (ctas > 1) cluster_wait();  // ... once they have all started
-    const int per_cta = blockDim.x / group, n_groups = per_cta * ctas;
-    if (tid % group == 0)
+    const int per_cta = n_threads >> log2_group, n_groups = per_cta * ctas;
+    if ((tid & (group - 1)) == 0)
         for (int c = 0; c < ctas; ++c) {
-            float *slot = &sh.group_max[rank * per_cta + tid / group];
+            float *slot = &sh.group_max[rank * per_cta + (tid >> log2_group)];
             if (ctas > 1) peer_store(peer_addr(slot, c), g);
             else *slot = g;
         }
-    if (lane < ctas) {
+    if (want_lse && lane < ctas) {
         float2 *slot = &sh.sums[rank * n_warps + warp];
         if (ctas > 1) peer_store2(peer_addr(slot, lane), m, sum);
         else *slot = make_float2(m, sum);
     }
+    if (tid == 0) sh.thr = kNegInf;
     cluster_sync(ctas);
 
-    if (tid == 0) sh.thr = kNegInf;
-    __syncthreads();
-    for (int i = tid; i < n_groups; i += blockDim.x) {
+    for (int i = tid; i < n_groups; i += n_threads) {
         const float v = sh.group_max[i];
         int above = 0;
-        for (int j = 0; j < n_groups; ++j) {
-            const float w = sh.group_max[j];
-            above += w > v || (w == v && j < i);
+        for (int j = 0; j < n_groups; j += 4) {  // (a multiple of 4)
+            const float4 w = *reinterpret_cast<const float4 *>(&sh.group_max[j]);
+            above += (w.x > v || (w.x == v && j < i)) + (w.y > v || (w.y == v && j + 1 < i)) +
+                     (w.z > v || (w.z == v && j + 2 < i)) + (w.w > v || (w.w == v && j + 3 < i));
         }
         if (above == a.k - 1) sh.thr = v;
     }
     __syncthreads();
     const float thr = fmaxf(sh.thr, -FLT_MAX);  // above -inf: masked entries are never candidates
 
-    const auto collect = [&](auto taken) {
-        int mine = 0;
-        each_value<T, kR>(share, reg, [&](float x, int64_t e) { mine += taken(x, e); });
-        if (mine) {
-            const uint32_t counter = peer_addr(&sh.count[0], 0);
-            uint32_t at = ctas > 1 ? peer_add(counter, mine) : atomicAdd(&sh.count[0], mine);
-            each_value<T, kR>(share, reg, [&](float x, int64_t e) {
-                if (taken(x, e)) {
-                    if (at < kMaxCand) {
-                        if (ctas > 1) peer_store64(peer_addr(&sh.cand[at], 0), composite(x, e));
-                        else sh.cand[at] = composite(x, e);
-                    }
-                    ++at;
+    // a warp looks at one lane's batch together, a value a lane
+    constexpr int kN = Vec<T>::kN;
+    bool room = true;
+    for (int s = 0; s <= slots; ++s) {
+        uint32_t todo = __ballot_sync(0xffffffffu, !(batch_max[s * n_threads + tid] < thr));
+        while (todo && room) {
+            const int owner = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int edge = __shfl_sync(0xffffffffu, batches.edge(), owner);
+            const int q0 = s == slots ? 0 : s * per, q1 = s == slots ? 1 : min(q0 + per, batches.whole);
+            for (int q = q0; q < q1 && room; ++q) {
+                const int i = lane / kN;
+                const int v = s == slots ? edge : batches.vector(q, i) - lane + owner;
+                const int64_t e = share.first(v) + lane % kN;
+                const bool there = i < kBatch && (s == slots ? i == 0 && e >= 0 && e < a.n : v < share.hi);
+                const float f = there ? to_f32(share.p[e]) : kNegInf;
+                const uint32_t hits = __ballot_sync(0xffffffffu, !(f < thr));
+                if (!hits) continue;
+                uint32_t at = 0;
+                if (lane == 0) at = ctas > 1 ? peer_add(peer_addr(&sh.count[0], 0), __popc(hits)) : atomicAdd(&sh.count[0], __popc(hits));
+                at = __shfl_sync(0xffffffffu, at, 0);
+                room = at + __popc(hits) <= kMaxCand;  // full: whoever finds more need not say so
+                if (room && (hits >> lane & 1)) {
+                    at += __popc(hits & ((1u << lane) - 1));
+                    if (ctas > 1) peer_store64(peer_addr(&sh.cand[at], 0), composite(f, e));
+                    else sh.cand[at] = composite(f, e);
                 }
-            });
+            }
         }
-    };
-    collect([&](float x, int64_t) { return !(x < thr); });
+    }
+    __syncwarp();
     cluster_sync(ctas);
     uint32_t found = ctas > 1 ? peer_load(peer_addr(&sh.count[0], 0)) : sh.count[0];
-    if (found > kMaxCand) {
-        unsigned long long lo = static_cast<unsigned long long>(order_key(thr)) << 32, hi = ~0ull, cut = lo;
-        for (int step = 0; step < 64 && found > kMaxCand; ++step) {
-            cut = lo + (hi - lo) / 2;
-            int mine = 0;
-            each_value<T, kR>(share, reg,
-                              [&](float x, int64_t e) { mine += x != kNegInf && composite(x, e) >= cut; });
-            mine = warp_sum(mine);
-            const int slot = 1 + step % 3;
-            if (lane < ctas && mine) {
-                if (ctas > 1) peer_add(peer_addr(&sh.count[slot], lane), mine);
-                else atomicAdd(&sh.count[slot], mine);
-            }
-            cluster_sync(ctas);
-            found = sh.count[slot];
-            if (tid == 0) sh.count[1 + (step + 2) % 3] = 0;  // last read before the previous barrier
-            if (found > kMaxCand) lo = cut;
-            else if (found < static_cast<uint32_t>(a.k)) {
-                hi = cut;
-                found = kMaxCand + 1;
-            }
-        }
-        if (tid == 0) sh.count[0] = 0;
-        cluster_sync(ctas);
-        collect([&](float x, int64_t e) { return x != kNegInf && composite(x, e) >= cut; });
-        cluster_sync(ctas);
-        found = ctas > 1 ? peer_load(peer_addr(&sh.count[0], 0)) : sh.count[0];
-    }
+    if (found > kMaxCand) found = collect_by_bisection<T>(a, sh, batches, ctas, thr);
     // the first CTA stays until the others have read its count; they have nothing left to do
     if (ctas > 1) {
         cluster_arrive();
@@ -249,8 +348,8 @@ __global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group
         if (rank != 0) return;
     }
 
-    // rank 0: the candidates in order, the row's sum
-    if (warp == 0 && want_lse) {
+    // rank 0: the candidates in order, the row's sum (by the last warp)
+    if (warp == n_warps - 1 && want_lse) {
         float mm = kNegInf;
         for (int i = lane; i < n_warps * ctas; i += 32) mm = fmaxf(mm, sh.sums[i].x);
         mm = reference_of(warp_max(mm));
@@ -267,7 +366,7 @@ __global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group
         }
     }
     const int n_cand = static_cast<int>(found < kMaxCand ? found : kMaxCand);
-    for (int i = tid; i < n_cand; i += blockDim.x) {
+    for (int i = tid; i < n_cand; i += n_threads) {
         const unsigned long long c = sh.cand[i];
         int above = 0;
         for (int j = 0; j < n_cand; ++j) above += sh.cand[j] > c;
@@ -278,7 +377,7 @@ __global__ void __launch_bounds__(512) k_topk_row(TopArgs a, int ctas, int group
             a.vals[r * a.k + above] = v;
         }
     }
-    for (int j = n_cand + tid; j < a.k; j += blockDim.x) {
+    for (int j = n_cand + tid; j < a.k; j += n_threads) {
         sh.top_vals[j] = kNegInf;
         a.ids[r * a.k + j] = -1;
         a.vals[r * a.k + j] = kNegInf;
@@ -324,11 +423,11 @@ __global__ void __launch_bounds__(256) k_topk_grad(TopGradArgs a) {
     constexpr int kN = Vec<T>::kN;
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t r = item / a.pieces;
+    const int64_t r = a.pieces == 1 ? item : item / a.pieces;
     if (r >= a.rows) return;
     T *out = static_cast<T *>(a.dx) + r * a.lddx;
     const RowView<T> view(out, a.n);
-    const Share<T> piece(view, static_cast<uint32_t>(item - r * a.pieces), static_cast<int>(a.pieces));
+    const Share<T> piece(view, (item - r * a.pieces) * (kGradPiece / kN), int64_t(kGradPiece / kN));
     const int32_t *ids = a.ids + r * a.k;
     const float *w = a.weights + r * a.k, *dw = a.dweights + r * a.k;
     float s = 0.0f;
@@ -371,8 +470,24 @@ cudaError_t launch_topk_warp(const TopArgs &a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_topk_row(const TopArgs &a, cudaStream_t s) {
-    const int threads = 512, ctas = 1, group = 1;
-    return launch_rows(k_topk_row<T, 0>, a.rows * ctas, threads, ctas, 0, s, a, ctas, group);
+    constexpr int kSms = 152;
+    const int64_t vectors = row_vectors<T>(a.n, a.x, a.ldx);
+    // few rows: more CTAs a row while SMs would be idle and each thread still has a batch
+    int ctas = 1;
+    while (ctas < kMaxCluster && a.rows * ctas < kSms && vectors > ctas * 512 * kBatch) ctas *= 2;
+    if (const char *e = getenv("TOPK_C")) ctas = atoi(e);//TUNE
+    const int64_t share = ceil_div(vectors, ctas);
+    int threads = share <= 512 && a.k <= 64 ? 128 : share <= 2048 && a.k <= 128 ? 256 : 512;
+    if (const char *e = getenv("TOPK_T")) threads = atoi(e);//TUNE
+    // at least twice as many groups as entries wanted, so that the threshold passes few others
+    int log2_group = 5, log2_ctas = 0;
+    while (log2_group > 0 && ctas * threads >> log2_group < 2 * a.k) --log2_group;
+    while (1 << log2_ctas < ctas) ++log2_ctas;
+    const int64_t batches = ceil_div(share, static_cast<int64_t>(threads) * kBatch);
+    const int per = static_cast<int>(ceil_div(batches, kBatchMaxima));
+    const int slots = static_cast<int>(ceil_div(batches, per));
+    const size_t smem = static_cast<size_t>(slots + 1) * threads * sizeof(float);
+    return launch_rows(k_topk_row<T>, a.rows * ctas, threads, ctas, smem, s, a, log2_ctas, log2_group, per, slots);
 }
 
 template <typename T>

@@ -16,41 +16,39 @@ own; nothing is recorded by autograd.  The semantics are those of ``include/spmv
 """
 from __future__ import annotations
 
+import contextlib
+import functools
+
 import torch
 
 from ._abi import SPMV_BF16, SPMV_F16, SPMV_F32, WEIGHTINGS, _check, lib
 
 _DTYPES = {torch.float32: SPMV_F32, torch.float16: SPMV_F16, torch.bfloat16: SPMV_BF16}
+_F32, _I32, _empty = torch.float32, torch.int32, torch.empty
+
+# the handle of a device's current stream, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-class _On:
-    """The stream of a call: ``handle`` for the library; on a stream other than the current
-    one, allocations are made for it and the inputs are kept until it has read them."""
+def _current(t):
+    """The current stream of a tensor's device (a host tensor is left for the library to refuse)."""
+    device = t.get_device()
+    return _raw_stream(device) if device >= 0 else None
 
-    __slots__ = ("handle", "_ctx")
 
-    def __init__(self, stream, inputs):
-        self._ctx = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream().cuda_stream
-            return
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        self.handle = stream.cuda_stream
-        if self.handle != torch.cuda.current_stream().cuda_stream:
-            self._ctx = torch.cuda.stream(stream)
-            for t in inputs:
-                if t is not None and t.is_cuda:
-                    t.record_stream(stream)
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+@contextlib.contextmanager
+def _on(stream, *inputs):
+    """Make `stream` current for a call: results are allocated for it, and inputs of another
+    stream are kept until it has read them."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream != torch.cuda.current_stream():
+        for t in inputs:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        yield
 
 
 def _matrix(t, name, rows=None, cols=None, dtype=None):
@@ -87,7 +85,7 @@ def _plain(t, name, shape, dtype):
 def _out(t, name, like, rows, cols):
     """A new matrix of `like`'s type, or the checked one given, with its leading dimension."""
     if t is None:
-        return torch.empty((rows, cols), dtype=like.dtype, device=like.device), cols
+        return _empty((rows, cols), dtype=like.dtype, device=like.device), cols
     return t, _matrix(t, name, rows, cols, like.dtype)[1]
 
 
@@ -99,17 +97,20 @@ class TopRows:
 
     def grad(self, dweights, out=None, stream=None):
         """The gradient in x of a loss whose gradient in the weights is ``dweights``."""
+        if stream is not None:
+            with _on(stream, self._x, self.ids, self.weights, self.lse, dweights, out):
+                return self.grad(dweights, out)
         if not self._weighting:
             raise ValueError("topk_rows was called without weights")
-        x, (rows, k) = self._x, self.ids.shape
+        x, ids, lse = self._x, self.ids, self.lse
+        rows, k = ids.shape
+        n = x.shape[1]
         code, ldx = _matrix(x, "x")
-        dw = _plain(dweights, "dweights", self.ids.shape, torch.float32)
-        with _On(stream, (x, self.ids, self.weights, self.lse, dweights, out)) as s:
-            dx, lddx = _out(out, "out", x, rows, x.shape[1])
-            _check(lib.spmv_topk_rows_grad(rows, x.shape[1], k, self.ids.data_ptr(), self.weights.data_ptr(), dw,
-                                           self._weighting, self._temperature, x.data_ptr(), ldx,
-                                           self.lse.data_ptr() if self.lse is not None else None, dx.data_ptr(), lddx,
-                                           code, s))
+        dw = _plain(dweights, "dweights", ids.shape, _F32)
+        dx, lddx = _out(out, "out", x, rows, n)
+        _check(lib.spmv_topk_rows_grad(rows, n, k, ids.data_ptr(), self.weights.data_ptr(), dw, self._weighting,
+                                       self._temperature, x.data_ptr(), ldx, None if lse is None else lse.data_ptr(),
+                                       dx.data_ptr(), lddx, code, _current(x)))
         return dx
 
 
@@ -118,24 +119,31 @@ def topk_rows(x, k, temperature=1.0, weights=None, lse=False, stream=None) -> To
     -inf is never taken (its id is -1).  ``weights``: None, "selected" (softmax over the
     chosen) or "row" (softmax over the row); ``lse``: also the row's log-sum-exp.  Both at
     ``temperature``.  1 <= k <= min(n, 256)."""
+    if stream is not None:
+        with _on(stream, x):
+            return topk_rows(x, k, temperature, weights, lse)
     code, ldx = _matrix(x, "x")
     rows, n = x.shape
-    top = TopRows()
-    top._x, top._weighting, top._temperature = x, WEIGHTINGS[weights], float(temperature)
-    if not 1 <= k <= min(n, 256):
+    weighting = WEIGHTINGS[weights]
+    if not 1 <= k <= n or k > 256:
         raise ValueError("k must lie in [1, min(n, 256)]")
-    with _On(stream, (x,)) as s:
-        top.ids = torch.empty((rows, k), dtype=torch.int32, device=x.device)
-        top.vals = torch.empty((rows, k), dtype=torch.float32, device=x.device)
-        top.weights = torch.empty_like(top.vals) if top._weighting else None
-        # the gradient of weights over the row needs lse too
-        top.lse = (torch.empty((rows,), dtype=torch.float32, device=x.device)
-                   if lse or top._weighting == WEIGHTINGS["row"] else None)
-        _check(lib.spmv_topk_rows(rows, n, k, x.data_ptr(), ldx, code, top._temperature, top._weighting,
-                                  top.ids.data_ptr(), top.vals.data_ptr(),
-                                  top.weights.data_ptr() if top._weighting else None,
-                                  top.lse.data_ptr() if top.lse is not None else None, s))
+    top, device = TopRows(), x.device
+    top._x, top._weighting, top._temperature = x, weighting, temperature
+    top.ids = _empty((rows, k), dtype=_I32, device=device)
+    top.vals = _empty((rows, k), dtype=_F32, device=device)
+    top.weights = _empty((rows, k), dtype=_F32, device=device) if weighting else None
+    # the gradient of weights over the row needs lse too
+    top.lse = _empty((rows,), dtype=_F32, device=device) if lse or weighting == 2 else None
+    _check(lib.spmv_topk_rows(rows, n, k, x.data_ptr(), ldx, code, temperature, weighting, top.ids.data_ptr(),
+                              top.vals.data_ptr(), top.weights.data_ptr() if weighting else None,
+                              None if top.lse is None else top.lse.data_ptr(), _current(x)))
     return top
+
+
+@functools.lru_cache(maxsize=4096)
+def _plan_sizes(tokens, k, experts, align):
+    """(rows of the sorted matrix, bytes of the plan's workspace)"""
+    return (_check(lib.spmv_route_rows(tokens, k, experts, align)), _check(lib.spmv_route_workspace(tokens, k, experts)))
 
 
 class RoutePlan:
@@ -143,71 +151,78 @@ class RoutePlan:
     outside [0, experts) is dropped).  ``rows`` is the sorted matrix's number of rows;
     ``offsets`` (experts + 1), ``slots`` (tokens x k) and ``sources`` (rows) as in spmv.h."""
 
+    __slots__ = ("tokens", "k", "experts", "align", "rows", "_buf", "_slots", "_sources", "_offsets")
+
     def __init__(self, ids, experts, align=1, stream=None):
+        if stream is not None:
+            with _on(stream, ids):
+                return self.__init__(ids, experts, align)
         if ids.dim() != 2:
             raise ValueError("ids must be a matrix")
-        ptr = _plain(ids, "ids", ids.shape, torch.int32)
-        self.tokens, self.k = ids.shape
-        self.experts, self.align = int(experts), int(align)
-        self.rows = _check(lib.spmv_route_rows(self.tokens, self.k, self.experts, self.align))
-        work = _check(lib.spmv_route_workspace(self.tokens, self.k, self.experts))
-        m, dev = self.tokens * self.k, ids.device
-        with _On(stream, (ids,)) as s:
-            # one allocation: slots, sources, offsets, workspace
-            self._buf = torch.empty((m + self.rows + self.experts + 1 + work // 4,), dtype=torch.int32, device=dev)
-            base = self._buf.data_ptr()
-            self._slots, self._sources = base, base + 4 * m
-            self._offsets = self._sources + 4 * self.rows
-            _check(lib.spmv_route_plan(self.tokens, self.k, self.experts, self.align, ptr, self._offsets, self._slots,
-                                       self._sources, self._offsets + 4 * (self.experts + 1), work, s))
+        ptr = _plain(ids, "ids", ids.shape, _I32)
+        self.tokens, self.k = tokens, k = ids.shape
+        self.experts, self.align = experts, align
+        self.rows, work = _plan_sizes(tokens, k, experts, align)
+        m = tokens * k
+        # one allocation: slots, sources, offsets, workspace
+        self._buf = _empty((m + self.rows + experts + 1 + work // 4,), dtype=_I32, device=ids.device)
+        self._slots = self._buf.data_ptr()
+        self._sources = self._slots + 4 * m
+        self._offsets = self._sources + 4 * self.rows
+        _check(lib.spmv_route_plan(tokens, k, experts, align, ptr, self._offsets, self._slots, self._sources,
+                                   self._offsets + 4 * (experts + 1), work, _current(ids)))
 
     @property
     def slots(self):
-        return self._buf[:self.tokens * self.k].view(self.tokens, self.k)
+        return self._buf.as_strided((self.tokens, self.k), (self.k, 1))
 
     @property
     def sources(self):
-        a = self.tokens * self.k
-        return self._buf[a:a + self.rows]
+        return self._buf.as_strided((self.rows,), (1,), self.tokens * self.k)
 
     @property
     def offsets(self):
-        a = self.tokens * self.k + self.rows
-        return self._buf[a:a + self.experts + 1]
+        return self._buf.as_strided((self.experts + 1,), (1,), self.tokens * self.k + self.rows)
 
     def dispatch(self, x, out=None, stream=None):
         """The tokens' rows sorted by expert (rows x d); rows without a source are 0."""
+        if stream is not None:
+            with _on(stream, self._buf, x, out):
+                return self.dispatch(x, out)
         code, ldx = _matrix(x, "x", self.tokens)
         d = x.shape[1]
-        with _On(stream, (x, out, self._buf)) as s:
-            xs, ldxs = _out(out, "out", x, self.rows, d)
-            _check(lib.spmv_route_dispatch(self.tokens, self.k, self.rows, d, self._slots, self._sources, x.data_ptr(),
-                                           ldx, xs.data_ptr(), ldxs, code, s))
+        xs, ldxs = _out(out, "out", x, self.rows, d)
+        _check(lib.spmv_route_dispatch(self.tokens, self.k, self.rows, d, self._slots, self._sources, x.data_ptr(), ldx,
+                                       xs.data_ptr(), ldxs, code, _current(x)))
         return xs
 
     def combine(self, ys, weights=None, out=None, stream=None):
         """y[t] = sum over j of weights[t, j] ys[slots[t, j]] (weights None: all 1)."""
+        if stream is not None:
+            with _on(stream, self._buf, ys, weights, out):
+                return self.combine(ys, weights, out)
         code, ldys = _matrix(ys, "ys", self.rows)
         d = ys.shape[1]
-        w = None if weights is None else _plain(weights, "weights", (self.tokens, self.k), torch.float32)
-        with _On(stream, (ys, weights, out, self._buf)) as s:
-            y, ldy = _out(out, "out", ys, self.tokens, d)
-            _check(lib.spmv_route_combine(self.tokens, self.k, self.rows, d, self._slots, w, ys.data_ptr(), ldys,
-                                          y.data_ptr(), ldy, code, s))
+        w = None if weights is None else _plain(weights, "weights", (self.tokens, self.k), _F32)
+        y, ldy = _out(out, "out", ys, self.tokens, d)
+        _check(lib.spmv_route_combine(self.tokens, self.k, self.rows, d, self._slots, w, ys.data_ptr(), ldys,
+                                      y.data_ptr(), ldy, code, _current(ys)))
         return y
 
     def combine_grad(self, dy, ys, weights, out=None, stream=None):
         """(dys, dweights): the gradients of combine in ys and in the weights."""
+        if stream is not None:
+            with _on(stream, self._buf, dy, ys, weights, out):
+                return self.combine_grad(dy, ys, weights, out)
         code, lddy = _matrix(dy, "dy", self.tokens)
         d = dy.shape[1]
         ldys = _matrix(ys, "ys", self.rows, d, dy.dtype)[1]
-        w = _plain(weights, "weights", (self.tokens, self.k), torch.float32)
-        with _On(stream, (dy, ys, weights, out, self._buf)) as s:
-            dys, lddys = _out(out, "out", dy, self.rows, d)
-            dw = torch.empty((self.tokens, self.k), dtype=torch.float32, device=dy.device)
-            _check(lib.spmv_route_combine_grad(self.tokens, self.k, self.rows, d, self._slots, self._sources, w,
-                                               dy.data_ptr(), lddy, ys.data_ptr(), ldys, dys.data_ptr(), lddys,
-                                               dw.data_ptr(), code, s))
+        w = _plain(weights, "weights", (self.tokens, self.k), _F32)
+        dys, lddys = _out(out, "out", dy, self.rows, d)
+        dw = _empty((self.tokens, self.k), dtype=_F32, device=dy.device)
+        _check(lib.spmv_route_combine_grad(self.tokens, self.k, self.rows, d, self._slots, self._sources, w,
+                                           dy.data_ptr(), lddy, ys.data_ptr(), ldys, dys.data_ptr(), lddys,
+                                           dw.data_ptr(), code, _current(dy)))
         return dys, dw
 
     def dispatch_grad(self, dxs, out=None, stream=None):
@@ -224,29 +239,32 @@ class DistillLoss:
         """scale * dloss[t] * d loss[t] / d z[t] (dloss float32, None = all 1).  ``out`` may be
         the logits themselves, which the gradient then replaces."""
         z, ids, teacher, lse, temperature = self._args
+        if stream is not None:
+            with _on(stream, z, ids, teacher, lse, self.stats, dloss, out):
+                return self.grad(dloss, scale, out)
         code, ldz = _matrix(z, "z")
         rows, vocab = z.shape
-        g = None if dloss is None else _plain(dloss, "dloss", (rows,), torch.float32)
-        with _On(stream, (z, ids, teacher, lse, self.stats, dloss, out)) as s:
-            dz, lddz = _out(out, "out", z, rows, vocab)
-            _check(lib.spmv_distill_grad(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, ids.data_ptr(),
-                                         teacher.data_ptr(), _DTYPES[teacher.dtype],
-                                         None if lse is None else lse.data_ptr(), temperature, self.stats.data_ptr(),
-                                         scale, g, dz.data_ptr(), lddz, s))
+        g = None if dloss is None else _plain(dloss, "dloss", (rows,), _F32)
+        dz, lddz = _out(out, "out", z, rows, vocab)
+        _check(lib.spmv_distill_grad(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, ids.data_ptr(),
+                                     teacher.data_ptr(), _DTYPES[teacher.dtype],
+                                     None if lse is None else lse.data_ptr(), temperature, self.stats.data_ptr(), scale,
+                                     g, dz.data_ptr(), lddz, _current(z)))
         return dz
 
 
 def _distill_args(z, ids, teacher, teacher_lse):
     code, ldz = _matrix(z, "z")
     rows = z.shape[0]
-    if ids.dim() != 2 or ids.shape[0] != rows:
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != rows:
         raise ValueError(f"ids must be a matrix of {rows} rows")
-    i = _plain(ids, "ids", ids.shape, torch.int32)
+    i = _plain(ids, "ids", shape, _I32)
     tcode = _DTYPES.get(teacher.dtype)
     if tcode is None:
         raise TypeError(f"teacher must be float32, float16 or bfloat16, not {teacher.dtype}")
-    t = _plain(teacher, "teacher", ids.shape, teacher.dtype)
-    lse = None if teacher_lse is None else _plain(teacher_lse, "teacher_lse", (rows,), torch.float32)
+    t = _plain(teacher, "teacher", shape, teacher.dtype)
+    lse = None if teacher_lse is None else _plain(teacher_lse, "teacher_lse", (rows,), _F32)
     return code, ldz, i, t, tcode, lse
 
 
@@ -256,15 +274,17 @@ def distill_loss(z, ids, teacher, teacher_lse=None, temperature=1.0, stream=None
     ``teacher_lse`` (the teacher's log-sum-exp over the whole vocabulary at the same
     temperature) the other columns count as one more class; without it the teacher's
     distribution is the softmax over the given entries."""
+    if stream is not None:
+        with _on(stream, z, ids, teacher, teacher_lse):
+            return distill_loss(z, ids, teacher, teacher_lse, temperature)
     code, ldz, i, t, tcode, lse = _distill_args(z, ids, teacher, teacher_lse)
     rows, vocab = z.shape
     res = DistillLoss()
-    res._args = (z, ids, teacher, teacher_lse, float(temperature))
-    with _On(stream, (z, ids, teacher, teacher_lse)) as s:
-        res.loss = torch.empty((rows,), dtype=torch.float32, device=z.device)
-        res.stats = torch.empty((rows, 4), dtype=torch.float32, device=z.device)
-        _check(lib.spmv_distill_loss(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, i, t, tcode, lse,
-                                     res._args[4], res.loss.data_ptr(), res.stats.data_ptr(), s))
+    res._args = (z, ids, teacher, teacher_lse, temperature)
+    res.loss = _empty((rows,), dtype=_F32, device=z.device)
+    res.stats = _empty((rows, 4), dtype=_F32, device=z.device)
+    _check(lib.spmv_distill_loss(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, i, t, tcode, lse, temperature,
+                                 res.loss.data_ptr(), res.stats.data_ptr(), _current(z)))
     return res
 
 
@@ -272,12 +292,14 @@ def distill_loss_grad(z, ids, teacher, teacher_lse=None, temperature=1.0, scale=
                       stream=None):
     """(loss, dz): :func:`distill_loss` and its gradient scale * row_scale[t] * d loss[t] / d z[t],
     reading z once.  ``out`` may be z itself, which the gradient then replaces."""
+    if stream is not None:
+        with _on(stream, z, ids, teacher, teacher_lse, row_scale, out):
+            return distill_loss_grad(z, ids, teacher, teacher_lse, temperature, scale, row_scale, out)
     code, ldz, i, t, tcode, lse = _distill_args(z, ids, teacher, teacher_lse)
     rows, vocab = z.shape
-    g = None if row_scale is None else _plain(row_scale, "row_scale", (rows,), torch.float32)
-    with _On(stream, (z, ids, teacher, teacher_lse, row_scale, out)) as s:
-        loss = torch.empty((rows,), dtype=torch.float32, device=z.device)
-        dz, lddz = _out(out, "out", z, rows, vocab)
-        _check(lib.spmv_distill_loss_grad(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, i, t, tcode, lse,
-                                          float(temperature), loss.data_ptr(), scale, g, dz.data_ptr(), lddz, s))
+    g = None if row_scale is None else _plain(row_scale, "row_scale", (rows,), _F32)
+    loss = _empty((rows,), dtype=_F32, device=z.device)
+    dz, lddz = _out(out, "out", z, rows, vocab)
+    _check(lib.spmv_distill_loss_grad(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, i, t, tcode, lse, temperature,
+                                      loss.data_ptr(), scale, g, dz.data_ptr(), lddz, _current(z)))
     return loss, dz

@@ -263,7 +263,7 @@ def test_route_rows_past_32_bits(spmv):
 
 
 def some_target(rows, vocab, k, g, absent=0.1):
-    ids = torch.stack([torch.randperm(vocab, generator=g)[:k] if vocab < 100000 else
+    ids = torch.stack([torch.randperm(vocab, generator=g)[:k] if vocab * rows < 100000 else
                        torch.randint(0, vocab // k, (k,), generator=g) + torch.arange(k) * (vocab // k)
                        for _ in range(rows)]).to(torch.int32) if rows else torch.zeros(0, k, dtype=torch.int32)
     if ids.shape[1] < k:
@@ -355,7 +355,8 @@ def teacher_lse_of(ids, teacher, vocab, tau, g):
 @pytest.mark.parametrize("rows,vocab,k", [(1, 1, 1), (3, 2, 1), (4, 7, 3), (5, 33, 8), (9, 257, 16), (4, 1000, 33),
                                           (6, 4097, 64), (3, 8192, 512), (3, 20011, 20), (1, 32768, 16), (2, 50021, 64),
                                           (1, 131072, 64), (1, 151937, 100), (1, 262144, 8), (1, 300007, 64),
-                                          (1, 600011, 30)])
+                                          (1, 600011, 30), (160, 9000, 20), (330, 17001, 64), (153, 70001, 33),
+                                          (155, 131072, 64), (200, 33000, 300), (152, 270001, 5)])
 def test_distill(spmv, dtype, tail, rows, vocab, k):
     g = gen(vocab + k)
     tau = 1.0 if vocab % 2 else 2.0
@@ -368,40 +369,40 @@ def test_distill(spmv, dtype, tail, rows, vocab, k):
 @pytest.mark.parametrize("dtype", ALL)
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("shift,pad", [(1, 0), (3, 5), (0, 8)])
-@pytest.mark.parametrize("vocab", [1, 131, 9001])
-def test_distill_any_address_and_in_place(spmv, dtype, tail, shift, pad, vocab):
+@pytest.mark.parametrize("rows,vocab", [(5, 1), (5, 131), (5, 9001), (310, 9001)])
+def test_distill_any_address_and_in_place(spmv, dtype, tail, shift, pad, rows, vocab):
     g = gen(vocab + shift)
-    ids, teacher = some_target(5, vocab, min(6, vocab), g)
-    z, _ = placed((torch.randn(5, vocab, generator=g) * 2).to(dtype), shift, pad)
+    ids, teacher = some_target(rows, vocab, min(6, vocab), g)
+    z, _ = placed((torch.randn(rows, vocab, generator=g) * 2).to(dtype), shift, pad)
     lse = teacher_lse_of(ids, teacher, vocab, 1.0, g) if tail else None
-    out, buf = placed(torch.zeros(5, vocab, dtype=dtype), shift, pad)
+    out, buf = placed(torch.zeros(rows, vocab, dtype=dtype), shift, pad)
     check_distill(spmv, z, ids, teacher, lse, 1.0, out=out)
     assert surroundings_untouched(out, buf)
-    out, buf = placed(torch.zeros(5, vocab, dtype=dtype), shift + 1, pad)  # another offset than z's
+    out, buf = placed(torch.zeros(rows, vocab, dtype=dtype), shift + 1, pad)  # another offset than z's
     check_distill(spmv, z, ids, teacher, lse, 1.0, out=out)
     assert surroundings_untouched(out, buf)
     kw = {"teacher_lse": None if lse is None else lse.cuda()}
     args = (ids.cuda(), teacher.cuda())
-    loss, dz = spmv.distill_loss_grad(z, *args, **kw)
-    for fused in (True, False):
+    for fused in (True, False):  # in place gives the bits that another output gets
         here, buf = placed(z, shift, pad)
         if fused:
+            loss, dz = spmv.distill_loss_grad(z, *args, **kw)
             l2, d2 = spmv.distill_loss_grad(here, *args, **kw, out=here)
         else:
+            res = spmv.distill_loss(z, *args, **kw)
+            loss, dz = res.loss, res.grad()
             res = spmv.distill_loss(here, *args, **kw)
             l2, d2 = res.loss, res.grad(out=here)
-        assert torch.equal(l2, loss) and d2.data_ptr() == here.data_ptr()
-        # the same numbers from the same registers, or again from stats
-        assert torch.equal(d2, dz) if fused else torch.allclose(d2.float(), dz.float(), rtol=2 * H[dtype] + 1e-5, atol=1e-6)
+        assert torch.equal(l2, loss) and torch.equal(d2, dz) and d2.data_ptr() == here.data_ptr()
         assert surroundings_untouched(here, buf)
 
 
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("teacher_dtype", ALL)
-@pytest.mark.parametrize("vocab", [300, 40000])
-def test_distill_masks_and_teacher_types(spmv, tail, teacher_dtype, vocab):
+@pytest.mark.parametrize("rows,vocab", [(8, 300), (8, 40000), (170, 40000)])
+def test_distill_masks_and_teacher_types(spmv, tail, teacher_dtype, rows, vocab):
     g = gen(vocab)
-    rows, k = 8, 12
+    k = 12
     ids, teacher = some_target(rows, vocab, k, g)
     teacher = teacher.to(teacher_dtype).float()
     z = torch.randn(rows, vocab, generator=g) * 2
