@@ -12,6 +12,7 @@ constexpr int kMaxTop = 256;
 constexpr int kGateMaxN = 512;    // rows up to this length are taken by one warp each
 constexpr int kGateMaxK = 32;     // ... with one lane per chosen entry
 constexpr int kMaxCand = 1024;    // candidates that one CTA sorts
+constexpr int kMaxBatches = 1024; // batches that are read again
 constexpr int kMaxGroups = 1024;  // maxima that set the first threshold
 
 // (key of the value, column) as one number: unique within a row, larger = taken earlier.
@@ -109,9 +110,9 @@ __global__ void __launch_bounds__(256) k_topk_warp(TopArgs a) {
 // 1. Every thread reads its share once, a few vectors (a batch) at a time, and keeps its maximum
 //    and its batches' maxima (in shared memory).  The k-th largest of the maxima of groups of
 //    threads is a lower bound of the row's k-th largest entry that passes few others.
-// 2. The few batches that reach it are read again (from L2), a warp at a time, and their entries
-//    at or above it go to the first CTA's candidate list.
-// 3. If the list overflows (values bunched in one group, or many ties), the threshold is
+// 2. The few batches that reach it are listed and read again (from L2), all at once, and their
+//    entries at or above it go to the first CTA's candidate list.
+// 3. If a list overflows (values bunched in one group, or many ties), the threshold is
 //    bisected on (value, column) numbers, which are unique, until between k and kMaxCand
 //    pass: at most 64 counting passes, whatever the row holds.
 // 4. The first CTA ranks the candidates by counting and writes the k largest.
@@ -123,7 +124,8 @@ struct TopShared {
     float group_max[kMaxGroups];
     float2 sums[kMaxCluster * 16];  // per warp of the cluster: maximum, sum of exponentials
     float top_vals[kMaxTop];
-    uint32_t count[4];  // [0] candidates (first CTA's), [1..3] the bisection's counts
+    uint32_t batch[kMaxBatches];  // listed: thread and slot of the maximum
+    uint32_t count[5];  // [0] candidates (first CTA's), [1..3] the bisection's counts, [4] listed batches
     float thr, lse_m, lse_sum;
 };
 
@@ -224,7 +226,7 @@ __device__ __noinline__ uint32_t collect_by_bisection(const TopArgs &a, TopShare
 
 // per: batches that share a maximum; slots: maxima a thread has for its whole batches.
 template <typename T>
-__global__ void __launch_bounds__(512, 2) k_topk_row(TopArgs a, int log2_ctas, int log2_group, int per, int slots) {
+__global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, int log2_group, int per, int slots) {
     __shared__ __align__(16) TopShared sh;
     extern __shared__ float batch_max[];  // [slots + 1][threads]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_threads = blockDim.x, n_warps = n_threads >> 5;
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(512, 2) k_topk_row(TopArgs a, int log2_ctas, i
     const Batches<T> batches(share, tid, n_threads);
     const bool want_lse = a.lse || a.weighting == SPMV_WEIGHTS_ROW;
     if (ctas > 1) cluster_arrive();  // the peers' shared memory may be written from here on ...
-    if (tid < 4) sh.count[tid] = 0;
+    if (tid < 5) sh.count[tid] = 0;
 
     Running run;  // its maximum passes over NaNs; the batches' maxima hand them on
     const auto take = [&](const uint4 *x, int n) {
@@ -307,35 +309,49 @@ __global__ void __launch_bounds__(512, 2) k_topk_row(TopArgs a, int log2_ctas, i
     __syncthreads();
     const float thr = fmaxf(sh.thr, -FLT_MAX);  // above -inf: masked entries are never candidates
 
-    // a warp looks at one lane's batch together, a value a lane
     constexpr int kN = Vec<T>::kN;
-    bool room = true;
-    for (int s = 0; s <= slots; ++s) {
-        uint32_t todo = __ballot_sync(0xffffffffu, !(batch_max[s * n_threads + tid] < thr));
-        while (todo && room) {
-            const int owner = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int edge = __shfl_sync(0xffffffffu, batches.edge(), owner);
-            const int q0 = s == slots ? 0 : s * per, q1 = s == slots ? 1 : min(q0 + per, batches.whole);
-            for (int q = q0; q < q1 && room; ++q) {
-                const int i = lane / kN;
-                const int v = s == slots ? edge : batches.vector(q, i) - lane + owner;
-                const int64_t e = share.first(v) + lane % kN;
-                const bool there = i < kBatch && (s == slots ? i == 0 && e >= 0 && e < a.n : v < share.hi);
-                const float f = there ? to_f32(share.p[e]) : kNegInf;
-                const uint32_t hits = __ballot_sync(0xffffffffu, !(f < thr));
-                if (!hits) continue;
-                uint32_t at = 0;
-                if (lane == 0) at = ctas > 1 ? peer_add(peer_addr(&sh.count[0], 0), __popc(hits)) : atomicAdd(&sh.count[0], __popc(hits));
-                at = __shfl_sync(0xffffffffu, at, 0);
-                room = at + __popc(hits) <= kMaxCand;  // full: whoever finds more need not say so
-                if (room && (hits >> lane & 1)) {
-                    at += __popc(hits & ((1u << lane) - 1));
-                    if (ctas > 1) peer_store64(peer_addr(&sh.cand[at], 0), composite(f, e));
-                    else sh.cand[at] = composite(f, e);
+    for (int s = 0; s <= slots; ++s)
+        if (!(batch_max[s * n_threads + tid] < thr)) {
+            const uint32_t at = atomicAdd(&sh.count[4], 1u);
+            if (at < kMaxBatches) sh.batch[at] = static_cast<uint32_t>(s) << 16 | tid;
+        }
+    __syncthreads();
+    const uint32_t listed = sh.count[4];
+    if (listed <= kMaxBatches) {
+        // value i of the listed batches: a thread takes those n_threads apart, its loads in flight
+        // together
+        const int per_listed = per * kBatch * kN, values = static_cast<int>(listed) * per_listed;
+        for (int i0 = tid; i0 < values; i0 += 4 * n_threads) {
+            float f[4];
+            int64_t e[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * n_threads, at = i / per_listed, in = i - at * per_listed;
+                f[u] = kNegInf;
+                e[u] = -1;
+                if (i < values) {
+                    const uint32_t b = sh.batch[at], s = b >> 16, owner = b & 0xffff;
+                    // the owner's vector in / kN of this slot, or its vector at the row's ends
+                    const int v = s == static_cast<uint32_t>(slots) ? (owner == 0 && share.lo == 1 ? 0 : share.hi)
+                                                                    : share.lo + static_cast<int>(owner) + (static_cast<int>(s) * per * kBatch + in / kN) * n_threads;
+                    const bool edge = s == static_cast<uint32_t>(slots);
+                    e[u] = share.first(v) + in % kN;
+                    if (edge ? in < kN && e[u] >= 0 && e[u] < a.n : v < share.hi) f[u] = to_f32(share.p[e[u]]);
                 }
             }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (!(f[u] < thr)) {
+                    const uint32_t at = ctas > 1 ? peer_add(peer_addr(&sh.count[0], 0), 1) : atomicAdd(&sh.count[0], 1u);
+                    if (at < kMaxCand) {
+                        if (ctas > 1) peer_store64(peer_addr(&sh.cand[at], 0), composite(f[u], e[u]));
+                        else sh.cand[at] = composite(f[u], e[u]);
+                    }
+                }
         }
+    } else if (tid == 0) {
+        if (ctas > 1) peer_add(peer_addr(&sh.count[0], 0), kMaxCand + 1);
+        else atomicAdd(&sh.count[0], kMaxCand + 1);
     }
     __syncwarp();
     cluster_sync(ctas);
@@ -475,10 +491,9 @@ cudaError_t launch_topk_row(const TopArgs &a, cudaStream_t s) {
     // few rows: more CTAs a row while SMs would be idle and each thread still has a batch
     int ctas = 1;
     while (ctas < kMaxCluster && a.rows * ctas < kSms && vectors > ctas * 512 * kBatch) ctas *= 2;
-    if (const char *e = getenv("TOPK_C")) ctas = atoi(e);//TUNE
     const int64_t share = ceil_div(vectors, ctas);
-    int threads = share <= 512 && a.k <= 64 ? 128 : share <= 2048 && a.k <= 128 ? 256 : 512;
-    if (const char *e = getenv("TOPK_T")) threads = atoi(e);//TUNE
+    // many rows: CTAs small enough to hide each other's barriers
+    const int threads = share <= 512 && a.k <= 64 ? 128 : (share <= 2048 || a.rows * ctas >= 4 * kSms) && a.k <= 128 ? 256 : 512;
     // at least twice as many groups as entries wanted, so that the threshold passes few others
     int log2_group = 5, log2_ctas = 0;
     while (log2_group > 0 && ctas * threads >> log2_group < 2 * a.k) --log2_group;
