@@ -22,7 +22,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libspmv_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["api.cu", "build.cu", "sell.cu", "sellmm.cu", "vector.cu", "merge.cu", "vecops.cu", "noalloc.cu", "solve.cu", "sellg.cu", "order.cu", "sellv.cu", "probe.cu", "sellb.cu",
-           "topk.cu", "route.cu", "distill.cu", "distill_f32.cu", "distill_f16.cu", "distill_bf16.cu"]
+           "topk.cu", "gate.cu", "route.cu", "distill.cu", "distill_f32.cu", "distill_f16.cu", "distill_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -50,7 +50,7 @@ def _compile(src: str, extra: list[str]) -> str:
     obj = os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o")
     deps = [os.path.join(CSRC, src), os.path.join(CSRC, "spmv_internal.cuh"), os.path.join(CSRC, "device_util.cuh"),
             os.path.join(CSRC, "sell_common.cuh"), os.path.join(CSRC, "rows_common.cuh"),
-            os.path.join(CSRC, "distill.cuh"), os.path.join(INCLUDE, "spmv.h")]
+            os.path.join(CSRC, "topk.cuh"), os.path.join(CSRC, "distill.cuh"), os.path.join(INCLUDE, "spmv.h")]
     if _newer(obj, deps):
         return obj
     cmd = [nvcc_path()] + common_flags() + extra + ["-c", os.path.join(CSRC, src), "-o", obj]

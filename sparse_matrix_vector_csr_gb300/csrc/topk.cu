@@ -1,7 +1,7 @@
 // The k largest entries of every row of a dense matrix: dense rows to sparse rows.  Values
 // descend, ties go to the lowest column, -inf is never taken.  With them the row's
 // log-sum-exp (the same pass over the row) and softmax weights, and the weights' gradient.
-#include "rows_common.cuh"
+#include "topk.cuh"
 
 namespace spmv {
 namespace {
@@ -9,8 +9,8 @@ namespace {
 using namespace rows;
 
 constexpr int kMaxTop = 256;
-constexpr int kGateMaxN = 512;    // rows up to this length are taken by one warp each
-constexpr int kGateMaxK = 32;     // ... with one lane per chosen entry
+constexpr int kWarpMaxN = 512;    // rows up to this length are taken by one warp each
+constexpr int kWarpMaxK = 32;     // ... with one lane per chosen entry
 constexpr int kMaxCand = 1024;    // candidates that one CTA sorts
 constexpr int kMaxBatches = 1024; // batches that are read again
 constexpr int kMaxGroups = 1024;  // maxima that set the first threshold
@@ -22,15 +22,6 @@ __device__ __forceinline__ unsigned long long composite(float v, int64_t col) {
 __device__ __forceinline__ int32_t composite_col(unsigned long long c) {
     return static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
 }
-
-struct TopArgs {
-    int64_t rows, n, ldx;
-    int k, weighting;
-    float scale, inv_temperature;  // scale = log2(e) / temperature
-    const void *x;
-    int32_t *ids;
-    float *vals, *weights, *lse;
-};
 
 // ----------------------------------------------------------------------------
 // short rows: one warp per row
@@ -424,16 +415,6 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
 // row; __syncwarp orders its plain stores before the stores to the chosen columns.
 constexpr int kGradPiece = 1024;  // values per warp
 
-struct TopGradArgs {
-    int64_t rows, n, ldx, lddx, pieces;
-    int k, weighting;
-    float inv_temperature;
-    const int32_t *ids;
-    const float *weights, *dweights, *lse;
-    const void *x;
-    void *dx;
-};
-
 template <typename T>
 __global__ void __launch_bounds__(256) k_topk_grad(TopGradArgs a) {
     constexpr int kN = Vec<T>::kN;
@@ -507,7 +488,7 @@ cudaError_t launch_topk_row(const TopArgs &a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_topk(const TopArgs &a, cudaStream_t s) {
-    return a.n <= kGateMaxN && a.k <= kGateMaxK ? launch_topk_warp<T>(a, s) : launch_topk_row<T>(a, s);
+    return a.n <= kWarpMaxN && a.k <= kWarpMaxK ? launch_topk_warp<T>(a, s) : launch_topk_row<T>(a, s);
 }
 
 int check_top(int64_t rows, int64_t n, int32_t k, int dtype, double temperature) {
@@ -550,6 +531,10 @@ extern "C" SPMV_API int spmv_topk_rows(int64_t rows, int64_t n, int32_t k, const
     const TopArgs a{rows, n, ldx, k, weighting, static_cast<float>(1.4426950408889634 / temperature),
                     static_cast<float>(1.0 / temperature), x, ids, vals, weights, lse};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n <= kGateMaxN && k <= kGateMaxK) {
+        SPMV_TRY_CUDA(launch_gate(a, dtype, s));
+        return SPMV_OK;
+    }
     SPMV_TRY_CUDA(dtype == SPMV_F32   ? launch_topk<float>(a, s)
                   : dtype == SPMV_F16 ? launch_topk<__half>(a, s)
                                       : launch_topk<__nv_bfloat16>(a, s));
@@ -586,6 +571,10 @@ extern "C" SPMV_API int spmv_topk_rows_grad(int64_t rows, int64_t n, int32_t k, 
     const TopGradArgs a{rows, n, ldx, lddx, pieces, k, weighting,
                         static_cast<float>(1.0 / temperature), ids, weights, dweights, lse, x, dx};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n <= kGateMaxN && k <= kGateMaxK) {
+        SPMV_TRY_CUDA(launch_gate_grad(a, dtype, s));
+        return SPMV_OK;
+    }
     const unsigned grid = static_cast<unsigned>(ceil_div(rows * pieces, 8));
     if (dtype == SPMV_F32) k_topk_grad<float><<<grid, 256, 0, s>>>(a);
     else if (dtype == SPMV_F16) k_topk_grad<__half><<<grid, 256, 0, s>>>(a);
