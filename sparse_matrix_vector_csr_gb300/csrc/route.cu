@@ -7,8 +7,10 @@
 // bytes, so each row is read once and written once, tokens first: a token's row sits in
 // registers while its k sorted copies are written (or its k sorted rows are summed).
 #include <initializer_list>
+#include <type_traits>
 #include <utility>
 
+#include "device_util.cuh"
 #include "rows_common.cuh"
 
 namespace spmv {
@@ -18,7 +20,7 @@ using namespace rows;
 
 constexpr int kPlanThreads = 512;
 constexpr int kMaxExperts = 4096;
-constexpr int64_t kPlanChunk = 2048;  // entries per CTA of the plan, at least
+constexpr int64_t kPlanChunk = 1024;  // entries per CTA of the plan, at least
 constexpr int64_t kPlanCtas = 128;    // CTAs of the plan, at most
 
 struct PlanShape {
@@ -35,6 +37,8 @@ PlanShape plan_shape(int64_t tokens, int32_t k, int32_t experts) {
     p.ctas = static_cast<int>(ceil_div(p.entries, p.chunk));
     if (p.ctas < 1) p.ctas = 1;
     p.warps = kPlanThreads / 32;
+    const int64_t most = p.entries < p.chunk ? p.entries : p.chunk;
+    while (p.warps > 1 && p.warps * 16 >= most) p.warps /= 2;  // no more than there are 32s of entries
     while (p.warps > 1 && static_cast<int64_t>(p.warps) * experts > 16384) p.warps /= 2;
     p.smem = static_cast<size_t>(p.warps + 2) * static_cast<size_t>(experts) * sizeof(int32_t);
     return p;
@@ -45,7 +49,7 @@ __device__ __forceinline__ int32_t expert_of(const int32_t *ids, int64_t i, int3
     return static_cast<uint32_t>(e) < static_cast<uint32_t>(experts) ? e : -1;
 }
 
-// hist[b * experts + e] = entries of expert e in CTA b's share
+// hist[e * CTAs + b] = entries of expert e in CTA b's share
 __global__ void __launch_bounds__(kPlanThreads) k_route_hist(int64_t entries, int64_t chunk, int32_t experts,
                                                             const int32_t *__restrict__ ids, int32_t *__restrict__ hist) {
     extern __shared__ int32_t count[];
@@ -58,7 +62,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_route_hist(int64_t entries, in
     }
     __syncthreads();
     for (int e = threadIdx.x; e < experts; e += kPlanThreads)
-        hist[static_cast<int64_t>(blockIdx.x) * experts + e] = count[e];
+        hist[static_cast<int64_t>(e) * gridDim.x + blockIdx.x] = count[e];
+    dev::allow_dependents();
 }
 
 // Every CTA takes its share of the entries in order, each of its ranking warps a run of
@@ -92,24 +97,36 @@ __global__ void __launch_bounds__(kPlanThreads) k_route_place(int64_t entries, i
         }
     __syncthreads();
 
-    // per expert: entries in all and in earlier CTAs; then the warps' counts become places
-    // relative to the expert's segment
-    for (int e = tid; e < experts; e += kPlanThreads) {
-        int32_t before = 0, sum = 0;
-        if (hist) {
-            for (int b = 0; b < gridDim.x; ++b) {
-                const int32_t c = hist[static_cast<int64_t>(b) * experts + e];
-                if (b < blockIdx.x) before += c;
+    // per expert: entries in all and in earlier CTAs (a warp per expert, at most four counts a
+    // lane); then the warps' counts become places relative to the expert's segment
+    if (hist) {
+        dev::grid_wait();
+        for (int e = warp; e < experts; e += kPlanThreads / 32) {
+            int32_t before = 0, sum = 0;
+#pragma unroll
+            for (int i = 0; i < kPlanCtas / 32; ++i) {
+                const int b = i * 32 + lane;
+                const int32_t c = b < gridDim.x ? hist[static_cast<int64_t>(e) * gridDim.x + b] : 0;
+                before += b < blockIdx.x ? c : 0;
                 sum += c;
             }
+            before = warp_sum(before);
+            sum = warp_sum(sum);
+            if (lane == 0) {
+                start[e] = before;
+                total[e] = sum;
+            }
         }
-        int32_t at = before;
+        __syncthreads();
+    }
+    for (int e = tid; e < experts; e += kPlanThreads) {
+        int32_t at = hist ? start[e] : 0;
         for (int w = 0; w < n_warps; ++w) {
             const int32_t c = wcount[w * experts + e];
             wcount[w * experts + e] = at;
             at += c;
         }
-        total[e] = hist ? sum : at;
+        if (!hist) total[e] = at;
     }
     __syncthreads();
 
@@ -190,34 +207,48 @@ struct Unit<4> { using type = uint32_t; };
 template <>
 struct Unit<2> { using type = uint16_t; };
 
-// Zero the sorted rows without a source among the 32 that this warp looks at.
+// Zero the sorted rows without a source among 32 that the CTA looks at: padding comes in runs
+// (behind each segment, and behind the last), so each warp takes every eighth.
+constexpr int kPadRows = 32;  // per CTA
 template <typename U>
 __device__ void zero_padding(int64_t first, int64_t rows, const int32_t *sources, int64_t units, U *out, int64_t ld) {
-    const int lane = threadIdx.x & 31;
-    const bool pad = first + lane < rows && sources[first + lane] < 0;
-    uint32_t todo = __ballot_sync(0xffffffffu, pad);
-    while (todo) {
-        U *row = out + (first + __ffs(todo) - 1) * ld;
-        todo &= todo - 1;
-        for (int64_t u = lane; u < units; u += 32) row[u] = U{};
-    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t pad = __ballot_sync(0xffffffffu, first + lane < rows && sources[first + lane] < 0);
+    for (int i = warp; i < 32; i += kRowWarps)
+        if (pad >> i & 1) {
+            U *row = out + (first + i) * ld;
+            for (int64_t u = lane; u < units; u += 32) row[u] = U{};
+        }
 }
+// A token's entries 32 at a time, a lane each: sorted row (-1: none) and weight.
+struct Entries {
+    int32_t slot;
+    float weight;
+    __device__ __forceinline__ Entries(int64_t t, int k, int j0, int64_t rows, const int32_t *slots, const float *weights) {
+        const int j = j0 + (threadIdx.x & 31);
+        slot = j < k ? slots[t * k + j] : -1;
+        if (slot >= rows) slot = -1;
+        weight = weights && slot >= 0 ? weights[t * k + j] : 1.0f;
+    }
+    __device__ __forceinline__ int32_t row(int j) const { return __shfl_sync(0xffffffffu, slot, j); }
+    __device__ __forceinline__ float of(int j) const { return __shfl_sync(0xffffffffu, weight, j); }
+};
 
 // xs[slots[t, j]] = x[t] for every entry; xs[s] = 0 for rows without a source.  A warp
 // takes kU x 32 units of one token's row (units: the widest loads that the alignment of
-// every row allows); the CTAs behind the tokens' zero the padding.
+// every row allows); the first CTAs zero the padding.
 template <typename U, int kU>
 __global__ void __launch_bounds__(kRowThreads) k_dispatch(int64_t tokens, int k, int64_t rows, int64_t units,
-                                                         int64_t parts, int64_t token_ctas,
+                                                         int64_t parts, int64_t pad_ctas,
                                                          const int32_t *__restrict__ slots,
                                                          const int32_t *__restrict__ sources, const U *__restrict__ x,
                                                          int64_t ldx, U *__restrict__ xs, int64_t ldxs) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x >= token_ctas) {
-        zero_padding(((blockIdx.x - token_ctas) * kRowWarps + warp) * 32, rows, sources, units, xs, ldxs);
+    if (blockIdx.x < pad_ctas) {
+        zero_padding(static_cast<int64_t>(blockIdx.x) * kPadRows, rows, sources, units, xs, ldxs);
         return;
     }
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
+    const int64_t item = (blockIdx.x - pad_ctas) * kRowWarps + warp;
     const int64_t t = item / parts;
     if (t >= tokens) return;
     const int64_t u0 = (item - t * parts) * (32 * kU) + lane;
@@ -226,13 +257,17 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(int64_t tokens, int k,
 #pragma unroll
     for (int i = 0; i < kU; ++i)
         if (u0 + i * 32 < units) v[i] = src[u0 + i * 32];
-    for (int j = 0; j < k; ++j) {
-        const int64_t s = slots[t * k + j];
-        if (s < 0 || s >= rows) continue;
-        U *dst = xs + s * ldxs;
+    for (int j0 = 0; j0 < k; j0 += 32) {
+        const Entries entries(t, k, j0, rows, slots, nullptr);
+        const int n = min(k - j0, 32);
+        for (int j = 0; j < n; ++j) {
+            const int64_t s = entries.row(j);
+            if (s < 0) continue;
+            U *dst = xs + s * ldxs;
 #pragma unroll
-        for (int i = 0; i < kU; ++i)
-            if (u0 + i * 32 < units) dst[u0 + i * 32] = v[i];
+            for (int i = 0; i < kU; ++i)
+                if (u0 + i * 32 < units) dst[u0 + i * 32] = v[i];
+        }
     }
 }
 
@@ -254,8 +289,11 @@ __device__ __forceinline__ U unit_from_f32(const float *in) {
     return u;
 }
 
-// y[t] = sum over j of weights[t, j] ys[slots[t, j]], j ascending, in 32 bits, rounded once.
-template <typename T, typename U, int kU>
+// y[t] = sum over j of weights[t, j] ys[slots[t, j]], j ascending, in 32 bits, rounded once.  A
+// warp has kU x 32 units of kJ entries' rows in flight.  Many tokens: 2 x 2 keeps 40 warps on an
+// SM (16384 tokens x 8 rows of 4096 bf16 values 197 us; 4 x 2 with 20 warps 277 us).  Few tokens:
+// one load's latency for four entries (4 tokens x 8 rows 4.9 us; one by one 8.8 us).
+template <typename T, typename U, int kJ, int kU>
 __global__ void __launch_bounds__(kRowThreads) k_combine(int64_t tokens, int k, int64_t rows, int64_t units,
                                                         int64_t parts, const int32_t *__restrict__ slots,
                                                         const float *__restrict__ weights, const U *__restrict__ ys,
@@ -267,23 +305,38 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(int64_t tokens, int k, 
     if (t >= tokens) return;
     const int64_t u0 = (item - t * parts) * (32 * kU) + lane;
     float acc[kU][kN] = {};
-    for (int j = 0; j < k; ++j) {
-        const int64_t s = slots[t * k + j];
-        if (s < 0 || s >= rows) continue;
-        const float w = weights ? weights[t * k + j] : 1.0f;
-        const U *src = ys + s * ldys;
-        U v[kU];
+    for (int j0 = 0; j0 < k; j0 += 32) {
+        const Entries entries(t, k, j0, rows, slots, weights);
+        const int n = min(k - j0, 32);
+        for (int j = 0; j < n; j += kJ) {
+            U v[kJ][kU];
+            float w[kJ];
+            bool some[kJ];
 #pragma unroll
-        for (int i = 0; i < kU; ++i)
-            if (u0 + i * 32 < units) v[i] = src[u0 + i * 32];
+            for (int q = 0; q < kJ; ++q) {
+                const int64_t s = entries.row(j + q);  // (-1 past the last)
+                w[q] = entries.of(j + q);
+                some[q] = s >= 0;
+                if (some[q]) {
+                    const U *src = ys + s * ldys;
 #pragma unroll
-        for (int i = 0; i < kU; ++i)
-            if (u0 + i * 32 < units) {
-                float f[kN];
-                unit_to_f32<T>(v[i], f);
-#pragma unroll
-                for (int q = 0; q < kN; ++q) acc[i][q] = fmaf(w, f[q], acc[i][q]);
+                    for (int i = 0; i < kU; ++i)
+                        if (u0 + i * 32 < units) v[q][i] = src[u0 + i * 32];
+                }
             }
+#pragma unroll
+            for (int q = 0; q < kJ; ++q)
+                if (some[q]) {
+#pragma unroll
+                    for (int i = 0; i < kU; ++i)
+                        if (u0 + i * 32 < units) {
+                            float f[kN];
+                            unit_to_f32<T>(v[q][i], f);
+#pragma unroll
+                            for (int p = 0; p < kN; ++p) acc[i][p] = fmaf(w[q], f[p], acc[i][p]);
+                        }
+                }
+        }
     }
     U *dst = y + t * ldy;
 #pragma unroll
@@ -294,9 +347,9 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(int64_t tokens, int k, 
 // dys[slots[t, j]] = weights[t, j] dy[t] and dweights[t, j] = <dy[t], ys[slots[t, j]]>: one CTA
 // per token, so that its products reduce inside the CTA in a fixed order (no atomics); entries
 // are taken four at a time, dy coming from L1 from the second time on.  Rows of dys without
-// a source are zeroed by the CTAs behind the tokens'.
+// a source are zeroed by the first CTAs.
 template <typename T, typename U>
-__global__ void __launch_bounds__(kRowThreads) k_combine_grad(int64_t tokens, int k, int64_t rows, int64_t units,
+__global__ void __launch_bounds__(kRowThreads) k_combine_grad(int64_t pad_ctas, int k, int64_t rows, int64_t units,
                                                              const int32_t *__restrict__ slots,
                                                              const int32_t *__restrict__ sources,
                                                              const float *__restrict__ weights, const U *__restrict__ dy,
@@ -307,11 +360,11 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_grad(int64_t tokens, in
     constexpr int kJ = 4;
     __shared__ float part[kJ][kRowWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x >= tokens) {
-        zero_padding(((blockIdx.x - tokens) * kRowWarps + warp) * 32, rows, sources, units, dys, lddys);
+    if (blockIdx.x < pad_ctas) {
+        zero_padding(static_cast<int64_t>(blockIdx.x) * kPadRows, rows, sources, units, dys, lddys);
         return;
     }
-    const int64_t t = blockIdx.x;
+    const int64_t t = blockIdx.x - pad_ctas;
     const U *g = dy + t * lddy;
     for (int j0 = 0; j0 < k; j0 += kJ) {
         int64_t s[kJ];
@@ -403,19 +456,24 @@ constexpr int units_per_lane(int bytes) { return bytes == 16 ? 4 : 8; }
 template <typename T>
 void launch_combine(int unit, int64_t tokens, int k, int64_t rows, int64_t d, const int32_t *slots,
                     const float *weights, const void *ys, int64_t ldys, void *y, int64_t ldy, cudaStream_t s) {
-    auto go = [&](auto tag) {
+    auto go = [&](auto tag, auto entries, auto per_lane) {
         using U = decltype(tag);
-        constexpr int kU = sizeof(U) == 16 ? 2 : 4;
+        constexpr int kJ = decltype(entries)::value, kU = decltype(per_lane)::value;
         constexpr int64_t kN = sizeof(U) / sizeof(T);
         const int64_t units = d / kN, parts = ceil_div(units, 32 * kU);
-        k_combine<T, U, kU><<<static_cast<unsigned>(ceil_div(tokens * parts, kRowWarps)), kRowThreads, 0, s>>>(
+        k_combine<T, U, kJ, kU><<<static_cast<unsigned>(ceil_div(tokens * parts, kRowWarps)), kRowThreads, 0, s>>>(
             tokens, k, rows, units, parts, slots, weights, static_cast<const U *>(ys), ldys / kN, static_cast<U *>(y),
             ldy / kN);
     };
-    if (unit == 16) go(uint4{});
-    else if (unit == 8) go(uint2{});
-    else if (unit == 4) go(uint32_t{});
-    else if constexpr (sizeof(T) == 2) go(uint16_t{});
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 2> two;
+    constexpr std::integral_constant<int, 4> four;
+    // few tokens: as many warps as there are 512-byte pieces
+    const bool few = tokens * d * static_cast<int64_t>(sizeof(T)) < int64_t(152) * 16 * 1024;
+    if (unit == 16) few ? go(uint4{}, four, one) : go(uint4{}, two, two);
+    else if (unit == 8) go(uint2{}, two, two);
+    else if (unit == 4) go(uint32_t{}, two, four);
+    else if constexpr (sizeof(T) == 2) go(uint16_t{}, two, four);
 }
 
 template <typename T>
@@ -425,8 +483,8 @@ void launch_combine_grad(int unit, int64_t tokens, int k, int64_t rows, int64_t 
     auto go = [&](auto tag) {
         using U = decltype(tag);
         constexpr int64_t kN = sizeof(U) / sizeof(T);
-        k_combine_grad<T, U><<<static_cast<unsigned>(tokens + ceil_div(rows, 32 * kRowWarps)), kRowThreads, 0, s>>>(
-            tokens, k, rows, d / kN, slots, sources, weights, static_cast<const U *>(dy), lddy / kN,
+        k_combine_grad<T, U><<<static_cast<unsigned>(tokens + ceil_div(rows, kPadRows)), kRowThreads, 0, s>>>(
+            ceil_div(rows, kPadRows), k, rows, d / kN, slots, sources, weights, static_cast<const U *>(dy), lddy / kN,
             static_cast<const U *>(ys), ldys / kN, static_cast<U *>(dys), lddys / kN, dweights);
     };
     if (unit == 16) go(uint4{});
@@ -489,9 +547,19 @@ extern "C" SPMV_API int spmv_route_plan(int64_t tokens, int32_t k, int32_t exper
         k_route_hist<<<p.ctas, kPlanThreads, static_cast<size_t>(experts) * 4, s>>>(m, p.chunk, experts, ids, hist);
         SPMV_TRY_CUDA(cudaGetLastError());
     }
-    k_route_place<<<p.ctas, kPlanThreads, p.smem, s>>>(m, p.chunk, experts, align, rows, p.warps, ids, hist, offsets,
-                                                       slots, sources);
-    SPMV_TRY_CUDA(cudaGetLastError());
+    // the second kernel counts its own share while the first one ends
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = hist ? 1 : 0;
+    SPMV_TRY_CUDA(cudaLaunchKernelEx(&cfg, k_route_place, m, p.chunk, experts, align, rows, p.warps, ids,
+                                     static_cast<const int32_t *>(hist), offsets, slots, sources));
     return SPMV_OK;
 }
 
@@ -517,9 +585,9 @@ extern "C" SPMV_API int spmv_route_dispatch(int64_t tokens, int32_t k, int64_t r
         using U = Unit<B>::type;                                                                               \
         constexpr int kU = units_per_lane(B);                                                                  \
         const int64_t units = d * vb / B, parts = ceil_div(units, 32 * kU);                                    \
-        const int64_t ctas = ceil_div(tokens * parts, kRowWarps);                                              \
-        k_dispatch<U, kU><<<static_cast<unsigned>(ctas + ceil_div(rows, 32 * kRowWarps)), kRowThreads, 0, s>>>( \
-            tokens, k, rows, units, parts, ctas, slots, sources, static_cast<const U *>(x), ldx * vb / B,      \
+        const int64_t pads = ceil_div(rows, kPadRows), ctas = ceil_div(tokens * parts, kRowWarps);             \
+        k_dispatch<U, kU><<<static_cast<unsigned>(pads + ctas), kRowThreads, 0, s>>>(                          \
+            tokens, k, rows, units, parts, pads, slots, sources, static_cast<const U *>(x), ldx * vb / B,      \
             static_cast<U *>(xs), ldxs * vb / B);                                                              \
     } while (0)
     SPMV_UNIT_SWITCH(unit, SPMV_DISPATCH)
