@@ -590,7 +590,7 @@ typedef enum { SPMV_WEIGHTS_NONE = 0, SPMV_WEIGHTS_SELECTED = 1, SPMV_WEIGHTS_RO
  *             An entry of -inf is never taken (a masked column): where a row has fewer than
  *             k others, the remaining ids are -1.  The type's lowest finite value is a value
  *             like any other.  A NaN counts as larger than +inf.
- *   vals      float[rows][k]: their values (-inf beside an id of -1).
+ *   vals      float[rows][k], or NULL: their values (-inf beside an id of -1).
  *   weights   float[rows][k] (weighting not NONE): exp(v / temperature) over the sum of the
  *             chosen entries' (SELECTED) or of the whole row's (ROW); 0 beside an id of -1.
  *   lse       float[rows], or NULL: log of the sum of exp(x / temperature) over the row

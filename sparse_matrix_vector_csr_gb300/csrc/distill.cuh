@@ -155,12 +155,19 @@ struct GradOf {
     }
 };
 
+constexpr int kBatchVectors = 4;  // in flight per thread where the row does not fit its registers
+constexpr int kKeepBatches = 2;   // of a row that is read twice: 92 KB of a CTA's shared memory
+
 template <typename T, int kR, int kMode>
-__global__ void __launch_bounds__(512, 2) k_distill(DistillArgs a, int log2_ctas) {
+__global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode == kGrad ? 3 : 4) k_distill(DistillArgs a, int log2_ctas) {
     constexpr int kN = Vec<T>::kN;
-    constexpr int kU = 4;  // vectors in flight per thread where the row is read twice
+    constexpr int kU = kBatchVectors;
     __shared__ DistillShared sh;
-    extern __shared__ uint32_t marks_mem[];  // with lse: a byte per vector of the CTA's share, a bit per value
+    constexpr int kKeep = kR == 0 && kMode == kLossGrad ? kKeepBatches : 0;
+    extern __shared__ __align__(16) unsigned char dynamic_mem[];
+    uint4 *keep = reinterpret_cast<uint4 *>(dynamic_mem) + threadIdx.x;
+    // with lse: a byte per vector of the CTA's share, a bit per value
+    uint32_t *marks_mem = reinterpret_cast<uint32_t *>(dynamic_mem + static_cast<size_t>(16) * kU * kKeep * (blockDim.x - 32));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
     const int workers = blockDim.x - 32;
     const bool entry_warp = tid >= workers;
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(512, 2) k_distill(DistillArgs a, int log2_ctas
                 ws = s2.x + s2.y;
             } else {
                 Running run;
-                stream_share<T, kU, kMode == kLoss>(share, tid, workers, [&](uint4 *x, int v, int have) {
+                stream_share<T, kU, kMode == kLoss, kKeep>(share, tid, workers, keep, [&](uint4 *x, int v, int have) {
                     if (tail) {
 #pragma unroll
                         for (int i = 0; i < kU; ++i)
@@ -315,11 +322,13 @@ __global__ void __launch_bounds__(512, 2) k_distill(DistillArgs a, int log2_ctas
                     for (int i = 0; i < kR; ++i)
                         if (i * workers + tid < share.count) share.store(dz, i * workers + tid, grad(reg[i]), congruent);
                 } else {
-                    stream_share<T, kU, true>(share, tid, workers, [&](uint4 *x, int v, int have) {
+                    const auto put = [&](uint4 *x, int v, int have) {
 #pragma unroll
                         for (int i = 0; i < kU; ++i)
                             if (i < have) share.store(dz, v + i * workers, grad(x[i]), congruent);
-                    });
+                    };
+                    if constexpr (kMode == kGrad) stream_share<T, kU, true, 0>(share, tid, workers, keep, put);
+                    else stream_back<T, kU, kKeep>(share, tid, workers, keep, put);
                 }
             }
         }
@@ -335,8 +344,8 @@ __global__ void __launch_bounds__(512, 2) k_distill(DistillArgs a, int log2_ctas
 template <typename T, int kR, int kMode>
 cudaError_t launch_distill_shape(const RowShape &shape, int64_t vectors, const DistillArgs &a, cudaStream_t s) {
     auto *kernel = k_distill<T, kR, kMode>;
-    size_t smem = 0;
-    if (kMode != kGrad && a.teacher_lse) smem = static_cast<size_t>(ceil_div(ceil_div(vectors, shape.ctas), 4) * 4);
+    size_t smem = kR == 0 && kMode == kLossGrad ? static_cast<size_t>(16) * kBatchVectors * kKeepBatches * (shape.threads - 32) : 0;
+    if (kMode != kGrad && a.teacher_lse) smem += static_cast<size_t>(ceil_div(ceil_div(vectors, shape.ctas), 4) * 4);
     if (smem + sizeof(DistillShared) > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) k_gate(TopArgs a) {
         const int j = t * kLanes + lane;
         if (j < a.k) {
             a.ids[r * a.k + j] = Key<T>::col(mine[t]);
-            a.vals[r * a.k + j] = Key<T>::value(mine[t]);
+            if (a.vals) a.vals[r * a.k + j] = Key<T>::value(mine[t]);
             if (a.weighting != SPMV_WEIGHTS_NONE) a.weights[r * a.k + j] = Key<T>::some(mine[t]) ? e[t] / sum : 0.0f;
         }
     }

@@ -220,13 +220,40 @@ __device__ __forceinline__ void load_share(const Share<T> &sh, int t, int worker
         }
     }
 }
+// the vectors at the row's ends, threads 0's and 1's (one vector may be both)
+template <typename T, int kU, typename F>
+__device__ __forceinline__ void stream_ends(const Share<T> &sh, int t, F f) {
+    const bool first = t == 0 && sh.lo == 1 && sh.count > 0, last = t == 1 && sh.hi < sh.count && sh.hi >= sh.lo;
+    if (first || last) {
+        const int edge = first ? 0 : sh.hi;
+        uint4 x[kU];
+        const uint4 none = splat<T>(kNegInf);
+#pragma unroll
+        for (int i = 1; i < kU; ++i) x[i] = none;
+        x[0] = sh.load(edge);
+        f(x, edge, 1);
+    }
+}
 // f(vectors[kU], index of the first, how many) over thread t's vectors, `workers` apart, read
 // from memory kU at a time (those past the count are -inf), the vectors inside the row first.
-template <typename T, int kU, bool kLast, typename F>
-__device__ __forceinline__ void stream_share(const Share<T> &sh, int t, int workers, F f) {
+// Rows that are read twice: the first kKeep whole batches go to slots of the thread's own in
+// shared memory (kKeep * kU of them, `workers` apart) for stream_back.
+template <typename T, int kU, bool kLast, int kKeep, typename F>
+__device__ __forceinline__ void stream_share(const Share<T> &sh, int t, int workers, uint4 *keep, F f) {
     uint4 x[kU];
+    const int step = kU * workers;
     int v = sh.lo + t;
-    for (; v + (kU - 1) * workers < sh.hi; v += kU * workers) {
+    if constexpr (kKeep > 0) {
+#pragma unroll 1
+        for (int q = 0; q < kKeep && v + (kU - 1) * workers < sh.hi; ++q, v += step) {
+#pragma unroll
+            for (int i = 0; i < kU; ++i) x[i] = sh.load_whole(v + i * workers);
+#pragma unroll
+            for (int i = 0; i < kU; ++i) keep[(q * kU + i) * workers] = x[i];
+            f(x, v, kU);
+        }
+    }
+    for (; v + (kU - 1) * workers < sh.hi; v += step) {
 #pragma unroll
         for (int i = 0; i < kU; ++i) x[i] = kLast ? sh.load_last(v + i * workers) : sh.load_whole(v + i * workers);
         f(x, v, kU);
@@ -240,15 +267,39 @@ __device__ __forceinline__ void stream_share(const Share<T> &sh, int t, int work
         }
         f(x, v, (sh.hi - v + workers - 1) / workers);
     }
-    // the vectors at the row's ends (one vector may be both)
-    const bool first = t == 0 && sh.lo == 1 && sh.count > 0, last = t == 1 && sh.hi < sh.count && sh.hi >= sh.lo;
-    if (first || last) {
-        const int edge = first ? 0 : sh.hi;
+    stream_ends<T, kU>(sh, t, f);
+}
+// the same vectors from the end: what was read last is likeliest to be in L2 still, what was read
+// first comes from the slots
+template <typename T, int kU, int kKeep, typename F>
+__device__ __forceinline__ void stream_back(const Share<T> &sh, int t, int workers, const uint4 *keep, F f) {
+    uint4 x[kU];
+    const int step = kU * workers, first = sh.lo + t;
+    int v = first + (sh.hi > first ? (sh.hi - first - 1) / step * step : -step), q = (v - first) / step;  // the last batch
+    const uint4 none = splat<T>(kNegInf);
+    if (v >= first && v + (kU - 1) * workers >= sh.hi) {
 #pragma unroll
-        for (int i = 1; i < kU; ++i) x[i] = none;
-        x[0] = sh.load(edge);
-        f(x, edge, 1);
+        for (int i = 0; i < kU; ++i) {
+            x[i] = none;
+            if (v + i * workers < sh.hi) x[i] = sh.load_whole(v + i * workers);
+        }
+        f(x, v, (sh.hi - v + workers - 1) / workers);
+        v -= step;
+        --q;
     }
+#pragma unroll 1
+    for (; q >= kKeep; --q, v -= step) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) x[i] = sh.load_last(v + i * workers);
+        f(x, v, kU);
+    }
+#pragma unroll 1
+    for (; q >= 0; --q, v -= step) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) x[i] = keep[(q * kU + i) * workers];
+        f(x, v, kU);
+    }
+    stream_ends<T, kU>(sh, t, f);
 }
 
 // ----------------------------------------------------------------------------

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) k_topk_warp(TopArgs a) {
     }
     if (lane < a.k) {
         a.ids[row * a.k + lane] = my_id;
-        a.vals[row * a.k + lane] = v;
+        if (a.vals) a.vals[row * a.k + lane] = v;
     }
     if (a.lse && lane == 0) a.lse[row] = fmaf(m, a.inv_temperature, logf(sum));
 }
@@ -381,13 +381,13 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
             const float v = key_value(static_cast<uint32_t>(c >> 32));
             sh.top_vals[above] = v;
             a.ids[r * a.k + above] = composite_col(c);
-            a.vals[r * a.k + above] = v;
+            if (a.vals) a.vals[r * a.k + above] = v;
         }
     }
     for (int j = n_cand + tid; j < a.k; j += n_threads) {
         sh.top_vals[j] = kNegInf;
         a.ids[r * a.k + j] = -1;
-        a.vals[r * a.k + j] = kNegInf;
+        if (a.vals) a.vals[r * a.k + j] = kNegInf;
     }
     if (a.weighting == SPMV_WEIGHTS_NONE) return;
     __syncthreads();
@@ -516,7 +516,7 @@ extern "C" SPMV_API int spmv_topk_rows(int64_t rows, int64_t n, int32_t k, const
     const int vb = row_value_bytes(dtype);
     SPMV_TRY(check_array(x, "x", vb));
     SPMV_TRY(check_array(ids, "ids", 4));
-    SPMV_TRY(check_array(vals, "vals", 4));
+    if (vals) SPMV_TRY(check_array(vals, "vals", 4));
     if (weighting != SPMV_WEIGHTS_NONE) SPMV_TRY(check_array(weights, "weights", 4));
     if (lse) SPMV_TRY(check_array(lse, "lse", 4));
     const size_t xb = span_bytes(rows, n, ldx, vb), m = static_cast<size_t>(rows) * k * 4;

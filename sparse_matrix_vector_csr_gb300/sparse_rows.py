@@ -90,8 +90,8 @@ def _out(t, name, like, rows, cols):
 
 
 class TopRows:
-    """The k largest entries of every row of ``x``: ``ids`` (int32, -1 = none), ``vals``, and,
-    where asked for, ``weights`` and ``lse`` (float32)."""
+    """The k largest entries of every row of ``x``: ``ids`` (int32, -1 = none), and, where asked
+    for, ``vals``, ``weights`` and ``lse`` (float32)."""
 
     __slots__ = ("ids", "vals", "weights", "lse", "_x", "_weighting", "_temperature")
 
@@ -114,14 +114,15 @@ class TopRows:
         return dx
 
 
-def topk_rows(x, k, temperature=1.0, weights=None, lse=False, stream=None) -> TopRows:
+def topk_rows(x, k, temperature=1.0, weights=None, lse=False, vals=None, stream=None) -> TopRows:
     """The k largest entries of every row of x, values descending, ties to the lowest column;
     -inf is never taken (its id is -1).  ``weights``: None, "selected" (softmax over the
     chosen) or "row" (softmax over the row); ``lse``: also the row's log-sum-exp.  Both at
-    ``temperature``.  1 <= k <= min(n, 256)."""
+    ``temperature``.  ``vals``: whether the values themselves are wanted (None: unless weights
+    are).  1 <= k <= min(n, 256)."""
     if stream is not None:
         with _on(stream, x):
-            return topk_rows(x, k, temperature, weights, lse)
+            return topk_rows(x, k, temperature, weights, lse, vals)
     code, ldx = _matrix(x, "x")
     rows, n = x.shape
     weighting = WEIGHTINGS[weights]
@@ -130,12 +131,13 @@ def topk_rows(x, k, temperature=1.0, weights=None, lse=False, stream=None) -> To
     top, device = TopRows(), x.device
     top._x, top._weighting, top._temperature = x, weighting, temperature
     top.ids = _empty((rows, k), dtype=_I32, device=device)
-    top.vals = _empty((rows, k), dtype=_F32, device=device)
+    top.vals = _empty((rows, k), dtype=_F32, device=device) if vals or (vals is None and not weighting) else None
     top.weights = _empty((rows, k), dtype=_F32, device=device) if weighting else None
     # the gradient of weights over the row needs lse too
     top.lse = _empty((rows,), dtype=_F32, device=device) if lse or weighting == 2 else None
     _check(lib.spmv_topk_rows(rows, n, k, x.data_ptr(), ldx, code, temperature, weighting, top.ids.data_ptr(),
-                              top.vals.data_ptr(), top.weights.data_ptr() if weighting else None,
+                              None if top.vals is None else top.vals.data_ptr(),
+                              top.weights.data_ptr() if weighting else None,
                               None if top.lse is None else top.lse.data_ptr(), _current(x)))
     return top
 
@@ -151,7 +153,7 @@ class RoutePlan:
     outside [0, experts) is dropped).  ``rows`` is the sorted matrix's number of rows;
     ``offsets`` (experts + 1), ``slots`` (tokens x k) and ``sources`` (rows) as in spmv.h."""
 
-    __slots__ = ("tokens", "k", "experts", "align", "rows", "_buf", "_slots", "_sources", "_offsets")
+    __slots__ = ("tokens", "k", "experts", "align", "rows", "offsets", "slots", "sources", "_slots", "_sources")
 
     def __init__(self, ids, experts, align=1, stream=None):
         if stream is not None:
@@ -163,31 +165,19 @@ class RoutePlan:
         self.tokens, self.k = tokens, k = ids.shape
         self.experts, self.align = experts, align
         self.rows, work = _plan_sizes(tokens, k, experts, align)
-        m = tokens * k
-        # one allocation: slots, sources, offsets, workspace
-        self._buf = _empty((m + self.rows + experts + 1 + work // 4,), dtype=_I32, device=ids.device)
-        self._slots = self._buf.data_ptr()
-        self._sources = self._slots + 4 * m
-        self._offsets = self._sources + 4 * self.rows
-        _check(lib.spmv_route_plan(tokens, k, experts, align, ptr, self._offsets, self._slots, self._sources,
-                                   self._offsets + 4 * (experts + 1), work, _current(ids)))
-
-    @property
-    def slots(self):
-        return self._buf.as_strided((self.tokens, self.k), (self.k, 1))
-
-    @property
-    def sources(self):
-        return self._buf.as_strided((self.rows,), (1,), self.tokens * self.k)
-
-    @property
-    def offsets(self):
-        return self._buf.as_strided((self.experts + 1,), (1,), self.tokens * self.k + self.rows)
+        device = ids.device
+        self.offsets = _empty((experts + 1,), dtype=_I32, device=device)
+        self.slots = _empty((tokens, k), dtype=_I32, device=device)
+        self.sources = _empty((self.rows,), dtype=_I32, device=device)
+        space = _empty((work,), dtype=torch.uint8, device=device) if work else None
+        self._slots, self._sources = self.slots.data_ptr(), self.sources.data_ptr()
+        _check(lib.spmv_route_plan(tokens, k, experts, align, ptr, self.offsets.data_ptr(), self._slots, self._sources,
+                                   space.data_ptr() if work else None, work, _current(ids)))
 
     def dispatch(self, x, out=None, stream=None):
         """The tokens' rows sorted by expert (rows x d); rows without a source are 0."""
         if stream is not None:
-            with _on(stream, self._buf, x, out):
+            with _on(stream, self.slots, self.sources, x, out):
                 return self.dispatch(x, out)
         code, ldx = _matrix(x, "x", self.tokens)
         d = x.shape[1]
@@ -199,7 +189,7 @@ class RoutePlan:
     def combine(self, ys, weights=None, out=None, stream=None):
         """y[t] = sum over j of weights[t, j] ys[slots[t, j]] (weights None: all 1)."""
         if stream is not None:
-            with _on(stream, self._buf, ys, weights, out):
+            with _on(stream, self.slots, ys, weights, out):
                 return self.combine(ys, weights, out)
         code, ldys = _matrix(ys, "ys", self.rows)
         d = ys.shape[1]
@@ -212,7 +202,7 @@ class RoutePlan:
     def combine_grad(self, dy, ys, weights, out=None, stream=None):
         """(dys, dweights): the gradients of combine in ys and in the weights."""
         if stream is not None:
-            with _on(stream, self._buf, dy, ys, weights, out):
+            with _on(stream, self.slots, self.sources, dy, ys, weights, out):
                 return self.combine_grad(dy, ys, weights, out)
         code, lddy = _matrix(dy, "dy", self.tokens)
         d = dy.shape[1]

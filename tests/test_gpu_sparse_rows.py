@@ -61,7 +61,7 @@ def gen(seed):
 
 
 def check_top(spmv, x, k, tau=1.0, weighting="row"):
-    top = spmv.topk_rows(x, k, temperature=tau, weights=weighting, lse=True)
+    top = spmv.topk_rows(x, k, temperature=tau, weights=weighting, lse=True, vals=True)
     ids, vals, w, lse = top.ids.cpu().numpy(), f64(top.vals), f64(top.weights), f64(top.lse)
     for r, row in enumerate(f64(x)):
         i, v = ref.topk_row(row, k)
