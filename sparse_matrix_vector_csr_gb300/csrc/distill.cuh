@@ -47,21 +47,26 @@ struct DistillArgs {
     void *dz;
 };
 
+// What a row's entries give: sum p log p, sum p, r (0 without lse), how many there are (0: no target).
+struct EntryScalars {
+    float entropy, mass, rest;
+    int valid;
+};
+
 struct DistillShared {
     // per warp of the cluster: maximum and sum of its columns (with lse: of those that are no
     // entries, and in z, w of its CTA's entries, from its last warp)
     float4 warp_part[kMaxCluster * 16];
     int32_t id[kMaxEntries];             // column, or -1
     float p[kMaxEntries], z[kMaxEntries];  // z: see load_entries
-    float entropy, mass, rest;           // sum p log p, sum p, r (0 without lse)
-    int valid;
+    EntryScalars sc;
 };
 
 // One warp: the entries' probabilities, and z at those of columns [e0, e1) (the CTA's own, or all
 // for the CTA that sums the loss).
 template <typename T>
-__device__ __forceinline__ void load_entries(const DistillArgs &a, DistillShared &sh, int64_t r, const T *z, int64_t e0,
-                                             int64_t e1) {
+__device__ __forceinline__ void load_entries(const DistillArgs &a, int32_t *sid, float *sp, float *sz, EntryScalars &sc,
+                                             int64_t r, const T *z, int64_t e0, int64_t e1) {
     const int lane = threadIdx.x & 31;
     const int32_t *ids = a.ids + r * a.k;
     float top = kNegInf;
@@ -72,12 +77,12 @@ __device__ __forceinline__ void load_entries(const DistillArgs &a, DistillShared
         if (id >= 0 && id < a.n) {
             t = load_any(a.teacher, r * a.k + j, a.teacher_dtype);
             ++valid;
-            if (id >= e0 && id < e1) sh.z[j] = to_f32(z[id]);
+            if (id >= e0 && id < e1) sz[j] = to_f32(z[id]);
         } else {
             id = -1;
         }
-        sh.id[j] = id;
-        sh.p[j] = t;
+        sid[j] = id;
+        sp[j] = t;
         top = fmaxf(top, t);
     }
     valid = warp_sum(valid);
@@ -88,26 +93,26 @@ __device__ __forceinline__ void load_entries(const DistillArgs &a, DistillShared
         log_norm = a.teacher_lse[r];
     } else {
         float s = 0.0f;
-        for (int j = lane; j < a.k; j += 32) s += expf((sh.p[j] - top) * a.inv_temperature);
+        for (int j = lane; j < a.k; j += 32) s += expf((sp[j] - top) * a.inv_temperature);
         shift = top;
         log_norm = logf(warp_sum(s));
     }
     float entropy = 0.0f, mass = 0.0f;
     for (int j = lane; j < a.k; j += 32) {
-        const float lp = fmaf(sh.p[j] - shift, a.inv_temperature, -log_norm);
-        const float p = sh.p[j] == kNegInf ? 0.0f : expf(lp);
+        const float lp = fmaf(sp[j] - shift, a.inv_temperature, -log_norm);
+        const float p = sp[j] == kNegInf ? 0.0f : expf(lp);
         if (p > 0.0f || p != p) entropy = fmaf(p, lp, entropy);
         mass += p;
-        sh.p[j] = p;
+        sp[j] = p;
     }
     entropy = warp_sum(entropy);
     mass = warp_sum(mass);
     if (lane == 0) {
         // no entry, or (without lse) none above -inf: no target, nothing to learn
-        sh.valid = valid && (a.teacher_lse || log_norm != kNegInf) ? valid : 0;
-        sh.entropy = entropy;
-        sh.mass = mass;
-        sh.rest = a.teacher_lse && valid < a.n ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
+        sc.valid = valid && (a.teacher_lse || log_norm != kNegInf) ? valid : 0;
+        sc.entropy = entropy;
+        sc.mass = mass;
+        sc.rest = a.teacher_lse && valid < a.n ? fmaxf(0.0f, 1.0f - mass) : 0.0f;
     }
 }
 
@@ -152,6 +157,94 @@ struct GradOf {
         uint4 o = pack<T>(x);
         if constexpr (sizeof(T) == 2) o = make_uint4(o.x ^ flip, o.y ^ flip, o.z ^ flip, o.w ^ flip);
         return o;
+    }
+};
+
+// A row's maximum and sum of exponentials (of z / T): of all columns, and with lse of those that
+// are no entries.
+struct RowSums {
+    float m, sum, m_rest, rest_sum;
+};
+__device__ __forceinline__ RowSums stored_sums(const float4 &s) { return RowSums{s.x, s.y, s.z, s.w}; }
+
+// A warp joins the parts of all warps that share the row; a part without a value above -inf adds
+// its 0 (or a NaN).
+__device__ __forceinline__ RowSums join_parts(const DistillArgs &a, const float4 *parts, int n) {
+    const int lane = threadIdx.x & 31;
+    const bool tail = a.teacher_lse != nullptr;
+    const auto scaled = [&](float part, float from, float to) {
+        return from == kNegInf ? part : part * ex2((from - to) * a.scale2);
+    };
+    RowSums s;
+    s.m_rest = kNegInf;
+    float em = kNegInf;
+    for (int i = lane; i < n; i += 32) {
+        s.m_rest = fmaxf(s.m_rest, parts[i].x);
+        em = fmaxf(em, parts[i].z);
+    }
+    s.m_rest = warp_max(s.m_rest);
+    s.m = reference_of(fmaxf(s.m_rest, tail ? warp_max(em) : kNegInf));
+    s.m_rest = reference_of(s.m_rest);
+    float es = 0.0f;
+    s.rest_sum = 0.0f;
+    for (int i = lane; i < n; i += 32) {
+        const float4 w = parts[i];
+        s.rest_sum += scaled(w.y, w.x, s.m_rest);
+        es += scaled(w.w, w.z, s.m);
+    }
+    s.rest_sum = warp_sum(s.rest_sum);
+    s.sum = s.rest_sum;
+    if (tail) s.sum = warp_sum(es) + (s.rest_sum != 0.0f ? scaled(s.rest_sum, s.m_rest, s.m) : 0.0f);
+    return s;
+}
+
+// the same for one warp that has the whole row: its columns (with lse: the others), the entries
+__device__ __forceinline__ RowSums join_two(const DistillArgs &a, float m_rest, float rest_sum, float em, float es) {
+    const bool tail = a.teacher_lse != nullptr;
+    RowSums s;
+    s.m = reference_of(fmaxf(m_rest, em));
+    s.rest_sum = rest_sum;
+    s.sum = rest_sum;
+    if (tail) s.sum = (em == kNegInf ? es : es * ex2((em - s.m) * a.scale2)) + (m_rest == kNegInf ? rest_sum : rest_sum * ex2((m_rest - s.m) * a.scale2));
+    s.m_rest = reference_of(m_rest);
+    return s;
+}
+
+// One warp sums the loss over the entries (z: all of them).
+__device__ __forceinline__ void write_loss(const DistillArgs &a, int64_t r, const int32_t *id, const float *p,
+                                           const float *z, const EntryScalars &sc, const RowSums &s) {
+    const int lane = threadIdx.x & 31;
+    float cross = 0.0f;  // sum p (z - m)
+    for (int j = lane; j < a.k; j += 32)
+        if (id[j] >= 0 && p[j] != 0.0f) cross = fmaf(p[j], z[j] - s.m, cross);
+    cross = warp_sum(cross);
+    if (lane == 0) {
+        const float log_sum = logf(s.sum);
+        float loss = sc.entropy - cross * a.inv_temperature + sc.mass * log_sum;
+        if (sc.rest > 0.0f && !(sc.rest < kRestRounding && s.rest_sum == 0.0f))
+            loss += sc.rest * (logf(sc.rest) - logf(s.rest_sum) + log_sum + (s.m - s.m_rest) * a.inv_temperature);
+        a.loss[r] = sc.valid ? loss : 0.0f;
+        if (a.stats) a.stats[r] = make_float4(s.m, s.sum, s.m_rest, s.rest_sum);
+    }
+}
+
+// The gradient's factors: g q at the entries (less g p); elsewhere g q, and with lse
+// g (q - r q_other), q_other the softmax over the other columns; both are multiples of
+// exp((z - m_rest) / T).
+struct GradScales {
+    float g, q, m, ref, other;
+    __device__ __forceinline__ GradScales(const DistillArgs &a, int64_t r, const EntryScalars &sc, const RowSums &s) {
+        g = a.scale * (a.row_scale ? a.row_scale[r] : 1.0f) * a.inv_temperature;
+        q = g / s.sum;
+        m = ref = s.m;
+        other = q;
+        if (a.teacher_lse) {
+            ref = s.m_rest;
+            other = s.rest_sum != 0.0f ? g * (ex2((s.m_rest - s.m) * a.scale2) / s.sum - sc.rest / s.rest_sum) : 0.0f;
+        }
+    }
+    __device__ __forceinline__ float at_entry(const DistillArgs &a, float p, float z) const {
+        return fmaf(ex2((z - m) * a.scale2), q, -p * g);
     }
 };
 
@@ -200,11 +293,10 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
     }
     if (entry_warp) {
         const bool sums_loss = kMode != kGrad && rank == 0;
-        load_entries<T>(a, sh, r, z, sums_loss ? 0 : share.e0, sums_loss ? a.n : share.first(share.count));
+        load_entries<T>(a, sh.id, sh.p, sh.z, sh.sc, r, z, sums_loss ? 0 : share.e0, sums_loss ? a.n : share.first(share.count));
     }
 
-    // of all columns; of the others (with lse)
-    float m, sum, m_rest = 0.0f, rest_sum = 0.0f;
+    RowSums sums;
     if constexpr (kMode != kGrad) {
         float wm = kNegInf, ws = 0.0f, em = kNegInf, es = 0.0f;
         if (!entry_warp) {
@@ -253,62 +345,16 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
             else *slot = make_float4(wm, ws, em, es);
         }
         cluster_sync(ctas);
-        // every warp joins all warps' sums; a part without a value above -inf adds its 0 (or a NaN)
-        const auto scaled = [&](float part, float from, float to) {
-            return from == kNegInf ? part : part * ex2((from - to) * a.scale2);
-        };
-        m_rest = kNegInf;
-        em = kNegInf;
-        for (int i = lane; i < n_warps * ctas; i += 32) {
-            m_rest = fmaxf(m_rest, sh.warp_part[i].x);
-            em = fmaxf(em, sh.warp_part[i].z);
-        }
-        m_rest = warp_max(m_rest);
-        m = reference_of(fmaxf(m_rest, tail ? warp_max(em) : kNegInf));
-        m_rest = reference_of(m_rest);
-        es = 0.0f;
-        for (int i = lane; i < n_warps * ctas; i += 32) {
-            const float4 w = sh.warp_part[i];
-            rest_sum += scaled(w.y, w.x, m_rest);
-            es += scaled(w.w, w.z, m);
-        }
-        rest_sum = warp_sum(rest_sum);
-        sum = rest_sum;
-        if (tail) sum = warp_sum(es) + (rest_sum != 0.0f ? scaled(rest_sum, m_rest, m) : 0.0f);
-        if (rank == 0 && entry_warp) {
-            float cross = 0.0f;  // sum p (z - m)
-            for (int j = lane; j < a.k; j += 32)
-                if (sh.id[j] >= 0 && sh.p[j] != 0.0f) cross = fmaf(sh.p[j], sh.z[j] - m, cross);
-            cross = warp_sum(cross);
-            if (lane == 0) {
-                const float log_sum = logf(sum), rest = sh.rest;
-                float loss = sh.entropy - cross * a.inv_temperature + sh.mass * log_sum;
-                if (rest > 0.0f && !(rest < kRestRounding && rest_sum == 0.0f))
-                    loss += rest * (logf(rest) - logf(rest_sum) + log_sum + (m - m_rest) * a.inv_temperature);
-                a.loss[r] = sh.valid ? loss : 0.0f;
-                if (a.stats) a.stats[r] = make_float4(m, sum, m_rest, rest_sum);
-            }
-        }
+        sums = join_parts(a, sh.warp_part, n_warps * ctas);
+        if (rank == 0 && entry_warp) write_loss(a, r, sh.id, sh.p, sh.z, sh.sc, sums);
     } else {
         __syncthreads();
-        const float4 st = a.stats[r];
-        m = st.x;
-        sum = st.y;
-        m_rest = st.z;
-        rest_sum = st.w;
+        sums = stored_sums(a.stats[r]);
     }
 
     if constexpr (kMode != kLoss) {
-        const bool live = sh.valid != 0;
-        const float g = a.scale * (a.row_scale ? a.row_scale[r] : 1.0f) * a.inv_temperature;
-        const float q_scale = g / sum;
-        // elsewhere than at the entries: g q, and with lse g (q - r q_other), q_other the softmax
-        // over the other columns; both are multiples of exp((z - m_rest) / T)
-        float ref = m, o_scale = q_scale;
-        if (tail) {
-            ref = m_rest;
-            o_scale = rest_sum != 0.0f ? g * (ex2((m_rest - m) * a.scale2) / sum - sh.rest / rest_sum) : 0.0f;
-        }
+        const bool live = sh.sc.valid != 0;
+        const GradScales gs(a, r, sh.sc, sums);
         T *dz = static_cast<T *>(a.dz) + r * a.lddz;
         const bool congruent = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
         if (!entry_warp) {
@@ -316,7 +362,7 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
                 const uint4 zero = splat<T>(0.0f);
                 for (int v = tid; v < share.count; v += workers) share.store(dz, v, zero, congruent);
             } else {
-                const GradOf<T> grad(ref, a.scale2, o_scale);
+                const GradOf<T> grad(gs.ref, a.scale2, gs.other);
                 if constexpr (kR > 0) {
 #pragma unroll
                     for (int i = 0; i < kR; ++i)
@@ -336,9 +382,93 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
         if (live)
             for (int j = tid; j < a.k; j += blockDim.x) {
                 const int32_t id = sh.id[j];
-                if (own(id)) dz[id] = from_f32<T>(fmaf(ex2((sh.z[j] - m) * a.scale2), q_scale, -sh.p[j] * g));
+                if (own(id)) dz[id] = from_f32<T>(gs.at_entry(a, sh.p[j], sh.z[j]));
             }
     }
+}
+
+// Many short rows: a warp per row, its registers hold it, no barrier.  (A CTA per row spends 6 to
+// 8 us on a row's latencies: 12832 rows of 500 float values with 127 entries 84 us.)
+constexpr int kWarpRows = 4;  // per CTA
+template <typename T, int kR, int kMode>
+__global__ void __launch_bounds__(32 * kWarpRows, kR == 4 ? 8 : kR == 8 ? 5 : 3) k_distill_warp(DistillArgs a, int k_padded, int mark_words) {
+    constexpr int kN = Vec<T>::kN;
+    extern __shared__ __align__(16) unsigned char dynamic_mem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * kWarpRows + warp;
+    if (r >= a.rows) return;
+    EntryScalars &sc = reinterpret_cast<EntryScalars *>(dynamic_mem)[warp];
+    int32_t *id = reinterpret_cast<int32_t *>(reinterpret_cast<EntryScalars *>(dynamic_mem) + kWarpRows) + warp * k_padded;
+    float *p = reinterpret_cast<float *>(id + (kWarpRows - warp) * k_padded) + warp * k_padded, *zk = p + kWarpRows * k_padded;
+    uint32_t *marks = reinterpret_cast<uint32_t *>(zk + (kWarpRows - warp) * k_padded) + warp * mark_words;
+    const T *z = static_cast<const T *>(a.z) + r * a.ldz;
+    const Share<T> share(RowView<T>(z, a.n), uint32_t(0), 0);
+    const bool tail = a.teacher_lse != nullptr;
+    uint4 reg[kR];
+    load_share<T, kR>(share, lane, 32, reg);
+    if (kMode != kGrad && tail)
+        for (int i = lane; i < mark_words; i += 32) marks[i] = 0;
+    load_entries<T>(a, id, p, zk, sc, r, z, 0, a.n);
+    __syncwarp();
+    RowSums sums;
+    if constexpr (kMode != kGrad) {
+        float em = kNegInf, es = 0.0f;
+        if (tail) {
+            for (int j = lane; j < a.k; j += 32)
+                if (id[j] >= 0) {
+                    const uint32_t at = static_cast<uint32_t>(id[j] - share.e0), byte = at / kN;
+                    atomicOr(&marks[byte / 4], 1u << (byte % 4 * 8 + at % kN));
+                    em = fmaxf(em, zk[j]);
+                }
+            em = warp_max(em);
+            const float m0 = reference_of(em);
+            for (int j = lane; j < a.k; j += 32)
+                if (id[j] >= 0) es += ex2((zk[j] - m0) * a.scale2);
+            es = warp_sum(es);
+            __syncwarp();
+            const uint8_t *bytes = reinterpret_cast<const uint8_t *>(marks);
+#pragma unroll
+            for (int i = 0; i < kR; ++i)
+                if (i * 32 + lane < share.count) mask_vec<T>(reg[i], bytes[i * 32 + lane]);
+        }
+        uint4 top = reg[0];
+#pragma unroll
+        for (int i = 1; i < kR; ++i) top = vec_max2(top, reg[i], T());
+        const float wm = warp_max(vec_max(top, T()));
+        const float w0 = reference_of(wm);
+        float2 s2 = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < kR; ++i) s2 = exp_sum<T>(reg[i], w0, a.scale2, s2);
+        sums = join_two(a, wm, warp_sum(s2.x + s2.y), em, es);
+        write_loss(a, r, id, p, zk, sc, sums);
+    } else {
+        sums = stored_sums(a.stats[r]);
+    }
+    if constexpr (kMode != kLoss) {
+        const GradScales gs(a, r, sc, sums);
+        T *dz = static_cast<T *>(a.dz) + r * a.lddz;
+        const bool live = sc.valid != 0, congruent = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+        const GradOf<T> grad(gs.ref, a.scale2, gs.other);
+#pragma unroll
+        for (int i = 0; i < kR; ++i)
+            if (i * 32 + lane < share.count) share.store(dz, i * 32 + lane, live ? grad(reg[i]) : splat<T>(0.0f), congruent);
+        __syncwarp();  // the entries' columns are written after the plain stores
+        if (live)
+            for (int j = lane; j < a.k; j += 32)
+                if (id[j] >= 0) dz[id[j]] = from_f32<T>(gs.at_entry(a, p[j], zk[j]));
+    }
+}
+
+constexpr int kWarpVectors = 512;  // a warp's registers hold up to this
+template <typename T, int kMode>
+cudaError_t launch_distill_warp(int64_t vectors, const DistillArgs &a, cudaStream_t s) {
+    const int k_padded = (a.k + 3) / 4 * 4;
+    const int mark_words = kMode != kGrad && a.teacher_lse ? static_cast<int>(ceil_div(vectors, 4)) : 0;
+    const size_t smem = kWarpRows * (sizeof(EntryScalars) + static_cast<size_t>(12) * k_padded + static_cast<size_t>(4) * mark_words);
+    const int64_t grid = ceil_div(a.rows, kWarpRows);
+    if (vectors <= 4 * 32) return launch_rows(k_distill_warp<T, 4, kMode>, grid, 32 * kWarpRows, 1, smem, s, a, k_padded, mark_words);
+    if (vectors <= 8 * 32) return launch_rows(k_distill_warp<T, 8, kMode>, grid, 32 * kWarpRows, 1, smem, s, a, k_padded, mark_words);
+    return launch_rows(k_distill_warp<T, 16, kMode>, grid, 32 * kWarpRows, 1, smem, s, a, k_padded, mark_words);
 }
 
 template <typename T, int kR, int kMode>
@@ -357,6 +487,8 @@ cudaError_t launch_distill_shape(const RowShape &shape, int64_t vectors, const D
 template <typename T, int kMode>
 cudaError_t launch_distill_mode(const DistillArgs &a, cudaStream_t s) {
     const int64_t vectors = row_vectors<T>(a.n, a.z, a.ldz);
+    // (fewer rows than warps that run at once: a CTA's warps share a row sooner)
+    if (vectors <= kWarpVectors && a.rows >= 1216) return launch_distill_warp<T, kMode>(vectors, a, s);
     const RowShape shape = row_shape(a.rows, vectors);
     switch (shape.regs) {
         case 2: return launch_distill_shape<T, 2, kMode>(shape, vectors, a, s);

@@ -94,6 +94,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 template <typename H2>
 __device__ __forceinline__ H2 as_pair(uint32_t w) { return *reinterpret_cast<const H2 *>(&w); }
+// value by value
+__device__ __forceinline__ uint4 vec_max2(const uint4 &a, const uint4 &b, float) {
+    return make_uint4(__float_as_uint(fmaxf(__uint_as_float(a.x), __uint_as_float(b.x))),
+                      __float_as_uint(fmaxf(__uint_as_float(a.y), __uint_as_float(b.y))),
+                      __float_as_uint(fmaxf(__uint_as_float(a.z), __uint_as_float(b.z))),
+                      __float_as_uint(fmaxf(__uint_as_float(a.w), __uint_as_float(b.w))));
+}
+template <typename H2>
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+    const H2 m = __hmax2(as_pair<H2>(a), as_pair<H2>(b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+__device__ __forceinline__ uint4 vec_max2(const uint4 &a, const uint4 &b, __half) {
+    return make_uint4(pair_max<__half2>(a.x, b.x), pair_max<__half2>(a.y, b.y), pair_max<__half2>(a.z, b.z),
+                      pair_max<__half2>(a.w, b.w));
+}
+__device__ __forceinline__ uint4 vec_max2(const uint4 &a, const uint4 &b, __nv_bfloat16) {
+    return make_uint4(pair_max<__nv_bfloat162>(a.x, b.x), pair_max<__nv_bfloat162>(a.y, b.y),
+                      pair_max<__nv_bfloat162>(a.z, b.z), pair_max<__nv_bfloat162>(a.w, b.w));
+}
 __device__ __forceinline__ float vec_max(const uint4 &v, float) {
     return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
 }

@@ -356,7 +356,8 @@ def teacher_lse_of(ids, teacher, vocab, tau, g):
                                           (6, 4097, 64), (3, 8192, 512), (3, 20011, 20), (1, 32768, 16), (2, 50021, 64),
                                           (1, 131072, 64), (1, 151937, 100), (1, 262144, 8), (1, 300007, 64),
                                           (1, 600011, 30), (160, 9000, 20), (330, 17001, 64), (153, 70001, 33),
-                                          (155, 131072, 64), (200, 33000, 300), (152, 270001, 5)])
+                                          (155, 131072, 64), (200, 33000, 300), (152, 270001, 5), (1300, 40, 5),
+                                          (1217, 700, 33), (1250, 2001, 12)])
 def test_distill(spmv, dtype, tail, rows, vocab, k):
     g = gen(vocab + k)
     tau = 1.0 if vocab % 2 else 2.0
@@ -369,7 +370,7 @@ def test_distill(spmv, dtype, tail, rows, vocab, k):
 @pytest.mark.parametrize("dtype", ALL)
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("shift,pad", [(1, 0), (3, 5), (0, 8)])
-@pytest.mark.parametrize("rows,vocab", [(5, 1), (5, 131), (5, 9001), (310, 9001)])
+@pytest.mark.parametrize("rows,vocab", [(5, 1), (5, 131), (5, 9001), (310, 9001), (1217, 131)])
 def test_distill_any_address_and_in_place(spmv, dtype, tail, shift, pad, rows, vocab):
     g = gen(vocab + shift)
     ids, teacher = some_target(rows, vocab, min(6, vocab), g)
@@ -399,7 +400,7 @@ def test_distill_any_address_and_in_place(spmv, dtype, tail, shift, pad, rows, v
 
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("teacher_dtype", ALL)
-@pytest.mark.parametrize("rows,vocab", [(8, 300), (8, 40000), (170, 40000)])
+@pytest.mark.parametrize("rows,vocab", [(8, 300), (8, 40000), (170, 40000), (1300, 300)])
 def test_distill_masks_and_teacher_types(spmv, tail, teacher_dtype, rows, vocab):
     g = gen(vocab)
     k = 12
