@@ -502,31 +502,47 @@ int64_t row_vectors(int64_t n, const void *p, int64_t ld) {
     return ceil_div(n + (aligned ? 0 : Vec<T>::kN - 1), Vec<T>::kN);
 }
 // How a row of `vectors` 16-byte vectors is shared out: `ctas` CTAs (a cluster) of `threads`
-// threads with `regs` vectors in registers each, or regs = 0 where the largest cluster's
-// registers do not hold it.
+// threads, one warp of each not taking part in the row itself; with `regs` vectors in registers
+// each, or 0: read a batch at a time.
 struct RowShape {
     int ctas, threads, regs;
     int log2_ctas() const { return ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3; }
 };
-constexpr int kRowRegs = 8;  // 32 registers of data: two CTAs of 512 threads fit an SM
-// One warp of each CTA does not take part in the row itself (`threads` counts it).
-inline RowShape row_shape(int64_t rows, int64_t vectors) {
-    constexpr int64_t kFull = 480 * kRowRegs;
-    constexpr int kSms = 152;
+constexpr int kRowRegs = 8;  // 32 registers of data
+constexpr int kSms = 152;
+inline RowShape row_shape(int64_t rows, int64_t vectors, bool read_twice) {
     RowShape s{1, 512, 0};
-    // few rows: more CTAs a row while SMs would be idle and each thread still has a vector
-    while (s.ctas < kMaxCluster && rows * s.ctas < kSms && vectors > s.ctas * 480) s.ctas *= 2;
-    if (vectors > s.ctas * kFull) {
-        // read twice: small CTAs hide each other's barriers, but the rows in flight have to stay
-        // in L2 (65536 fp16 values, loss: 61 us with 256 threads, 76 with 512; 131072 bf16
-        // values, loss and gradient: 944 and 808)
-        if (ceil_div(vectors, s.ctas) <= 8192) s.threads = 256;
+    if (rows < kSms) {
+        // few rows: more CTAs a row while SMs would be idle and each thread still has a vector;
+        // in registers where they hold it, which is one reading and no loop
+        while (s.ctas < kMaxCluster && rows * s.ctas < kSms && vectors > s.ctas * 480) s.ctas *= 2;
+        if (vectors > s.ctas * 480 * kRowRegs) return s;
+        const int64_t share = ceil_div(vectors, s.ctas);
+        s.threads = share <= 192 ? 128 : share <= 896 ? 256 : 512;
+        s.regs = 2;
+        while (static_cast<int64_t>(s.regs) * (s.threads - 32) < share) s.regs *= 2;
         return s;
     }
-    const int64_t share = ceil_div(vectors, s.ctas);
-    s.threads = share <= 192 ? 128 : share <= 896 ? 256 : 512;
-    s.regs = 2;
-    while (static_cast<int64_t>(s.regs) * (s.threads - 32) < share) s.regs *= 2;
+    // Many rows: CTAs small enough to hide each other's barriers (3000 x 16000 bf16 values, loss
+    // and gradient: 49 us with 128 threads, 54 with 256, 72 with 512; in registers, 288 threads:
+    // 50), but large where the rows in flight would not stay in L2 for a second reading
+    // (8192 x 131072 bf16 values: 950 us with 256, 761 with 512).
+    if (vectors <= 4096) {
+        s.threads = 128;
+    } else if (vectors <= 8192 || !read_twice) {
+        s.threads = 256;
+    } else {
+        // two CTAs an SM: a few waves of long rows end evenly where a cluster takes each (400 x
+        // 150000 float values: 125 us with one CTA a row, 99 with two)
+        double best = 1e30;
+        for (int c = 1; c <= 4; c *= 2) {
+            const double waves = static_cast<double>(ceil_div(rows * c, 2 * kSms)) / c * (c == 1 ? 1.0 : c == 2 ? 1.05 : 1.15);
+            if (waves < best && (c == 1 || vectors > c * 8192)) {
+                best = waves;
+                s.ctas = c;
+            }
+        }
+    }
     return s;
 }
 

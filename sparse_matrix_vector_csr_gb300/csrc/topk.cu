@@ -467,7 +467,6 @@ cudaError_t launch_topk_warp(const TopArgs &a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_topk_row(const TopArgs &a, cudaStream_t s) {
-    constexpr int kSms = 152;
     const int64_t vectors = row_vectors<T>(a.n, a.x, a.ldx);
     // few rows: more CTAs a row while SMs would be idle and each thread still has a batch
     int ctas = 1;
