@@ -22,7 +22,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libspmv_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["api.cu", "build.cu", "sell.cu", "sellmm.cu", "vector.cu", "merge.cu", "vecops.cu", "noalloc.cu", "solve.cu", "sellg.cu", "order.cu", "sellv.cu", "probe.cu", "sellb.cu",
-           "topk.cu", "gate.cu", "route.cu", "distill.cu", "distill_f32.cu", "distill_f16.cu", "distill_bf16.cu"]
+           "rows_check.cu", "topk.cu", "gate.cu", "route.cu", "distill.cu", "distill_f32.cu", "distill_f16.cu", "distill_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
