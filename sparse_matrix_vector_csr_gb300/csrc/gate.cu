@@ -1,19 +1,20 @@
 // A router's choice: the k <= 16 largest of short rows, with softmax weights, and the weights' gradient.
 //
-// Eight lanes share a row.  Each sorts its values in blocks of kK (a bitonic network on keys that
-// hold the value's order and its column, so that no two are equal and ties go to the lowest
-// column) and merges the blocks, keeping the kK largest; three exchanges with the lanes 1, 2
-// and 4 away merge the lanes' lists.  Every operation is a minimum or maximum on registers that
-// four rows a warp share: rounds of "largest of the warp" cost five times as many instructions a
-// row (256 bf16 values, 8 of them: 780).  The row is read once.
+// Eight lanes share a row (with four, a fifth fewer instructions a row but half the warps: 32768 rows
+// of 256 bf16 values, 8 chosen, with gradient, 20.8 us against 18.7).  Each sorts its values in blocks of kK (a sorting network on keys that hold the value's order and its column,
+// so that no two are equal and ties go to the lowest column) and merges the blocks, keeping the kK
+// largest; exchanges with the lanes 1, 2 and 4 away merge the lanes' lists.  Every operation is a
+// minimum or maximum on registers that four rows a warp share: rounds of "largest of
+// the warp" cost five times as many instructions a row (256 bf16 values, 8 of them: 780).  The
+// row is read once, its sum of exponentials taken along.
 #include "topk.cuh"
 
 namespace spmv {
 namespace rows {
 namespace {
 
+constexpr int kThreads = 128;
 constexpr int kLanes = 8;  // per row
-constexpr int kThreads = 256;
 
 // Keys in the order of (value, lower column first): the value's order above the complement of its
 // column, so 0 (no value) is below all.  Adding +0 makes one zero of both and the one positive NaN
@@ -108,9 +109,9 @@ __device__ __forceinline__ void keep_largest(K *x, const K *y) {
 }
 
 template <typename V>
-__device__ __forceinline__ V from_lane_away(V v, int d) { return __shfl_xor_sync(0xffffffffu, v, d, kLanes); }
+__device__ __forceinline__ V from_lane_away(V v, int d) { return __shfl_xor_sync(0xffffffffu, v, d); }
 
-// kV vectors a lane, lists of kK.
+// kV vectors a lane at a time, lists of kK.
 template <typename T, int kV, int kK>
 __global__ void __launch_bounds__(kThreads) k_gate(TopArgs a) {
     using K = typename Key<T>::type;
@@ -120,26 +121,33 @@ __global__ void __launch_bounds__(kThreads) k_gate(TopArgs a) {
     const bool there = r < a.rows;  // lanes of no row go along with the exchanges
     const RowView<T> row(static_cast<const T *>(a.x) + (there ? r : 0) * a.ldx, there ? a.n : 0);
     const Share<T> share(row, uint32_t(0), 0);
-    uint4 vec[kV];
-    load_share<T, kV>(share, lane, kLanes, vec);
+    const bool whole_row = a.lse || a.weighting == SPMV_WEIGHTS_ROW;
     K best[kK];
+    Running run;
     constexpr int kValues = kV * kN, kBlocks = (kValues + kK - 1) / kK;
-    K key[kBlocks * kK];
+    for (int v0 = 0; v0 == 0 || v0 < share.count; v0 += kV * kLanes) {
+        uint4 vec[kV];
+        load_share<T, kV>(share, v0 + lane, kLanes, vec);
+        K key[kBlocks * kK];
 #pragma unroll
-    for (int i = 0; i < kV; ++i)  // (what is not there is -inf, whatever column it says)
-        Key<T>::make(vec[i], static_cast<int>(share.first(i * kLanes + lane)), key + i * kN);
+        for (int i = 0; i < kV; ++i)  // (what is not there is -inf, whatever column it says)
+            Key<T>::make(vec[i], static_cast<int>(share.first(v0 + i * kLanes + lane)), key + i * kN);
 #pragma unroll
-    for (int i = kValues; i < kBlocks * kK; ++i) key[i] = 0;
+        for (int i = kValues; i < kBlocks * kK; ++i) key[i] = 0;
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-        sort_down<kK>(key + b * kK);
-        if (b == 0) {
+        for (int b = 0; b < kBlocks; ++b) {
+            sort_down<kK>(key + b * kK);
+            if (b > 0) keep_largest<kK>(key, key + b * kK);
+        }
+        if (v0 == 0) {
 #pragma unroll
             for (int i = 0; i < kK; ++i) best[i] = key[i];
         } else {
-            keep_largest<kK>(best, key + b * kK);
+            keep_largest<kK>(best, key);
         }
+        if (whole_row) run.add<T, kV>(vec, Key<T>::value(key[0]), a.scale);
     }
+    float m_lane = run.m, sum = run.sum();
 #pragma unroll
     for (int d = 1; d < kLanes; d *= 2) {
         K other[kK];
@@ -148,18 +156,13 @@ __global__ void __launch_bounds__(kThreads) k_gate(TopArgs a) {
         keep_largest<kK>(best, other);
     }
     const float m = reference_of(Key<T>::value(best[0]));
-    float sum = 0.0f;
-    const bool whole_row = a.lse || a.weighting == SPMV_WEIGHTS_ROW;
     if (whole_row) {
-        float2 s2 = both(0.0f);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) s2 = exp_sum<T>(vec[i], m, a.scale, s2);
-        sum = s2.x + s2.y;
+        if (m_lane != kNegInf) sum *= ex2((m_lane - m) * a.scale);
 #pragma unroll
         for (int d = 1; d < kLanes; d *= 2) sum += from_lane_away(sum, d);
         if (a.lse && lane == 0 && there) a.lse[r] = Key<T>::some(best[0]) ? fmaf(m, a.inv_temperature, logf(sum)) : kNegInf;
     }
-    // entries lane, lane + 8 of the row are this lane's
+    // entries lane, lane + kLanes, ... of the row are this lane's
     constexpr int kMine = (kK + kLanes - 1) / kLanes;
     float e[kMine], chosen = 0.0f;
     K mine[kMine];
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) k_gate(TopArgs a) {
     }
 }
 
-// The gradient (see topk.cu for the formulas): eight lanes write a row's vectors, then, after
+// The gradient (see topk.cu for the formulas): the lanes write a row's vectors, then, after
 // __syncwarp has ordered the stores, its chosen columns.
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
@@ -222,25 +225,28 @@ __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
     for (int d = 1; d < kLanes; d *= 2) s += from_lane_away(s, d);
     // a row of nothing but -inf has an lse of -inf: 0 everywhere
     const float lse = whole_row && there && a.lse[r] != kNegInf ? a.lse[r] : 0.0f, factor = -s * a.inv_temperature;
+    for (int v0 = 0; v0 < share.count; v0 += kV * kLanes) {
+        if (v0 && whole_row) load_share<T, kV>(share, v0 + lane, kLanes, vec);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int v = i * kLanes + lane;
-        if (v < share.count) {
-            uint4 o = splat<T>(0.0f);
-            if (whole_row) {
-                float f[kN];
-                unpack<T>(vec[i], f);
+        for (int i = 0; i < kV; ++i) {
+            const int v = v0 + i * kLanes + lane;
+            if (v < share.count) {
+                uint4 o = splat<T>(0.0f);
+                if (whole_row) {
+                    float f[kN];
+                    unpack<T>(vec[i], f);
 #pragma unroll
-                for (int q = 0; q < kN; q += 2) {
-                    float2 d = fma2(make_float2(f[q], f[q + 1]), both(a.inv_temperature), both(-lse));
-                    d = mul2(d, both(kLog2e));
-                    d = mul2(make_float2(ex2(d.x), ex2(d.y)), both(factor));
-                    f[q] = d.x;
-                    f[q + 1] = d.y;
+                    for (int q = 0; q < kN; q += 2) {
+                        float2 d = fma2(make_float2(f[q], f[q + 1]), both(a.inv_temperature), both(-lse));
+                        d = mul2(d, both(kLog2e));
+                        d = mul2(make_float2(ex2(d.x), ex2(d.y)), both(factor));
+                        f[q] = d.x;
+                        f[q + 1] = d.y;
+                    }
+                    o = pack<T>(f);
                 }
-                o = pack<T>(f);
+                share.store(out, v, o, congruent);
             }
-            share.store(out, v, o, congruent);
         }
     }
     __syncwarp();
@@ -250,33 +256,26 @@ __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
 }
 
 template <typename T, int kV>
-struct Launch {
-    static cudaError_t run(const TopArgs &a, unsigned grid, cudaStream_t s) {
-        if (a.k <= 4) k_gate<T, kV, 4><<<grid, kThreads, 0, s>>>(a);
-        else if (a.k <= 8) k_gate<T, kV, 8><<<grid, kThreads, 0, s>>>(a);
-        else k_gate<T, kV, 16><<<grid, kThreads, 0, s>>>(a);
-        return cudaGetLastError();
-    }
-    static cudaError_t run(const TopGradArgs &a, unsigned grid, cudaStream_t s) {
-        k_gate_grad<T, kV><<<grid, kThreads, 0, s>>>(a);
-        return cudaGetLastError();
-    }
-};
+cudaError_t launch(const TopArgs &a, cudaStream_t s) {
+    const unsigned grid = static_cast<unsigned>(ceil_div(a.rows, kThreads / kLanes));
+    if (a.k <= 4) k_gate<T, kV, 4><<<grid, kThreads, 0, s>>>(a);
+    else if (a.k <= 8) k_gate<T, kV, 8><<<grid, kThreads, 0, s>>>(a);
+    else k_gate<T, kV, 16><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <typename T, int kV>
+cudaError_t launch(const TopGradArgs &a, cudaStream_t s) {
+    k_gate_grad<T, kV><<<static_cast<unsigned>(ceil_div(a.rows, kThreads / kLanes)), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
 
 // by the vectors that a row of the matrix p may reach into
 template <typename T, typename Args>
 cudaError_t launch_by_vectors(const Args &a, const void *p, int64_t ld, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(ceil_div(a.rows, kThreads / kLanes));
     const int64_t vectors = row_vectors<T>(a.n, p, ld);
-    if (vectors <= kLanes) return Launch<T, 1>::run(a, grid, s);
-    if (vectors <= 2 * kLanes) return Launch<T, 2>::run(a, grid, s);
-    if (vectors <= 4 * kLanes) return Launch<T, 4>::run(a, grid, s);
-    if constexpr (sizeof(T) == 4) {
-        if (vectors <= 8 * kLanes) return Launch<T, 8>::run(a, grid, s);
-        return Launch<T, 17>::run(a, grid, s);  // 512 values from an odd address
-    } else {
-        return Launch<T, 9>::run(a, grid, s);
-    }
+    if (vectors <= kLanes) return launch<T, 1>(a, s);
+    if (vectors <= 2 * kLanes) return launch<T, 2>(a, s);
+    return launch<T, 4>(a, s);
 }
 
 template <typename Args>

@@ -215,13 +215,13 @@ __device__ __noinline__ uint32_t collect_by_bisection(const TopArgs &a, TopShare
     return ctas > 1 ? peer_load(peer_addr(&sh.count[0], 0)) : sh.count[0];
 }
 
-// per: batches that share a maximum; slots: maxima a thread has for its whole batches.
+// 2^log2_per batches share a maximum; slots: maxima a thread has for its whole batches.
 template <typename T>
-__global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, int log2_group, int per, int slots) {
+__global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, int log2_group, int log2_per, int slots) {
     __shared__ __align__(16) TopShared sh;
     extern __shared__ float batch_max[];  // [slots + 1][threads]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_threads = blockDim.x, n_warps = n_threads >> 5;
-    const int ctas = 1 << log2_ctas, group = 1 << log2_group;
+    const int ctas = 1 << log2_ctas, group = 1 << log2_group, per = 1 << log2_per;
     const int64_t r = blockIdx.x >> log2_ctas;
     const uint32_t rank = blockIdx.x & (ctas - 1);
     const RowView<T> row(static_cast<const T *>(a.x) + r * a.ldx, a.n);
@@ -311,13 +311,14 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     if (listed <= kMaxBatches) {
         // value i of the listed batches: a thread takes those n_threads apart, its loads in flight
         // together
-        const int per_listed = per * kBatch * kN, values = static_cast<int>(listed) * per_listed;
+        constexpr int kLog2Batch = kN == 8 ? 5 : 4;  // of a batch's values
+        const int log2_listed = log2_per + kLog2Batch, values = static_cast<int>(listed) << log2_listed;
         for (int i0 = tid; i0 < values; i0 += 4 * n_threads) {
             float f[4];
             int64_t e[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * n_threads, at = i / per_listed, in = i - at * per_listed;
+                const int i = i0 + u * n_threads, at = i >> log2_listed, in = i & ((1 << log2_listed) - 1);
                 f[u] = kNegInf;
                 e[u] = -1;
                 if (i < values) {
@@ -479,10 +480,11 @@ cudaError_t launch_topk_row(const TopArgs &a, cudaStream_t s) {
     while (log2_group > 0 && ctas * threads >> log2_group < 2 * a.k) --log2_group;
     while (1 << log2_ctas < ctas) ++log2_ctas;
     const int64_t batches = ceil_div(share, static_cast<int64_t>(threads) * kBatch);
-    const int per = static_cast<int>(ceil_div(batches, kBatchMaxima));
-    const int slots = static_cast<int>(ceil_div(batches, per));
+    int log2_per = 0;
+    while (ceil_div(batches, int64_t(1) << log2_per) > kBatchMaxima) ++log2_per;
+    const int slots = static_cast<int>(ceil_div(batches, int64_t(1) << log2_per));
     const size_t smem = static_cast<size_t>(slots + 1) * threads * sizeof(float);
-    return launch_rows(k_topk_row<T>, a.rows * ctas, threads, ctas, smem, s, a, log2_ctas, log2_group, per, slots);
+    return launch_rows(k_topk_row<T>, a.rows * ctas, threads, ctas, smem, s, a, log2_ctas, log2_group, log2_per, slots);
 }
 
 template <typename T>
