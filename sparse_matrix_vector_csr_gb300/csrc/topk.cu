@@ -124,7 +124,7 @@ struct TopShared {
 // the row; batch `whole` is, for threads 0 and 1, the vector at the row's start and end.
 template <typename T>
 struct Batches {
-    const Share<T> &share;
+    const Share<T> share;
     int t, w, whole;
     __device__ __forceinline__ Batches(const Share<T> &s, int t_, int w_)
         : share(s), t(t_), w(w_), whole(s.hi > s.lo ? (s.hi - s.lo + kBatch * w_ - 1) / (kBatch * w_) : 0) {}
@@ -134,21 +134,6 @@ struct Batches {
         return -1;
     }
     __device__ __forceinline__ int vector(int q, int i) const { return share.lo + t + (q * kBatch + i) * w; }
-    // absent vectors are -inf
-    __device__ __forceinline__ void load(int q, uint4 *x) const {
-        const int v = vector(q, 0);
-        if (v + (kBatch - 1) * w < share.hi) {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) x[i] = share.load_whole(v + i * w);
-        } else {
-            const uint4 none = splat<T>(kNegInf);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                x[i] = none;
-                if (v + i * w < share.hi) x[i] = share.load_whole(v + i * w);
-            }
-        }
-    }
     // f(vector, its index) over all of the thread's vectors
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
@@ -167,11 +152,15 @@ __device__ __forceinline__ void each_value(const Share<T> &share, const uint4 &v
     for (int q = 0; q < Vec<T>::kN; ++q) f(x[q], e + q);
 }
 
-// The list overflowed: candidates by bisection on (value, column); returns how many.
+// The list overflowed: candidates by bisection on (value, column); returns how many.  Out of line, by
+// values that are at hand (a reference to the caller's would keep them in memory all along).
 template <typename T>
-__device__ __noinline__ uint32_t collect_by_bisection(const TopArgs &a, TopShared &sh, const Batches<T> &batches, int ctas,
-                                                      float thr) {
-    const int tid = threadIdx.x, lane = tid & 31;
+__device__ __noinline__ uint32_t collect_by_bisection(const T *x, int64_t n, int k, uint32_t rank, int log2_ctas, float thr,
+                                                      uint32_t shared) {
+    TopShared &sh = *static_cast<TopShared *>(__cvta_shared_to_generic(shared));
+    const Share<T> share(RowView<T>(x, n), rank, log2_ctas);
+    const Batches<T> batches(share, threadIdx.x, blockDim.x);
+    const int tid = threadIdx.x, lane = tid & 31, ctas = 1 << log2_ctas;
     unsigned long long lo = static_cast<unsigned long long>(order_key(thr)) << 32, hi = ~0ull, cut = lo;
     uint32_t found = kMaxCand + 1;
     for (int step = 0; step < 64 && found > kMaxCand; ++step) {
@@ -191,7 +180,7 @@ __device__ __noinline__ uint32_t collect_by_bisection(const TopArgs &a, TopShare
         found = sh.count[slot];
         if (tid == 0) sh.count[1 + (step + 2) % 3] = 0;  // last read before the previous barrier
         if (found > kMaxCand) lo = cut;
-        else if (found < static_cast<uint32_t>(a.k)) {
+        else if (found < static_cast<uint32_t>(k)) {
             hi = cut;
             found = kMaxCand + 1;
         }
@@ -232,11 +221,12 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     if (tid < 5) sh.count[tid] = 0;
 
     Running run;  // its maximum passes over NaNs; the batches' maxima hand them on
-    const auto take = [&](const uint4 *x, int n) {
+    const auto take = [&](const uint4 *x, int n) {  // n = kBatch or 1
         float top = vec_max_nan(x[0], T());
+        if (n == kBatch) {
 #pragma unroll
-        for (int i = 1; i < kBatch; ++i)
-            if (i < n) top = max_nan(top, vec_max_nan(x[i], T()));
+            for (int i = 1; i < kBatch; ++i) top = max_nan(top, vec_max_nan(x[i], T()));
+        }
         if (want_lse) {
             if (n == kBatch) run.add<T, kBatch>(x, top, a.scale);
             else run.add<T, 1>(x, top, a.scale);
@@ -248,9 +238,20 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     for (int s = 0; s < slots; ++s) {
         float top = kNegInf;
         for (int q = s * per; q < (s + 1) * per && q < batches.whole; ++q) {
+            const int v = batches.vector(q, 0);
             uint4 x[kBatch];
-            batches.load(q, x);
-            top = max_nan(top, take(x, kBatch));
+            if (v + (kBatch - 1) * n_threads < share.hi) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) x[i] = share.load_whole(v + i * n_threads);
+                top = max_nan(top, take(x, kBatch));
+            } else if (v < share.hi) {
+#pragma unroll
+                for (int i = 0; i < kBatch - 1; ++i)
+                    if (v + i * n_threads < share.hi) x[i] = share.load_whole(v + i * n_threads);
+#pragma unroll
+                for (int i = 0; i < kBatch - 1; ++i)
+                    if (v + i * n_threads < share.hi) top = max_nan(top, take(x + i, 1));
+            }
         }
         batch_max[s * n_threads + tid] = top;
     }
@@ -309,26 +310,31 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     __syncthreads();
     const uint32_t listed = sh.count[4];
     if (listed <= kMaxBatches) {
-        // value i of the listed batches: a thread takes those n_threads apart, its loads in flight
-        // together
-        constexpr int kLog2Batch = kN == 8 ? 5 : 4;  // of a batch's values
-        const int log2_listed = log2_per + kLog2Batch, values = static_cast<int>(listed) << log2_listed;
-        for (int i0 = tid; i0 < values; i0 += 4 * n_threads) {
+        // a warp takes whole batches, a value a lane (two batches at once of 32-bit values), four
+        // loads in flight
+        constexpr int kLog2Batch = kN == 8 ? 5 : 4, kSide = 32 >> kLog2Batch;
+        const int in = lane & ((1 << kLog2Batch) - 1);
+        const int64_t at_lane = static_cast<int64_t>(in / kN) * n_threads * kN + in % kN;  // from the batch's first value
+        const int items = static_cast<int>(listed) << log2_per;  // batches, a slot's one after the other
+        for (int i0 = warp * kSide + (lane >> kLog2Batch); i0 - (lane >> kLog2Batch) < items; i0 += 4 * kSide * n_warps) {
             float f[4];
             int64_t e[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * n_threads, at = i >> log2_listed, in = i & ((1 << log2_listed) - 1);
+                const int i = i0 + u * kSide * n_warps;
                 f[u] = kNegInf;
                 e[u] = -1;
-                if (i < values) {
-                    const uint32_t b = sh.batch[at], s = b >> 16, owner = b & 0xffff;
-                    // the owner's vector in / kN of this slot, or its vector at the row's ends
-                    const int v = s == static_cast<uint32_t>(slots) ? (owner == 0 && share.lo == 1 ? 0 : share.hi)
-                                                                    : share.lo + static_cast<int>(owner) + (static_cast<int>(s) * per * kBatch + in / kN) * n_threads;
-                    const bool edge = s == static_cast<uint32_t>(slots);
-                    e[u] = share.first(v) + in % kN;
-                    if (edge ? in < kN && e[u] >= 0 && e[u] < a.n : v < share.hi) f[u] = to_f32(share.p[e[u]]);
+                if (i < items) {
+                    const uint32_t b = sh.batch[i >> log2_per];
+                    const int owner = static_cast<int>(b & 0xffff), s = static_cast<int>(b >> 16), sub = i & (per - 1);
+                    if (s == slots) {  // the owner's vector at the row's start or end
+                        e[u] = share.first(owner == 0 && share.lo == 1 ? 0 : share.hi) + in;
+                        if (sub == 0 && in < kN && e[u] >= 0 && e[u] < a.n) f[u] = to_f32(share.p[e[u]]);
+                    } else {
+                        const int v = share.lo + owner + ((s << log2_per) + sub) * kBatch * n_threads;
+                        e[u] = share.first(v) + at_lane;
+                        if (v + in / kN * n_threads < share.hi) f[u] = to_f32(share.p[e[u]]);
+                    }
                 }
             }
 #pragma unroll
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     __syncwarp();
     cluster_sync(ctas);
     uint32_t found = ctas > 1 ? peer_load(peer_addr(&sh.count[0], 0)) : sh.count[0];
-    if (found > kMaxCand) found = collect_by_bisection<T>(a, sh, batches, ctas, thr);
+    if (found > kMaxCand) found = collect_by_bisection<T>(row.p, a.n, a.k, rank, log2_ctas, thr, smem_addr(&sh));
     // the first CTA stays until the others have read its count; they have nothing left to do
     if (ctas > 1) {
         cluster_arrive();
