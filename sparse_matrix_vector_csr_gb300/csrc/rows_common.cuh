@@ -174,7 +174,8 @@ template <typename T>
 struct Share {
     static constexpr int kN = Vec<T>::kN;
     const T *p;        // the row
-    int64_t n, e0;     // its length; the first value of vector 0 (negative in front of the row)
+    const uint4 *vec;  // its vector 0 of this share (which may begin in front of the row)
+    int64_t n, e0;     // the row's length; the first value of vector 0 (negative in front of the row)
     int count, lo, hi;
     // the rank-th of 2^log2_ctas equal shares (the last may be shorter)
     __device__ __forceinline__ Share(const RowView<T> &row, uint32_t rank, int log2_ctas)
@@ -185,6 +186,7 @@ struct Share {
         if (v0 > nv) v0 = nv;
         const int64_t v1 = v0 + per < nv ? v0 + per : nv;
         e0 = row.first(v0);
+        vec = reinterpret_cast<const uint4 *>(p + e0);
         count = static_cast<int>(v1 - v0);
         lo = e0 < 0 ? 1 : 0;
         hi = e0 + static_cast<int64_t>(count) * kN > n ? count - 1 : count;
@@ -193,8 +195,8 @@ struct Share {
     __device__ __forceinline__ bool whole(int v) const { return v >= lo && v < hi; }
     __device__ __forceinline__ int64_t first(int v) const { return e0 + static_cast<int64_t>(v) * kN; }
     __device__ __forceinline__ bool owns(int64_t e) const { return e >= e0 && e < first(count); }
-    __device__ __forceinline__ uint4 load_whole(int v) const { return *reinterpret_cast<const uint4 *>(p + first(v)); }
-    __device__ __forceinline__ uint4 load_last(int v) const { return __ldcs(reinterpret_cast<const uint4 *>(p + first(v))); }
+    __device__ __forceinline__ uint4 load_whole(int v) const { return vec[v]; }
+    __device__ __forceinline__ uint4 load_last(int v) const { return __ldcs(vec + v); }
     // any vector of the share; values outside the row read as -inf
     __device__ __forceinline__ uint4 load(int v) const {
         if (whole(v)) return load_whole(v);
@@ -207,10 +209,10 @@ struct Share {
     // one vector of a row of the same length; `congruent`: it starts at the same offset from
     // a 16-byte boundary as this one (otherwise values go one by one)
     __device__ __forceinline__ void store(T *row, int v, const uint4 &x, bool congruent) const {
-        const int64_t e = first(v);
         if (congruent && whole(v)) {
-            __stcs(reinterpret_cast<uint4 *>(row + e), x);
+            __stcs(reinterpret_cast<uint4 *>(row + e0) + v, x);
         } else {
+            const int64_t e = first(v);
             float f[kN];
             unpack<T>(x, f);
 #pragma unroll
