@@ -249,7 +249,8 @@ struct GradScales {
 };
 
 constexpr int kBatchVectors = 4;  // in flight per thread where the row does not fit its registers
-constexpr int kKeepBatches = 2;   // of a row that is read twice: 92 KB of a CTA's shared memory
+constexpr int kPrefetch = 8;      // vectors of a thread that L2 fetches first (16: no faster)
+constexpr int kKeepBatches = 2;   // of a row that is read twice: 61 KB of a CTA's shared memory
 
 template <typename T, int kR, int kMode>
 __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode == kGrad ? 3 : 4) k_distill(DistillArgs a, int log2_ctas) {
@@ -275,6 +276,12 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
     uint4 reg[kR > 0 ? kR : 1];
     if constexpr (kR > 0)
         if (!entry_warp) load_share<T, kR>(share, tid, workers, reg);
+    if (kR == 0 && kMode == kGrad && !entry_warp) {
+        // the row waits for its entries (the gradient's factors): L2 meanwhile fetches
+#pragma unroll
+        for (int i = 0; i < kPrefetch; ++i)
+            if (share.whole(i * workers + tid)) asm volatile("prefetch.global.L2 [%0];" ::"l"(share.vec + i * workers + tid));
+    }
     if (kMode != kGrad && ctas > 1) cluster_arrive();  // the peers' shared memory may be written ...
     const uint8_t *marks = reinterpret_cast<const uint8_t *>(marks_mem);
     if (kMode != kGrad && tail) {
@@ -476,8 +483,10 @@ cudaError_t launch_distill_shape(const RowShape &shape, int64_t vectors, const D
     auto *kernel = k_distill<T, kR, kMode>;
     size_t smem = kR == 0 && kMode == kLossGrad ? static_cast<size_t>(16) * kBatchVectors * kKeepBatches * (shape.threads - 32) : 0;
     if (kMode != kGrad && a.teacher_lse) smem += static_cast<size_t>(ceil_div(ceil_div(vectors, shape.ctas), 4) * 4);
+    // (always the same limit: another thread's call may set it at the same time)
     if (smem + sizeof(DistillShared) > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(227 * 1024 - sizeof(DistillShared)));
         if (e != cudaSuccess) return e;
     }
     // the gradient alone needs no exchange: its CTAs are no cluster

@@ -22,6 +22,7 @@ constexpr int kPlanThreads = 512;
 constexpr int kMaxExperts = 4096;
 constexpr int64_t kPlanChunk = 1024;  // entries per CTA of the plan, at least
 constexpr int64_t kPlanCtas = 128;    // CTAs of the plan, at most
+constexpr int kPlanSmem = 128 * 1024; // limit of its shared memory (4096 experts: 96 KB)
 
 struct PlanShape {
     int64_t entries, chunk;
@@ -541,8 +542,7 @@ extern "C" SPMV_API int spmv_route_plan(int64_t tokens, int32_t k, int32_t exper
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int32_t *hist = p.ctas > 1 ? static_cast<int32_t *>(workspace) : nullptr;
     if (p.smem > 48 * 1024)
-        SPMV_TRY_CUDA(cudaFuncSetAttribute(k_route_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(p.smem)));
+        SPMV_TRY_CUDA(cudaFuncSetAttribute(k_route_place, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem));
     if (hist) {
         k_route_hist<<<p.ctas, kPlanThreads, static_cast<size_t>(experts) * 4, s>>>(m, p.chunk, experts, ids, hist);
         SPMV_TRY_CUDA(cudaGetLastError());

@@ -125,7 +125,7 @@ def topk_rows(x, k, temperature=1.0, weights=None, lse=False, vals=None, stream=
             return topk_rows(x, k, temperature, weights, lse, vals)
     code, ldx = _matrix(x, "x")
     rows, n = x.shape
-    weighting = WEIGHTINGS[weights]
+    weighting, k = WEIGHTINGS[weights], int(k)
     if not 1 <= k <= n or k > 256:
         raise ValueError("k must lie in [1, min(n, 256)]")
     top, device = TopRows(), x.device
@@ -163,7 +163,7 @@ class RoutePlan:
             raise ValueError("ids must be a matrix")
         ptr = _plain(ids, "ids", ids.shape, _I32)
         self.tokens, self.k = tokens, k = ids.shape
-        self.experts, self.align = experts, align
+        self.experts, self.align = experts, align = int(experts), int(align)
         self.rows, work = _plan_sizes(tokens, k, experts, align)
         device = ids.device
         self.offsets = _empty((experts + 1,), dtype=_I32, device=device)

@@ -82,7 +82,7 @@ def check_top(spmv, x, k, tau=1.0, weighting="row"):
 
 @pytest.mark.parametrize("dtype", ALL)
 @pytest.mark.parametrize("rows,n,k", [(1, 1, 1), (3, 2, 2), (9, 7, 3), (8, 64, 4), (5, 100, 32), (33, 256, 8),
-                                      (4, 512, 16), (3, 513, 8), (2, 300, 33), (3, 1000, 256), (2, 4097, 64),
+                                      (4, 512, 16), (3, 513, 8), (2, 300, 33), (3, 1000, 256), (2, 1500, 256), (200, 5000, 200), (2, 4097, 64),
                                       (1, 50021, 200), (3, 33000, 1), (1, 131072, 64), (2, 70001, 128),
                                       (1, 262144, 50), (1, 300001, 20), (1, 700003, 256)])
 def test_topk_rows(spmv, dtype, rows, n, k):
@@ -139,9 +139,13 @@ def test_topk_rows_grad(spmv, dtype, rows, n, k, weighting, shift, pad):
     tau = 1.5
     top = spmv.topk_rows(x, k, temperature=tau, weights=weighting)
     dw = torch.randn(rows, k, generator=g).cuda()
+    other, buf = placed(torch.zeros(rows, n, dtype=dtype), shift + 1, pad + 2)  # at another offset than x
+    top.grad(dw, out=other)
+    assert surroundings_untouched(other, buf)
     out, buf = placed(torch.zeros(rows, n, dtype=dtype), shift, pad)
     assert top.grad(dw, out=out) is out
     assert surroundings_untouched(out, buf)
+    assert torch.equal(out, other)
     ids, w, d = top.ids.cpu().numpy(), f64(top.weights), f64(dw)
     for r, row in enumerate(f64(x)):
         want = ref.top_weights_grad(row, ids[r], w[r], d[r], weighting, tau)
@@ -470,7 +474,7 @@ def test_distill_whole_vocabulary_as_entries(spmv):
 def test_given_stream_and_graph(spmv):
     g = gen(8)
     z = torch.randn(16, 5000, generator=g).cuda()
-    x = torch.randn(16, 64, generator=g).cuda()
+    x = torch.randn(3000, 64, generator=g).cuda()  # (a plan of several CTAs, two kernels)
     ids, teacher = (t.cuda() for t in some_target(16, 5000, 10, g))
     torch.cuda.synchronize()
 
