@@ -498,7 +498,10 @@ cudaError_t launch_distill_mode(const DistillArgs &a, cudaStream_t s) {
     const int64_t vectors = row_vectors<T>(a.n, a.z, a.ldz);
     // (fewer rows than warps that run at once: a CTA's warps share a row sooner)
     if (vectors <= kWarpVectors && a.rows >= 1216) return launch_distill_warp<T, kMode>(vectors, a, s);
-    const RowShape shape = row_shape(a.rows, vectors, kMode == kLossGrad);
+    RowShape shape = row_shape(a.rows, vectors, kMode == kLossGrad);
+    // with lse a CTA keeps a byte per vector of its share (2^22 float values: a cluster of 8)
+    if (kMode != kGrad && a.teacher_lse)
+        while (shape.ctas < kMaxCluster && ceil_div(vectors, shape.ctas) > 140 * 1024) shape.ctas *= 2;
     switch (shape.regs) {
         case 2: return launch_distill_shape<T, 2, kMode>(shape, vectors, a, s);
         case 4: return launch_distill_shape<T, 4, kMode>(shape, vectors, a, s);

@@ -451,6 +451,22 @@ def test_distill_gradient_is_the_difference(spmv):
                 assert abs((f(a) - f(b)) / 2e-5 - float(dz[r, c])) < 2e-5
 
 
+@pytest.mark.parametrize("rows,vocab", [(1, 1 << 22), (60, 1 << 22), (153, 1000003)])
+def test_distill_largest_vocabularies(spmv, rows, vocab):
+    g = gen(vocab)
+    z = torch.randn(rows, vocab, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    ids, teacher = some_target(rows, vocab, 7, g)
+    lse = teacher_lse_of(ids, teacher, vocab, 1.0, g)
+    loss, dz = spmv.distill_loss_grad(z, ids.cuda(), teacher.cuda(), teacher_lse=lse.cuda())
+    res = spmv.distill_loss(z, ids.cuda(), teacher.cuda(), teacher_lse=lse.cuda())
+    assert torch.isfinite(loss).all() and torch.isfinite(dz).all()
+    torch.testing.assert_close(res.loss, loss, rtol=1e-4, atol=1e-4)
+    for r in (0, rows - 1):
+        check_distill(spmv, z[r:r + 1], ids[r:r + 1], teacher[r:r + 1], lse[r:r + 1], 1.0, modes=("fused",))
+        want = ref.distill_loss(f64(z[r]), ids[r].numpy(), f64(teacher[r]), float(lse[r]))
+        assert abs(float(loss[r]) - want) < 1e-3 * (1 + abs(want))
+
+
 def test_distill_whole_vocabulary_as_entries(spmv):
     """With every column an entry there is no other class, whatever rounding leaves of r."""
     g = gen(4)
