@@ -1,6 +1,8 @@
 // The k largest entries of every row of a dense matrix: dense rows to sparse rows.  Values
 // descend, ties go to the lowest column, -inf is never taken.  With them the row's
 // log-sum-exp (the same pass over the row) and softmax weights, and the weights' gradient.
+#include <type_traits>
+
 #include "topk.cuh"
 
 namespace spmv {
@@ -11,9 +13,9 @@ using namespace rows;
 constexpr int kMaxTop = 256;
 constexpr int kWarpMaxN = 512;    // rows up to this length are taken by one warp each
 constexpr int kWarpMaxK = 32;     // ... with one lane per chosen entry
-constexpr int kMaxCand = 1024;    // candidates that one CTA sorts
-constexpr int kMaxBatches = 1024; // batches that are read again
-constexpr int kMaxGroups = 1024;  // maxima that set the first threshold
+constexpr int kMaxCand = 640;     // candidates that one CTA sorts
+constexpr int kMaxPieces = 512;  // pieces that are read again
+constexpr int kMaxGroups = 512;   // maxima that set the threshold
 
 // (key of the value, column) as one number: unique within a row, larger = taken earlier.
 __device__ __forceinline__ unsigned long long composite(float v, int64_t col) {
@@ -98,42 +100,41 @@ __global__ void __launch_bounds__(256) k_topk_warp(TopArgs a) {
 // ----------------------------------------------------------------------------
 // long rows: a CTA, or a cluster of CTAs, per row
 // ----------------------------------------------------------------------------
-// 1. Every thread reads its share once, a few vectors (a batch) at a time, and keeps its maximum
-//    and its batches' maxima (in shared memory).  The k-th largest of the maxima of groups of
-//    threads is a lower bound of the row's k-th largest entry that passes few others.
-// 2. The few batches that reach it are listed and read again (from L2), all at once, and their
+// 1. Every thread reads its share once, a few vectors at a time, and keeps its maximum and the maxima
+//    of pieces of 16 values (in shared memory).  The k-th largest of the maxima of groups of
+//    threads is a lower bound of the row's k-th largest entry that passes few others; a warp
+//    finds it to 20 bits of its order, which keeps it one.
+// 2. The few pieces that reach it are listed and read again (from L2), all at once, and their
 //    entries at or above it go to the first CTA's candidate list.
 // 3. If a list overflows (values bunched in one group, or many ties), the threshold is
 //    bisected on (value, column) numbers, which are unique, until between k and kMaxCand
 //    pass: at most 64 counting passes, whatever the row holds.
 // 4. The first CTA ranks the candidates by counting and writes the k largest.
 constexpr int kBatch = 4;        // vectors a thread loads at a time
-constexpr int kBatchMaxima = 15; // a thread's batches share this many maxima (and one for the row's ends)
+constexpr int kPieceMaxima = 15; // a thread's pieces share this many maxima (and one for the row's ends)
 
 struct TopShared {
     unsigned long long cand[kMaxCand];
-    float group_max[kMaxGroups];
+    uint32_t group_max[kMaxGroups];  // as order keys
     float2 sums[kMaxCluster * 16];  // per warp of the cluster: maximum, sum of exponentials
     float top_vals[kMaxTop];
-    uint32_t batch[kMaxBatches];  // listed: thread and slot of the maximum
-    uint32_t count[5];  // [0] candidates (first CTA's), [1..3] the bisection's counts, [4] listed batches
+    uint32_t piece[kMaxPieces];  // listed: thread and slot of the maximum
+    uint32_t count[5];  // [0] candidates (first CTA's), [1..3] the bisection's counts, [4] listed pieces
     float thr, lse_m, lse_sum;
 };
 
-// Thread t's batches of a share: batch q < whole covers the vectors lo + t + (q kBatch + i) W inside
-// the row; batch `whole` is, for threads 0 and 1, the vector at the row's start and end.
+// Thread t's vectors of a share: lo + t + i w inside the row, and, for threads 0 and 1, the vector at
+// the row's start and end.
 template <typename T>
 struct Batches {
     const Share<T> share;
-    int t, w, whole;
-    __device__ __forceinline__ Batches(const Share<T> &s, int t_, int w_)
-        : share(s), t(t_), w(w_), whole(s.hi > s.lo ? (s.hi - s.lo + kBatch * w_ - 1) / (kBatch * w_) : 0) {}
+    int t, w;
+    __device__ __forceinline__ Batches(const Share<T> &s, int t_, int w_) : share(s), t(t_), w(w_) {}
     __device__ __forceinline__ int edge() const {
         if (t == 0 && share.lo == 1 && share.count > 0) return 0;
         if (t == 1 && share.hi < share.count && share.hi >= share.lo) return share.hi;
         return -1;
     }
-    __device__ __forceinline__ int vector(int q, int i) const { return share.lo + t + (q * kBatch + i) * w; }
     // f(vector, its index) over all of the thread's vectors
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
@@ -204,11 +205,27 @@ __device__ __noinline__ uint32_t collect_by_bisection(const T *x, int64_t n, int
     return ctas > 1 ? peer_load(peer_addr(&sh.count[0], 0)) : sh.count[0];
 }
 
-// 2^log2_per batches share a maximum; slots: maxima a thread has for its whole batches.
+// A piece's maximum in 16 bits, 32-bit values rounded up: shared memory is what L1 has less of for
+// loads in flight (32 largest of 4096 x 50021 fp16 rows: 99 us so, 106 with 32-bit maxima).
+template <typename T>
+struct PieceMax {
+    using type = T;
+    static __device__ __forceinline__ T of(float v) { return from_f32<T>(v); }
+};
+template <>
+struct PieceMax<float> {
+    using type = __nv_bfloat16;
+    static __device__ __forceinline__ __nv_bfloat16 of(float v) { return __float2bfloat16_ru(v); }
+};
+
+// 2^log2_per pieces share a maximum; slots: maxima a thread has for its whole vectors.
 template <typename T>
 __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, int log2_group, int log2_per, int slots) {
+    constexpr int kN = Vec<T>::kN, kPiece = 16 / kN;  // vectors of a piece
     __shared__ __align__(16) TopShared sh;
-    extern __shared__ float batch_max[];  // [slots + 1][threads]
+    extern __shared__ __align__(16) unsigned char piece_mem[];
+    using Bound = typename PieceMax<T>::type;
+    Bound *piece_max = reinterpret_cast<Bound *>(piece_mem);  // [slots + 1][threads]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_threads = blockDim.x, n_warps = n_threads >> 5;
     const int ctas = 1 << log2_ctas, group = 1 << log2_group, per = 1 << log2_per;
     const int64_t r = blockIdx.x >> log2_ctas;
@@ -220,48 +237,64 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     if (ctas > 1) cluster_arrive();  // the peers' shared memory may be written from here on ...
     if (tid < 5) sh.count[tid] = 0;
 
-    Running run;  // its maximum passes over NaNs; the batches' maxima hand them on
-    const auto take = [&](const uint4 *x, int n) {  // n = kBatch or 1
-        float top = vec_max_nan(x[0], T());
-        if (n == kBatch) {
-#pragma unroll
-            for (int i = 1; i < kBatch; ++i) top = max_nan(top, vec_max_nan(x[i], T()));
-        }
-        if (want_lse) {
-            if (n == kBatch) run.add<T, kBatch>(x, top, a.scale);
-            else run.add<T, 1>(x, top, a.scale);
-        } else if (top > run.m) {
-            run.m = top;
-        }
-        return top;
+    Running run;  // its maximum passes over NaNs; the pieces' maxima hand them on
+    const auto note = [&](const uint4 *x, float top, auto n) {
+        if (want_lse) run.add<T, decltype(n)::value>(x, top, a.scale);
+        else if (top > run.m) run.m = top;
     };
-    for (int s = 0; s < slots; ++s) {
-        float top = kNegInf;
-        for (int q = s * per; q < (s + 1) * per && q < batches.whole; ++q) {
-            const int v = batches.vector(q, 0);
-            uint4 x[kBatch];
-            if (v + (kBatch - 1) * n_threads < share.hi) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) x[i] = share.load_whole(v + i * n_threads);
-                top = max_nan(top, take(x, kBatch));
-            } else if (v < share.hi) {
-#pragma unroll
-                for (int i = 0; i < kBatch - 1; ++i)
-                    if (v + i * n_threads < share.hi) x[i] = share.load_whole(v + i * n_threads);
-#pragma unroll
-                for (int i = 0; i < kBatch - 1; ++i)
-                    if (v + i * n_threads < share.hi) top = max_nan(top, take(x + i, 1));
-            }
+    int left = per;
+    float so_far = kNegInf;
+    Bound *next = piece_max + tid, *const last = next + slots * n_threads;
+    const auto piece = [&](float top) {
+        so_far = max_nan(so_far, top);
+        if (--left == 0) {
+            *next = PieceMax<T>::of(so_far);
+            next += n_threads;
+            so_far = kNegInf;
+            left = per;
         }
-        batch_max[s * n_threads + tid] = top;
+    };
+    int v = share.lo + tid;
+    for (; v + (kBatch - 1) * n_threads < share.hi; v += kBatch * n_threads) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) x[i] = share.load_whole(v + i * n_threads);
+        float all = kNegInf;
+#pragma unroll
+        for (int i = 0; i < kBatch; i += kPiece) {
+            float top = vec_max_nan(x[i], T());
+#pragma unroll
+            for (int q = 1; q < kPiece; ++q) top = max_nan(top, vec_max_nan(x[i + q], T()));
+            piece(top);
+            all = max_nan(all, top);
+        }
+        note(x, all, std::integral_constant<int, kBatch>());
     }
     {
+        uint4 x[kBatch - 1];
+#pragma unroll
+        for (int i = 0; i < kBatch - 1; ++i)
+            if (v + i * n_threads < share.hi) x[i] = share.load_whole(v + i * n_threads);
         float top = kNegInf;
-        if (batches.edge() >= 0) {
-            const uint4 x = share.load(batches.edge());
-            top = take(&x, 1);
+#pragma unroll
+        for (int i = 0; i < kBatch - 1; ++i) {
+            if (v + i * n_threads < share.hi) {
+                const float one = vec_max_nan(x[i], T());
+                top = max_nan(top, one);
+                note(x + i, one, std::integral_constant<int, 1>());
+            }
+            if (i % kPiece == kPiece - 1 || i == kBatch - 2) {  // the last piece may lack vectors, or have none
+                if (next < last) piece(top);
+                top = kNegInf;
+            }
         }
-        batch_max[slots * n_threads + tid] = top;
+        for (; next < last; next += n_threads, so_far = kNegInf) *next = PieceMax<T>::of(so_far);
+        if (batches.edge() >= 0) {
+            x[0] = share.load(batches.edge());
+            top = vec_max_nan(x[0], T());
+            note(x, top, std::integral_constant<int, 1>());
+        }
+        *last = PieceMax<T>::of(top);
     }
     float g = run.m;
     for (int o = 1; o < group; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
@@ -276,64 +309,77 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     const int per_cta = n_threads >> log2_group, n_groups = per_cta * ctas;
     if ((tid & (group - 1)) == 0)
         for (int c = 0; c < ctas; ++c) {
-            float *slot = &sh.group_max[rank * per_cta + (tid >> log2_group)];
-            if (ctas > 1) peer_store(peer_addr(slot, c), g);
-            else *slot = g;
+            uint32_t *at = &sh.group_max[rank * per_cta + (tid >> log2_group)];
+            if (ctas > 1) peer_store(peer_addr(at, c), __uint_as_float(order_key(g)));
+            else *at = order_key(g);
         }
     if (want_lse && lane < ctas) {
-        float2 *slot = &sh.sums[rank * n_warps + warp];
-        if (ctas > 1) peer_store2(peer_addr(slot, lane), m, sum);
-        else *slot = make_float2(m, sum);
+        float2 *at = &sh.sums[rank * n_warps + warp];
+        if (ctas > 1) peer_store2(peer_addr(at, lane), m, sum);
+        else *at = make_float2(m, sum);
     }
     if (tid == 0) sh.thr = kNegInf;
     cluster_sync(ctas);
 
-    for (int i = tid; i < n_groups; i += n_threads) {
-        const float v = sh.group_max[i];
-        int above = 0;
-        for (int j = 0; j < n_groups; j += 4) {  // (a multiple of 4)
-            const float4 w = *reinterpret_cast<const float4 *>(&sh.group_max[j]);
-            above += (w.x > v || (w.x == v && j < i)) + (w.y > v || (w.y == v && j + 1 < i)) +
-                     (w.z > v || (w.z == v && j + 2 < i)) + (w.w > v || (w.w == v && j + 3 < i));
+    if (n_groups <= (ctas > 1 ? 128 : 64)) {  // few, or little else to do: by counting, a thread each
+        for (int i = tid; i < n_groups; i += n_threads) {
+            const uint32_t key = sh.group_max[i];
+            int above = 0;
+            for (int j = 0; j < n_groups; j += 4) {  // (a multiple of 4)
+                const uint4 w = *reinterpret_cast<const uint4 *>(&sh.group_max[j]);
+                above += (w.x > key || (w.x == key && j < i)) + (w.y > key || (w.y == key && j + 1 < i)) +
+                         (w.z > key || (w.z == key && j + 2 < i)) + (w.w > key || (w.w == key && j + 3 < i));
+            }
+            if (above == a.k - 1) sh.thr = key_value(key);
         }
-        if (above == a.k - 1) sh.thr = v;
+    } else if (warp == 0) {  // by bits of the order, a count for each
+        uint32_t key[kMaxGroups / 32];
+#pragma unroll
+        for (int i = 0; i < kMaxGroups / 32; ++i) key[i] = i * 32 + lane < n_groups ? sh.group_max[i * 32 + lane] : 0;
+        uint32_t found_key = 0;
+        for (int bit = 31; bit >= 12; --bit) {
+            const uint32_t cut = found_key | 1u << bit;
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kMaxGroups / 32; ++i)
+                if (i * 32 < n_groups) n += key[i] >= cut;
+            if (warp_sum(n) >= a.k) found_key = cut;
+        }
+        if (lane == 0) sh.thr = key_value(found_key);  // (a NaN below -inf's key: no bound)
     }
     __syncthreads();
     const float thr = fmaxf(sh.thr, -FLT_MAX);  // above -inf: masked entries are never candidates
 
-    constexpr int kN = Vec<T>::kN;
     for (int s = 0; s <= slots; ++s)
-        if (!(batch_max[s * n_threads + tid] < thr)) {
+        if (!(to_f32(piece_max[s * n_threads + tid]) < thr)) {
             const uint32_t at = atomicAdd(&sh.count[4], 1u);
-            if (at < kMaxBatches) sh.batch[at] = static_cast<uint32_t>(s) << 16 | tid;
+            if (at < kMaxPieces) sh.piece[at] = static_cast<uint32_t>(s) << 16 | tid;
         }
     __syncthreads();
     const uint32_t listed = sh.count[4];
-    if (listed <= kMaxBatches) {
-        // a warp takes whole batches, a value a lane (two batches at once of 32-bit values), four
-        // loads in flight
-        constexpr int kLog2Batch = kN == 8 ? 5 : 4, kSide = 32 >> kLog2Batch;
-        const int in = lane & ((1 << kLog2Batch) - 1);
-        const int64_t at_lane = static_cast<int64_t>(in / kN) * n_threads * kN + in % kN;  // from the batch's first value
-        const int items = static_cast<int>(listed) << log2_per;  // batches, a slot's one after the other
-        for (int i0 = warp * kSide + (lane >> kLog2Batch); i0 - (lane >> kLog2Batch) < items; i0 += 4 * kSide * n_warps) {
+    if (listed <= kMaxPieces) {
+        // half a warp a piece, a value a lane, four loads in flight
+        const int in = lane & 15, half = tid >> 4, halves = n_threads >> 4;
+        const int64_t at_lane = static_cast<int64_t>(in / kN) * n_threads * kN + in % kN;  // from the piece's first value
+        const int items = static_cast<int>(listed) << log2_per;  // pieces, a slot's one after the other
+        for (int i0 = half; i0 < items; i0 += 4 * halves) {
             float f[4];
             int64_t e[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * kSide * n_warps;
+                const int i = i0 + u * halves;
                 f[u] = kNegInf;
                 e[u] = -1;
                 if (i < items) {
-                    const uint32_t b = sh.batch[i >> log2_per];
+                    const uint32_t b = sh.piece[i >> log2_per];
                     const int owner = static_cast<int>(b & 0xffff), s = static_cast<int>(b >> 16), sub = i & (per - 1);
                     if (s == slots) {  // the owner's vector at the row's start or end
                         e[u] = share.first(owner == 0 && share.lo == 1 ? 0 : share.hi) + in;
                         if (sub == 0 && in < kN && e[u] >= 0 && e[u] < a.n) f[u] = to_f32(share.p[e[u]]);
                     } else {
-                        const int v = share.lo + owner + ((s << log2_per) + sub) * kBatch * n_threads;
-                        e[u] = share.first(v) + at_lane;
-                        if (v + in / kN * n_threads < share.hi) f[u] = to_f32(share.p[e[u]]);
+                        const int first = share.lo + owner + ((s << log2_per) + sub) * kPiece * n_threads;
+                        e[u] = share.first(first) + at_lane;
+                        if (first + in / kN * n_threads < share.hi) f[u] = to_f32(share.p[e[u]]);
                     }
                 }
             }
@@ -485,11 +531,11 @@ cudaError_t launch_topk_row(const TopArgs &a, cudaStream_t s) {
     int log2_group = 5, log2_ctas = 0;
     while (log2_group > 0 && ctas * threads >> log2_group < 2 * a.k) --log2_group;
     while (1 << log2_ctas < ctas) ++log2_ctas;
-    const int64_t batches = ceil_div(share, static_cast<int64_t>(threads) * kBatch);
+    const int64_t pieces = ceil_div(share, static_cast<int64_t>(threads) * (16 / Vec<T>::kN));
     int log2_per = 0;
-    while (ceil_div(batches, int64_t(1) << log2_per) > kBatchMaxima) ++log2_per;
-    const int slots = static_cast<int>(ceil_div(batches, int64_t(1) << log2_per));
-    const size_t smem = static_cast<size_t>(slots + 1) * threads * sizeof(float);
+    while (ceil_div(pieces, int64_t(1) << log2_per) > kPieceMaxima) ++log2_per;
+    const int slots = static_cast<int>(ceil_div(pieces, int64_t(1) << log2_per));
+    const size_t smem = static_cast<size_t>(slots + 1) * threads * sizeof(typename PieceMax<T>::type);
     return launch_rows(k_topk_row<T>, a.rows * ctas, threads, ctas, smem, s, a, log2_ctas, log2_group, log2_per, slots);
 }
 
