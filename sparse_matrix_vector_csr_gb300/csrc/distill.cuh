@@ -53,13 +53,31 @@ struct EntryScalars {
     int valid;
 };
 
+// A CTA's shared memory (dynamic, no larger than the call needs: L1 has the rest for the loads in
+// flight).  With slots for the batches that a row read twice keeps; per warp of the cluster its
+// columns' maximum and sum (with lse: of those that are no entries, and in z, w of its CTA's entries,
+// from its last warp); the entries' columns (-1: none), probabilities and z (see load_entries);
+// with lse a byte per vector of the CTA's share, a bit per value.
 struct DistillShared {
-    // per warp of the cluster: maximum and sum of its columns (with lse: of those that are no
-    // entries, and in z, w of its CTA's entries, from its last warp)
-    float4 warp_part[kMaxCluster * 16];
-    int32_t id[kMaxEntries];             // column, or -1
-    float p[kMaxEntries], z[kMaxEntries];  // z: see load_entries
-    EntryScalars sc;
+    uint4 *keep;
+    float4 *part;
+    EntryScalars *sc;
+    int32_t *id;
+    float *p, *z;
+    uint32_t *marks;
+    __host__ __device__ static int padded(int k) { return (k + 3) & ~3; }
+    __device__ DistillShared(unsigned char *mem, int keep_slots, int parts, int k) {
+        keep = reinterpret_cast<uint4 *>(mem);
+        part = reinterpret_cast<float4 *>(keep + keep_slots);
+        sc = reinterpret_cast<EntryScalars *>(part + parts);
+        id = reinterpret_cast<int32_t *>(sc + 1);
+        p = reinterpret_cast<float *>(id + padded(k));
+        z = p + padded(k);
+        marks = reinterpret_cast<uint32_t *>(z + padded(k));
+    }
+    static size_t bytes(int64_t keep_slots, int parts, int k, int64_t marks) {
+        return static_cast<size_t>(16 * (keep_slots + parts + 1) + 12 * padded(k) + (marks + 3) / 4 * 4);
+    }
 };
 
 // One warp: the entries' probabilities, and z at those of columns [e0, e1) (the CTA's own, or all
@@ -256,16 +274,15 @@ template <typename T, int kR, int kMode>
 __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode == kGrad ? 3 : 4) k_distill(DistillArgs a, int log2_ctas) {
     constexpr int kN = Vec<T>::kN;
     constexpr int kU = kBatchVectors;
-    __shared__ DistillShared sh;
     constexpr int kKeep = kR == 0 && kMode == kLossGrad ? kKeepBatches : 0;
     extern __shared__ __align__(16) unsigned char dynamic_mem[];
-    uint4 *keep = reinterpret_cast<uint4 *>(dynamic_mem) + threadIdx.x;
-    // with lse: a byte per vector of the CTA's share, a bit per value
-    uint32_t *marks_mem = reinterpret_cast<uint32_t *>(dynamic_mem + static_cast<size_t>(16) * kU * kKeep * (blockDim.x - 32));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
     const int workers = blockDim.x - 32;
     const bool entry_warp = tid >= workers;
     const int ctas = 1 << log2_ctas;
+    const DistillShared sh(dynamic_mem, kU * kKeep * workers, ctas * n_warps, a.k);
+    uint4 *const keep = sh.keep + tid;
+    uint32_t *const marks_mem = sh.marks;
     const int64_t r = blockIdx.x >> log2_ctas;
     const uint32_t rank = blockIdx.x & (ctas - 1);
     const T *z = static_cast<const T *>(a.z) + r * a.ldz;
@@ -300,7 +317,7 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
     }
     if (entry_warp) {
         const bool sums_loss = kMode != kGrad && rank == 0;
-        load_entries<T>(a, sh.id, sh.p, sh.z, sh.sc, r, z, sums_loss ? 0 : share.e0, sums_loss ? a.n : share.first(share.count));
+        load_entries<T>(a, sh.id, sh.p, sh.z, *sh.sc, r, z, sums_loss ? 0 : share.e0, sums_loss ? a.n : share.first(share.count));
     }
 
     RowSums sums;
@@ -347,21 +364,21 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
         ws = warp_sum(ws);
         if (ctas > 1) cluster_wait();  // ... once they have started
         if (lane < ctas) {
-            float4 *slot = &sh.warp_part[rank * n_warps + warp];
+            float4 *slot = &sh.part[rank * n_warps + warp];
             if (ctas > 1) peer_store4(peer_addr(slot, lane), wm, ws, em, es);
             else *slot = make_float4(wm, ws, em, es);
         }
         cluster_sync(ctas);
-        sums = join_parts(a, sh.warp_part, n_warps * ctas);
-        if (rank == 0 && entry_warp) write_loss(a, r, sh.id, sh.p, sh.z, sh.sc, sums);
+        sums = join_parts(a, sh.part, n_warps * ctas);
+        if (rank == 0 && entry_warp) write_loss(a, r, sh.id, sh.p, sh.z, *sh.sc, sums);
     } else {
         __syncthreads();
         sums = stored_sums(a.stats[r]);
     }
 
     if constexpr (kMode != kLoss) {
-        const bool live = sh.sc.valid != 0;
-        const GradScales gs(a, r, sh.sc, sums);
+        const bool live = sh.sc->valid != 0;
+        const GradScales gs(a, r, *sh.sc, sums);
         T *dz = static_cast<T *>(a.dz) + r * a.lddz;
         const bool congruent = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
         if (!entry_warp) {
@@ -481,12 +498,11 @@ cudaError_t launch_distill_warp(int64_t vectors, const DistillArgs &a, cudaStrea
 template <typename T, int kR, int kMode>
 cudaError_t launch_distill_shape(const RowShape &shape, int64_t vectors, const DistillArgs &a, cudaStream_t s) {
     auto *kernel = k_distill<T, kR, kMode>;
-    size_t smem = kR == 0 && kMode == kLossGrad ? static_cast<size_t>(16) * kBatchVectors * kKeepBatches * (shape.threads - 32) : 0;
-    if (kMode != kGrad && a.teacher_lse) smem += static_cast<size_t>(ceil_div(ceil_div(vectors, shape.ctas), 4) * 4);
-    // (always the same limit: another thread's call may set it at the same time)
-    if (smem + sizeof(DistillShared) > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(227 * 1024 - sizeof(DistillShared)));
+    const int64_t keep = kR == 0 && kMode == kLossGrad ? static_cast<int64_t>(kBatchVectors) * kKeepBatches * (shape.threads - 32) : 0;
+    const int64_t marks = kMode != kGrad && a.teacher_lse ? ceil_div(vectors, shape.ctas) : 0;
+    const size_t smem = DistillShared::bytes(keep, shape.ctas * shape.threads / 32, a.k, marks);
+    if (smem > 48 * 1024) {  // (always the same limit: another thread's call may set it at the same time)
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
     }
     // the gradient alone needs no exchange: its CTAs are no cluster
