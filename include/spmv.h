@@ -670,8 +670,7 @@ SPMV_API int spmv_route_combine_grad(int64_t tokens, int32_t k, int64_t rows, in
  * logit of -inf has p = 0.  The loss is not scaled: neither by temperature^2 nor to a mean.
  *   k 1..512 (k may exceed vocab only by absent entries), vocab 1..2^22, temperature in
  *   [1e-6, 1e6].
- *   stats    float[rows][4], 16-byte aligned, or NULL: what the gradient needs of the row
- *            (z's maximum and its sum of exponentials, of all and of the other columns).
+ *   stats    float[rows][4], 16-byte aligned, or NULL: what spmv_distill_grad needs of the row.
  *   dz       rows x vocab, z's type, overwritten:
  *            scale * row_scale[t] * d loss[t] / d z[t] (row_scale float[rows], NULL = all 1).
  *            It may be z itself (same address and leading dimension): the gradient then

@@ -43,7 +43,7 @@ struct DistillArgs {
     const void *teacher;
     const float *teacher_lse, *row_scale;
     float *loss;
-    float4 *stats;  // per row: m, sum exp((z - m) / T) over all columns; with lse the same of the others
+    float4 *stats;  // per row, for the gradient: see RowFactors
     void *dz;
 };
 
@@ -183,7 +183,6 @@ struct GradOf {
 struct RowSums {
     float m, sum, m_rest, rest_sum;
 };
-__device__ __forceinline__ RowSums stored_sums(const float4 &s) { return RowSums{s.x, s.y, s.z, s.w}; }
 
 // A warp joins the parts of all warps that share the row; a part without a value above -inf adds
 // its 0 (or a NaN).
@@ -228,6 +227,31 @@ __device__ __forceinline__ RowSums join_two(const DistillArgs &a, float m_rest, 
     return s;
 }
 
+// What a row's gradient takes of it: q_i = inv_sum exp((z_i - m) / T) at the entries (less p_i), and
+// elsewhere other exp((z_i - ref) / T): q_i, and with lse q_i - r q'_i, q' the softmax over the
+// other columns.  All factors 0: no target, no gradient.  The loss leaves it for a gradient
+// that is taken later, which so need not wait for the row's entries.
+struct RowFactors {
+    float ref, other, m, inv_sum;
+    __device__ __forceinline__ explicit RowFactors(const float4 &s) : ref(s.x), other(s.y), m(s.z), inv_sum(s.w) {}
+    __device__ __forceinline__ RowFactors(const DistillArgs &a, const EntryScalars &sc, const RowSums &s)
+        : ref(s.m), other(0.0f), m(s.m), inv_sum(0.0f) {
+        if (!sc.valid) return;
+        other = inv_sum = 1.0f / s.sum;
+        if (a.teacher_lse) {
+            ref = s.m_rest;
+            other = s.rest_sum != 0.0f ? ex2((s.m_rest - s.m) * a.scale2) / s.sum - sc.rest / s.rest_sum : 0.0f;
+        }
+    }
+    __device__ __forceinline__ bool live() const { return inv_sum != 0.0f || other != 0.0f; }
+    __device__ __forceinline__ float at_entry(const DistillArgs &a, float g, float p, float z) const {
+        return g * fmaf(ex2((z - m) * a.scale2), inv_sum, -p);
+    }
+};
+__device__ __forceinline__ float row_gain(const DistillArgs &a, int64_t r) {
+    return a.scale * (a.row_scale ? a.row_scale[r] : 1.0f) * a.inv_temperature;
+}
+
 // One warp sums the loss over the entries (z: all of them).
 __device__ __forceinline__ void write_loss(const DistillArgs &a, int64_t r, const int32_t *id, const float *p,
                                            const float *z, const EntryScalars &sc, const RowSums &s) {
@@ -242,29 +266,12 @@ __device__ __forceinline__ void write_loss(const DistillArgs &a, int64_t r, cons
         if (sc.rest > 0.0f && !(sc.rest < kRestRounding && s.rest_sum == 0.0f))
             loss += sc.rest * (logf(sc.rest) - logf(s.rest_sum) + log_sum + (s.m - s.m_rest) * a.inv_temperature);
         a.loss[r] = sc.valid ? loss : 0.0f;
-        if (a.stats) a.stats[r] = make_float4(s.m, s.sum, s.m_rest, s.rest_sum);
-    }
-}
-
-// The gradient's factors: g q at the entries (less g p); elsewhere g q, and with lse
-// g (q - r q_other), q_other the softmax over the other columns; both are multiples of
-// exp((z - m_rest) / T).
-struct GradScales {
-    float g, q, m, ref, other;
-    __device__ __forceinline__ GradScales(const DistillArgs &a, int64_t r, const EntryScalars &sc, const RowSums &s) {
-        g = a.scale * (a.row_scale ? a.row_scale[r] : 1.0f) * a.inv_temperature;
-        q = g / s.sum;
-        m = ref = s.m;
-        other = q;
-        if (a.teacher_lse) {
-            ref = s.m_rest;
-            other = s.rest_sum != 0.0f ? g * (ex2((s.m_rest - s.m) * a.scale2) / s.sum - sc.rest / s.rest_sum) : 0.0f;
+        if (a.stats) {
+            const RowFactors f(a, sc, s);
+            a.stats[r] = make_float4(f.ref, f.other, f.m, f.inv_sum);
         }
     }
-    __device__ __forceinline__ float at_entry(const DistillArgs &a, float p, float z) const {
-        return fmaf(ex2((z - m) * a.scale2), q, -p * g);
-    }
-};
+}
 
 constexpr int kBatchVectors = 4;  // in flight per thread where the row does not fit its registers
 constexpr int kPrefetch = 8;      // vectors of a thread that L2 fetches first (16: no faster)
@@ -294,7 +301,7 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
     if constexpr (kR > 0)
         if (!entry_warp) load_share<T, kR>(share, tid, workers, reg);
     if (kR == 0 && kMode == kGrad && !entry_warp) {
-        // the row waits for its entries (the gradient's factors): L2 meanwhile fetches
+        // the row waits for its factors: L2 meanwhile fetches
 #pragma unroll
         for (int i = 0; i < kPrefetch; ++i)
             if (share.whole(i * workers + tid)) asm volatile("prefetch.global.L2 [%0];" ::"l"(share.vec + i * workers + tid));
@@ -371,14 +378,14 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
         cluster_sync(ctas);
         sums = join_parts(a, sh.part, n_warps * ctas);
         if (rank == 0 && entry_warp) write_loss(a, r, sh.id, sh.p, sh.z, *sh.sc, sums);
-    } else {
-        __syncthreads();
-        sums = stored_sums(a.stats[r]);
+    } else if (a.dz == a.z) {
+        __syncthreads();  // in place: z at the entries is read before any of the row is written
     }
 
     if constexpr (kMode != kLoss) {
-        const bool live = sh.sc->valid != 0;
-        const GradScales gs(a, r, *sh.sc, sums);
+        const RowFactors rf = kMode == kGrad ? RowFactors(a.stats[r]) : RowFactors(a, *sh.sc, sums);
+        const bool live = rf.live();
+        const float g = row_gain(a, r);
         T *dz = static_cast<T *>(a.dz) + r * a.lddz;
         const bool congruent = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
         if (!entry_warp) {
@@ -386,7 +393,7 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
                 const uint4 zero = splat<T>(0.0f);
                 for (int v = tid; v < share.count; v += workers) share.store(dz, v, zero, congruent);
             } else {
-                const GradOf<T> grad(gs.ref, a.scale2, gs.other);
+                const GradOf<T> grad(rf.ref, a.scale2, g * rf.other);
                 if constexpr (kR > 0) {
 #pragma unroll
                     for (int i = 0; i < kR; ++i)
@@ -406,7 +413,7 @@ __global__ void __launch_bounds__(512, kR > 0 || kMode == kLossGrad ? 2 : kMode 
         if (live)
             for (int j = tid; j < a.k; j += blockDim.x) {
                 const int32_t id = sh.id[j];
-                if (own(id)) dz[id] = from_f32<T>(gs.at_entry(a, sh.p[j], sh.z[j]));
+                if (own(id)) dz[id] = from_f32<T>(rf.at_entry(a, g, sh.p[j], sh.z[j]));
             }
     }
 }
@@ -465,21 +472,20 @@ __global__ void __launch_bounds__(32 * kWarpRows, kR == 4 ? 8 : kR == 8 ? 5 : 3)
         for (int i = 0; i < kR; ++i) s2 = exp_sum<T>(reg[i], w0, a.scale2, s2);
         sums = join_two(a, wm, warp_sum(s2.x + s2.y), em, es);
         write_loss(a, r, id, p, zk, sc, sums);
-    } else {
-        sums = stored_sums(a.stats[r]);
     }
     if constexpr (kMode != kLoss) {
-        const GradScales gs(a, r, sc, sums);
+        const RowFactors rf = kMode == kGrad ? RowFactors(a.stats[r]) : RowFactors(a, sc, sums);
+        const float g = row_gain(a, r);
         T *dz = static_cast<T *>(a.dz) + r * a.lddz;
-        const bool live = sc.valid != 0, congruent = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-        const GradOf<T> grad(gs.ref, a.scale2, gs.other);
+        const bool live = rf.live(), congruent = ((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+        const GradOf<T> grad(rf.ref, a.scale2, g * rf.other);
 #pragma unroll
         for (int i = 0; i < kR; ++i)
             if (i * 32 + lane < share.count) share.store(dz, i * 32 + lane, live ? grad(reg[i]) : splat<T>(0.0f), congruent);
         __syncwarp();  // the entries' columns are written after the plain stores
         if (live)
             for (int j = lane; j < a.k; j += 32)
-                if (id[j] >= 0) dz[id[j]] = from_f32<T>(gs.at_entry(a, p[j], zk[j]));
+                if (id[j] >= 0) dz[id[j]] = from_f32<T>(rf.at_entry(a, g, p[j], zk[j]));
     }
 }
 
