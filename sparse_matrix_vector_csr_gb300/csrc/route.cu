@@ -293,7 +293,9 @@ __device__ __forceinline__ U unit_from_f32(const float *in) {
 // y[t] = sum over j of weights[t, j] ys[slots[t, j]], j ascending, in 32 bits, rounded once.  A
 // warp has kU x 32 units of kJ entries' rows in flight.  Many tokens: 2 x 2 keeps 40 warps on an
 // SM (16384 tokens x 8 rows of 4096 bf16 values 197 us; 4 x 2 with 20 warps 277 us).  Few tokens:
-// one load's latency for four entries (4 tokens x 8 rows 4.9 us; one by one 8.8 us).
+// one load's latency for four entries (4 tokens x 8 rows 4.9 us; one by one 8.8 us).  Narrower
+// units: as many bytes in flight as the registers of their sums allow (8192 tokens x 4 rows of
+// 4095 bf16 values 86 us, of 2047 float values 62; 16-byte rows 62 and 56).
 template <typename T, typename U, int kJ, int kU>
 __global__ void __launch_bounds__(kRowThreads) k_combine(int64_t tokens, int k, int64_t rows, int64_t units,
                                                         int64_t parts, const int32_t *__restrict__ slots,
@@ -469,12 +471,14 @@ void launch_combine(int unit, int64_t tokens, int k, int64_t rows, int64_t d, co
     constexpr std::integral_constant<int, 1> one;
     constexpr std::integral_constant<int, 2> two;
     constexpr std::integral_constant<int, 4> four;
+    constexpr std::integral_constant<int, 8> eight;
+    constexpr std::integral_constant<int, 16> sixteen;
     // few tokens: as many warps as there are 512-byte pieces
     const bool few = tokens * d * static_cast<int64_t>(sizeof(T)) < int64_t(152) * 16 * 1024;
     if (unit == 16) few ? go(uint4{}, four, one) : go(uint4{}, two, two);
-    else if (unit == 8) go(uint2{}, two, two);
-    else if (unit == 4) go(uint32_t{}, two, four);
-    else if constexpr (sizeof(T) == 2) go(uint16_t{}, two, four);
+    else if (unit == 8) sizeof(T) == 4 ? go(uint2{}, two, eight) : go(uint2{}, one, four);
+    else if (unit == 4) go(uint32_t{}, two, eight);
+    else if constexpr (sizeof(T) == 2) go(uint16_t{}, two, sixteen);
 }
 
 template <typename T>
