@@ -209,13 +209,13 @@ template <>
 struct Unit<2> { using type = uint16_t; };
 
 // Zero the sorted rows without a source among 32 that the CTA looks at: padding comes in runs
-// (behind each segment, and behind the last), so each warp takes every eighth.
+// (behind each segment, and behind the last), so the CTA's warps take turns.
 constexpr int kPadRows = 32;  // per CTA
 template <typename U>
 __device__ void zero_padding(int64_t first, int64_t rows, const int32_t *sources, int64_t units, U *out, int64_t ld) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
     const uint32_t pad = __ballot_sync(0xffffffffu, first + lane < rows && sources[first + lane] < 0);
-    for (int i = warp; i < 32; i += kRowWarps)
+    for (int i = warp; i < 32; i += n_warps)
         if (pad >> i & 1) {
             U *row = out + (first + i) * ld;
             for (int64_t u = lane; u < units; u += 32) row[u] = U{};
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(int64_t tokens, int k, 
 }
 
 // dys[slots[t, j]] = weights[t, j] dy[t] and dweights[t, j] = <dy[t], ys[slots[t, j]]>: one CTA
-// per token, so that its products reduce inside the CTA in a fixed order (no atomics); entries
+// per token (of one warp to eight, by the row's length), so that its products reduce inside the CTA in a fixed order (no atomics); entries
 // are taken four at a time, dy coming from L1 from the second time on.  Rows of dys without
 // a source are zeroed by the first CTAs.
 template <typename T, typename U>
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_grad(int64_t pad_ctas, 
     constexpr int kN = sizeof(U) / sizeof(T);
     constexpr int kJ = 4;
     __shared__ float part[kJ][kRowWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_threads = blockDim.x, n_warps = n_threads >> 5;
     if (blockIdx.x < pad_ctas) {
         zero_padding(static_cast<int64_t>(blockIdx.x) * kPadRows, rows, sources, units, dys, lddys);
         return;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_grad(int64_t pad_ctas, 
             if (s[j] >= rows) s[j] = -1;
             w[j] = s[j] >= 0 ? weights[t * k + j0 + j] : 0.0f;
         }
-        for (int64_t u = threadIdx.x; u < units; u += kRowThreads) {
+        for (int64_t u = threadIdx.x; u < units; u += n_threads) {
             U v[kJ];
             const U gu = g[u];
 #pragma unroll
@@ -404,13 +404,15 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_grad(int64_t pad_ctas, 
             const float sum = warp_sum(acc[j]);
             if (lane == 0) part[j][warp] = sum;
         }
-        __syncthreads();
+        if (n_warps > 1) __syncthreads();
+        else __syncwarp();
         if (threadIdx.x < kJ && j0 + static_cast<int>(threadIdx.x) < k) {
             float sum = 0.0f;
-            for (int i = 0; i < kRowWarps; ++i) sum += part[threadIdx.x][i];
+            for (int i = 0; i < n_warps; ++i) sum += part[threadIdx.x][i];
             dweights[t * k + j0 + threadIdx.x] = sum;
         }
-        __syncthreads();
+        if (n_warps > 1) __syncthreads();
+        else __syncwarp();
     }
 }
 
@@ -488,8 +490,10 @@ void launch_combine_grad(int unit, int64_t tokens, int k, int64_t rows, int64_t 
     auto go = [&](auto tag) {
         using U = decltype(tag);
         constexpr int64_t kN = sizeof(U) / sizeof(T);
-        k_combine_grad<T, U><<<static_cast<unsigned>(tokens + ceil_div(rows, kPadRows)), kRowThreads, 0, s>>>(
-            ceil_div(rows, kPadRows), k, rows, d / kN, slots, sources, weights, static_cast<const U *>(dy), lddy / kN,
+        const int64_t units = d / kN;
+        const int threads = units >= 512 ? 256 : units >= 128 ? 128 : units > 64 ? 64 : 32;
+        k_combine_grad<T, U><<<static_cast<unsigned>(tokens + ceil_div(rows, kPadRows)), threads, 0, s>>>(
+            ceil_div(rows, kPadRows), k, rows, units, slots, sources, weights, static_cast<const U *>(dy), lddy / kN,
             static_cast<const U *>(ys), ldys / kN, static_cast<U *>(dys), lddys / kN, dweights);
     };
     if (unit == 16) go(uint4{});
