@@ -128,7 +128,8 @@ def distill_grad(z, ids, teacher, teacher_lse=None, tau=1.0):
         return np.zeros(len(z))
     z, cols, p, _, rest, others, lse_rest, norm = t
     g = np.exp(z - norm)
-    if rest > 0:
-        g[others] -= rest * np.exp(z[others] - lse_rest)
+    if rest > 0 and lse_rest > NEG_INF:
+        share = np.exp(z[others] - z[others].max())  # (lse_rest itself would absorb the count at -1e38)
+        g[others] -= rest * share / share.sum()
     g[cols] -= p
     return g / tau

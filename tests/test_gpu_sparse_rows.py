@@ -482,6 +482,33 @@ def test_distill_whole_vocabulary_as_entries(spmv):
     assert torch.isfinite(res.loss).all() and torch.isfinite(res.grad()).all()
 
 
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows", [3, 1300])
+def test_distill_all_other_columns_masked(spmv, dtype, rows):
+    """By the lowest value: they share the remainder's gradient evenly.  By -inf: the loss is +inf (the
+    teacher has mass where the student cannot), the entries' gradient stays, the others' is 0."""
+    vocab, k = 24, 20
+    ids = torch.arange(k, dtype=torch.int32).repeat(rows, 1) + 4
+    teacher = torch.linspace(0, 2, k).repeat(rows, 1)
+    lse = (torch.logsumexp(teacher.double(), 1) + 0.1).float()
+    rest = 1 - math.exp(-0.1)
+    args = (ids.cuda(), teacher.cuda())
+    for low in (torch.finfo(dtype).min, -math.inf):
+        z = torch.linspace(-1, 1, vocab).repeat(rows, 1)
+        z[:, :4] = low
+        z = z.to(dtype).cuda()
+        loss, dz = spmv.distill_loss_grad(z, *args, teacher_lse=lse.cuda())
+        res = spmv.distill_loss(z, *args, teacher_lse=lse.cuda())
+        for got_loss, got in ((loss, dz), (res.loss, res.grad())):
+            got = f64(got)
+            want = ref.distill_grad(f64(z[0]), ids[0].numpy(), f64(teacher[0]), float(lse[0]))
+            assert np.abs(got - want).max() <= 1e-5 + H[dtype] * np.abs(want).max()
+            if low == -math.inf:
+                assert torch.isinf(got_loss).all() and not got[:, :4].any()
+            else:  # the remainder to float rounding of lse, then the output's
+                assert np.abs(got[:, :4] + rest / 4).max() <= 1e-5 + H[dtype] * rest
+
+
 # --------------------------------------------------------------------------- #
 # streams, graphs, errors
 # --------------------------------------------------------------------------- #
