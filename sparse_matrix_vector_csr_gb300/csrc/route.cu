@@ -41,7 +41,8 @@ PlanShape plan_shape(int64_t tokens, int32_t k, int32_t experts) {
     const int64_t most = p.entries < p.chunk ? p.entries : p.chunk;
     while (p.warps > 1 && p.warps * 16 >= most) p.warps /= 2;  // no more than there are 32s of entries
     while (p.warps > 1 && static_cast<int64_t>(p.warps) * experts > 16384) p.warps /= 2;
-    p.smem = static_cast<size_t>(p.warps + 2) * static_cast<size_t>(experts) * sizeof(int32_t);
+    // all of it dynamic, the scan's partial sums too, so that p.smem is what the default limit is held against
+    p.smem = (static_cast<size_t>(p.warps + 2) * static_cast<size_t>(experts) + kPlanThreads / 32) * sizeof(int32_t);
     return p;
 }
 
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_route_place(int64_t entries, i
     int32_t *wcount = shared;                       // [n_warps][experts]: counts, then next places
     int32_t *total = wcount + n_warps * experts;    // [experts]
     int32_t *start = total + experts;               // [experts]: first row of the expert's segment
-    __shared__ int32_t warp_part[kPlanThreads / 32];
+    int32_t *warp_part = start + experts;           // [kPlanThreads / 32]: the scan's, one a warp
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t begin = blockIdx.x * chunk, end = begin + chunk < entries ? begin + chunk : entries;
     // runs of whole 32s
