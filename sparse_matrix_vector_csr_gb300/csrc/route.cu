@@ -133,12 +133,17 @@ __global__ void __launch_bounds__(kPlanThreads) k_route_place(int64_t entries, i
     }
     __syncthreads();
 
-    // exclusive scan of the padded segment lengths
+    // exclusive scan of the padded segment lengths (unsigned: a padded length is below 2^31, a length
+    // plus align - 1 need not be)
+    const auto padded = [&](int e) {
+        const uint32_t tile = static_cast<uint32_t>(align);
+        return static_cast<int32_t>((static_cast<uint32_t>(total[e]) + tile - 1) / tile * tile);
+    };
     const int per = (experts + kPlanThreads - 1) / kPlanThreads;
     int32_t mine = 0;
     for (int i = 0; i < per; ++i) {
         const int e = tid * per + i;
-        if (e < experts) mine += (total[e] + align - 1) / align * align;
+        if (e < experts) mine += padded(e);
     }
     int32_t incl = mine;
 #pragma unroll
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_route_place(int64_t entries, i
         if (e < experts) {
             start[e] = at;
             if (blockIdx.x == 0) offsets[e] = at;
-            at += (total[e] + align - 1) / align * align;
+            at += padded(e);
             if (blockIdx.x == 0 && e == experts - 1) offsets[experts] = at;
         }
     }
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_route_place(int64_t entries, i
     const int n_cta = gridDim.x;
     for (int e = blockIdx.x * (kPlanThreads / 32) + warp; e < experts; e += n_cta * (kPlanThreads / 32)) {
         const int64_t a = static_cast<int64_t>(start[e]) + total[e];
-        const int64_t b = start[e] + (static_cast<int64_t>(total[e]) + align - 1) / align * align;
+        const int64_t b = static_cast<int64_t>(start[e]) + padded(e);
         for (int64_t s = a + lane; s < b; s += 32) sources[s] = -1;
     }
     for (int64_t s = used + static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; s < rows;

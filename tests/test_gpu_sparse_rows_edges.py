@@ -70,3 +70,13 @@ def test_route_plan_at_the_shared_memory_limit(spmv, tokens, k, experts):
     run = subprocess.run([sys.executable, "-c", PLAN, str(tokens), str(k), str(experts)], cwd=ROOT, timeout=300,
                          capture_output=True, text=True)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_route_plan_of_nearly_2_to_the_31_entries(spmv):
+    """One expert has them all, and its segment's end, rounded up to whole tiles, passes 2^31 on the way."""
+    m = 2 ** 31 - 2  # a multiple of 3; m + 2 is 2^31
+    plan = spmv.RoutePlan(torch.zeros(m, 1, dtype=torch.int32, device="cuda"), 1, align=3)
+    assert plan.rows == m and plan.offsets.tolist() == [0, m]
+    for a in range(0, m, 1 << 28):
+        want = torch.arange(a, min(m, a + (1 << 28)), dtype=torch.int32, device="cuda")
+        assert torch.equal(plan.slots[a:a + len(want), 0], want) and torch.equal(plan.sources[a:a + len(want)], want)
