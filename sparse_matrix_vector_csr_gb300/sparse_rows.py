@@ -151,9 +151,10 @@ def _plan_sizes(tokens, k, experts, align):
 class RoutePlan:
     """Rows sorted by expert: the plan of one choice ``ids`` (int32, tokens x k; an entry
     outside [0, experts) is dropped).  ``rows`` is the sorted matrix's number of rows;
-    ``offsets`` (experts + 1), ``slots`` (tokens x k) and ``sources`` (rows) as in spmv.h."""
+    ``offsets`` (experts + 1), ``slots`` (tokens x k) and ``sources`` (rows) as in spmv.h.
+    Every call takes the tensors that these attributes have by then."""
 
-    __slots__ = ("tokens", "k", "experts", "align", "rows", "offsets", "slots", "sources", "_slots", "_sources")
+    __slots__ = ("tokens", "k", "experts", "align", "rows", "offsets", "slots", "sources", "_known")
 
     def __init__(self, ids, experts, align=1, stream=None):
         if stream is not None:
@@ -169,10 +170,19 @@ class RoutePlan:
         self.offsets = _empty((experts + 1,), dtype=_I32, device=device)
         self.slots = _empty((tokens, k), dtype=_I32, device=device)
         self.sources = _empty((self.rows,), dtype=_I32, device=device)
+        self._known = self.slots, self.sources
         space = _empty((work,), dtype=torch.uint8, device=device) if work else None
-        self._slots, self._sources = self.slots.data_ptr(), self.sources.data_ptr()
-        _check(lib.spmv_route_plan(tokens, k, experts, align, ptr, self.offsets.data_ptr(), self._slots, self._sources,
+        _check(lib.spmv_route_plan(tokens, k, experts, align, ptr, self.offsets.data_ptr(), *self._pointers(),
                                    space.data_ptr() if work else None, work, _current(ids)))
+
+    def _pointers(self):
+        """Addresses of slots and sources, which are checked where they are not the last call's."""
+        slots, sources = self.slots, self.sources
+        if slots is not self._known[0] or sources is not self._known[1]:
+            _plain(slots, "slots", (self.tokens, self.k), _I32)
+            _plain(sources, "sources", (self.rows,), _I32)
+            self._known = slots, sources
+        return slots.data_ptr(), sources.data_ptr()
 
     def dispatch(self, x, out=None, stream=None):
         """The tokens' rows sorted by expert (rows x d); rows without a source are 0."""
@@ -182,7 +192,7 @@ class RoutePlan:
         code, ldx = _matrix(x, "x", self.tokens)
         d = x.shape[1]
         xs, ldxs = _out(out, "out", x, self.rows, d)
-        _check(lib.spmv_route_dispatch(self.tokens, self.k, self.rows, d, self._slots, self._sources, x.data_ptr(), ldx,
+        _check(lib.spmv_route_dispatch(self.tokens, self.k, self.rows, d, *self._pointers(), x.data_ptr(), ldx,
                                        xs.data_ptr(), ldxs, code, _current(x)))
         return xs
 
@@ -193,9 +203,10 @@ class RoutePlan:
                 return self.combine(ys, weights, out)
         code, ldys = _matrix(ys, "ys", self.rows)
         d = ys.shape[1]
+        slots, _ = self._pointers()
         w = None if weights is None else _plain(weights, "weights", (self.tokens, self.k), _F32)
         y, ldy = _out(out, "out", ys, self.tokens, d)
-        _check(lib.spmv_route_combine(self.tokens, self.k, self.rows, d, self._slots, w, ys.data_ptr(), ldys,
+        _check(lib.spmv_route_combine(self.tokens, self.k, self.rows, d, slots, w, ys.data_ptr(), ldys,
                                       y.data_ptr(), ldy, code, _current(ys)))
         return y
 
@@ -210,7 +221,7 @@ class RoutePlan:
         w = _plain(weights, "weights", (self.tokens, self.k), _F32)
         dys, lddys = _out(out, "out", dy, self.rows, d)
         dw = _empty((self.tokens, self.k), dtype=_F32, device=dy.device)
-        _check(lib.spmv_route_combine_grad(self.tokens, self.k, self.rows, d, self._slots, self._sources, w,
+        _check(lib.spmv_route_combine_grad(self.tokens, self.k, self.rows, d, *self._pointers(), w,
                                            dy.data_ptr(), lddy, ys.data_ptr(), ldys, dys.data_ptr(), lddys,
                                            dw.data_ptr(), code, _current(dy)))
         return dys, dw
