@@ -604,8 +604,9 @@ SPMV_API int spmv_topk_rows(int64_t rows, int64_t n, int32_t k, const void *x, i
 /*
  * The gradient of spmv_topk_rows' weights (the choice itself has none): with dweights the
  * loss's gradient in the weights, dx (rows x n, of type `dtype`, overwritten) is its gradient
- * in x.  ids and weights are the forward call's.  weighting ROW also reads x and the forward
- * call's lse; with SELECTED they may be NULL.
+ * in x.  ids and weights are the forward call's.  weighting ROW also reads x; with SELECTED it
+ * may be NULL.  lse is not read (the shares of a row come from its largest entry and that entry's
+ * weight) and may be NULL.
  */
 SPMV_API int spmv_topk_rows_grad(int64_t rows, int64_t n, int32_t k, const int32_t *ids, const float *weights,
                                  const float *dweights, int weighting, double temperature, const void *x,

@@ -27,17 +27,26 @@ def topk_row(x, k):
     return ids, vals
 
 
+def shares(x, tau):
+    """Softmax of x / tau, by differences to the maximum (a log-sum of values near 1e38 would absorb
+    how many there are); 0 where nothing is above -inf."""
+    x = np.asarray(x, np.float64)
+    m = x.max(initial=NEG_INF)
+    e = np.exp((x - m) / tau) if m != NEG_INF else np.zeros(len(x))
+    return e / e.sum() if m != NEG_INF else e
+
+
 def top_weights(x, ids, vals, weighting, tau):
     """Softmax weights of the chosen entries, over the chosen or over the row."""
-    norm = lse(vals / tau) if weighting == "selected" else lse(np.asarray(x, np.float64) / tau)
-    return np.array([0.0 if i < 0 else np.exp(v / tau - norm) for i, v in zip(ids, vals)])
+    q = shares(vals, tau) if weighting == "selected" else shares(x, tau)[ids]
+    return np.array([0.0 if i < 0 else p for i, p in zip(ids, q)])
 
 
 def top_weights_grad(x, ids, weights, dweights, weighting, tau):
     """Gradient in x of <dweights, weights>, from the softmax's Jacobian, written out."""
     x = np.asarray(x, np.float64)
     dx = np.zeros(len(x))
-    norm = lse(x / tau)
+    q = shares(x, tau)
     chosen = [j for j, i in enumerate(ids) if i >= 0]
     for j in chosen:  # d w_j / d x_i = w_j ([i = id_j] - p_i) / tau
         dx[ids[j]] += dweights[j] * weights[j] / tau
@@ -45,7 +54,7 @@ def top_weights_grad(x, ids, weights, dweights, weighting, tau):
             for i in chosen:
                 dx[ids[i]] -= dweights[j] * weights[j] * weights[i] / tau
         else:
-            dx -= dweights[j] * weights[j] * np.exp(x / tau - norm) / tau
+            dx -= dweights[j] * weights[j] * q / tau
     return dx
 
 

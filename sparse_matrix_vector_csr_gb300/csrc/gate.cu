@@ -223,8 +223,12 @@ __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
     }
 #pragma unroll
     for (int d = 1; d < kLanes; d *= 2) s += from_lane_away(s, d);
-    // a row of nothing but -inf has an lse of -inf: 0 everywhere
-    const float lse = whole_row && there && a.lse[r] != kNegInf ? a.lse[r] : 0.0f, factor = -s * a.inv_temperature;
+    // (a row without entries has nothing above -inf: 0 everywhere)
+    const int32_t first = __shfl_sync(0xffffffffu, id[0], 0, kLanes);
+    const float w0 = __shfl_sync(0xffffffffu, w[0], 0, kLanes);
+    const bool some = whole_row && first >= 0 && first < a.n;
+    const RowShare q{some ? to_f32(x[first]) : 0.0f, some ? w0 * (-s * a.inv_temperature) : 0.0f,
+                     a.inv_temperature * kLog2e};
     for (int v0 = 0; v0 < share.count; v0 += kV * kLanes) {
         if (v0 && whole_row) load_share<T, kV>(share, v0 + lane, kLanes, vec);
 #pragma unroll
@@ -232,16 +236,15 @@ __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
             const int v = v0 + i * kLanes + lane;
             if (v < share.count) {
                 uint4 o = splat<T>(0.0f);
-                if (whole_row) {
+                if (some) {
                     float f[kN];
                     unpack<T>(vec[i], f);
 #pragma unroll
-                    for (int q = 0; q < kN; q += 2) {
-                        float2 d = fma2(make_float2(f[q], f[q + 1]), both(a.inv_temperature), both(-lse));
-                        d = mul2(d, both(kLog2e));
-                        d = mul2(make_float2(ex2(d.x), ex2(d.y)), both(factor));
-                        f[q] = d.x;
-                        f[q + 1] = d.y;
+                    for (int j = 0; j < kN; j += 2) {
+                        float2 d = mul2(add2(make_float2(f[j], f[j + 1]), both(-q.x0)), both(q.scale));
+                        d = mul2(make_float2(ex2(d.x), ex2(d.y)), both(q.w0));
+                        f[j] = d.x;
+                        f[j + 1] = d.y;
                     }
                     o = pack<T>(f);
                 }

@@ -467,8 +467,8 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
 // gradient of the weights
 // ----------------------------------------------------------------------------
 // With s = sum over j of w_j dw_j, both weightings give dx[id_j] = w_j (dw_j - s) / temperature;
-// elsewhere dx is 0 (weights over the chosen entries) or -q s / temperature with
-// q = exp(x / temperature - lse) (weights over the whole row).  A warp writes a piece of a
+// elsewhere dx is 0 (weights over the chosen entries) or -q s / temperature with q the softmax of
+// the row (weights over the whole row; see RowShare).  A warp writes a piece of a
 // row; __syncwarp orders its plain stores before the stores to the chosen columns.
 constexpr int kGradPiece = 1024;  // values per warp
 
@@ -490,18 +490,17 @@ __global__ void __launch_bounds__(256) k_topk_grad(TopGradArgs a) {
     s = warp_sum(s);
     const bool whole_row = a.weighting == SPMV_WEIGHTS_ROW;
     const T *x = static_cast<const T *>(a.x) + (whole_row ? r * a.ldx : 0);
-    const float lse = whole_row ? a.lse[r] : 0.0f;
-    const float factor = -s * a.inv_temperature;
+    // (a row without entries has nothing above -inf: 0 everywhere)
+    const bool some = whole_row && ids[0] >= 0 && ids[0] < a.n;
+    const RowShare q{some ? to_f32(x[ids[0]]) : 0.0f, some ? w[0] * (-s * a.inv_temperature) : 0.0f,
+                     a.inv_temperature * kLog2e};
     for (int v = lane; v < piece.count; v += 32) {
         float f[kN] = {};
-        if (whole_row) {
+        if (some) {
             const int64_t e = piece.first(v);
 #pragma unroll
             for (int i = 0; i < kN; ++i)
-                if (e + i >= 0 && e + i < a.n) {
-                    const float xi = to_f32(x[e + i]);
-                    f[i] = xi == kNegInf ? 0.0f : factor * ex2(fmaf(xi, a.inv_temperature, -lse) * kLog2e);
-                }
+                if (e + i >= 0 && e + i < a.n) f[i] = q.of(to_f32(x[e + i]));
         }
         piece.store(out, v, pack<T>(f), true);
     }
@@ -615,7 +614,7 @@ extern "C" SPMV_API int spmv_topk_rows_grad(int64_t rows, int64_t n, int32_t k, 
     SPMV_TRY(check_array(dx, "dx", vb));
     if (whole_row) {
         SPMV_TRY(check_array(x, "x", vb));
-        SPMV_TRY(check_array(lse, "lse", 4));
+        if (lse) SPMV_TRY(check_array(lse, "lse", 4));
     }
     const size_t out = span_bytes(rows, n, lddx, vb), m = static_cast<size_t>(rows) * k * 4;
     const struct { const void *p; size_t bytes; const char *name; } in[] = {
@@ -626,7 +625,7 @@ extern "C" SPMV_API int spmv_topk_rows_grad(int64_t rows, int64_t n, int32_t k, 
     // a row may start up to 15 bytes behind a 16-byte boundary: one vector more
     const int64_t pieces = ceil_div(n + 16 / vb - 1, kGradPiece);
     const TopGradArgs a{rows, n, ldx, lddx, pieces, k, weighting,
-                        static_cast<float>(1.0 / temperature), ids, weights, dweights, lse, x, dx};
+                        static_cast<float>(1.0 / temperature), ids, weights, dweights, x, dx};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (n <= kGateMaxN && k <= kGateMaxK) {
         SPMV_TRY_CUDA(launch_gate_grad(a, dtype, s));

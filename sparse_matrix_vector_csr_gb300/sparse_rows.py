@@ -98,19 +98,19 @@ class TopRows:
     def grad(self, dweights, out=None, stream=None):
         """The gradient in x of a loss whose gradient in the weights is ``dweights``."""
         if stream is not None:
-            with _on(stream, self._x, self.ids, self.weights, self.lse, dweights, out):
+            with _on(stream, self._x, self.ids, self.weights, dweights, out):
                 return self.grad(dweights, out)
         if not self._weighting:
             raise ValueError("topk_rows was called without weights")
-        x, ids, lse = self._x, self.ids, self.lse
+        x, ids = self._x, self.ids
         rows, k = ids.shape
         n = x.shape[1]
         code, ldx = _matrix(x, "x")
         dw = _plain(dweights, "dweights", ids.shape, _F32)
         dx, lddx = _out(out, "out", x, rows, n)
         _check(lib.spmv_topk_rows_grad(rows, n, k, ids.data_ptr(), self.weights.data_ptr(), dw, self._weighting,
-                                       self._temperature, x.data_ptr(), ldx, None if lse is None else lse.data_ptr(),
-                                       dx.data_ptr(), lddx, code, _current(x)))
+                                       self._temperature, x.data_ptr(), ldx, None, dx.data_ptr(), lddx, code,
+                                       _current(x)))
         return dx
 
 
@@ -133,7 +133,7 @@ def topk_rows(x, k, temperature=1.0, weights=None, lse=False, vals=None, stream=
     top.ids = _empty((rows, k), dtype=_I32, device=device)
     top.vals = _empty((rows, k), dtype=_F32, device=device) if vals or (vals is None and not weighting) else None
     top.weights = _empty((rows, k), dtype=_F32, device=device) if weighting else None
-    # the gradient of weights over the row needs lse too
+    # (weights over the row come with it)
     top.lse = _empty((rows,), dtype=_F32, device=device) if lse or weighting == 2 else None
     _check(lib.spmv_topk_rows(rows, n, k, x.data_ptr(), ldx, code, temperature, weighting, top.ids.data_ptr(),
                               None if top.vals is None else top.vals.data_ptr(),

@@ -80,3 +80,52 @@ def test_route_plan_of_nearly_2_to_the_31_entries(spmv):
     for a in range(0, m, 1 << 28):
         want = torch.arange(a, min(m, a + (1 << 28)), dtype=torch.int32, device="cuda")
         assert torch.equal(plan.slots[a:a + len(want), 0], want) and torch.equal(plan.sources[a:a + len(want)], want)
+
+
+# --------------------------------------------------------------------------- #
+# the k largest entries of each row
+# --------------------------------------------------------------------------- #
+
+
+def check_weights_grad(spmv, x, k, weighting, tau, seed):
+    """dx against the softmax's Jacobian in 64 bits, from differences to the row's maximum."""
+    rows, n = x.shape
+    top = spmv.topk_rows(x, k, temperature=tau, weights=weighting)
+    dw = torch.randn(rows, k, generator=gen(seed)).cuda()
+    got, ids, d = f64(top.grad(dw)), top.ids.cpu().numpy(), f64(dw)
+    for r, row in enumerate(f64(x)):
+        cols, dj = ids[r][ids[r] >= 0], d[r][ids[r] >= 0]
+        assert len(cols) == min(k, int((row > -np.inf).sum()))
+        share = np.zeros(n)
+        over = cols if weighting == "selected" else np.flatnonzero(row > -np.inf)
+        if len(cols):
+            share[over] = np.exp((row[over] - row.max()) / tau)
+            share /= share.sum()
+        dot = (share[cols] * dj).sum()
+        want = -share * dot
+        want[cols] += share[cols] * dj
+        size = share * np.abs(share[cols] * dj).sum()
+        size[cols] += np.abs(share[cols] * dj)
+        # an exponential's argument is a difference, rounded relative to itself; weights and sums: 2 SUM each
+        np.testing.assert_array_less(np.abs(got[r] - want / tau),
+                                     4 * SUM * size / tau + H[x.dtype] * np.abs(want) / tau + TINY[x.dtype])
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("weighting", ["row", "selected"])
+@pytest.mark.parametrize("tau", [0.7, 1.0, 2.0])
+@pytest.mark.parametrize("n,k", [(40, 3), (300, 16), (512, 5), (40, 20), (700, 3), (5000, 40)])
+def test_weights_gradient_of_lowest_values_and_far_from_0(spmv, dtype, weighting, tau, n, k):
+    low = torch.finfo(dtype).min
+    x = torch.randn(8, n, generator=gen(n)) * 2
+    x[0] = low                    # wholly masked by the lowest value: n equal shares
+    x[1] = low
+    x[1, n // 3] = 1.0            # one column left
+    x[2, n // 2:] = low
+    x[3] += 1e4                   # ordinary differences, far from 0
+    x[4] -= 1e4
+    x[5, ::2] = -math.inf
+    x[5, 1::2] = low              # both masks
+    x[6] = -math.inf
+    x[7] = -3e4 if dtype == torch.float16 else -1e30
+    check_weights_grad(spmv, x.to(dtype).cuda(), k, weighting, tau, n + k)
