@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
             id[t] = a.ids[r * a.k + j];
             w[t] = a.weights[r * a.k + j];
             dw[t] = a.dweights[r * a.k + j];
+            if (id[t] >= a.n) id[t] = -1;  // outside: no entry
             if (id[t] >= 0) s = fmaf(w[t], dw[t], s);
         }
     }
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
     // (a row without entries has nothing above -inf: 0 everywhere)
     const int32_t first = __shfl_sync(0xffffffffu, id[0], 0, kLanes);
     const float w0 = __shfl_sync(0xffffffffu, w[0], 0, kLanes);
-    const bool some = whole_row && first >= 0 && first < a.n;
+    const bool some = whole_row && first >= 0;
     const RowShare q{some ? to_f32(x[first]) : 0.0f, some ? w0 * (-s * a.inv_temperature) : 0.0f,
                      a.inv_temperature * kLog2e};
     for (int v0 = 0; v0 < share.count; v0 += kV * kLanes) {
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
     __syncwarp();
 #pragma unroll
     for (int t = 0; t < kMine; ++t)
-        if (id[t] >= 0 && id[t] < a.n) out[id[t]] = from_f32<T>(w[t] * (dw[t] - s) * a.inv_temperature);
+        if (id[t] >= 0) out[id[t]] = from_f32<T>(w[t] * (dw[t] - s) * a.inv_temperature);
 }
 
 template <typename T, int kV>

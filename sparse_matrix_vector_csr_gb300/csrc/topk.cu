@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(256) k_topk_grad(TopGradArgs a) {
     const float *w = a.weights + r * a.k, *dw = a.dweights + r * a.k;
     float s = 0.0f;
     for (int j = lane; j < a.k; j += 32)
-        if (ids[j] >= 0) s = fmaf(w[j], dw[j], s);
+        if (ids[j] >= 0 && ids[j] < a.n) s = fmaf(w[j], dw[j], s);
     s = warp_sum(s);
     const bool whole_row = a.weighting == SPMV_WEIGHTS_ROW;
     const T *x = static_cast<const T *>(a.x) + (whole_row ? r * a.ldx : 0);

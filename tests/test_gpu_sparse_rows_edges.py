@@ -129,3 +129,21 @@ def test_weights_gradient_of_lowest_values_and_far_from_0(spmv, dtype, weighting
     x[6] = -math.inf
     x[7] = -3e4 if dtype == torch.float16 else -1e30
     check_weights_grad(spmv, x.to(dtype).cuda(), k, weighting, tau, n + k)
+
+
+@pytest.mark.parametrize("weighting", [1, 2])
+@pytest.mark.parametrize("n,k", [(40, 6), (40, 20), (700, 6)])
+def test_weights_gradient_leaves_out_columns_outside(spmv, weighting, n, k):
+    """An entry whose column is n or more is no entry, as one of -1 is none: its weight enters nothing."""
+    g = gen(n)
+    x = torch.randn(3, n, generator=g).cuda()
+    ids, lse = (torch.empty(s, dtype=t, device="cuda") for s, t in (((3, k), torch.int32), ((3,), torch.float32)))
+    w, dw = torch.empty(3, k, device="cuda"), torch.randn(3, k, generator=g).cuda()
+    spmv.spmv_topk_rows(3, n, k, x, n, 1, 1.0, weighting, ids, None, w, lse)
+    got = []
+    for outside in (-1, n, 2 ** 31 - 1):
+        ids[:, 2], ids[1, 4] = outside, outside
+        dx = torch.full_like(x, math.nan)
+        spmv.spmv_topk_rows_grad(3, n, k, ids, w, dw, weighting, 1.0, x, n, lse, dx, n, 1)
+        got.append(dx)
+    assert torch.isfinite(got[0]).all() and torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
