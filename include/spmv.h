@@ -594,7 +594,8 @@ typedef enum { SPMV_WEIGHTS_NONE = 0, SPMV_WEIGHTS_SELECTED = 1, SPMV_WEIGHTS_RO
  *   weights   float[rows][k] (weighting not NONE): exp(v / temperature) over the sum of the
  *             chosen entries' (SELECTED) or of the whole row's (ROW); 0 beside an id of -1.
  *   lse       float[rows], or NULL: log of the sum of exp(x / temperature) over the row
- *             (-inf for a row without an entry above -inf).
+ *             (-inf for a row without an entry above -inf, +inf for one with a +inf and no NaN;
+ *             the weights over such a row, or over entries with a +inf, are NaN).
  *   temperature  in [1e-6, 1e6].
  */
 SPMV_API int spmv_topk_rows(int64_t rows, int64_t n, int32_t k, const void *x, int64_t ldx, int dtype,

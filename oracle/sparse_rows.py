@@ -8,10 +8,10 @@ NEG_INF = -np.inf
 
 
 def lse(x):
-    """log sum exp, -inf for nothing above -inf."""
+    """log sum exp, -inf for nothing above -inf, +inf for a +inf, NaN for a NaN."""
     x = np.asarray(x, np.float64)
     m = x.max(initial=NEG_INF)
-    return m if m == NEG_INF else m + np.log(np.exp(x - m).sum())
+    return m if not np.isfinite(m) else m + np.log(np.exp(x - m).sum())
 
 
 def topk_row(x, k):
@@ -32,8 +32,11 @@ def shares(x, tau):
     how many there are); 0 where nothing is above -inf."""
     x = np.asarray(x, np.float64)
     m = x.max(initial=NEG_INF)
-    e = np.exp((x - m) / tau) if m != NEG_INF else np.zeros(len(x))
-    return e / e.sum() if m != NEG_INF else e
+    if m == NEG_INF:
+        return np.zeros(len(x))
+    with np.errstate(invalid="ignore"):  # of a row with +inf or a NaN: NaN
+        e = np.exp((x - m) / tau)
+    return e / e.sum()
 
 
 def top_weights(x, ids, vals, weighting, tau):

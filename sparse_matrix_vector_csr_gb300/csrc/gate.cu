@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) k_gate(TopArgs a) {
         if (m_lane != kNegInf) sum *= ex2((m_lane - m) * a.scale);
 #pragma unroll
         for (int d = 1; d < kLanes; d *= 2) sum += from_lane_away(sum, d);
-        if (a.lse && lane == 0 && there) a.lse[r] = Key<T>::some(best[0]) ? fmaf(m, a.inv_temperature, logf(sum)) : kNegInf;
+        if (a.lse && lane == 0 && there) a.lse[r] = Key<T>::some(best[0]) ? log_sum(m, sum, a.inv_temperature) : kNegInf;
     }
     // entries lane, lane + kLanes, ... of the row are this lane's
     constexpr int kMine = (kK + kLanes - 1) / kLanes;

@@ -399,6 +399,11 @@ struct Running {
 // The reference point of a sum of exponentials: the maximum, or 0 if nothing is above -inf
 // (so that -inf - m is -inf and never NaN).
 __device__ __forceinline__ float reference_of(float m) { return m == kNegInf ? 0.0f : m; }
+// The log of a row's sum of exponentials from its reference point and its sum relative to that; +inf
+// where the row's largest value is (whose difference from itself makes the relative sum a NaN).
+__device__ __forceinline__ float log_sum(float m, float sum, float inv_temperature) {
+    return m == INFINITY ? INFINITY : fmaf(m, inv_temperature, logf(sum));
+}
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(256) k_topk_warp(TopArgs a) {
         a.ids[row * a.k + lane] = my_id;
         if (a.vals) a.vals[row * a.k + lane] = v;
     }
-    if (a.lse && lane == 0) a.lse[row] = fmaf(m, a.inv_temperature, logf(sum));
+    if (a.lse && lane == 0) a.lse[row] = log_sum(m, sum, a.inv_temperature);
 }
 
 // ----------------------------------------------------------------------------
@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     }
 
     // rank 0: the candidates in order, the row's sum (by the last warp)
+    const int n_cand = static_cast<int>(found < kMaxCand ? found : kMaxCand);
     if (warp == n_warps - 1 && want_lse) {
         float mm = kNegInf;
         for (int i = lane; i < n_warps * ctas; i += 32) mm = fmaxf(mm, sh.sums[i].x);
@@ -423,13 +424,17 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
             s += w.x == kNegInf ? w.y : w.y * ex2((w.x - mm) * a.scale);
         }
         s = warp_sum(s);
+        bool nan = false;  // mm has passed over NaNs; beside +inf one tells from the candidates, where it comes first
+        if (mm == INFINITY) {
+            for (int i = lane; i < n_cand; i += 32) nan |= sh.cand[i] >> 32 > order_key(INFINITY);
+            nan = __any_sync(0xffffffffu, nan);
+        }
         if (lane == 0) {
             sh.lse_m = mm;
             sh.lse_sum = s;
-            if (a.lse) a.lse[r] = fmaf(mm, a.inv_temperature, logf(s));
+            if (a.lse) a.lse[r] = nan ? s : log_sum(mm, s, a.inv_temperature);
         }
     }
-    const int n_cand = static_cast<int>(found < kMaxCand ? found : kMaxCand);
     for (int i = tid; i < n_cand; i += n_threads) {
         const unsigned long long c = sh.cand[i];
         int above = 0;

@@ -147,3 +147,25 @@ def test_weights_gradient_leaves_out_columns_outside(spmv, weighting, n, k):
         spmv.spmv_topk_rows_grad(3, n, k, ids, w, dw, weighting, 1.0, x, n, lse, dx, n, 1)
         got.append(dx)
     assert torch.isfinite(got[0]).all() and torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("n,k", [(40, 3), (512, 16), (40, 20), (600, 3), (3000, 8), (150000, 8)])
+def test_log_sum_of_a_row_with_infinity(spmv, dtype, n, k):
+    """The sum of exponentials is +inf, and so is its log; with a NaN beside it, NaN."""
+    x = torch.randn(6, n, generator=gen(n))
+    x[0, n // 2] = math.inf
+    x[1] = math.inf
+    x[2, [1, n - 1]] = math.inf
+    x[2, 3:n - 3] = -math.inf
+    x[3, 5], x[3, n - 2] = math.inf, math.nan
+    x[4, n - 1] = math.nan
+    x = x.to(dtype).cuda()
+    for tau in (0.5, 1.0, 3.0):
+        top = spmv.topk_rows(x, k, temperature=tau, lse=True)
+        lse = f64(top.lse)
+        assert (lse[:3] == math.inf).all() and np.isnan(lse[3:5]).all() and np.isfinite(lse[5])
+        assert top.ids[:3, 0].tolist() == [n // 2, 0, 1]
+        with np.errstate(invalid="ignore"):
+            want = [ref.lse(row / tau) for row in f64(x)]
+        np.testing.assert_array_equal(lse[:5], want[:5])
