@@ -666,8 +666,9 @@ SPMV_API int spmv_route_combine_grad(int64_t tokens, int32_t k, int64_t rows, in
  *       the other columns count as one class, of probability r = max(0, 1 - sum p_j) for the
  *       teacher and 1 - sum q_j for the student (summed over those columns, not subtracted):
  *       loss[t] = sum p_j (log p_j - log q_j) + r (log r - log(1 - sum q_j)).
- *       Where every other column of z is -inf, an r below 1e-5 is rounding and counts as 0;
- *       a larger one makes the loss +inf, and the gradient is 0 in those columns.
+ *       Where every other column of z is -inf, or so low that their mass is 0 in 32 bits (the
+ *       type's lowest value), an r below 1e-5 is rounding and counts as 0.  Beside -inf a larger
+ *       one makes the loss +inf, and the gradient is 0 in those columns.
  * A row without entries (padding, say) has loss 0 and gradient 0, whatever z holds.  A teacher
  * logit of -inf has p = 0.  The loss is not scaled: neither by temperature^2 nor to a mean.
  *   k 1..512 (k may exceed vocab only by absent entries), vocab 1..2^22, temperature in

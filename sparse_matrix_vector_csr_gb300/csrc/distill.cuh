@@ -28,7 +28,8 @@ namespace rows {
 constexpr int kMaxEntries = 512;
 constexpr int64_t kMaxVocab = int64_t(1) << 22;
 // A remainder of the teacher's mass below this is the rounding of 32-bit logits and of lse; it
-// only matters where the student has no mass on the other columns at all, and counts as 0 there.
+// only matters where the student's mass on the other columns is 0 in 32 bits (masked by -inf or by the
+// type's lowest value: 1e-7 of 1e38 would be the loss), and counts as 0 there (see rest_of).
 constexpr float kRestRounding = 1e-5f;
 
 enum DistillMode { kLoss = 0, kLossGrad = 1, kGrad = 2 };
@@ -227,6 +228,12 @@ __device__ __forceinline__ RowSums join_two(const DistillArgs &a, float m_rest, 
     return s;
 }
 
+// The remainder that counts.  A rest_sum is relative to m_rest, so it is 0 under a mask of -inf alone.
+__device__ __forceinline__ float rest_of(const DistillArgs &a, const EntryScalars &sc, const RowSums &s) {
+    const bool none = s.rest_sum == 0.0f || ex2((s.m_rest - s.m) * a.scale2) == 0.0f;
+    return sc.rest < kRestRounding && none ? 0.0f : sc.rest;
+}
+
 // What a row's gradient takes of it: q_i = inv_sum exp((z_i - m) / T) at the entries (less p_i), and
 // elsewhere other exp((z_i - ref) / T): q_i, and with lse q_i - r q'_i, q' the softmax over the
 // other columns.  All factors 0: no target, no gradient.  The loss leaves it for a gradient
@@ -240,7 +247,7 @@ struct RowFactors {
         other = inv_sum = 1.0f / s.sum;
         if (a.teacher_lse) {
             ref = s.m_rest;
-            other = s.rest_sum != 0.0f ? ex2((s.m_rest - s.m) * a.scale2) / s.sum - sc.rest / s.rest_sum : 0.0f;
+            other = s.rest_sum != 0.0f ? ex2((s.m_rest - s.m) * a.scale2) / s.sum - rest_of(a, sc, s) / s.rest_sum : 0.0f;
         }
     }
     __device__ __forceinline__ bool live() const { return inv_sum != 0.0f || other != 0.0f; }
@@ -263,8 +270,9 @@ __device__ __forceinline__ void write_loss(const DistillArgs &a, int64_t r, cons
     if (lane == 0) {
         const float log_sum = logf(s.sum);
         float loss = sc.entropy - cross * a.inv_temperature + sc.mass * log_sum;
-        if (sc.rest > 0.0f && !(sc.rest < kRestRounding && s.rest_sum == 0.0f))
-            loss += sc.rest * (logf(sc.rest) - logf(s.rest_sum) + log_sum + (s.m - s.m_rest) * a.inv_temperature);
+        const float rest = rest_of(a, sc, s);
+        if (rest > 0.0f)  // (the distance times rest first: a mask's may be near the largest float)
+            loss += rest * (logf(rest) - logf(s.rest_sum) + log_sum) + rest * (s.m - s.m_rest) * a.inv_temperature;
         a.loss[r] = sc.valid ? loss : 0.0f;
         if (a.stats) {
             const RowFactors f(a, sc, s);

@@ -169,3 +169,46 @@ def test_log_sum_of_a_row_with_infinity(spmv, dtype, n, k):
         with np.errstate(invalid="ignore"):
             want = [ref.lse(row / tau) for row in f64(x)]
         np.testing.assert_array_equal(lse[:5], want[:5])
+
+
+# --------------------------------------------------------------------------- #
+# distillation
+# --------------------------------------------------------------------------- #
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows", [3, 1300])
+@pytest.mark.parametrize("vocab", [24, 9000])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 2.0])
+def test_distill_remainder_where_the_others_are_lowest(spmv, dtype, rows, vocab, tau):
+    """The student has the teacher's logits and every other column masked by the type's lowest value.  A
+    remainder that is the rounding of lse counts as 0, as it does beside a mask of -inf: no loss, no gradient.
+    A real one meets the logits that are there, and overflows no sooner than the loss itself."""
+    k = 20
+    ids = torch.arange(k, dtype=torch.int32).repeat(rows, 1) + 2
+    low = torch.finfo(dtype).min
+    z = torch.full((rows, vocab), low)
+    z[:, 2:2 + k] = torch.linspace(0, 2, k).to(dtype).float()
+    z = z.to(dtype).cuda()
+    teacher = z[:, 2:2 + k].float()
+    args = (z, ids.cuda(), teacher.contiguous())
+    full = torch.logsumexp(teacher.double() / tau, 1)
+    for extra in (2e-6, 0.1):
+        lse = (full + extra).float()
+        loss, dz = spmv.distill_loss_grad(*args, teacher_lse=lse, temperature=tau)
+        res = spmv.distill_loss(*args, teacher_lse=lse, temperature=tau)
+        rest = -math.expm1(-extra)
+        for got_loss, got in ((loss, dz), (res.loss, res.grad())):
+            if extra < 1e-5:
+                # p and q agree to the rounding of lse (2^-23 of it, and 2e-6), the loss is of their first order
+                assert got_loss.abs().max() <= 1e-5 + SUM
+                assert not got[:, :2].any() and not got[:, 2 + k:].any()
+                assert got.float().abs().max() <= (1e-5 + SUM) / tau
+                continue
+            # rest, from 32 bits, to 1e-5 of 0.1
+            want = rest * (2.0 - float(low)) / tau
+            got = f64(got)
+            assert np.abs(f64(got_loss) / want - 1).max() <= 1e-3
+            others = np.delete(got, np.arange(2, 2 + k), 1)
+            size = rest / (vocab - k) / tau
+            assert np.abs(others + size).max() <= (1e-3 + H[dtype]) * size + TINY[dtype]
