@@ -12,7 +12,9 @@
 
 Every function takes CUDA tensors, enqueues on the current (or given) stream and returns
 without waiting.  Results are allocated on that stream.  Gradients are functions of their
-own; nothing is recorded by autograd.  The semantics are those of ``include/spmv.h``.
+own; nothing is recorded by autograd.  They read the forward call's inputs and results again, where
+no in-place change is noticed: a new tensor for scaled weights, no ``top.weights.mul_``.  The
+semantics are those of ``include/spmv.h``.
 """
 from __future__ import annotations
 
@@ -93,22 +95,24 @@ class TopRows:
     """The k largest entries of every row of ``x``: ``ids`` (int32, -1 = none), and, where asked
     for, ``vals``, ``weights`` and ``lse`` (float32)."""
 
-    __slots__ = ("ids", "vals", "weights", "lse", "_x", "_weighting", "_temperature")
+    __slots__ = ("ids", "vals", "weights", "lse", "_x", "_ids", "_weights", "_weighting", "_temperature")
 
     def grad(self, dweights, out=None, stream=None):
-        """The gradient in x of a loss whose gradient in the weights is ``dweights``."""
+        """The gradient in x of a loss whose gradient in the weights is ``dweights``: the weights that
+        topk_rows gave, whatever tensors the attributes have by then.  Neither they nor the ids may have been
+        changed in place, nor, with weights over the row, x."""
         if stream is not None:
-            with _on(stream, self._x, self.ids, self.weights, dweights, out):
+            with _on(stream, self._x, self._ids, self._weights, dweights, out):
                 return self.grad(dweights, out)
         if not self._weighting:
             raise ValueError("topk_rows was called without weights")
-        x, ids = self._x, self.ids
+        x, ids, weights = self._x, self._ids, self._weights
         rows, k = ids.shape
         n = x.shape[1]
         code, ldx = _matrix(x, "x")
         dw = _plain(dweights, "dweights", ids.shape, _F32)
         dx, lddx = _out(out, "out", x, rows, n)
-        _check(lib.spmv_topk_rows_grad(rows, n, k, ids.data_ptr(), self.weights.data_ptr(), dw, self._weighting,
+        _check(lib.spmv_topk_rows_grad(rows, n, k, ids.data_ptr(), weights.data_ptr(), dw, self._weighting,
                                        self._temperature, x.data_ptr(), ldx, None, dx.data_ptr(), lddx, code,
                                        _current(x)))
         return dx
@@ -139,6 +143,7 @@ def topk_rows(x, k, temperature=1.0, weights=None, lse=False, vals=None, stream=
                               None if top.vals is None else top.vals.data_ptr(),
                               top.weights.data_ptr() if weighting else None,
                               None if top.lse is None else top.lse.data_ptr(), _current(x)))
+    top._ids, top._weights = top.ids, top.weights
     return top
 
 
@@ -234,14 +239,16 @@ class RoutePlan:
 class DistillLoss:
     """``loss`` (float32, one a row, neither averaged nor scaled) and what its gradient needs."""
 
-    __slots__ = ("loss", "stats", "_args")
+    __slots__ = ("loss", "stats", "_args", "_stats")
 
     def grad(self, dloss=None, scale=1.0, out=None, stream=None):
         """scale * dloss[t] * d loss[t] / d z[t] (dloss float32, None = all 1).  ``out`` may be
-        the logits themselves, which the gradient then replaces."""
+        the logits themselves, which the gradient then replaces (it can be taken once).  Neither the
+        call's inputs nor ``stats`` may have been changed in place."""
         z, ids, teacher, lse, temperature = self._args
+        stats = self._stats
         if stream is not None:
-            with _on(stream, z, ids, teacher, lse, self.stats, dloss, out):
+            with _on(stream, z, ids, teacher, lse, stats, dloss, out):
                 return self.grad(dloss, scale, out)
         code, ldz = _matrix(z, "z")
         rows, vocab = z.shape
@@ -249,7 +256,7 @@ class DistillLoss:
         dz, lddz = _out(out, "out", z, rows, vocab)
         _check(lib.spmv_distill_grad(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, ids.data_ptr(),
                                      teacher.data_ptr(), _DTYPES[teacher.dtype],
-                                     None if lse is None else lse.data_ptr(), temperature, self.stats.data_ptr(), scale,
+                                     None if lse is None else lse.data_ptr(), temperature, stats.data_ptr(), scale,
                                      g, dz.data_ptr(), lddz, _current(z)))
         return dz
 
@@ -286,6 +293,7 @@ def distill_loss(z, ids, teacher, teacher_lse=None, temperature=1.0, stream=None
     res.stats = _empty((rows, 4), dtype=_F32, device=z.device)
     _check(lib.spmv_distill_loss(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, i, t, tcode, lse, temperature,
                                  res.loss.data_ptr(), res.stats.data_ptr(), _current(z)))
+    res._stats = res.stats
     return res
 
 

@@ -212,3 +212,31 @@ def test_distill_remainder_where_the_others_are_lowest(spmv, dtype, rows, vocab,
             others = np.delete(got, np.arange(2, 2 + k), 1)
             size = rest / (vocab - k) / tau
             assert np.abs(others + size).max() <= (1e-3 + H[dtype]) * size + TINY[dtype]
+
+
+# --------------------------------------------------------------------------- #
+# states between two calls
+# --------------------------------------------------------------------------- #
+
+
+def test_weights_gradient_is_that_of_the_weights_given(spmv):
+    """Other tensors in the attributes' place (scaled weights, dropped entries) change nothing."""
+    x = torch.randn(30, 64, generator=gen(5)).cuda()
+    dw = torch.randn(30, 4, generator=gen(6)).cuda()
+    for weighting in ("selected", "row"):
+        top = spmv.topk_rows(x, 4, weights=weighting)
+        want = top.grad(dw)
+        top.weights, top.ids, top.lse = top.weights * 2.5, top.ids[:2], None
+        assert torch.equal(top.grad(dw), want)
+        assert torch.equal(copy.deepcopy(top).grad(dw), want)
+
+
+def test_distill_gradient_is_that_of_the_loss_given(spmv):
+    z = torch.randn(30, 64, generator=gen(5)).cuda()
+    ids = torch.arange(4, dtype=torch.int32, device="cuda").repeat(30, 1)
+    teacher = torch.randn(30, 4, generator=gen(6)).cuda()
+    res = spmv.distill_loss(z, ids, teacher)
+    want = res.grad()
+    res.stats, res.loss = torch.zeros_like(res.stats), None
+    assert torch.equal(res.grad(), want)
+    assert torch.equal(copy.deepcopy(res).grad(), want)
