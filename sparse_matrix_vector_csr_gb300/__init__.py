@@ -14,6 +14,9 @@ anew at each step: a router's choice and the rows sorted by it (:func:`topk_rows
 """
 from __future__ import annotations
 
+import sys
+from importlib.util import find_spec
+
 from . import _abi
 from ._abi import (  # noqa: F401
     FORMATS,
@@ -59,10 +62,13 @@ from ._abi import (  # noqa: F401
     spmv_distill_loss_grad,
 )
 
-#: names of ``sparse_rows``, which needs torch and is imported with the first of them
+#: names of ``sparse_rows``, which needs torch and is imported with the first of them (by a star import
+#: too, so they are among its names only where torch is installed)
 _SPARSE_ROWS = ("TopRows", "RoutePlan", "DistillLoss", "topk_rows", "distill_loss", "distill_loss_grad")
 
-__all__ = ["SpmvMatrix", "SpmvError", "FORMATS", "ORDERINGS"] + list(_SPARSE_ROWS) + [n for n in _abi.EXPORTS]
+__all__ = ["SpmvMatrix", "SpmvError", "FORMATS", "ORDERINGS"] + [n for n in _abi.EXPORTS]
+if sys.modules.get("torch") or find_spec("torch"):
+    __all__ += _SPARSE_ROWS
 
 
 def __getattr__(name):

@@ -73,3 +73,22 @@ def test_a_plan_refuses_other_tensors_in_its_place(rows, name, value, error):
         plan.dispatch(torch.zeros(6, 8))
     with pytest.raises(error):
         plan.combine_grad(torch.zeros(6, 8), torch.zeros(plan.rows, 8), torch.zeros(6, 2))
+
+
+STAR = """
+import sys
+sys.modules["torch"] = None  # as where it is not installed
+from sparse_matrix_vector_csr_gb300 import *
+assert SpmvMatrix and spmv_apply and "topk_rows" not in globals()
+"""
+
+
+def test_star_import_without_torch(rows):
+    run = subprocess.run([sys.executable, "-c", STAR], cwd=ROOT, timeout=300, capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_star_import_has_the_sparse_rows(rows):
+    names = {}
+    exec("from sparse_matrix_vector_csr_gb300 import *", names)
+    assert all(n in names for n in ("topk_rows", "RoutePlan", "distill_loss", "SpmvMatrix", "spmv_apply"))
