@@ -171,6 +171,65 @@ def test_log_sum_of_a_row_with_infinity(spmv, dtype, n, k):
         np.testing.assert_array_equal(lse[:5], want[:5])
 
 
+def order_keys(x):
+    """(value's order, lowest column first) as one int64 a value; -inf below everything."""
+    f = x.float() + 0.0
+    bits = f.view(torch.int32)
+    bits = torch.where(bits < 0, bits ^ 0x7FFFFFFF, bits).to(torch.int64)
+    bits = torch.where(torch.isnan(f), torch.full_like(bits, 0x7F800001), bits)
+    return bits * (1 << 32) + (x.shape[1] - 1 - torch.arange(x.shape[1], device=x.device))
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows,n,k", [(620, 131077, 64), (620, 131077, 200), (613, 300001, 17)])
+def test_topk_of_many_long_rows(spmv, dtype, rows, n, k):
+    """Rows so long that several pieces share a maximum, in batches as a teacher's logits come in."""
+    x = torch.randn(rows, n, generator=torch.Generator(device="cuda").manual_seed(n + k), device="cuda").mul_(2).to(dtype)
+    size = x.element_size()
+    per_vec, threads = 16 // size, 256 if k <= 128 else 512
+    pieces = -(-(-(-(n + per_vec - 1) // per_vec)) // (threads * (16 // per_vec)))
+    per = 1
+    while -(-pieces // per) > 15:
+        per *= 2
+    assert per > 1
+    for r in range(0, 12):  # the largest entries at a slot's last piece, at the row's ends, behind one another
+        head = (x[r].data_ptr() % 16) // size
+        lo = 1 if head else 0
+        at = []
+        for j in range(k):
+            t, s = (37 * j + r) % threads, j % (pieces // per)
+            piece = s * per + (per - 1 if r % 2 == 0 else j % per)
+            vec = lo + t + (piece * (16 // per_vec) + j % (16 // per_vec)) * threads
+            at.append(vec * per_vec - head + (j % per_vec))
+        if r in (1, 2):
+            at = [0, n - 1, 1, n - 2] + at
+        if r == 3:
+            at = list(range(n - k, n))
+        if r == 4:
+            at = list(range(k))
+        at = torch.tensor([c for c in at if 0 <= c < n])
+        x[r, at] = (20 + torch.rand(len(at), generator=gen(r)) * 8).to(dtype).cuda()
+    x[12] = 1.0
+    x[13] = torch.arange(n, device="cuda").div(n)
+    x[14, :-3] = -math.inf
+    x[15, n // 2], x[15, n - 1] = math.nan, math.nan
+    x[16] = torch.finfo(dtype).min
+    top = spmv.topk_rows(x, k, lse=True)
+    for a in range(0, rows, 100):
+        part = x[a:a + 100]
+        cols = n - 1 - (order_keys(part).topk(k, dim=1).values & 0xFFFFFFFF)
+        vals = part.float().gather(1, cols)
+        cols = torch.where(vals == -math.inf, torch.full_like(cols, -1), cols)
+        assert torch.equal(top.ids[a:a + 100].long(), cols)
+        assert torch.equal(torch.nan_to_num(top.vals[a:a + 100], nan=7.0), torch.nan_to_num(vals, nan=7.0))
+        norm = torch.logsumexp(part.double(), 1)
+        near = (top.lse[a:a + 100].double() - norm).abs() <= SUM + 4 * E * norm.abs()
+        assert (near | torch.isnan(norm)).all() and torch.equal(torch.isnan(norm), torch.isnan(top.lse[a:a + 100]))
+    for r in (0, 3, 12, 14, 15, 100):
+        ids, vals = ref.topk_row(f64(x[r]), k)
+        assert np.array_equal(top.ids[r].cpu().numpy(), ids) and np.array_equal(f64(top.vals[r]), vals, equal_nan=True)
+
+
 # --------------------------------------------------------------------------- #
 # distillation
 # --------------------------------------------------------------------------- #
