@@ -413,7 +413,6 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
     }
 
     // rank 0: the candidates in order, the row's sum (by the last warp)
-    const int n_cand = static_cast<int>(found < kMaxCand ? found : kMaxCand);
     if (warp == n_warps - 1 && want_lse) {
         float mm = kNegInf;
         for (int i = lane; i < n_warps * ctas; i += 32) mm = fmaxf(mm, sh.sums[i].x);
@@ -424,17 +423,13 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
             s += w.x == kNegInf ? w.y : w.y * ex2((w.x - mm) * a.scale);
         }
         s = warp_sum(s);
-        bool nan = false;  // mm has passed over NaNs; beside +inf one tells from the candidates, where it comes first
-        if (mm == INFINITY) {
-            for (int i = lane; i < n_cand; i += 32) nan |= sh.cand[i] >> 32 > order_key(INFINITY);
-            nan = __any_sync(0xffffffffu, nan);
-        }
         if (lane == 0) {
             sh.lse_m = mm;
             sh.lse_sum = s;
-            if (a.lse) a.lse[r] = nan ? s : log_sum(mm, s, a.inv_temperature);
+            if (a.lse && s == s) a.lse[r] = fmaf(mm, a.inv_temperature, logf(s));
         }
     }
+    const int n_cand = static_cast<int>(found < kMaxCand ? found : kMaxCand);
     for (int i = tid; i < n_cand; i += n_threads) {
         const unsigned long long c = sh.cand[i];
         int above = 0;
@@ -444,6 +439,8 @@ __global__ void __launch_bounds__(512, 3) k_topk_row(TopArgs a, int log2_ctas, i
             sh.top_vals[above] = v;
             a.ids[r * a.k + above] = composite_col(c);
             if (a.vals) a.vals[r * a.k + above] = v;
+            // a sum that is NaN comes from the row's largest entry, and so does its log: +inf or NaN
+            if (above == 0 && !(v < INFINITY) && a.lse) a.lse[r] = v;
         }
     }
     for (int j = n_cand + tid; j < a.k; j += n_threads) {
