@@ -159,7 +159,8 @@ class RoutePlan:
     ``offsets`` (experts + 1), ``slots`` (tokens x k) and ``sources`` (rows) as in spmv.h.
     Every call takes the tensors that these attributes have by then."""
 
-    __slots__ = ("tokens", "k", "experts", "align", "rows", "offsets", "slots", "sources", "_known")
+    __slots__ = ("tokens", "k", "experts", "align", "rows", "offsets", "slots", "sources", "_known_slots",
+                 "_known_sources")
 
     def __init__(self, ids, experts, align=1, stream=None):
         if stream is not None:
@@ -173,32 +174,31 @@ class RoutePlan:
         self.rows, work = _plan_sizes(tokens, k, experts, align)
         device = ids.device
         self.offsets = _empty((experts + 1,), dtype=_I32, device=device)
-        self.slots = _empty((tokens, k), dtype=_I32, device=device)
-        self.sources = _empty((self.rows,), dtype=_I32, device=device)
-        self._known = self.slots, self.sources
+        self.slots = self._known_slots = slots = _empty((tokens, k), dtype=_I32, device=device)
+        self.sources = self._known_sources = sources = _empty((self.rows,), dtype=_I32, device=device)
         space = _empty((work,), dtype=torch.uint8, device=device) if work else None
-        _check(lib.spmv_route_plan(tokens, k, experts, align, ptr, self.offsets.data_ptr(), *self._pointers(),
-                                   space.data_ptr() if work else None, work, _current(ids)))
+        _check(lib.spmv_route_plan(tokens, k, experts, align, ptr, self.offsets.data_ptr(), slots.data_ptr(),
+                                   sources.data_ptr(), space.data_ptr() if work else None, work, _current(ids)))
 
-    def _pointers(self):
-        """Addresses of slots and sources, which are checked where they are not the last call's."""
-        slots, sources = self.slots, self.sources
-        if slots is not self._known[0] or sources is not self._known[1]:
-            _plain(slots, "slots", (self.tokens, self.k), _I32)
-            _plain(sources, "sources", (self.rows,), _I32)
-            self._known = slots, sources
-        return slots.data_ptr(), sources.data_ptr()
+    def _check_tensors(self):
+        """The tensors that slots and sources have by now, where they are not the last call's."""
+        _plain(self.slots, "slots", (self.tokens, self.k), _I32)
+        _plain(self.sources, "sources", (self.rows,), _I32)
+        self._known_slots, self._known_sources = self.slots, self.sources
 
     def dispatch(self, x, out=None, stream=None):
         """The tokens' rows sorted by expert (rows x d); rows without a source are 0."""
         if stream is not None:
             with _on(stream, self.slots, self.sources, x, out):
                 return self.dispatch(x, out)
+        slots, sources = self.slots, self.sources
+        if slots is not self._known_slots or sources is not self._known_sources:
+            self._check_tensors()
         code, ldx = _matrix(x, "x", self.tokens)
         d = x.shape[1]
         xs, ldxs = _out(out, "out", x, self.rows, d)
-        _check(lib.spmv_route_dispatch(self.tokens, self.k, self.rows, d, *self._pointers(), x.data_ptr(), ldx,
-                                       xs.data_ptr(), ldxs, code, _current(x)))
+        _check(lib.spmv_route_dispatch(self.tokens, self.k, self.rows, d, slots.data_ptr(), sources.data_ptr(),
+                                       x.data_ptr(), ldx, xs.data_ptr(), ldxs, code, _current(x)))
         return xs
 
     def combine(self, ys, weights=None, out=None, stream=None):
@@ -206,12 +206,14 @@ class RoutePlan:
         if stream is not None:
             with _on(stream, self.slots, ys, weights, out):
                 return self.combine(ys, weights, out)
+        slots = self.slots
+        if slots is not self._known_slots:
+            self._check_tensors()
         code, ldys = _matrix(ys, "ys", self.rows)
         d = ys.shape[1]
-        slots, _ = self._pointers()
         w = None if weights is None else _plain(weights, "weights", (self.tokens, self.k), _F32)
         y, ldy = _out(out, "out", ys, self.tokens, d)
-        _check(lib.spmv_route_combine(self.tokens, self.k, self.rows, d, slots, w, ys.data_ptr(), ldys,
+        _check(lib.spmv_route_combine(self.tokens, self.k, self.rows, d, slots.data_ptr(), w, ys.data_ptr(), ldys,
                                       y.data_ptr(), ldy, code, _current(ys)))
         return y
 
@@ -220,13 +222,16 @@ class RoutePlan:
         if stream is not None:
             with _on(stream, self.slots, self.sources, dy, ys, weights, out):
                 return self.combine_grad(dy, ys, weights, out)
+        slots, sources = self.slots, self.sources
+        if slots is not self._known_slots or sources is not self._known_sources:
+            self._check_tensors()
         code, lddy = _matrix(dy, "dy", self.tokens)
         d = dy.shape[1]
         ldys = _matrix(ys, "ys", self.rows, d, dy.dtype)[1]
         w = _plain(weights, "weights", (self.tokens, self.k), _F32)
         dys, lddys = _out(out, "out", dy, self.rows, d)
         dw = _empty((self.tokens, self.k), dtype=_F32, device=dy.device)
-        _check(lib.spmv_route_combine_grad(self.tokens, self.k, self.rows, d, *self._pointers(), w,
+        _check(lib.spmv_route_combine_grad(self.tokens, self.k, self.rows, d, slots.data_ptr(), sources.data_ptr(), w,
                                            dy.data_ptr(), lddy, ys.data_ptr(), ldys, dys.data_ptr(), lddys,
                                            dw.data_ptr(), code, _current(dy)))
         return dys, dw
