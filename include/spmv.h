@@ -669,8 +669,9 @@ SPMV_API int spmv_route_combine_grad(int64_t tokens, int32_t k, int64_t rows, in
  *       Where every other column of z is -inf, or so low that their mass is 0 in 32 bits (the
  *       type's lowest value), an r below 1e-5 is rounding and counts as 0.  Beside -inf a larger
  *       one makes the loss +inf, and the gradient is 0 in those columns.
- * A row without entries (padding, say) has loss 0 and gradient 0, whatever z holds.  A teacher
- * logit of -inf has p = 0.  The loss is not scaled: neither by temperature^2 nor to a mean.
+ * A row without entries (padding, say) has loss 0 and gradient 0, whatever z holds.  A row with
+ * entries whose z is -inf everywhere has no softmax: its loss and its entries' gradient are NaN.
+ * A teacher logit of -inf has p = 0.  The loss is not scaled: neither by temperature^2 nor to a mean.
  *   k 1..512 (k may exceed vocab only by absent entries), vocab 1..2^22, temperature in
  *   [1e-6, 1e6].
  *   stats    float[rows][4], 16-byte aligned, or NULL: what spmv_distill_grad needs of the row.

@@ -273,6 +273,26 @@ def test_distill_remainder_where_the_others_are_lowest(spmv, dtype, rows, vocab,
             assert np.abs(others + size).max() <= (1e-3 + H[dtype]) * size + TINY[dtype]
 
 
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows,vocab", [(3, 40), (3, 9000), (1300, 40)])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_rows_whose_mask_leaves_nothing(spmv, dtype, rows, vocab, tail):
+    """No softmax, so NaN where there is a target, 0 where there is none; the rows beside them as ever."""
+    z = (torch.randn(rows, vocab, generator=gen(vocab)) * 2).to(dtype).cuda()
+    ids = torch.arange(5, dtype=torch.int32).repeat(rows, 1).cuda() * 7
+    teacher = torch.randn(rows, 5, generator=gen(rows)).cuda()
+    lse = torch.logsumexp(teacher, 1) + 0.2 if tail else None
+    plain = spmv.distill_loss_grad(z, ids, teacher, teacher_lse=lse)
+    z[0], z[1] = -math.inf, -math.inf
+    ids[1] = -1
+    loss, dz = spmv.distill_loss_grad(z, ids, teacher, teacher_lse=lse)
+    res = spmv.distill_loss(z, ids, teacher, teacher_lse=lse)
+    for got_loss, got in ((loss, dz), (res.loss, res.grad())):
+        assert torch.isnan(got_loss[0]) and torch.isnan(got[0, ids[0].long()]).all()
+        assert got_loss[1] == 0 and not got[1].any()
+    assert torch.equal(loss[2:], plain[0][2:]) and torch.equal(dz[2:], plain[1][2:])
+
+
 # --------------------------------------------------------------------------- #
 # states between two calls
 # --------------------------------------------------------------------------- #
