@@ -286,7 +286,7 @@ constexpr int kPrefetch = 8;      // vectors of a thread that L2 fetches first (
 constexpr int kKeepBatches = 2;   // of a row that is read twice: 61 KB of a CTA's shared memory
 
 // kR: vectors of a thread in registers, 0: batches from memory.  Bound by DRAM: 8192 x 131072 bf16 rows,
-// 64 entries, loss and gradient in 752 us, 5.7 TB/s of z and dz (a copy runs at 6.8); with its
+// 64 entries, loss and gradient in 752 us, 5.7 TB/s of z and dz (a copy runs at 6.7); with its
 // arithmetic left out the same reads and writes took 95 % of the time.  What misses is the part
 // of the rows in flight that L2 has dropped before the second reading (7 % of z).  The gradient
 // alone 5.1 TB/s, the loss alone 5.2: the chain of loads behind a row's entries and the barrier,
@@ -534,7 +534,13 @@ cudaError_t launch_distill_shape(const RowShape &shape, int64_t vectors, const D
 template <typename T, int kMode>
 cudaError_t launch_distill_mode(const DistillArgs &a, cudaStream_t s) {
     const int64_t vectors = row_vectors<T>(a.n, a.z, a.ldz);
-    // (fewer rows than warps that run at once: a CTA's warps share a row sooner)
+    // Many rows are eight an SM or more.  us for loss and gradient, the loss alone, with a warp / a
+    // CTA (below 152 rows a cluster) a row, 32 entries:
+    //   rows    500 floats               4000 bf16 values
+    //   608     4.8, 3.4 / 5.8, 4.2      8.5, 3.8 / 7.1, 4.6
+    //   1215    4.9, 3.6 / 6.8, 5.0      8.9, 4.4 / 9.9, 5.9
+    //   1824    5.1, 3.8 / 10.2, 6.2     9.5, 4.9 / 15.0, 7.5
+    //   16384   19.8, 12.4 / 70.8, 32.7  76.4, 33.9 / 103, 44.2
     if (vectors <= kWarpVectors && a.rows >= 1216) return launch_distill_warp<T, kMode>(vectors, a, s);
     RowShape shape = row_shape(a.rows, vectors, kMode == kLossGrad);
     // with lse a CTA keeps a byte per vector of its share (2^22 float values: a cluster of 8)

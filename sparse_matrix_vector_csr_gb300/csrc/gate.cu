@@ -1,8 +1,9 @@
 // A router's choice: the k <= 16 largest of short rows, with softmax weights, and the weights' gradient.
 //
 // Eight lanes share a row (with four, a fifth fewer instructions a row but half the warps: 32768 rows
-// of 256 bf16 values, 8 chosen, with gradient, 20.8 us against 18.7).  Each sorts its values in blocks of kK (a sorting network on keys that hold the value's order and its column,
-// so that no two are equal and ties go to the lowest column) and merges the blocks, keeping the kK
+// of 256 bf16 values, 8 chosen, with gradient, 20.8 us against 18.7).  Each sorts its values in blocks of kK
+// (a sorting network on keys that hold the value's order and its column, so that no two are equal and ties
+// go to the lowest column) and merges the blocks, keeping the kK
 // largest; exchanges with the lanes 1, 2 and 4 away merge the lanes' lists.  Every operation is a
 // minimum or maximum on registers that four rows a warp share: rounds of "largest of
 // the warp" cost five times as many instructions a row (256 bf16 values, 8 of them: 780).  The
@@ -193,7 +194,8 @@ __global__ void __launch_bounds__(kThreads) k_gate(TopArgs a) {
 }
 
 // The gradient (see topk.cu for the formulas): the lanes write a row's vectors, then, after
-// __syncwarp has ordered the stores, its chosen columns.
+// __syncwarp has ordered the stores, its chosen columns.  8 of 256 for 32768 bf16 rows, over the row: 5.5 us
+// one after the other, 9.3 with cold caches, bound by the latency of its loads.
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads) k_gate_grad(TopGradArgs a) {
     constexpr int kN = Vec<T>::kN;

@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(int64_t tokens, int k, 
 }
 
 // dys[slots[t, j]] = weights[t, j] dy[t] and dweights[t, j] = <dy[t], ys[slots[t, j]]>: one CTA
-// per token (of one warp to eight, by the row's length), so that its products reduce inside the CTA in a fixed order (no atomics); entries
-// are taken four at a time, dy coming from L1 from the second time on.  Rows of dys without
+// per token (of one warp to eight, by the row's length), so that its products reduce inside the CTA in a
+// fixed order (no atomics); entries are taken four at a time, dy coming from L1 from the second time on.  Rows of dys without
 // a source are zeroed by the first CTAs.  16384 tokens x 4 of 2048 bf16 values: 94 us, 6.4 TB/s of
 // dy, ys and dys.
 template <typename T, typename U>
@@ -465,6 +465,9 @@ int check_apart(const void *out, size_t out_bytes, const char *out_name, const v
         default: CALL(2); break;           \
     }
 
+// Units of a row that a lane of k_dispatch holds: 64 bytes where they are 16 (16384 tokens x 4 of 2048 bf16
+// values: 53.4 us; with two 52.6, with eight 55.6), else eight (8192 x 4 of 4095 bf16 values:
+// 65.9 us; with four 65.7, with sixteen 68.3): enough in flight, few copies of a row's slots.
 constexpr int units_per_lane(int bytes) { return bytes == 16 ? 4 : 8; }
 
 template <typename T>
@@ -500,6 +503,14 @@ void launch_combine_grad(int unit, int64_t tokens, int k, int64_t rows, int64_t 
         using U = decltype(tag);
         constexpr int64_t kN = sizeof(U) / sizeof(T);
         const int64_t units = d / kN;
+        // two to eight units a thread: fewer leave warps without work behind the sums' barriers, more
+        // leave too little in flight.  us with 32, 64, 128, 256 threads for 4 rows a token of
+        //   8 units (16384 bf16 tokens)     11.8  17.3  20.8  41.6
+        //   64                              25.2  26.8  37.2  70.1
+        //   128                             48.1  47.6  50.8  79.5
+        //   256                             93.2  91.3  90.5  104
+        //   1024 (4096 tokens)              102   94.8  92.8  91.4
+        //   4095 of 2 bytes (8192 tokens)   230   170   154   149
         const int threads = units >= 512 ? 256 : units >= 128 ? 128 : units > 64 ? 64 : 32;
         k_combine_grad<T, U><<<static_cast<unsigned>(tokens + ceil_div(rows, kPadRows)), threads, 0, s>>>(
             ceil_div(rows, kPadRows), k, rows, units, slots, sources, weights, static_cast<const U *>(dy), lddy / kN,
