@@ -649,7 +649,8 @@ SPMV_API int spmv_route_combine(int64_t tokens, int32_t k, int64_t rows, int64_t
                                 int dtype, void *stream);
 
 /* The gradients of combine: dys[slots[t][j]] = weights[t][j] * dy[t], 0 in rows without a source
- * (dys: rows x d), and dweights[t][j] = <dy[t], ys[slots[t][j]]>, 0 for a dropped entry. */
+ * (dys: rows x d), and dweights[t][j] = <dy[t], ys[slots[t][j]]>, 0 for a dropped entry.
+ * tokens + rows / 32 < 2^31. */
 SPMV_API int spmv_route_combine_grad(int64_t tokens, int32_t k, int64_t rows, int64_t d, const int32_t *slots,
                                      const int32_t *sources, const float *weights, const void *dy, int64_t lddy,
                                      const void *ys, int64_t ldys, void *dys, int64_t lddys, float *dweights,

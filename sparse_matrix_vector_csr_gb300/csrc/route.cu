@@ -657,6 +657,8 @@ extern "C" SPMV_API int spmv_route_combine_grad(int64_t tokens, int32_t k, int64
     SPMV_TRY(check_matrix(dy, "dy", tokens, d, lddy, dtype));
     SPMV_TRY(check_matrix(ys, "ys", rows, d, ldys, dtype));
     SPMV_TRY(check_matrix(dys, "dys", rows, d, lddys, dtype));
+    if (tokens + ceil_div(rows, kPadRows) >= int64_t(1) << 31)  // CTAs
+        return set_error(SPMV_ERR_TOO_LARGE, "tokens + rows / " + std::to_string(kPadRows) + " must be below 2^31");
     if (rows) SPMV_TRY(check_array(sources, "sources", 4));
     if (tokens) {
         SPMV_TRY(check_array(slots, "slots", 4));

@@ -92,3 +92,14 @@ def test_star_import_has_the_sparse_rows(rows):
     names = {}
     exec("from sparse_matrix_vector_csr_gb300 import *", names)
     assert all(n in names for n in ("topk_rows", "RoutePlan", "distill_loss", "SpmvMatrix", "spmv_apply"))
+
+
+def test_gradient_of_combine_refuses_more_ctas_than_a_grid_has():
+    import numpy as np
+    import sparse_matrix_vector_csr_gb300 as spmv
+
+    h, m = np.zeros(8, np.float32), (1 << 31) - 1
+    for tokens, rows, status in ((m, 1, -5), (m - 10, 640, -5), (m - 10, 320, -1)):  # (-1: host memory)
+        with pytest.raises(spmv.SpmvError) as e:
+            spmv.spmv_route_combine_grad(tokens, 1, rows, 0, h, h, h, None, 0, None, 0, None, 0, h, 1, stream=0)
+        assert e.value.status == status, (tokens, rows, str(e.value))
