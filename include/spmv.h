@@ -696,6 +696,74 @@ SPMV_API int spmv_distill_loss_grad(int64_t rows, int64_t vocab, int32_t k, cons
                                     const float *teacher_lse, double temperature, float *loss, double scale,
                                     const float *row_scale, void *dz, int64_t lddz, void *stream);
 
+/*
+ * Rows of a table by token: x[t] = scale * table[ids[t]] (ids int32[tokens]; table: vocab x d, x: tokens x
+ * d), 0 for an id outside [0, vocab) (padding, -1 by convention).  With scale 1 the values are copied, else
+ * each product is rounded once.  tokens, vocab < 2^31, tokens * d < 2^40.
+ */
+SPMV_API int spmv_embed_rows(int64_t tokens, int64_t vocab, int64_t d, const int32_t *ids, const void *table,
+                             int64_t ldtable, double scale, void *x, int64_t ldx, int dtype, void *stream);
+
+/*
+ * The gradient of spmv_embed_rows in the table: dtable[v] = scale * sum of dx[t] over the tokens with
+ * ids[t] = v, in the tokens' order, in 32 bits, rounded once; 0 for a row without tokens.  With `accumulate`
+ * not 0 it is added to what dtable holds (one rounding of the sum), and rows without tokens are not
+ * touched.  dx is of type `dtype`, dtable (vocab x d) of type `out_dtype`: the same, or SPMV_F32.
+ * The workspace (spmv_embed_workspace gives its bytes, or a negative status) starts at a multiple
+ * of 16 bytes and is free for other use when the call's kernels have run.
+ */
+SPMV_API int64_t spmv_embed_workspace(int64_t tokens, int64_t vocab, int64_t d);
+SPMV_API int spmv_embed_rows_grad(int64_t tokens, int64_t vocab, int64_t d, const int32_t *ids, const void *dx,
+                                  int64_t lddx, int dtype, double scale, int accumulate, void *dtable,
+                                  int64_t lddtable, int out_dtype, void *workspace, int64_t workspace_bytes,
+                                  void *stream);
+
+/* activations of spmv_feed_forward: x / (1 + exp(-x)); x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2;
+ * max(x, 0) */
+typedef enum { SPMV_ACT_SILU = 0, SPMV_ACT_GELU_TANH = 1, SPMV_ACT_RELU = 2 } spmv_activation;
+
+/*
+ * The gated feed-forward block of each expert over its segment of rows:
+ *   gate = x Wg^T,  up = x Wu^T,  h = act(gate) * up,  y = h Wd^T
+ * with x, y: rows x d, and for each of `experts` experts matrices Wg, Wu of f rows of d values, Wd of d rows
+ * of f.
+ *   offsets  int32[experts + 1] as spmv_route_plan gives them: expert e has the rows [offsets[e],
+ *            offsets[e + 1]).  Rows from offsets[experts] on have no expert: their x is not looked at
+ *            and their y, gate and up become 0.  NULL with experts 1: one block for all rows.
+ *   w_gate, w_up   row i of expert e's matrix starts at e * w_expert + i * ldw (the same for both), w_down's at
+ *            e * wd_expert + i * ldwd, in values (16-byte aligned rows run fastest).
+ *   gate, up rows x f (leading dimension ldg), what spmv_feed_forward_grad needs of the forward call, or both
+ *            NULL.
+ * Sums are in 32 bits; h, gate, up and y are each rounded once to the type.  No product of a value that no
+ * row or matrix holds enters a sum: NaN and infinities of a row stay in that row.
+ *   1 <= d, f <= 2^20; 1 <= experts <= 4096.
+ * The workspace starts at a multiple of 16 bytes and is free for other use when the call's kernels have run.
+ * spmv_feed_forward_workspace gives its bytes (gradient 0: spmv_feed_forward's, else
+ * spmv_feed_forward_grad's), or a negative status.
+ */
+SPMV_API int64_t spmv_feed_forward_workspace(int64_t rows, int64_t d, int64_t f, int dtype, int gradient);
+SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, int32_t experts, const int32_t *offsets,
+                               const void *x, int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw,
+                               int64_t w_expert, const void *w_down, int64_t ldwd, int64_t wd_expert, int activation,
+                               void *gate, void *up, int64_t ldg, void *y, int64_t ldy, int dtype, void *workspace,
+                               int64_t workspace_bytes, void *stream);
+
+/*
+ * The gradients of spmv_feed_forward, with dy (rows x d) the loss's gradient in y, from that call's arguments
+ * and the gate and up that it kept:
+ *   dx       rows x d: the gradient in x, 0 in rows without an expert; NULL where it is not wanted.
+ *   dw_gate, dw_up (experts x f x d), dw_down (experts x d x f), contiguous: the gradients in the weights, sums
+ *            over each expert's rows, 0 for an expert without rows; each may be NULL.
+ * Rows without an expert enter nothing, whatever x and dy hold there.  Sums are in 32 bits; the gradients in
+ * gate and up, and h, are rounded once to the type for the products that follow.
+ */
+SPMV_API int spmv_feed_forward_grad(int64_t rows, int64_t d, int64_t f, int32_t experts, const int32_t *offsets,
+                                    const void *x, int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw,
+                                    int64_t w_expert, const void *w_down, int64_t ldwd, int64_t wd_expert,
+                                    int activation, const void *gate, const void *up, int64_t ldg, const void *dy,
+                                    int64_t lddy, void *dx, int64_t lddx, void *dw_gate, void *dw_up, void *dw_down,
+                                    int dtype, void *workspace, int64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

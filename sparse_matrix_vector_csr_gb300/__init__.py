@@ -10,7 +10,8 @@ entry points one to one; :class:`SpmvMatrix` wraps a handle for torch tensors.
 
 ``sparse_rows`` has the operators of matrices with at most k entries a row that are made
 anew at each step: a router's choice and the rows sorted by it (:func:`topk_rows`,
-:class:`RoutePlan`), and distillation from a teacher's top logits (:func:`distill_loss`).
+:class:`RoutePlan`), the experts' gated feed-forward block over those rows (:meth:`RoutePlan.feed_forward`),
+rows of a table by token (:func:`embed_rows`), and distillation from a teacher's top logits (:func:`distill_loss`).
 """
 from __future__ import annotations
 
@@ -60,11 +61,18 @@ from ._abi import (  # noqa: F401
     spmv_distill_loss,
     spmv_distill_grad,
     spmv_distill_loss_grad,
+    spmv_embed_rows,
+    spmv_embed_workspace,
+    spmv_embed_rows_grad,
+    spmv_feed_forward_workspace,
+    spmv_feed_forward,
+    spmv_feed_forward_grad,
 )
 
 #: names of ``sparse_rows``, which needs torch and is imported with the first of them (by a star import
 #: too, so they are among its names only where torch is installed)
-_SPARSE_ROWS = ("TopRows", "RoutePlan", "DistillLoss", "topk_rows", "distill_loss", "distill_loss_grad")
+_SPARSE_ROWS = ("TopRows", "RoutePlan", "DistillLoss", "FeedForward", "topk_rows", "distill_loss", "distill_loss_grad",
+                "embed_rows", "embed_rows_grad", "feed_forward")
 
 __all__ = ["SpmvMatrix", "SpmvError", "FORMATS", "ORDERINGS"] + [n for n in _abi.EXPORTS]
 if sys.modules.get("torch") or find_spec("torch"):

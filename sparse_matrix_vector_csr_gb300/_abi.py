@@ -31,11 +31,15 @@ EXPORTS = (
     "spmv_gmres", "spmv_probe_gather", "spmv_device_status", "spmv_device_memory",
     "spmv_topk_rows", "spmv_topk_rows_grad", "spmv_route_rows", "spmv_route_workspace", "spmv_route_plan",
     "spmv_route_dispatch", "spmv_route_combine", "spmv_route_combine_grad", "spmv_distill_loss",
-    "spmv_distill_grad", "spmv_distill_loss_grad",
+    "spmv_distill_grad", "spmv_distill_loss_grad", "spmv_embed_rows", "spmv_embed_workspace", "spmv_embed_rows_grad",
+    "spmv_feed_forward_workspace", "spmv_feed_forward", "spmv_feed_forward_grad",
 )
 
 #: spmv_weighting codes
 WEIGHTINGS = {None: 0, "none": 0, "selected": 1, "row": 2}
+
+#: spmv_activation codes
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1, "relu": 2}
 
 #: spmv_ordering codes
 ORDERINGS = {"natural": 0, "row_length": 1, "rcm": 2, "user": 3}
@@ -150,7 +154,19 @@ def _load():
     lib.spmv_distill_loss_grad.argtypes = [i64, i64, i32, vp, i64, c_int, vp, vp, c_int, vp, f64, vp, f64, vp, vp, i64,
                                            vp]
     lib.spmv_distill_loss_grad.restype = c_int
-    del i32
+    lib.spmv_embed_rows.argtypes = [i64, i64, i64, vp, vp, i64, f64, vp, i64, c_int, vp]
+    lib.spmv_embed_rows.restype = c_int
+    lib.spmv_embed_workspace.argtypes = [i64, i64, i64]
+    lib.spmv_embed_workspace.restype = i64
+    lib.spmv_embed_rows_grad.argtypes = [i64, i64, i64, vp, vp, i64, c_int, f64, c_int, vp, i64, c_int, vp, i64, vp]
+    lib.spmv_embed_rows_grad.restype = c_int
+    lib.spmv_feed_forward_workspace.argtypes = [i64, i64, i64, c_int, c_int]
+    lib.spmv_feed_forward_workspace.restype = i64
+    block = [i64, i64, i64, i32, vp, vp, i64, vp, vp, i64, i64, vp, i64, i64, c_int, vp, vp, i64]
+    lib.spmv_feed_forward.argtypes = block + [vp, i64, c_int, vp, i64, vp]
+    lib.spmv_feed_forward.restype = c_int
+    lib.spmv_feed_forward_grad.argtypes = block + [vp, i64, vp, i64, vp, vp, vp, c_int, vp, i64, vp]
+    lib.spmv_feed_forward_grad.restype = c_int
     return lib
 
 
@@ -457,4 +473,50 @@ def spmv_distill_loss_grad(rows, vocab, k, z, ldz, dtype, ids, teacher, teacher_
     _check(lib.spmv_distill_loss_grad(int(rows), int(vocab), int(k), _ptr(z), int(ldz), int(dtype), _ptr(ids),
                                       _ptr(teacher), int(teacher_dtype), _ptr(teacher_lse), float(temperature),
                                       _ptr(loss), float(scale), _ptr(row_scale), _ptr(dz), int(lddz),
+                                      _stream(stream)))
+
+
+def spmv_embed_rows(tokens, vocab, d, ids, table, ldtable, scale, x, ldx, dtype, stream=None) -> None:
+    """Rows of a table by token (see spmv.h)."""
+    _check(lib.spmv_embed_rows(int(tokens), int(vocab), int(d), _ptr(ids), _ptr(table), int(ldtable), float(scale),
+                               _ptr(x), int(ldx), int(dtype), _stream(stream)))
+
+
+def spmv_embed_workspace(tokens, vocab, d) -> int:
+    """Bytes of workspace that spmv_embed_rows_grad needs."""
+    return int(_check(lib.spmv_embed_workspace(int(tokens), int(vocab), int(d))))
+
+
+def spmv_embed_rows_grad(tokens, vocab, d, ids, dx, lddx, dtype, scale, accumulate, dtable, lddtable, out_dtype,
+                         workspace, workspace_bytes, stream=None) -> None:
+    """The gradient of spmv_embed_rows in the table (see spmv.h)."""
+    _check(lib.spmv_embed_rows_grad(int(tokens), int(vocab), int(d), _ptr(ids), _ptr(dx), int(lddx), int(dtype),
+                                    float(scale), int(accumulate), _ptr(dtable), int(lddtable), int(out_dtype),
+                                    _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def spmv_feed_forward_workspace(rows, d, f, dtype, gradient=False) -> int:
+    """Bytes of workspace that spmv_feed_forward or spmv_feed_forward_grad needs."""
+    return int(_check(lib.spmv_feed_forward_workspace(int(rows), int(d), int(f), int(dtype), int(gradient))))
+
+
+def spmv_feed_forward(rows, d, f, experts, offsets, x, ldx, w_gate, w_up, ldw, w_expert, w_down, ldwd, wd_expert,
+                      activation, gate, up, ldg, y, ldy, dtype, workspace, workspace_bytes, stream=None) -> None:
+    """The gated feed-forward block of each expert over its segment of rows (see spmv.h)."""
+    _check(lib.spmv_feed_forward(int(rows), int(d), int(f), int(experts), _ptr(offsets), _ptr(x), int(ldx),
+                                 _ptr(w_gate), _ptr(w_up), int(ldw), int(w_expert), _ptr(w_down), int(ldwd),
+                                 int(wd_expert), int(ACTIVATIONS.get(activation, activation)), _ptr(gate), _ptr(up),
+                                 int(ldg), _ptr(y), int(ldy), int(dtype), _ptr(workspace), int(workspace_bytes),
+                                 _stream(stream)))
+
+
+def spmv_feed_forward_grad(rows, d, f, experts, offsets, x, ldx, w_gate, w_up, ldw, w_expert, w_down, ldwd, wd_expert,
+                           activation, gate, up, ldg, dy, lddy, dx, lddx, dw_gate, dw_up, dw_down, dtype, workspace,
+                           workspace_bytes, stream=None) -> None:
+    """The gradients of spmv_feed_forward (see spmv.h)."""
+    _check(lib.spmv_feed_forward_grad(int(rows), int(d), int(f), int(experts), _ptr(offsets), _ptr(x), int(ldx),
+                                      _ptr(w_gate), _ptr(w_up), int(ldw), int(w_expert), _ptr(w_down), int(ldwd),
+                                      int(wd_expert), int(ACTIVATIONS.get(activation, activation)), _ptr(gate),
+                                      _ptr(up), int(ldg), _ptr(dy), int(lddy), _ptr(dx), int(lddx), _ptr(dw_gate),
+                                      _ptr(dw_up), _ptr(dw_down), int(dtype), _ptr(workspace), int(workspace_bytes),
                                       _stream(stream)))

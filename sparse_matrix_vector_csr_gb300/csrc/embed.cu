@@ -1,0 +1,587 @@
+// Rows of a table by token, and the gradient of that lookup.  The tokens of a batch are a sparse
+// tokens x vocab matrix P with one entry of value `scale` a row (none where the token is padding);
+// the lookup is P times the table, its gradient the transposed product P^T dx.  For the latter the
+// entries are put in the order of their columns (a stable radix sort), equal shares of that order go
+// to the warps whatever the columns' lengths, and a column that reaches over several shares is joined
+// from their partial sums, as the merge-path product joins its rows.  Both are bound by their rows'
+// bytes.
+#include <type_traits>
+
+#include "device_util.cuh"
+#include "rows_common.cuh"
+
+namespace spmv {
+namespace {
+
+using namespace rows;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ bool is_entry(int32_t id, int64_t vocab) { return id >= 0 && id < vocab; }
+
+// ----------------------------------------------------------------------------
+// lookup
+// ----------------------------------------------------------------------------
+// A warp takes kU x 32 units of one token's row.
+template <typename T, typename U, int kU, bool kScaled>
+__global__ void __launch_bounds__(kThreads) k_embed(int64_t tokens, int64_t vocab, int64_t units, int64_t parts,
+                                                   float scale, const int32_t *__restrict__ ids,
+                                                   const U *__restrict__ table, int64_t ldt, U *__restrict__ x,
+                                                   int64_t ldx) {
+    constexpr int kN = sizeof(U) / sizeof(T);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int64_t t = item / parts;
+    if (t >= tokens) return;
+    const int64_t u0 = (item - t * parts) * (32 * kU) + lane;
+    const int32_t id = ids[t];
+    const bool there = is_entry(id, vocab);
+    const U *src = table + static_cast<int64_t>(there ? id : 0) * ldt;
+    U *dst = x + t * ldx;
+    U v[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+        v[i] = U{};
+        if (there && u0 + i * 32 < units) v[i] = src[u0 + i * 32];
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i)
+        if (u0 + i * 32 < units) {
+            if constexpr (kScaled) {
+                float f[kN];
+                unit_to_f32<T>(v[i], f);
+#pragma unroll
+                for (int j = 0; j < kN; ++j) f[j] *= scale;
+                if (there) v[i] = unit_from_f32<T, U>(f);  // (0 without a token, whatever the scale)
+            }
+            dst[u0 + i * 32] = v[i];
+        }
+}
+
+template <typename T>
+void launch_embed(int unit, int64_t tokens, int64_t vocab, int64_t d, float scale, const int32_t *ids, const void *table,
+                  int64_t ldt, void *x, int64_t ldx, cudaStream_t s) {
+    auto go = [&](auto tag, auto per_lane, auto scaled) {
+        using U = decltype(tag);
+        constexpr int kU = decltype(per_lane)::value;
+        constexpr int64_t kN = sizeof(U) / sizeof(T);
+        const int64_t units = d / kN, parts = ceil_div(units, 32 * kU);
+        k_embed<T, U, kU, decltype(scaled)::value><<<static_cast<unsigned>(ceil_div(tokens * parts, kWarps)), kThreads, 0, s>>>(
+            tokens, vocab, units, parts, scale, ids, static_cast<const U *>(table), ldt / kN, static_cast<U *>(x), ldx / kN);
+    };
+    auto either = [&](auto tag, auto per_lane) {
+        scale == 1.0f ? go(tag, per_lane, std::false_type{}) : go(tag, per_lane, std::true_type{});
+    };
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 4> four;
+    constexpr std::integral_constant<int, 8> eight;
+    const bool few = tokens * d * static_cast<int64_t>(sizeof(T)) < int64_t(kSms) * 16 * 1024;
+    if (unit == 16) few ? either(uint4{}, one) : either(uint4{}, four);
+    else if (unit == 8) either(uint2{}, four);
+    else if (unit == 4) either(uint32_t{}, eight);
+    else if constexpr (sizeof(T) == 2) either(uint16_t{}, eight);
+}
+
+// ----------------------------------------------------------------------------
+// tokens in the order of their rows
+// ----------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 9;
+constexpr int64_t kSortShare = 4096;  // tokens a CTA sorts, at least
+
+struct SortShape {
+    int ctas;    // a cluster
+    int passes;  // digits of the row number, lowest first
+    int bits;    // of a digit
+    size_t smem;
+};
+SortShape sort_shape(int64_t tokens, int64_t vocab) {
+    SortShape s;
+    s.ctas = 1;
+    while (s.ctas < kMaxCluster && tokens > s.ctas * kSortShare) s.ctas *= 2;
+    int bits = 1;
+    while ((int64_t(1) << bits) < vocab) ++bits;
+    s.passes = static_cast<int>(ceil_div(bits, kDigitBits));
+    s.bits = static_cast<int>(ceil_div(bits, s.passes));
+    s.smem = ((kSortWarps + kMaxCluster + 1) * (size_t(1) << s.bits) + kSortWarps) * sizeof(int32_t);
+    return s;
+}
+
+struct SortArgs {
+    int64_t tokens, vocab;
+    int passes, bits;
+    const int32_t *ids;
+    int32_t *key[2], *src[2];  // the last pass writes the first of each
+    int32_t *count;            // tokens that are entries
+};
+struct ZeroArgs {  // rows x row_bytes at a distance of ld bytes
+    char *p;
+    int64_t rows, row_bytes, ld;
+};
+
+__device__ __forceinline__ void zero_bytes(char *p, int64_t n, int64_t worker, int64_t workers) {
+    // 2-byte values up to the first 16-byte boundary and behind the last one
+    int64_t head = static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15);
+    if (head > n) head = n;
+    const int64_t vecs = (n - head) / 16, tail = head + vecs * 16;
+    uint4 *v = reinterpret_cast<uint4 *>(p + head);
+    for (int64_t i = worker; i < vecs; i += workers) __stcs(v + i, make_uint4(0, 0, 0, 0));
+    if (worker < head / 2) reinterpret_cast<uint16_t *>(p)[worker] = 0;
+    if (worker < (n - tail) / 2) reinterpret_cast<uint16_t *>(p + tail)[worker] = 0;
+}
+
+// The first cluster sorts the entries by row, stably (tokens of a row stay in their order, so sums over
+// them do not depend on timing); the other CTAs meanwhile write zeros over the whole gradient, of
+// which most rows have no token.  Every pass counts each warp's run of tokens by digit, exchanges
+// the CTAs' counts through the cluster's shared memory, and writes each token to its place.
+__global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArgs z, int ctas) {
+    extern __shared__ int32_t shared[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x >= ctas) {
+        const int64_t worker = (static_cast<int64_t>(blockIdx.x) - ctas) * kSortThreads + tid;
+        const int64_t workers = (static_cast<int64_t>(gridDim.x) - ctas) * kSortThreads;
+        if (z.ld == z.row_bytes) {
+            zero_bytes(z.p, z.rows * z.row_bytes, worker, workers);
+        } else {
+            for (int64_t r = worker / 32; r < z.rows; r += workers / 32) zero_bytes(z.p + r * z.ld, z.row_bytes, lane, 32);
+        }
+        dev::allow_dependents();
+        return;
+    }
+    const int bins = 1 << a.bits, rank = blockIdx.x;
+    int32_t *wcount = shared;                         // [warps][bins]: counts, then next places
+    int32_t *hist = wcount + kSortWarps * bins;       // [kMaxCluster][bins]: the CTAs' counts
+    int32_t *place0 = hist + kMaxCluster * bins;      // [bins]: this CTA's first place
+    int32_t *warp_part = place0 + bins;               // [warps]
+    int64_t n = a.tokens;
+    if (ctas > 1) cluster_sync(ctas);  // every CTA is there before its shared memory is written
+    for (int p = 0; p < a.passes; ++p) {
+        const int32_t *key_in = p == 0 ? a.ids : a.key[(a.passes - p) & 1];
+        const int32_t *src_in = p == 0 ? nullptr : a.src[(a.passes - p) & 1];
+        int32_t *key_out = a.key[(a.passes - 1 - p) & 1], *src_out = a.src[(a.passes - 1 - p) & 1];
+        const int shift = p * a.bits;
+        const int64_t share = (n + ctas - 1) / ctas, begin = min(n, rank * share), end = min(n, begin + share);
+        const int64_t run = (end - begin + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32;
+        const int64_t r0 = begin + warp * run, r1 = min(end, r0 + run);
+        int32_t *mine = wcount + warp * bins;
+        // (from L2: other SMs of the cluster wrote it in the pass before)
+        const auto key_at = [&](int64_t i) { return __ldcg(key_in + i); };
+        const auto digit = [&](int32_t key) { return (key >> shift) & (bins - 1); };
+
+        for (int i = tid; i < kSortWarps * bins; i += kSortThreads) wcount[i] = 0;
+        __syncthreads();
+        for (int64_t i0 = r0; i0 < r1; i0 += 32) {
+            const int32_t key = i0 + lane < r1 ? key_at(i0 + lane) : -1;
+            const int dig = is_entry(key, a.vocab) ? digit(key) : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, dig);
+            if (dig >= 0 && (same & ((1u << lane) - 1)) == 0) mine[dig] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int b = tid; b < bins; b += kSortThreads) {  // (at most one a thread)
+            int32_t at = 0;
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int32_t c = wcount[w * bins + b];
+                wcount[w * bins + b] = at;
+                at += c;
+            }
+            if (ctas == 1) {
+                hist[b] = at;
+            } else {
+                for (int r = 0; r < ctas; ++r)
+                    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer_addr(hist + rank * bins + b, r)), "r"(at)
+                                 : "memory");
+            }
+        }
+        cluster_sync(ctas);
+        int32_t before = 0, total = 0;
+        if (tid < bins)
+            for (int r = 0; r < ctas; ++r) {
+                const int32_t c = hist[r * bins + tid];
+                before += r < rank ? c : 0;
+                total += c;
+            }
+        int32_t incl = total;  // scan over the digits
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) warp_part[warp] = incl;
+        __syncthreads();
+        int32_t at = incl - total, all = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            at += w < warp ? warp_part[w] : 0;
+            all += warp_part[w];
+        }
+        if (tid < bins) place0[tid] = at + before;
+        __syncthreads();
+        for (int64_t i0 = r0; i0 < r1; i0 += 32) {
+            const int64_t i = i0 + lane;
+            const int32_t key = i < r1 ? key_at(i) : -1;
+            const int dig = is_entry(key, a.vocab) ? digit(key) : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, dig);
+            const int earlier = __popc(same & ((1u << lane) - 1));
+            const int32_t to = dig >= 0 ? place0[dig] + mine[dig] + earlier : 0;
+            __syncwarp();
+            if (dig >= 0 && earlier == 0) mine[dig] += __popc(same);
+            __syncwarp();
+            if (dig >= 0) {
+                key_out[to] = key;
+                src_out[to] = src_in ? __ldcg(src_in + i) : static_cast<int32_t>(i);
+            }
+        }
+        n = all;
+        cluster_sync(ctas);  // the places are written, the counts read
+    }
+    if (rank == 0 && tid == 0) *a.count = static_cast<int32_t>(n);
+    dev::allow_dependents();
+}
+
+// ----------------------------------------------------------------------------
+// sums over each row's tokens
+// ----------------------------------------------------------------------------
+constexpr int64_t kMaxChunks = 4096;
+// entries that one warp sums
+int64_t chunk_entries(int64_t tokens) {
+    int64_t c = 32;
+    while (ceil_div(tokens, c) > kMaxChunks) c *= 2;
+    return c;
+}
+constexpr int kJoinChunks = 8;    // per CTA of k_embed_join
+constexpr int kJoinCols = 4 * 32;  // of a row, per CTA
+
+struct SumArgs {
+    int64_t d, chunk, parts;
+    float scale;
+    int accumulate;
+    const int32_t *key, *src, *count;
+    float *carry;  // [chunks][2][ldc]: sum up to the end of a row begun in front of the chunk; from the start of a row open at its end
+    int64_t ldc;
+};
+
+template <typename O, int kN>
+__device__ __forceinline__ void load_values(const O *p, float *f) {
+    constexpr int kBytes = kN * static_cast<int>(sizeof(O)) > 16 ? 16 : kN * static_cast<int>(sizeof(O));
+    using U = typename Unit<kBytes>::type;
+    constexpr int kEach = kBytes / static_cast<int>(sizeof(O));
+#pragma unroll
+    for (int i = 0; i < kN; i += kEach) unit_to_f32<O>(*reinterpret_cast<const U *>(p + i), f + i);
+}
+template <typename O, int kN>
+__device__ __forceinline__ void store_values(O *p, const float *f) {
+    constexpr int kBytes = kN * static_cast<int>(sizeof(O)) > 16 ? 16 : kN * static_cast<int>(sizeof(O));
+    using U = typename Unit<kBytes>::type;
+    constexpr int kEach = kBytes / static_cast<int>(sizeof(O));
+#pragma unroll
+    for (int i = 0; i < kN; i += kEach) *reinterpret_cast<U *>(p + i) = unit_from_f32<O, U>(f + i);
+}
+
+// A warp sums kU x 32 units of kN values of the rows of one chunk of sorted entries, kR rows' loads in
+// flight, in 32 bits, in the tokens' order.
+template <typename T, typename O, int kN, int kU>
+__global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T *__restrict__ dx, int64_t lddx, O *out, int64_t ldo) {
+    using U = typename Unit<kN * static_cast<int>(sizeof(T))>::type;
+    constexpr int kR = 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    dev::grid_wait();
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp, c = item / a.parts;
+    const int64_t total = *a.count, lo = c * a.chunk, hi = min(lo + a.chunk, total);
+    if (lo >= total) return;
+    const int64_t col0 = ((item - c * a.parts) * (32 * kU) + lane) * kN;  // unit i's values: from col0 + i * 32 * kN
+    float acc[kU][kN] = {};
+    const auto flush = [&](int32_t row, float *carry) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+            const int64_t col = col0 + i * 32 * kN;
+            if (col < a.d) {
+                if (carry) {
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) carry[col + j] = acc[i][j];
+                } else {
+                    O *p = out + static_cast<int64_t>(row) * ldo + col;
+                    float f[kN] = {};
+                    if (a.accumulate) load_values<O, kN>(p, f);
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) f[j] = a.accumulate ? fmaf(acc[i][j], a.scale, f[j]) : acc[i][j] * a.scale;
+                    store_values<O, kN>(p, f);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kN; ++j) acc[i][j] = 0.0f;
+        }
+    };
+    float *carry = a.carry + 2 * c * a.ldc;
+    bool carried = lo > 0 && a.key[lo - 1] == a.key[lo];
+    for (int64_t g = lo; g < hi; g += 32) {
+        const int n = static_cast<int>(min(hi - g, int64_t(32)));
+        const int32_t key = lane < n ? a.key[g + lane] : -1, src = lane < n ? a.src[g + lane] : 0;
+        const int32_t behind = g + n < total ? a.key[g + n] : -1;
+        for (int q0 = 0; q0 < n; q0 += kR) {
+            U v[kR][kU];
+#pragma unroll
+            for (int q = 0; q < kR; ++q) {
+                const int64_t t = __shfl_sync(0xffffffffu, src, q0 + q);
+                if (q0 + q < n) {
+#pragma unroll
+                    for (int i = 0; i < kU; ++i)
+                        if (col0 + i * 32 * kN < a.d)
+                            v[q][i] = __ldcs(reinterpret_cast<const U *>(dx + t * lddx + col0 + i * 32 * kN));
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kR; ++q) {
+                const int32_t row = __shfl_sync(0xffffffffu, key, q0 + q);
+                const int32_t later = __shfl_sync(0xffffffffu, key, (q0 + q + 1) & 31);
+                if (q0 + q < n) {
+#pragma unroll
+                    for (int i = 0; i < kU; ++i)
+                        if (col0 + i * 32 * kN < a.d) {
+                            float f[kN];
+                            unit_to_f32<T>(v[q][i], f);
+#pragma unroll
+                            for (int j = 0; j < kN; ++j) acc[i][j] += f[j];
+                        }
+                    if ((q0 + q + 1 < n ? later : behind) != row) {
+                        flush(row, carried ? carry : nullptr);
+                        carried = false;
+                    } else if (q0 + q + 1 == n && g + n == hi) {  // the row goes on in the next chunk
+                        flush(row, carried ? carry : carry + a.ldc);
+                    }
+                }
+            }
+        }
+    }
+    dev::allow_dependents();
+}
+
+// The rows that reach over several chunks: the sum of the open end of the first chunk and what the next
+// chunks have of the row, each warp of a CTA an eighth of those, in a fixed order.
+template <typename O>
+__global__ void __launch_bounds__(kThreads) k_embed_join(SumArgs a, O *out, int64_t ldo) {
+    __shared__ float4 part[kWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    dev::grid_wait();
+    const int64_t total = *a.count, c0 = static_cast<int64_t>(blockIdx.x) * kJoinChunks;
+    const int64_t mine = c0 + (lane & (kJoinChunks - 1)), lo = mine * a.chunk, hi = lo + a.chunk;
+    bool opens = false;  // a row begins in this chunk and goes on behind it
+    if (hi < total) {
+        const int32_t last = a.key[hi - 1];
+        opens = a.key[hi] == last && !(lo > 0 && a.key[lo] == last && a.key[lo - 1] == last);
+    }
+    uint32_t open = __ballot_sync(0xffffffffu, opens) & ((1u << kJoinChunks) - 1);
+    const int64_t col = static_cast<int64_t>(blockIdx.y) * kJoinCols + lane * 4;
+    for (; open; open &= open - 1) {
+        const int64_t c = c0 + __ffs(open) - 1;
+        const int32_t row = a.key[(c + 1) * a.chunk - 1];
+        int64_t end = c + 1;  // the row's last chunk
+        for (;;) {
+            const int64_t behind = (end + lane + 1) * a.chunk;
+            const bool through = behind < total && a.key[behind - 1] == row && a.key[behind] == row;
+            const uint32_t stops = ~__ballot_sync(0xffffffffu, through);
+            if (stops) {
+                end += __ffs(stops) - 1;
+                break;
+            }
+            end += 32;
+        }
+        // carries of the row: its start in chunk c, then the heads of chunks c + 1 .. end
+        const int64_t n = end - c + 1;
+        float4 sum = make_float4(0, 0, 0, 0);
+        if (col < a.d) {
+            constexpr int kLoads = 8;
+            for (int64_t q0 = warp; q0 < n; q0 += kWarps * kLoads) {
+                float4 v[kLoads];
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int64_t q = q0 + i * kWarps;
+                    v[i] = make_float4(0, 0, 0, 0);
+                    if (q < n) v[i] = *reinterpret_cast<const float4 *>(a.carry + (2 * (c + q) + (q == 0 ? 1 : 0)) * a.ldc + col);
+                }
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    sum.x += v[i].x;
+                    sum.y += v[i].y;
+                    sum.z += v[i].z;
+                    sum.w += v[i].w;
+                }
+            }
+        }
+        part[warp][lane] = sum;
+        __syncthreads();
+        if (warp == 0) {
+            float f[4] = {0, 0, 0, 0};
+            for (int w = 0; w < kWarps; ++w) {
+                f[0] += part[w][lane].x;
+                f[1] += part[w][lane].y;
+                f[2] += part[w][lane].z;
+                f[3] += part[w][lane].w;
+            }
+            O *p = out + static_cast<int64_t>(row) * ldo + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col + j < a.d) p[j] = from_f32<O>(a.accumulate ? fmaf(f[j], a.scale, to_f32(p[j])) : f[j] * a.scale);
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, typename O>
+cudaError_t launch_sums(int values, const SumArgs &a, int64_t chunks, const void *dx, int64_t lddx, void *out, int64_t ldo,
+                        cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto go = [&](auto n_values, auto per_lane) {
+        constexpr int kN = decltype(n_values)::value, kU = decltype(per_lane)::value;
+        SumArgs b = a;
+        b.parts = ceil_div(a.d, 32 * kU * kN);
+        cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(chunks * b.parts, kWarps)));
+        return cudaLaunchKernelEx(&cfg, k_embed_sum<T, O, kN, kU>, b, static_cast<const T *>(dx), lddx, static_cast<O *>(out), ldo);
+    };
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 2> two;
+    constexpr std::integral_constant<int, 4> four;
+    constexpr std::integral_constant<int, 8> eight;
+    cudaError_t e;
+    if (values == 1) e = go(one, four);
+    else if (values == 2) e = go(two, four);
+    else if (values == 4) e = go(four, two);
+    else if constexpr (sizeof(T) == 2) e = go(eight, two);
+    else e = cudaErrorInvalidValue;
+    if (e != cudaSuccess || chunks < 2) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(chunks, kJoinChunks)), static_cast<unsigned>(ceil_div(a.d, kJoinCols)));
+    return cudaLaunchKernelEx(&cfg, k_embed_join<O>, a, static_cast<O *>(out), ldo);
+}
+
+constexpr int64_t kMaxEmbedWidth = 65535 * kJoinCols;  // a grid's second dimension
+
+int check_embed(int64_t tokens, int64_t vocab, int64_t d) {
+    if (tokens < 0 || tokens >= int64_t(1) << 31) return refuse("tokens must lie in [0, 2^31)");
+    if (vocab < 1 || vocab >= int64_t(1) << 31) return refuse("vocab must lie in [1, 2^31)");
+    if (d < 0 || d > kMaxEmbedWidth) return refuse("d must lie in [0, " + std::to_string(kMaxEmbedWidth) + "]");
+    if (tokens * ceil_div(d, 128) >= int64_t(1) << 33) return set_error(SPMV_ERR_TOO_LARGE, "tokens * d must be below 2^40");
+    return SPMV_OK;
+}
+
+// The parts of the gradient's workspace, each at a multiple of 16 bytes.
+struct EmbedSpace {
+    int64_t key[2], src[2], count, carry, bytes;
+    int64_t chunks, ldc;
+};
+EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t d) {
+    EmbedSpace w;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += ceil_div(bytes, 16) * 16;
+        return here;
+    };
+    const bool one = sort_shape(tokens, vocab).passes == 1;
+    w.key[0] = take(tokens * 4);
+    w.src[0] = take(tokens * 4);
+    w.key[1] = one ? 0 : take(tokens * 4);
+    w.src[1] = one ? 0 : take(tokens * 4);
+    w.count = take(4);
+    w.chunks = ceil_div(tokens, chunk_entries(tokens));
+    w.ldc = ceil_div(d, 4) * 4;
+    w.carry = take(w.chunks > 1 ? w.chunks * 2 * w.ldc * 4 : 0);
+    w.bytes = at;
+    return w;
+}
+
+}  // namespace
+}  // namespace spmv
+
+using namespace spmv;
+
+extern "C" SPMV_API int spmv_embed_rows(int64_t tokens, int64_t vocab, int64_t d, const int32_t *ids, const void *table,
+                                        int64_t ldtable, double scale, void *x, int64_t ldx, int dtype, void *stream) {
+    SPMV_TRY(check_embed(tokens, vocab, d));
+    if (!row_dtype_ok(dtype)) return refuse("dtype must be SPMV_F32, SPMV_F16 or SPMV_BF16");
+    if (tokens == 0 || d == 0) return SPMV_OK;
+    SPMV_TRY(check_array(ids, "ids", 4));
+    SPMV_TRY(check_matrix(table, "table", vocab, d, ldtable, dtype));
+    SPMV_TRY(check_matrix(x, "x", tokens, d, ldx, dtype));
+    const int vb = row_value_bytes(dtype);
+    const size_t out = span_bytes(tokens, d, ldx, vb);
+    SPMV_TRY(check_apart(x, out, "x", table, span_bytes(vocab, d, ldtable, vb), "table"));
+    SPMV_TRY(check_apart(x, out, "x", ids, static_cast<size_t>(tokens) * 4, "ids"));
+    const int unit = unit_bytes(vb, d, {{table, ldtable}, {x, ldx}});
+    const float f = static_cast<float>(scale);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == SPMV_F32) launch_embed<float>(unit, tokens, vocab, d, f, ids, table, ldtable, x, ldx, s);
+    else if (dtype == SPMV_F16) launch_embed<__half>(unit, tokens, vocab, d, f, ids, table, ldtable, x, ldx, s);
+    else launch_embed<__nv_bfloat16>(unit, tokens, vocab, d, f, ids, table, ldtable, x, ldx, s);
+    SPMV_TRY_CUDA(cudaGetLastError());
+    return SPMV_OK;
+}
+
+extern "C" SPMV_API int64_t spmv_embed_workspace(int64_t tokens, int64_t vocab, int64_t d) {
+    SPMV_TRY(check_embed(tokens, vocab, d));
+    return embed_space(tokens, vocab, d).bytes;
+}
+
+extern "C" SPMV_API int spmv_embed_rows_grad(int64_t tokens, int64_t vocab, int64_t d, const int32_t *ids, const void *dx,
+                                             int64_t lddx, int dtype, double scale, int accumulate, void *dtable,
+                                             int64_t lddtable, int out_dtype, void *workspace, int64_t workspace_bytes,
+                                             void *stream) {
+    SPMV_TRY(check_embed(tokens, vocab, d));
+    if (!row_dtype_ok(dtype)) return refuse("dtype must be SPMV_F32, SPMV_F16 or SPMV_BF16");
+    if (out_dtype != dtype && out_dtype != SPMV_F32) return refuse("out_dtype must be dtype or SPMV_F32");
+    if (d == 0 || (tokens == 0 && accumulate)) return SPMV_OK;
+    const EmbedSpace w = embed_space(tokens, vocab, d);
+    if (workspace_bytes < w.bytes) return refuse("the workspace has fewer bytes than spmv_embed_workspace says");
+    SPMV_TRY(check_matrix(dtable, "dtable", vocab, d, lddtable, out_dtype));
+    SPMV_TRY(check_array(workspace, "workspace", 16));
+    SPMV_TRY(check_matrix(dx, "dx", tokens, d, lddx, dtype));
+    if (tokens) SPMV_TRY(check_array(ids, "ids", 4));
+    const int vb = row_value_bytes(dtype), vo = row_value_bytes(out_dtype);
+    const struct { const void *p; size_t bytes; const char *name; } arrays[] = {
+        {ids, static_cast<size_t>(tokens) * 4, "ids"}, {dx, span_bytes(tokens, d, lddx, vb), "dx"},
+        {dtable, span_bytes(vocab, d, lddtable, vo), "dtable"}, {workspace, static_cast<size_t>(w.bytes), "workspace"}};
+    for (int i = 2; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            SPMV_TRY(check_apart(arrays[i].p, arrays[i].bytes, arrays[i].name, arrays[j].p, arrays[j].bytes, arrays[j].name));
+
+    char *base = static_cast<char *>(workspace);
+    const SortShape shape = sort_shape(tokens, vocab);
+    SortArgs sort{tokens, vocab, shape.passes, shape.bits, ids, {}, {}, reinterpret_cast<int32_t *>(base + w.count)};
+    for (int i = 0; i < 2; ++i) {
+        sort.key[i] = reinterpret_cast<int32_t *>(base + w.key[i]);
+        sort.src[i] = reinterpret_cast<int32_t *>(base + w.src[i]);
+    }
+    const ZeroArgs zero{static_cast<char *>(dtable), vocab, d * vo, lddtable * vo};
+    // CTAs that write zeros: two fit an SM; at least 64 KB each
+    int64_t fill = 0;
+    if (!accumulate) {
+        fill = ceil_div(vocab * d * vo, 64 * 1024);
+        if (fill > 2 * kSms - shape.ctas) fill = 2 * kSms - shape.ctas;
+        fill = ceil_div(fill, shape.ctas) * shape.ctas;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (shape.smem > 48 * 1024)
+        SPMV_TRY_CUDA(cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shape.smem)));
+    SPMV_TRY_CUDA(launch_rows(k_embed_sort, shape.ctas + fill, kSortThreads, shape.ctas, shape.smem, s, sort, zero, shape.ctas));
+    if (tokens == 0) return SPMV_OK;
+    // values of a lane's unit: what the alignment of both matrices' rows allows
+    const int in = unit_bytes(vb, d, {{dx, lddx}}) / vb, to = unit_bytes(vo, d, {{dtable, lddtable}});
+    const int values = to == 16 ? in : (in < to / vo ? in : to / vo);
+    const SumArgs sum{d, chunk_entries(tokens), 1, static_cast<float>(scale), accumulate, sort.key[0], sort.src[0], sort.count,
+                      reinterpret_cast<float *>(base + w.carry), w.ldc};
+    cudaError_t e;
+    if (dtype == SPMV_F32) e = launch_sums<float, float>(values, sum, w.chunks, dx, lddx, dtable, lddtable, s);
+    else if (dtype == SPMV_F16 && out_dtype == SPMV_F16) e = launch_sums<__half, __half>(values, sum, w.chunks, dx, lddx, dtable, lddtable, s);
+    else if (dtype == SPMV_F16) e = launch_sums<__half, float>(values, sum, w.chunks, dx, lddx, dtable, lddtable, s);
+    else if (out_dtype == SPMV_BF16) e = launch_sums<__nv_bfloat16, __nv_bfloat16>(values, sum, w.chunks, dx, lddx, dtable, lddtable, s);
+    else e = launch_sums<__nv_bfloat16, float>(values, sum, w.chunks, dx, lddx, dtable, lddtable, s);
+    SPMV_TRY_CUDA(e);
+    return SPMV_OK;
+}

@@ -6,9 +6,7 @@
 // <dy[t], ys[slot]> that are the gradient of R's values.  Every kernel is bound by its rows'
 // bytes, so each row is read once and written once, tokens first: a token's row sits in
 // registers while its k sorted copies are written (or its k sorted rows are summed).
-#include <initializer_list>
 #include <type_traits>
-#include <utility>
 
 #include "device_util.cuh"
 #include "rows_common.cuh"
@@ -204,17 +202,6 @@ __global__ void __launch_bounds__(kPlanThreads) k_route_place(int64_t entries, i
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 
-template <int kBytes>
-struct Unit;
-template <>
-struct Unit<16> { using type = uint4; };
-template <>
-struct Unit<8> { using type = uint2; };
-template <>
-struct Unit<4> { using type = uint32_t; };
-template <>
-struct Unit<2> { using type = uint16_t; };
-
 // Zero the sorted rows without a source among 32 that the CTA looks at: padding comes in runs
 // (behind each segment, and behind the last), so the CTA's warps take turns.
 constexpr int kPadRows = 32;  // per CTA
@@ -278,24 +265,6 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(int64_t tokens, int k,
                 if (u0 + i * 32 < units) dst[u0 + i * 32] = v[i];
         }
     }
-}
-
-// values of one unit of type T (kBytes >= sizeof(T)) as floats
-template <typename T, typename U>
-__device__ __forceinline__ void unit_to_f32(const U &u, float *out) {
-    constexpr int kN = sizeof(U) / sizeof(T);
-    const T *p = reinterpret_cast<const T *>(&u);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) out[i] = to_f32(p[i]);
-}
-template <typename T, typename U>
-__device__ __forceinline__ U unit_from_f32(const float *in) {
-    constexpr int kN = sizeof(U) / sizeof(T);
-    U u;
-    T *p = reinterpret_cast<T *>(&u);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) p[i] = from_f32<T>(in[i]);
-    return u;
 }
 
 // y[t] = sum over j of weights[t, j] ys[slots[t, j]], j ascending, in 32 bits, rounded once.  A
@@ -425,17 +394,6 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_grad(int64_t pad_ctas, 
     }
 }
 
-// The widest unit (16, 8, 4 or 2 bytes, at least the value size) that every row of every
-// array starts on and that divides a row's bytes.
-int unit_bytes(int value_size, int64_t d, std::initializer_list<std::pair<const void *, int64_t>> arrays) {
-    uint64_t bits = static_cast<uint64_t>(d) * value_size;
-    for (const auto &a : arrays)
-        bits |= reinterpret_cast<uintptr_t>(a.first) | static_cast<uint64_t>(a.second) * value_size;
-    for (int b = 16; b > value_size; b /= 2)
-        if (bits % b == 0) return b;
-    return value_size;
-}
-
 int check_route(int64_t tokens, int32_t k, int64_t rows) {
     if (tokens < 0 || tokens >= (int64_t(1) << 31)) return refuse("tokens must lie in [0, 2^31)");
     if (k < 1) return refuse("k must be at least 1");
@@ -443,27 +401,6 @@ int check_route(int64_t tokens, int32_t k, int64_t rows) {
     if (rows < 0 || rows >= (int64_t(1) << 31)) return refuse("rows must lie in [0, 2^31)");
     return SPMV_OK;
 }
-
-int check_matrix(const void *p, const char *name, int64_t rows, int64_t d, int64_t ld, int dtype) {
-    SPMV_TRY(check_shape(rows, d, ld, name));
-    return rows && d ? check_array(p, name, row_value_bytes(dtype)) : SPMV_OK;
-}
-
-// An output shares no byte with an input (both matrices of rows, or plain arrays).
-int check_apart(const void *out, size_t out_bytes, const char *out_name, const void *in, size_t in_bytes,
-                const char *in_name) {
-    if (out && in && out_bytes && in_bytes && spans_overlap(out, out_bytes, in, in_bytes))
-        return refuse(std::string(out_name) + " overlaps " + in_name);
-    return SPMV_OK;
-}
-
-#define SPMV_UNIT_SWITCH(bytes, CALL)      \
-    switch (bytes) {                       \
-        case 16: CALL(16); break;          \
-        case 8: CALL(8); break;            \
-        case 4: CALL(4); break;            \
-        default: CALL(2); break;           \
-    }
 
 // Units of a row that a lane of k_dispatch holds: 64 bytes where they are 16 (16384 tokens x 4 of 2048 bf16
 // values: 53.4 us; with two 52.6, with eight 55.6), else eight (8192 x 4 of 4095 bf16 values:

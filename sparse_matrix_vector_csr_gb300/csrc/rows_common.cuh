@@ -10,7 +10,9 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <string>
+#include <utility>
 
 #include "spmv_internal.cuh"
 
@@ -325,6 +327,38 @@ __device__ __forceinline__ void stream_back(const Share<T> &sh, int t, int worke
 }
 
 // ----------------------------------------------------------------------------
+// a row as units: the widest loads and stores that every row's address allows
+// ----------------------------------------------------------------------------
+template <int kBytes>
+struct Unit;
+template <>
+struct Unit<16> { using type = uint4; };
+template <>
+struct Unit<8> { using type = uint2; };
+template <>
+struct Unit<4> { using type = uint32_t; };
+template <>
+struct Unit<2> { using type = uint16_t; };
+
+// values of one unit of type T (kBytes >= sizeof(T)) as floats
+template <typename T, typename U>
+__device__ __forceinline__ void unit_to_f32(const U &u, float *out) {
+    constexpr int kN = sizeof(U) / sizeof(T);
+    const T *p = reinterpret_cast<const T *>(&u);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) out[i] = to_f32(p[i]);
+}
+template <typename T, typename U>
+__device__ __forceinline__ U unit_from_f32(const float *in) {
+    constexpr int kN = sizeof(U) / sizeof(T);
+    U u;
+    T *p = reinterpret_cast<T *>(&u);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) p[i] = from_f32<T>(in[i]);
+    return u;
+}
+
+// ----------------------------------------------------------------------------
 // arithmetic
 // ----------------------------------------------------------------------------
 // 2^x by the hardware unit: relative error about 2^-22, below the rounding of an argument of
@@ -581,6 +615,38 @@ inline int check_shape(int64_t rows, int64_t n, int64_t ld, const char *name) {
     if (ld < n || ld >= (int64_t(1) << 31)) return refuse(std::string(name) + ": the leading dimension is below the row length or too large");
     return SPMV_OK;
 }
+
+// The widest unit (16, 8, 4 or 2 bytes, at least the value size) that every row of every
+// array starts on and that divides a row's bytes.
+inline int unit_bytes(int value_size, int64_t d, std::initializer_list<std::pair<const void *, int64_t>> arrays) {
+    uint64_t bits = static_cast<uint64_t>(d) * value_size;
+    for (const auto &a : arrays)
+        bits |= reinterpret_cast<uintptr_t>(a.first) | static_cast<uint64_t>(a.second) * value_size;
+    for (int b = 16; b > value_size; b /= 2)
+        if (bits % b == 0) return b;
+    return value_size;
+}
+
+inline int check_matrix(const void *p, const char *name, int64_t rows, int64_t d, int64_t ld, int dtype) {
+    SPMV_TRY(check_shape(rows, d, ld, name));
+    return rows && d ? check_array(p, name, row_value_bytes(dtype)) : SPMV_OK;
+}
+
+// An output shares no byte with an input (both matrices of rows, or plain arrays).
+inline int check_apart(const void *out, size_t out_bytes, const char *out_name, const void *in, size_t in_bytes,
+                const char *in_name) {
+    if (out && in && out_bytes && in_bytes && spans_overlap(out, out_bytes, in, in_bytes))
+        return refuse(std::string(out_name) + " overlaps " + in_name);
+    return SPMV_OK;
+}
+
+#define SPMV_UNIT_SWITCH(bytes, CALL)      \
+    switch (bytes) {                       \
+        case 16: CALL(16); break;          \
+        case 8: CALL(8); break;            \
+        case 4: CALL(4); break;            \
+        default: CALL(2); break;           \
+    }
 
 }  // namespace rows
 }  // namespace spmv

@@ -1,11 +1,15 @@
 """Sparse rows: at most k entries in every row of a matrix that is made anew at each step.
 
+    x = spmv.embed_rows(table, tokens)                              # rows of a table by token
     top = spmv.topk_rows(router_logits, k, weights="selected")     # a router's choice
     plan = spmv.RoutePlan(top.ids, experts, align=128)              # rows sorted by expert
     xs = plan.dispatch(x)                                           # tokens out ...
-    y = plan.combine(ys, top.weights)                               # ... and back, weighted
-    dys, dw = plan.combine_grad(dy, ys, top.weights)
+    ff = plan.feed_forward(xs, w_gate, w_up, w_down, keep=True)     # ... through their experts' blocks ...
+    y = plan.combine(ff.y, top.weights)                             # ... and back, weighted
+    dys, dw = plan.combine_grad(dy, ff.y, top.weights)
+    dxs, dw_gate, dw_up, dw_down = ff.grad(dys)
     dx, dlogits = plan.dispatch_grad(dxs), top.grad(dw)
+    dtable = spmv.embed_rows_grad(dx, tokens, vocab)
 
     t = spmv.topk_rows(teacher_logits, 64, lse=True)                # a teacher's top logits
     loss, dz = spmv.distill_loss_grad(z, t.ids, t.vals, teacher_lse=t.lse, scale=1 / len(z))
@@ -23,7 +27,7 @@ import functools
 
 import torch
 
-from ._abi import SPMV_BF16, SPMV_F16, SPMV_F32, WEIGHTINGS, _check, lib
+from ._abi import ACTIVATIONS, SPMV_BF16, SPMV_F16, SPMV_F32, WEIGHTINGS, _check, lib
 
 _DTYPES = {torch.float32: SPMV_F32, torch.float16: SPMV_F16, torch.bfloat16: SPMV_BF16}
 _F32, _I32, _empty = torch.float32, torch.int32, torch.empty
@@ -240,6 +244,13 @@ class RoutePlan:
         """The gradient of dispatch: dx[t] = sum over j of dxs[slots[t, j]]."""
         return self.combine(dxs, None, out, stream)
 
+    def feed_forward(self, xs, w_gate, w_up, w_down, activation="silu", keep=False, out=None, stream=None):
+        """Each expert's gated feed-forward block over its segment of xs (rows x d): see
+        :func:`feed_forward`, with weights of one more leading dimension (experts).  Rows behind the
+        last segment become 0."""
+        offsets = _plain(self.offsets, "offsets", (self.experts + 1,), _I32) and self.offsets
+        return _feed_forward(xs, w_gate, w_up, w_down, activation, keep, out, stream, offsets, self.experts, self.rows)
+
 
 class DistillLoss:
     """``loss`` (float32, one a row, neither averaged nor scaled) and what its gradient needs."""
@@ -317,3 +328,136 @@ def distill_loss_grad(z, ids, teacher, teacher_lse=None, temperature=1.0, scale=
     _check(lib.spmv_distill_loss_grad(rows, vocab, ids.shape[1], z.data_ptr(), ldz, code, i, t, tcode, lse, temperature,
                                       loss.data_ptr(), scale, g, dz.data_ptr(), lddz, _current(z)))
     return loss, dz
+
+
+def _weights(t, name, experts, rows, cols, dtype):
+    """(row stride, expert stride) of a matrix, or of `experts` matrices, of row-major rows."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    shape = (rows, cols) if experts is None else (experts, rows, cols)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    ld = t.stride(-2) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    one = (rows - 1) * ld + cols
+    apart = t.stride(0) if experts is not None and experts > 1 else one
+    if apart < one:
+        raise ValueError(f"{name} has overlapping or interleaved experts")
+    return ld, apart
+
+
+def _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, stream, offsets, experts, rows):
+    if stream is not None:
+        with _on(stream, x, w_gate, w_up, w_down, out, offsets):
+            return _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, None, offsets, experts, rows)
+    code, ldx = _matrix(x, "x", rows)
+    rows, d = x.shape
+    if w_gate.dim() != (2 if experts is None else 3):
+        raise ValueError("w_gate must be a matrix" if experts is None else "w_gate must be experts x f x d")
+    f, dtype, device = w_gate.shape[-2], x.dtype, x.device
+    ldw, apart = _weights(w_gate, "w_gate", experts, f, d, dtype)
+    if _weights(w_up, "w_up", experts, f, d, dtype) != (ldw, apart):
+        raise ValueError("w_up must have the strides of w_gate")
+    ldd, apart_d = _weights(w_down, "w_down", experts, d, f, dtype)
+    act = ACTIVATIONS[activation]
+    res = FeedForward()
+    res.gate = res.up = None
+    wide = (f + 7) // 8 * 8  # rows that the tensor cores can be fed from
+    if keep:
+        res.gate, res.up = _empty((2, rows, wide), dtype=dtype, device=device)[:, :, :f].unbind(0)
+    res.y, ldy = _out(out, "out", x, rows, d)
+    work = _check(lib.spmv_feed_forward_workspace(rows, d, f, code, 0))
+    space = _empty((work,), dtype=torch.uint8, device=device)
+    call = (rows, d, f, experts or 1, None if offsets is None else offsets.data_ptr(), x.data_ptr() or None, ldx,
+            w_gate.data_ptr(), w_up.data_ptr(), ldw, apart, w_down.data_ptr(), ldd, apart_d, act,
+            res.gate.data_ptr() if keep else None, res.up.data_ptr() if keep else None, wide)
+    _check(lib.spmv_feed_forward(*call, res.y.data_ptr(), ldy, code, space.data_ptr() or None, work, _current(x)))
+    res._call, res._held = (call, code) if keep else None, (x, w_gate, w_up, w_down, offsets, res.gate, res.up)
+    return res
+
+
+class FeedForward:
+    """``y``, and with keep the ``gate`` and ``up`` rows that the gradient needs."""
+
+    __slots__ = ("y", "gate", "up", "_call", "_held")
+
+    def grad(self, dy, weights=True, out=None, stream=None):
+        """(dx, dw_gate, dw_up, dw_down) for dy, the loss's gradient in y; the last three None without
+        ``weights``.  Neither the call's inputs nor gate and up may have been changed in place."""
+        if self._call is None:
+            raise ValueError("feed_forward was called without keep")
+        if stream is not None:
+            with _on(stream, *self._held, dy, out):
+                return self.grad(dy, weights, out)
+        call, code = self._call
+        rows, d, f = call[:3]
+        x, w_gate, w_up, w_down = self._held[:4]
+        lddy = _matrix(dy, "dy", rows, d, x.dtype)[1]
+        dx, lddx = _out(out, "out", x, rows, d)
+        dws = [_empty(w.shape, dtype=x.dtype, device=x.device) if weights else None for w in (w_gate, w_up, w_down)]
+        work = _check(lib.spmv_feed_forward_workspace(rows, d, f, code, 1))
+        space = _empty((work,), dtype=torch.uint8, device=x.device)
+        _check(lib.spmv_feed_forward_grad(*call, dy.data_ptr() or None, lddy, dx.data_ptr() or None, lddx,
+                                          *[None if w is None else w.data_ptr() for w in dws], code,
+                                          space.data_ptr() or None, work, _current(x)))
+        return (dx, *dws)
+
+
+def feed_forward(x, w_gate, w_up, w_down, activation="silu", keep=False, out=None, stream=None) -> FeedForward:
+    """The gated feed-forward block y = (act(x w_gate^T) * (x w_up^T)) w_down^T of the rows of x
+    (rows x d), with w_gate and w_up f x d (of the same strides) and w_down d x f, all of x's type.
+    ``activation``: "silu", "gelu_tanh" or "relu".  ``keep``: also what :meth:`FeedForward.grad`
+    needs.  :meth:`RoutePlan.feed_forward` is the same for experts."""
+    return _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, stream, None, None, None)
+
+
+def _tokens(ids):
+    if ids.dim() != 1:
+        raise ValueError("ids must be a vector")
+    return _plain(ids, "ids", ids.shape, _I32)
+
+
+def embed_rows(table, ids, scale=1.0, out=None, stream=None):
+    """x[t] = scale * table[ids[t]] (ids int32, one a token; table vocab x d), 0 for an id outside the table
+    (padding: -1)."""
+    if stream is not None:
+        with _on(stream, table, ids, out):
+            return embed_rows(table, ids, scale, out)
+    code, ldt = _matrix(table, "table")
+    vocab, d = table.shape
+    i, tokens = _tokens(ids), ids.shape[0]
+    x, ldx = _out(out, "out", table, tokens, d)
+    _check(lib.spmv_embed_rows(tokens, vocab, d, i, table.data_ptr(), ldt, scale, x.data_ptr(), ldx, code,
+                               _current(table)))
+    return x
+
+
+def embed_rows_grad(dx, ids, vocab, scale=1.0, out=None, accumulate=False, dtype=None, stream=None):
+    """The gradient of :func:`embed_rows` in the table (vocab x d): the sums of scale * dx over each row's
+    tokens.  Its type is dx's, or float32 where ``dtype`` or ``out`` say so.  ``accumulate``: added to
+    ``out``."""
+    if stream is not None:
+        with _on(stream, dx, ids, out):
+            return embed_rows_grad(dx, ids, vocab, scale, out, accumulate, dtype)
+    code, lddx = _matrix(dx, "dx")
+    tokens, d = dx.shape
+    i = _tokens(ids)
+    if ids.shape[0] != tokens:
+        raise ValueError(f"ids must have {tokens} entries, not {ids.shape[0]}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = _empty((vocab, d), dtype=dx.dtype if dtype is None else dtype, device=dx.device)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, not {out.dtype}")
+    out_code, ldo = _matrix(out, "out", vocab, d)
+    if out_code not in (code, SPMV_F32):
+        raise TypeError(f"the gradient must be {dx.dtype} or float32, not {out.dtype}")
+    work = _check(lib.spmv_embed_workspace(tokens, vocab, d))
+    space = _empty((work,), dtype=torch.uint8, device=dx.device)
+    _check(lib.spmv_embed_rows_grad(tokens, vocab, d, i, dx.data_ptr() or None, lddx, code, scale, bool(accumulate),
+                                    out.data_ptr(), ldo, out_code, space.data_ptr(), work, _current(dx)))
+    return out
