@@ -764,6 +764,14 @@ SPMV_API int spmv_feed_forward_grad(int64_t rows, int64_t d, int64_t f, int32_t 
                                     int64_t lddy, void *dx, int64_t lddx, void *dw_gate, void *dw_up, void *dw_down,
                                     int dtype, void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * Synchronise `stream` and report whether a kernel of spmv_feed_forward or spmv_feed_forward_grad on the
+ * current device gave up a bounded wait (for its own copies or products, each about two seconds)
+ * since the last report: SPMV_ERR_TIMEOUT (results of the calls since then are invalid; the flag is
+ * cleared) or SPMV_OK.
+ */
+SPMV_API int spmv_feed_forward_status(void *stream);
+
 #ifdef __cplusplus
 }
 #endif

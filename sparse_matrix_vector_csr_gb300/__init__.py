@@ -67,6 +67,7 @@ from ._abi import (  # noqa: F401
     spmv_feed_forward_workspace,
     spmv_feed_forward,
     spmv_feed_forward_grad,
+    spmv_feed_forward_status,
 )
 
 #: names of ``sparse_rows``, which needs torch and is imported with the first of them (by a star import

@@ -33,6 +33,7 @@ EXPORTS = (
     "spmv_route_dispatch", "spmv_route_combine", "spmv_route_combine_grad", "spmv_distill_loss",
     "spmv_distill_grad", "spmv_distill_loss_grad", "spmv_embed_rows", "spmv_embed_workspace", "spmv_embed_rows_grad",
     "spmv_feed_forward_workspace", "spmv_feed_forward", "spmv_feed_forward_grad",
+    "spmv_feed_forward_status",
 )
 
 #: spmv_weighting codes
@@ -167,6 +168,8 @@ def _load():
     lib.spmv_feed_forward.restype = c_int
     lib.spmv_feed_forward_grad.argtypes = block + [vp, i64, vp, i64, vp, vp, vp, c_int, vp, i64, vp]
     lib.spmv_feed_forward_grad.restype = c_int
+    lib.spmv_feed_forward_status.argtypes = [vp]
+    lib.spmv_feed_forward_status.restype = c_int
     return lib
 
 
@@ -520,3 +523,8 @@ def spmv_feed_forward_grad(rows, d, f, experts, offsets, x, ldx, w_gate, w_up, l
                                       _ptr(up), int(ldg), _ptr(dy), int(lddy), _ptr(dx), int(lddx), _ptr(dw_gate),
                                       _ptr(dw_up), _ptr(dw_down), int(dtype), _ptr(workspace), int(workspace_bytes),
                                       _stream(stream)))
+
+
+def spmv_feed_forward_status(stream=None) -> None:
+    """Synchronise the stream; raise SPMV_ERR_TIMEOUT if a kernel of the feed-forward block gave up a wait."""
+    _check(lib.spmv_feed_forward_status(_stream(stream)))

@@ -23,7 +23,7 @@ LIB_NAME = "libspmv_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["api.cu", "build.cu", "sell.cu", "sellmm.cu", "vector.cu", "merge.cu", "vecops.cu", "noalloc.cu", "solve.cu", "sellg.cu", "order.cu", "sellv.cu", "probe.cu", "sellb.cu",
            "rows_check.cu", "topk.cu", "gate.cu", "route.cu", "distill.cu", "distill_f32.cu", "distill_f16.cu", "distill_bf16.cu",
-           "embed.cu", "ffn.cu", "ffn_simt.cu"]
+           "embed.cu", "ffn.cu", "ffn_simt.cu", "ffn_tc.cu", "ffn_tc_f16.cu", "ffn_tc_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -51,7 +51,7 @@ def _compile(src: str, extra: list[str]) -> str:
     obj = os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o")
     deps = [os.path.join(CSRC, src), os.path.join(CSRC, "spmv_internal.cuh"), os.path.join(CSRC, "device_util.cuh"),
             os.path.join(CSRC, "sell_common.cuh"), os.path.join(CSRC, "rows_common.cuh"),
-            os.path.join(CSRC, "topk.cuh"), os.path.join(CSRC, "distill.cuh"), os.path.join(CSRC, "ffn.cuh"), os.path.join(INCLUDE, "spmv.h")]
+            os.path.join(CSRC, "topk.cuh"), os.path.join(CSRC, "distill.cuh"), os.path.join(CSRC, "ffn.cuh"), os.path.join(CSRC, "ffn_tc.cuh"), os.path.join(INCLUDE, "spmv.h")]
     if _newer(obj, deps):
         return obj
     cmd = [nvcc_path()] + common_flags() + extra + ["-c", os.path.join(CSRC, src), "-o", obj]

@@ -44,6 +44,7 @@ int check_segments(int64_t rows, int32_t experts, const int32_t *offsets) {
     if (!offsets) return experts == 1 ? SPMV_OK : refuse("offsets is NULL, which means one segment of all rows, with experts not 1");
     return check_array(offsets, "offsets", 4);
 }
+using Launch = int (*)(int, const Block &, int, cudaStream_t);
 Matrix matrix(const void *p, int64_t ld, int64_t expert = 0) { return Matrix{const_cast<void *>(p), ld, expert}; }
 
 }  // namespace
@@ -101,7 +102,8 @@ extern "C" SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, in
     b.h = matrix(workspace, padded(f));
     b.y = matrix(y, ldy);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    for (int kind : {kGated, kDown}) SPMV_TRY(launch_simt(kind, b, dtype, s));
+    const Launch run = tc_supported(b, dtype) ? launch_tc : launch_simt;
+    for (int kind : {kGated, kDown}) SPMV_TRY(run(kind, b, dtype, s));
     return SPMV_OK;
 }
 
@@ -158,8 +160,10 @@ extern "C" SPMV_API int spmv_feed_forward_grad(int64_t rows, int64_t d, int64_t 
     b.dwd = matrix(dw_down, f, d * f);
     const bool weights = dw_gate || dw_up || dw_down;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (rows && (dx || weights)) SPMV_TRY(launch_simt(kBack, b, dtype, s));
-    if (rows && dx) SPMV_TRY(launch_simt(kInput, b, dtype, s));
-    if (weights) SPMV_TRY(launch_simt(kWeights, b, dtype, s));
+    // (no rows: the weights' gradients are 0, by the products that need no map of the rows)
+    const Launch run = rows && tc_supported(b, dtype) ? launch_tc : launch_simt;
+    if (rows && (dx || weights)) SPMV_TRY(run(kBack, b, dtype, s));
+    if (rows && dx) SPMV_TRY(run(kInput, b, dtype, s));
+    if (weights) SPMV_TRY(run(kWeights, b, dtype, s));
     return SPMV_OK;
 }

@@ -187,6 +187,11 @@ __host__ __device__ inline int64_t weight_rows(const Block &b, int which) { retu
 // ----------------------------------------------------------------------------
 // ffn_simt.cu: any type and address
 int launch_simt(int kind, const Block &b, int dtype, cudaStream_t s);
+// ffn_tc.cu: 16-bit values in rows that start at multiples of 16 bytes
+bool tc_supported(const Block &b, int dtype);
+int launch_tc(int kind, const Block &b, int dtype, cudaStream_t s);
+int launch_tc_f16(int kind, const Block &b, cudaStream_t s);
+int launch_tc_bf16(int kind, const Block &b, cudaStream_t s);
 
 }  // namespace ffn
 }  // namespace spmv

@@ -1,0 +1,8 @@
+// The feed-forward block's products by the tensor cores for bfloat16 values.
+#include "ffn_tc.cuh"
+
+namespace spmv {
+namespace ffn {
+int launch_tc_bf16(int kind, const Block &b, cudaStream_t s) { return tc::launch_kind<__nv_bfloat16>(kind, b, s); }
+}  // namespace ffn
+}  // namespace spmv

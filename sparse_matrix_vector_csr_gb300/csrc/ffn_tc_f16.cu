@@ -1,0 +1,8 @@
+// The feed-forward block's products by the tensor cores for half values.
+#include "ffn_tc.cuh"
+
+namespace spmv {
+namespace ffn {
+int launch_tc_f16(int kind, const Block &b, cudaStream_t s) { return tc::launch_kind<__half>(kind, b, s); }
+}  // namespace ffn
+}  // namespace spmv
