@@ -1,15 +1,16 @@
 // The products of the feed-forward block by the tensor cores: 16-bit values in matrices whose rows start at
 // multiples of 16 bytes.
 //
-// A CTA an SM, which takes tiles of D in turn.  One warp has the tiles of A and B brought to shared memory
-// (64 of k at a time, a ring of stages), one issues the products of a stage into an accumulator in tensor
-// memory, four read a finished accumulator and write what becomes of it (ffn.cuh, finish) while the next
-// tile's products go to the other accumulator.  Rows of a tile behind its segment's end are read (they
-// belong to the next segment, or lie behind the matrix and read as 0) and their values of D not written;
-// where sums run over rows (kWeights), they are replaced by 0 in shared memory, in A and in B, because 0
-// times a NaN is none.
+// A CTA an SM (or a pair of CTAs on two SMs), which takes tiles of D in turn.  One warp has the tiles of A and B
+// brought to shared memory (64 of k at a time, a ring of stages), one issues the products of a stage into an
+// accumulator in tensor memory, eight read a finished accumulator and write what becomes of it while the
+// next tile's products go to the other accumulator.  A pair has 256 x 256 values of D, each CTA its 128 rows:
+// each brings its rows of A and half of B, and the first CTA's products read both halves, so an SM takes in a
+// third less for each product.  Rows of a tile behind its segment's end are read (they belong to the next
+// segment, or lie behind the matrix and read as 0) and their values of D not written; where sums run over
+// rows (kWeights), they are replaced by 0 in shared memory, in A and in B, because 0 times a NaN is none.
 //
-// Every wait ends after a second or two at the latest: the kernel then sets a flag that
+// Every wait ends after about two seconds at the latest: the kernel then sets a flag that
 // spmv_feed_forward_status reports, lets its copies and products in flight end, gives its tensor memory
 // back and returns.
 #pragma once
@@ -22,19 +23,22 @@ namespace spmv {
 namespace ffn {
 namespace tc {
 
-constexpr int kThreads = 192;     // four warps that write D, one that copies, one that multiplies
-constexpr int kWriters = 4;
+constexpr int kWriters = 8;       // warps that write D; behind them one that copies and one that multiplies
+constexpr int kThreads = (kWriters + 2) * 32;
 constexpr int kRows = 128;        // of a tile of D: the accumulator's lanes
 constexpr int kDepth = 64;        // of a stage: 128 bytes, the width of the swizzle
 constexpr int kRowBytes = 128;
-constexpr int kGroup = 16;        // row tiles that take turns before the next column tile, so that both stay in L2
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr int kGroupRows = 2048;  // of the row tiles that take turns before the next column tile, so that both stay in L2
+constexpr int kSharedBytes = 227 * 1024;
+constexpr int kMaxStages = 16;
+constexpr long long kWaitCycles = 4000000000LL;  // about two seconds
 
 struct Args {
     CUtensorMap a[3], b[3];
     Block block;
     int products;      // kWeights: how many of the three, and
     int which[3];      // which
+    int stages;        // of the ring
     int *failed;
 };
 
@@ -50,6 +54,18 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// the same barrier in the pair's first CTA
+__device__ __forceinline__ uint32_t bar_first(uint32_t bar) {
+    uint32_t there;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(bar));
+    return there;
+}
+// arrives there; kRelease: what the warp wrote to shared memory is seen by whoever waits
+template <bool kRelease>
+__device__ __forceinline__ void bar_arrive_first(uint32_t bar) {
+    if constexpr (kRelease) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_first(bar)) : "memory");
+    else asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_first(bar)) : "memory");
+}
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -61,43 +77,65 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
+// true in one lane of a whole warp.  The copies and products take their operands from registers that a warp
+// shares; where the compiler cannot see that one lane alone is there, it walks over the lanes for each of them.
+__device__ __forceinline__ bool one_lane() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
 }
-// false after kWaitNs, or when another warp has given up
+// false after kWaitCycles, or when another warp has given up (the clock and the flag are looked at now and then only:
+// a wait's end is seen at once)
+template <bool kNap>
 static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up, int *failed) {
-    const unsigned long long t0 = now_ns();
-    while (!bar_try(bar, parity)) {
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i) {
+            if (bar_try(bar, parity)) return true;
+            if (kNap) __nanosleep(64);
+        }
         if (*gave_up) return false;
-        if (now_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitCycles) {
             *gave_up = 1;
             atomicExch(failed, 1);
             return false;
         }
     }
-    return true;
 }
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, int *failed) {
-    return bar_try(bar, parity) || bar_wait_slow(bar, parity, gave_up, failed);
+    return bar_try(bar, parity) || bar_wait_slow<false>(bar, parity, gave_up, failed);
 }
-// the same by a whole warp, one answer for all lanes
+// the same for a whole warp, by one of its lanes; kNap: one that does not mind to see it a little later
+template <bool kNap>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, int *failed) {
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up, failed));
+    bool ok = true;
+    if (one_lane()) ok = bar_try(bar, parity) || bar_wait_slow<kNap>(bar, parity, gave_up, failed);
+    return __all_sync(0xffffffffu, ok);
 }
-// one box of a tensor map to shared memory; the first coordinate is a multiple of 64 values
+// one box of a tensor map to shared memory, counted on a barrier of this CTA or (kPair) of either of the pair; the
+// first coordinate is a multiple of 64 values
+template <bool kPair>
 __device__ __forceinline__ void copy2(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
+    if constexpr (kPair)
+        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                     "l"(map), "r"(x), "r"(y), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                     "l"(map), "r"(x), "r"(y), "r"(bar)
+                     : "memory");
 }
+template <bool kPair>
 __device__ __forceinline__ void copy3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
+    if constexpr (kPair)
+        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                     "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                     : "memory");
 }
 // An operand's tile in shared memory, 128-byte swizzle: along k, rows of 128 bytes (64 of k), eight rows
 // 1024 bytes; along m or n, blocks of 64 of m or n, each of 64 rows (of k) of 128 bytes, so the next eight
@@ -112,33 +150,51 @@ template <bool kAcross>
 constexpr uint32_t kStep = (kAcross ? 16 * kRowBytes : 32) >> 4;
 
 // float accumulator, both operands of one 16-bit type
-template <typename T, int kKind, int kN>
+template <typename T, int kKind, int kN, bool kPair>
 __device__ __forceinline__ constexpr uint32_t product_shape() {
     constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
     return 1u << 4 | type << 7 | type << 10 | (a_transposed(kKind) ? 1u << 15 : 0u) | (b_transposed(kKind) ? 1u << 16 : 0u) |
-           static_cast<uint32_t>(kN >> 3) << 17 | static_cast<uint32_t>(kRows >> 4) << 24;
+           static_cast<uint32_t>(kN >> 3) << 17 | static_cast<uint32_t>((kPair ? 2 : 1) * kRows >> 4) << 24;
 }
+template <bool kPair>
 __device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u)
-        : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u)
+            : "memory");
 }
-// arrives when the products issued so far have been made
+// arrives (at the barrier of both CTAs of a pair) when the products issued so far have been made
+template <bool kPair>
 __device__ __forceinline__ void signal_done(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (kPair)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"(static_cast<uint16_t>(3))
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// 16 columns of the warp's 32 lanes of the accumulator
-__device__ __forceinline__ void read16(uint32_t addr, float *v) {
+// 32 columns of the warp's 32 lanes of the accumulator
+__device__ __forceinline__ void read32(uint32_t addr, float *v) {
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
 __device__ __forceinline__ void read_done() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -204,6 +260,7 @@ struct Tiles {
             r.e = lo;
             const int64_t i = t - prefix[lo] * columns;
             const int m = prefix[lo + 1] - prefix[lo];
+            constexpr int kGroup = kGroupRows / kTileRows;
             const int64_t g = i / (kGroup * columns), j = i - g * kGroup * columns;
             const int64_t in_group = min(static_cast<int64_t>(m) - g * kGroup, static_cast<int64_t>(kGroup));
             const Segments::Span s = b.seg.span(lo);
@@ -249,226 +306,445 @@ __device__ void count_tiles(const Segments &seg, int32_t *prefix) {
 }
 
 // ----------------------------------------------------------------------------
+// D's way out
+// ----------------------------------------------------------------------------
+// A warp's 32 rows x 32 columns of 16-bit values in shared memory: rows of 64 bytes, the 16-byte pieces of two
+// rows placed so that neither a row a lane nor four lanes a row meet in a bank.
+constexpr int kPatchBytes = 32 * 64;
+__device__ __forceinline__ uint32_t patch_piece(uint32_t patch, int row, int piece) {
+    return patch + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint4 patch_load(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void patch_store(uint32_t at, const uint4 &v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// the patch's first `rows` rows to p, `left` of a row's columns there; four lanes a row, 64 bytes
+template <typename T>
+__device__ __forceinline__ void patch_out(uint32_t patch, T *p, int64_t ld, int rows, int64_t left) {
+    const int lane = threadIdx.x & 31, piece = lane & 3;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4;
+        const uint4 v = patch_load(patch_piece(patch, r, piece));
+        if (r < rows) {
+            T *q = p + r * ld + piece * 8;
+            if (left >= piece * 8 + 8) {
+                *reinterpret_cast<uint4 *>(q) = v;
+            } else {
+                const T *values = reinterpret_cast<const T *>(&v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (piece * 8 + j < left) q[j] = values[j];
+            }
+        }
+    }
+    __syncwarp();
+}
+// the lane's row of the patch, rounded to the type
+template <typename T>
+__device__ __forceinline__ void patch_row(uint32_t patch, const float *v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) patch_store(patch_piece(patch, lane, i), pack<T>(v + 8 * i));
+}
+// asks for a patch's values from p (rows and columns outside: 0)
+template <typename T>
+__device__ __forceinline__ void patch_in(uint32_t patch, const T *p, int64_t ld, int rows, int64_t left) {
+    const int lane = threadIdx.x & 31, piece = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4;
+        const int64_t n = r < rows ? min(max(left - piece * 8, int64_t(0)), int64_t(8)) : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(patch_piece(patch, r, piece)),
+                     "l"(n ? p + r * ld + piece * 8 : p), "r"(static_cast<int>(n) * 2)
+                     : "memory");
+    }
+}
+
+// A whole warp: the rows (of k) from `left` to the next multiple of 16 of a stage of kWeights become 0 in A's tile and
+// in kColumns of B's.
+template <int kColumns>
+__device__ __forceinline__ void clear_rows(uint32_t a, uint32_t b, int left) {
+    constexpr int kBlocks = kRows / 64 + kColumns / 64;
+    const int rows = (left + 15) / 16 * 16 - left;
+    for (int j = threadIdx.x & 31; j < rows * kBlocks * 8; j += 32) {
+        const int piece = j & 7, block = (j >> 3) % kBlocks, row = left + (j >> 3) / kBlocks;
+        const uint32_t at = (block < kRows / 64 ? a + block * (kDepth * kRowBytes) : b + (block - kRows / 64) * (kDepth * kRowBytes)) +
+                            row * kRowBytes + piece * 16;
+        patch_store(at, make_uint4(0, 0, 0, 0));
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+// ----------------------------------------------------------------------------
 // the kernel
 // ----------------------------------------------------------------------------
-// kN columns of the accumulator (kGated: kN / 2 of gate, then as many of up); kLoaded rows of A's tile are
+// kN columns of the accumulator (kGated: half of them gate's, then as many of up); kLoaded rows of A's tile are
 // copied where segments are short (the accumulator's other lanes then hold sums of whatever lies behind
-// them in the ring, which nothing reads).
-template <int kKind, int kN, int kLoaded>
+// them in the ring, which nothing reads).  Products that follow on in one accumulator wait for one
+// another, about 150 cycles whatever their size (measured; 4 x 16 of k into one accumulator of 64 columns
+// 325 ns a stage, and copies of 8 KB a stage had to wait): narrow tiles take turns with four.
+template <int kKind, int kN, int kLoaded, bool kPair>
 struct Shape {
+    static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kCols = kKind == kGated ? kN / 2 : kN;
-    static constexpr int kTileRows = kKind == kWeights ? kRows : kLoaded;
-    static constexpr int kABytes = kTileRows * kRowBytes, kBBytes = kN * kRowBytes;
+    static constexpr int kMine = kKind == kWeights ? kRows : kLoaded;  // rows of D that a CTA has
+    static constexpr int kTileRows = kMine * kCtas;
+    static constexpr int kAccs = 256 / kN;
+    static constexpr int kABytes = kMine * kRowBytes, kBBytes = kN / kCtas * kRowBytes;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kSlack = kRows * kRowBytes - kABytes;  // behind the ring: what the last stage's product reads
-    static constexpr int kRoom = 200 * 1024 - kSlack;
-    static constexpr int kStages = kRoom / kStageBytes > 16 ? 16 : kRoom / kStageBytes;
-    static constexpr int kColumns = 2 * kN;  // of tensor memory: two accumulators
-    static size_t smem(int segments) { return 1024 + kStages * kStageBytes + kSlack + (2 * kStages + 5) * 8 + (segments + 2) * 4; }
+    static constexpr int kWriterBytes = kKind == kBack ? 5 * kPatchBytes : kPatchBytes;
+    static constexpr int kFixed = 1024 + kSlack + kWriters * kWriterBytes + (3 * kMaxStages + 5) * 8;
+    static constexpr int kColumns = 2 * kN * kAccs;  // of tensor memory: two buffers
+    static int stages(int segments) {
+        const int n = (kSharedBytes - 256 - kFixed - (segments + 2) * 4) / kStageBytes;
+        return n > kMaxStages ? kMaxStages : n;
+    }
+    static size_t smem(int segments, int stages) { return kFixed + stages * kStageBytes + (segments + 2) * 4; }
 };
 
-template <typename T, int kKind, int kN, int kLoaded>
-__global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Args args, bool whole) {
-    using S = Shape<kKind, kN, kLoaded>;
+template <typename T, int kKind, int kN, int kLoaded, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Args args) {
+    using S = Shape<kKind, kN, kLoaded, kPair>;
     constexpr bool kAcrossA = a_transposed(kKind), kAcrossB = b_transposed(kKind);
-    constexpr int kStages = S::kStages;
     extern __shared__ uint8_t raw[];
     __shared__ uint32_t tmem_at;
     __shared__ int gave_up_at;
+    const int stages = args.stages;
     const uint32_t ring_b = (smem_addr(raw) + 1023) & ~1023u;       // B's stages, then A's: each a multiple of 1024 bytes
-    const uint32_t ring_a = ring_b + kStages * S::kBBytes;
-    const uint32_t bars = ring_a + kStages * S::kABytes + S::kSlack;
+    const uint32_t ring_a = ring_b + stages * S::kBBytes;
+    const uint32_t patches = ring_a + stages * S::kABytes + S::kSlack;
+    const uint32_t bars = patches + kWriters * S::kWriterBytes;
     const auto full = [&](int s) { return bars + 8 * s; };
-    const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-    const auto acc_full = [&](int i) { return bars + 8 * (2 * kStages + i); };
-    const auto acc_empty = [&](int i) { return bars + 8 * (2 * kStages + 2 + i); };
-    const uint32_t drained = bars + 8 * (2 * kStages + 4);
-    int32_t *prefix = reinterpret_cast<int32_t *>(raw + (bars + 8 * (2 * kStages + 5) - smem_addr(raw)));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const auto empty = [&](int s) { return bars + 8 * (kMaxStages + s); };
+    const auto other_full = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };  // the second CTA's stage
+    const auto acc_full = [&](int i) { return bars + 8 * (3 * kMaxStages + i); };
+    const auto acc_empty = [&](int i) { return bars + 8 * (3 * kMaxStages + 2 + i); };
+    const uint32_t drained = bars + 8 * (3 * kMaxStages + 4);
+    int32_t *prefix = reinterpret_cast<int32_t *>(raw + (bars + 8 * (3 * kMaxStages + 5) - smem_addr(raw)));
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (seen to be the warp's)
+    const int rank = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // in the pair
+    const int64_t first = blockIdx.x / S::kCtas, step = gridDim.x / S::kCtas;
     volatile int *gave_up = &gave_up_at;
     int *failed = args.failed;
 
     if (threadIdx.x == 0) {
         gave_up_at = 0;
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             bar_init(full(s), 1);
             bar_init(empty(s), 1);
+            bar_init(other_full(s), 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(acc_full(i), 1);
-            bar_init(acc_empty(i), kWriters);
+            bar_init(acc_empty(i), kWriters * S::kCtas);
         }
         bar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kWriters + 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "n"(S::kColumns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "n"(S::kColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "n"(S::kColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
         fence_before();
     }
     if constexpr (kKind != kWeights) count_tiles<S::kTileRows>(args.block.seg, prefix);
     __syncthreads();
+    if constexpr (kPair) cluster_sync(2);
     fence_after();
     const uint32_t tmem = tmem_at;
     const Tiles<kKind, S::kTileRows, S::kCols> tiles(args, prefix);
     const auto stages_of = [&](const Tile &t) { return static_cast<int>((t.depth + kDepth - 1) / kDepth) * (kKind == kInput ? 2 : 1); };
 
     if (warp == kWriters) {
-        if (lane == 0) {
+        if (one_lane()) {
             int s = 0, round = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+            for (int64_t i = first; ok && i < tiles.total; i += step) {
                 const Tile t = tiles[i];
                 const int n = stages_of(t), once = kKind == kInput ? n / 2 : n;
+                const int row = static_cast<int>(t.row) + rank * S::kMine;
+                // this CTA's part of B: half of the columns (kGated: gate or up)
+                const int col = static_cast<int>(t.col) + (kKind == kGated ? 0 : rank * (kN / S::kCtas));
                 for (int q = 0; q < n; ++q) {
                     if (!(ok = bar_wait(empty(s), (round & 1) ^ 1, gave_up, failed))) break;
-                    bar_expect(full(s), S::kStageBytes);
+                    // a pair's copies are counted by its first CTA, but for a segment's last rows (kWeights), in which each
+                    // CTA has something to clear first
+                    const bool own = !kPair || (kKind == kWeights && t.depth - static_cast<int64_t>(q) * kDepth < kDepth);
+                    const uint32_t bar = own || rank == 0 ? full(s) : bar_first(full(s));
+                    if (own || rank == 0) bar_expect(full(s), own ? S::kStageBytes : 2 * S::kStageBytes);
                     const int pass = q >= once, k = (pass ? q - once : q) * kDepth;
                     const uint32_t a = ring_a + s * S::kABytes, b = ring_b + s * S::kBBytes;
-                    const int row = static_cast<int>(t.row), col = static_cast<int>(t.col);
                     if constexpr (kAcrossA) {
                         const int k0 = static_cast<int>(t.first) + k;
 #pragma unroll
-                        for (int j = 0; j < S::kTileRows / 64; ++j)
-                            copy2(a + j * (kDepth * kRowBytes), &args.a[t.which], row + j * 64, k0, full(s));
+                        for (int j = 0; j < S::kMine / 64; ++j)
+                            copy2<kPair>(a + j * (kDepth * kRowBytes), &args.a[t.which], row + j * 64, k0, bar);
 #pragma unroll
-                        for (int j = 0; j < kN / 64; ++j)
-                            copy2(b + j * (kDepth * kRowBytes), &args.b[t.which], col + j * 64, k0, full(s));
+                        for (int j = 0; j < kN / S::kCtas / 64; ++j)
+                            copy2<kPair>(b + j * (kDepth * kRowBytes), &args.b[t.which], col + j * 64, k0, bar);
                     } else {
-                        copy2(a, &args.a[pass], k, row, full(s));
-                        if constexpr (kKind == kGated) {
-                            copy3(b, &args.b[0], k, col, t.e, full(s));
-                            copy3(b + kN / 2 * kRowBytes, &args.b[1], k, col, t.e, full(s));
+                        copy2<kPair>(a, &args.a[pass], k, row, bar);
+                        if constexpr (kKind == kGated && kPair) {
+                            copy3<kPair>(b, &args.b[rank], k, col, t.e, bar);
+                        } else if constexpr (kKind == kGated) {
+                            copy3<kPair>(b, &args.b[0], k, col, t.e, bar);
+                            copy3<kPair>(b + kN / 2 * kRowBytes, &args.b[1], k, col, t.e, bar);
                         } else if constexpr (kAcrossB) {
 #pragma unroll
-                            for (int j = 0; j < kN / 64; ++j)
-                                copy3(b + j * (kDepth * kRowBytes), &args.b[pass], col + j * 64, k, t.e, full(s));
+                            for (int j = 0; j < kN / S::kCtas / 64; ++j)
+                                copy3<kPair>(b + j * (kDepth * kRowBytes), &args.b[pass], col + j * 64, k, t.e, bar);
                         } else {
-                            copy3(b, &args.b[0], k, col, t.e, full(s));
+                            copy3<kPair>(b, &args.b[0], k, col, t.e, bar);
                         }
                     }
-                    if (++s == kStages) {
+                    if (++s == stages) {
                         s = 0;
                         ++round;
                     }
                 }
             }
             // the ring is empty again (given up: at least every copy has landed)
-            for (int j = 0; j < kStages; ++j) {
+            for (int j = 0; j < stages; ++j) {
                 const int last = j < s ? round : round - 1;  // the round in which the stage was filled last
                 if (last < 0) continue;
                 if (ok) ok = bar_wait(empty(j), last & 1, gave_up, failed);
-                if (!ok) {
-                    const unsigned long long t0 = now_ns();
-                    while (!bar_try(full(j), last & 1) && now_ns() - t0 < kWaitNs) {}
+                if (!ok && rank == 0) {
+                    const long long t0 = clock64();
+                    while (!bar_try(full(j), last & 1) && clock64() - t0 < kWaitCycles) {}
                 }
             }
         }
         __syncwarp();
     } else if (warp == kWriters + 1) {
-        constexpr uint32_t shape = product_shape<T, kKind, kN>();
+        constexpr uint32_t shape = product_shape<T, kKind, kN, kPair>();
         int s = 0, round = 0, done = 0;
+        uint32_t own_parity = 0;  // of the stages' barriers in the second CTA, and of other_full: used for a segment's last rows only
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
-            const Tile t = tiles[i];
-            const int n = stages_of(t);
-            if (n == 0) continue;
-            const int which = done & 1;
-            if (!(ok = warp_wait(acc_empty(which), ((done >> 1) & 1) ^ 1, gave_up, failed))) break;
-            fence_after();
-            const uint32_t d = tmem + which * kN;
-            for (int q = 0; q < n; ++q) {
-                if (!(ok = warp_wait(full(s), round & 1, gave_up, failed))) break;
-                fence_after();
-                const uint32_t a = ring_a + s * S::kABytes, b = ring_b + s * S::kBBytes;
-                int steps = kDepth / 16;
-                if constexpr (kKind == kWeights) {
-                    const int64_t left = t.depth - static_cast<int64_t>(q) * kDepth;
-                    if (left < kDepth) {  // rows of other segments, up to a whole 16 of k
-                        steps = static_cast<int>((left + 15) / 16);
-                        constexpr int kBlocks = kRows / 64 + kN / 64;
-                        const int begin = static_cast<int>(left), rows = steps * 16 - begin;
-                        for (int j = lane; j < rows * kBlocks * 8; j += 32) {
-                            const int piece = j & 7, block = (j >> 3) % kBlocks, row = begin + (j >> 3) / kBlocks;
-                            const uint32_t at = (block < kRows / 64 ? a + block * (kDepth * kRowBytes)
-                                                                    : b + (block - kRows / 64) * (kDepth * kRowBytes)) +
-                                                row * kRowBytes + piece * 16;
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
-                }
-                if (lane == 0) {
-                    uint64_t da = operand<kAcrossA>(a), db = operand<kAcrossB>(b);
-                    for (int k = 0; k < steps; ++k) {
-                        multiply(d, da, db, shape, q > 0 || k > 0);
-                        da += kStep<kAcrossA>;
-                        db += kStep<kAcrossB>;
-                    }
-                    signal_done(empty(s));
-                    if (q == n - 1) signal_done(acc_full(which));
-                }
-                __syncwarp();
-                if (++s == kStages) {
-                    s = 0;
-                    ++round;
-                }
+        const auto next = [&] {
+            if (++s == stages) {
+                s = 0;
+                ++round;
             }
-            ++done;
+        };
+        // by one lane: stage s of a tile, `steps` 16s of k
+        const auto products = [&](int q, int n, int steps) {
+            fence_after();
+            const uint32_t d = tmem + (done & 1) * (kN * S::kAccs);
+            uint64_t da = operand<kAcrossA>(ring_a + s * S::kABytes), db = operand<kAcrossB>(ring_b + s * S::kBBytes);
+#pragma unroll
+            for (int k = 0; k < kDepth / 16; ++k) {
+                if (k < steps) multiply<kPair>(d + k % S::kAccs * kN, da, db, shape, q > 0 || k >= S::kAccs);
+                da += kStep<kAcrossA>;
+                db += kStep<kAcrossB>;
+            }
+            signal_done<kPair>(empty(s));
+            if (q == n - 1) signal_done<kPair>(acc_full(done & 1));
+        };
+        if constexpr (kKind != kWeights) {
+            if (rank == 0 && one_lane())
+                for (int64_t i = first; ok && i < tiles.total; i += step) {
+                    const int n = stages_of(tiles[i]);
+                    if (n == 0) continue;
+                    if (!(ok = bar_wait(acc_empty(done & 1), ((done >> 1) & 1) ^ 1, gave_up, failed))) break;
+                    for (int q = 0; q < n; ++q) {
+                        if (!(ok = bar_wait(full(s), round & 1, gave_up, failed))) break;
+                        products(q, n, kDepth / 16);
+                        next();
+                    }
+                    ++done;
+                }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+        } else {
+            for (int64_t i = first; ok && i < tiles.total; i += step) {
+                const Tile t = tiles[i];
+                const int n = stages_of(t), left = static_cast<int>(t.depth % kDepth);
+                if (n == 0) continue;
+                // one lane has the stages in which nothing is to be cleared, the warp the last one where something is
+                const int alone = left ? n - 1 : n;
+                if (rank == 0) {
+                    if (one_lane()) {
+                        const int s0 = s, round0 = round;
+                        ok = bar_wait(acc_empty(done & 1), ((done >> 1) & 1) ^ 1, gave_up, failed);
+                        for (int q = 0; ok && q < alone; ++q) {
+                            if (!(ok = bar_wait(full(s), round & 1, gave_up, failed))) break;
+                            products(q, n, kDepth / 16);
+                            next();
+                        }
+                        s = s0;
+                        round = round0;
+                    }
+                    __syncwarp();
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                }
+                round += (s + alone) / stages;
+                s = (s + alone) % stages;
+                if (left) {  // rows of other segments, up to a whole 16 of k
+                    if (!(ok = warp_wait<false>(full(s), rank == 0 ? round & 1 : own_parity >> s & 1, gave_up, failed))) break;
+                    clear_rows<kN / S::kCtas>(ring_a + s * S::kABytes, ring_b + s * S::kBBytes, left);
+                    if (kPair && rank == 1) {
+                        if (lane == 0) bar_arrive_first<true>(other_full(s));
+                        __syncwarp();
+                    } else if (kPair) {
+                        if (!(ok = warp_wait<false>(other_full(s), own_parity >> s & 1, gave_up, failed))) break;
+                        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    }
+                    own_parity ^= 1u << s;
+                    if (rank == 0 && one_lane()) products(n - 1, n, (left + 15) / 16);
+                    __syncwarp();
+                    next();
+                }
+                ++done;
+            }
         }
-        if (!ok && lane == 0) {  // given up: the products in flight end before their memory is given back
-            signal_done(drained);
-            const unsigned long long t0 = now_ns();
-            while (!bar_try(drained, 0) && now_ns() - t0 < kWaitNs) {}
+        if (!ok && rank == 0 && one_lane()) {  // given up: the products in flight end before their memory is given back
+            signal_done<kPair>(drained);
+            const long long t0 = clock64();
+            while (!bar_try(drained, 0) && clock64() - t0 < kWaitCycles) {}
         }
         __syncwarp();
     } else {
         int done = 0;
         const Block &b = args.block;
-        for (int64_t i = blockIdx.x; i < tiles.total; i += gridDim.x) {
+        const uint32_t mine = patches + warp * S::kWriterBytes;
+        constexpr int kHalves = S::kCols > 32 ? 2 : 1;  // the two warps of a quarter of the lanes take columns in turn
+        const int quarter = warp & 3, half = warp >> 2;
+        for (int64_t i = first; i < tiles.total; i += step) {
             const Tile t = tiles[i];
             const bool zero = stages_of(t) == 0;
             const int which = done & 1;
+            const int64_t row = t.row + rank * S::kMine + quarter * 32;
+            const int64_t columns = product_columns<kKind>(b, t.which) - t.col;  // from the tile's first on
+            const int rows = half >= kHalves || quarter * 32 >= S::kMine
+                                 ? 0
+                                 : static_cast<int>(max(min(t.end - row, static_cast<int64_t>(min(32, S::kMine))), int64_t(0)));
+            const int width = static_cast<int>(min(columns, static_cast<int64_t>(S::kCols)));
+            const auto at = [&](const Matrix &m, int c) { return static_cast<T *>(m.p) + row * m.ld + t.col + c; };
+            const auto ask = [&](int c) {  // kBack: gate and up of 32 columns, into one of two places
+                const uint32_t to = mine + kPatchBytes * (1 + (c / (32 * kHalves) & 1) * 2);
+                patch_in<T>(to, at(b.gate, c), b.gate.ld, rows, columns - c);
+                patch_in<T>(to + kPatchBytes, at(b.up, c), b.up.ld, rows, columns - c);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            if constexpr (kKind == kBack)
+                if (rows > 0 && half * 32 < width) ask(half * 32);
             if (!zero) {
-                if (!warp_wait(acc_full(which), (done >> 1) & 1, gave_up, failed)) break;
+                if (!warp_wait<true>(acc_full(which), (done >> 1) & 1, gave_up, failed)) break;
                 fence_after();
                 ++done;
             }
-            const int64_t row = t.row + warp * 32 + lane;
-            const bool mine = row < t.end && warp * 32 + lane < S::kTileRows;
-            const uint32_t from = tmem + which * kN + (static_cast<uint32_t>(warp * 32) << 16);
-            const int64_t columns = product_columns<kKind>(b, t.which);
-            if (warp * 32 < S::kTileRows) {
+            const uint32_t from = tmem + which * (kN * S::kAccs) + (static_cast<uint32_t>(quarter * 32) << 16);
+            // accumulators that have been written (kWeights: a segment of few rows leaves the others)
+            const int accs = kKind == kWeights && t.depth < 16 * S::kAccs ? static_cast<int>((t.depth + 15) / 16) : S::kAccs;
+            const auto take = [&](int c, float *v) {
+                read32(from + c, v);
+                read_done();
+                if constexpr (S::kAccs > 1) {
 #pragma unroll 1
-                for (int c = 0; c < S::kCols && t.col + c < columns; c += 16) {
-                    float v[16], w[16];
-                    if (!zero) {
-                        read16(from + c, v);
-                        if constexpr (kKind == kGated) read16(from + kN / 2 + c, w);
+                    for (int a = 1; a < accs; ++a) {
+                        float w[32];
+                        read32(from + a * kN + c, w);
                         read_done();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] += w[j];
+                    }
+                }
+            };
+            const int until = rows > 0 ? width : 0;
+#pragma unroll 1
+            for (int c = half * 32; c < until; c += 32 * kHalves) {
+                float v[32];
+                if (zero) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                } else {
+                    take(c, v);
+                }
+                const int64_t left = columns - c;
+                if constexpr (kKind == kGated) {
+                    float w[32];
+                    if (zero) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) w[j] = 0.0f;
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = w[j] = 0.0f;
+                        take(kN / 2 + c, w);
                     }
-                    if (mine) {
-#pragma unroll
-                        for (int j = 0; j < 16; j += 8)
-                            if (t.col + c + j < columns) finish<T, kKind, 8>(b, t.which, t.e, row, t.col + c + j, v + j, w + j, whole);
+                    if (b.gate.p) {
+                        patch_row<T>(mine, v);
+                        patch_out<T>(mine, at(b.gate, c), b.gate.ld, rows, left);
+                        patch_row<T>(mine, w);
+                        patch_out<T>(mine, at(b.up, c), b.up.ld, rows, left);
                     }
+                    if (!zero) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = activate<false>(v[j], b.act).value * w[j];
+                        // rounded to the type: the next product takes it so (one rounding of each term of y's sums)
+                        patch_row<T>(mine, v);
+                        patch_out<T>(mine, at(b.h, c), b.h.ld, rows, left);
+                    }
+                } else if constexpr (kKind == kBack) {
+                    const uint32_t gate = mine + kPatchBytes * (1 + (c / (32 * kHalves) & 1) * 2), up = gate + kPatchBytes;
+                    if (c + 32 * kHalves < width) {
+                        ask(c + 32 * kHalves);
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    } else {
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    }
+                    __syncwarp();
+                    // each result rounded once, to the type that the next products take
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        float g[8], u[8], h[8];
+                        unpack<T>(patch_load(patch_piece(gate, lane, p)), g);
+                        unpack<T>(patch_load(patch_piece(up, lane, p)), u);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const Activated a = activate<true>(g[j], b.act);
+                            g[j] = v[8 * p + j] * u[j] * a.slope;
+                            h[j] = a.value * u[j];
+                            u[j] = v[8 * p + j] * a.value;
+                        }
+                        patch_store(patch_piece(gate, lane, p), pack<T>(g));
+                        patch_store(patch_piece(up, lane, p), pack<T>(u));
+                        patch_store(patch_piece(mine, lane, p), pack<T>(h));
+                    }
+                    patch_out<T>(gate, at(b.dgate, c), b.dgate.ld, rows, left);
+                    patch_out<T>(up, at(b.dup, c), b.dup.ld, rows, left);
+                    patch_out<T>(mine, at(b.h, c), b.h.ld, rows, left);
+                } else {
+                    const Matrix &m = kKind == kDown ? b.y : kKind == kInput ? b.dx : t.which == 0 ? b.dwg : t.which == 1 ? b.dwu : b.dwd;
+                    patch_row<T>(mine, v);
+                    patch_out<T>(mine, at(m, c) + (kKind == kWeights ? t.e * m.expert : 0), m.ld, rows, left);
                 }
             }
             if (!zero) {
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(acc_empty(which));
+                if (lane == 0) {
+                    if (kPair && rank == 1) bar_arrive_first<false>(acc_empty(which));
+                    else bar_arrive(acc_empty(which));
+                }
             }
         }
     }
     __syncthreads();
+    if constexpr (kPair) cluster_sync(2);  // the other CTA's copies, products and barriers are done with
     if (warp == kWriters + 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kColumns) : "memory");
+        if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kColumns) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kColumns) : "memory");
     }
 }
 
@@ -495,18 +771,20 @@ bool make_map(CUtensorMap *map, const Matrix &m, int64_t n, int64_t rows, int64_
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int kKind, int kN, int kLoaded>
+template <typename T, int kKind, int kN, int kLoaded, bool kPair>
 int launch(const Block &b, cudaStream_t s) {
-    using S = Shape<kKind, kN, kLoaded>;
+    using S = Shape<kKind, kN, kLoaded, kPair>;
     Args args;
     args.block = b;
     args.failed = failure_flag();
     args.products = 0;
     const int64_t rows = b.seg.rows, d = b.d, f = b.f, count = b.seg.count;
+    args.stages = S::stages(static_cast<int>(count));
     const auto activation = [&](CUtensorMap *map, const Matrix &m, int64_t n) {
-        return make_map<T>(map, m, n, rows, 0, kKind == kWeights ? kDepth : S::kTileRows);
+        return make_map<T>(map, m, n, rows, 0, kKind == kWeights ? kDepth : S::kMine);
     };
-    bool ok = true;
+    const auto weight = [&](CUtensorMap *map, const Matrix &m, int64_t n, int64_t m_rows, int box) { return make_map<T>(map, m, n, m_rows, count, box); };
+    bool ok = args.failed != nullptr;
     int64_t tiles = 0;
     if (kKind == kWeights) {
         const Matrix *out[3] = {&b.dwg, &b.dwu, &b.dwd}, *in[3] = {&b.dgate, &b.dup, &b.dy};
@@ -514,43 +792,52 @@ int launch(const Block &b, cudaStream_t s) {
             if (!out[i]->p) continue;
             args.which[args.products++] = i;
             ok = ok && activation(&args.a[i], *in[i], weight_rows(b, i)) && activation(&args.b[i], i == 2 ? b.h : b.x, i == 2 ? f : d);
-            tiles += ceil_div(weight_rows(b, i), kRows) * ceil_div(product_columns<kKind>(b, i), kN) * count;
+            tiles += ceil_div(weight_rows(b, i), S::kTileRows) * ceil_div(product_columns<kKind>(b, i), kN) * count;
         }
     } else if (kKind == kGated) {
-        ok = activation(&args.a[0], b.x, d) && make_map<T>(&args.b[0], b.wg, d, f, count, kN / 2) && make_map<T>(&args.b[1], b.wu, d, f, count, kN / 2);
+        ok = ok && activation(&args.a[0], b.x, d) && weight(&args.b[0], b.wg, d, f, kN / 2) && weight(&args.b[1], b.wu, d, f, kN / 2);
     } else if (kKind == kDown) {
-        ok = activation(&args.a[0], b.h, f) && make_map<T>(&args.b[0], b.wd, f, d, count, kN);
+        ok = ok && activation(&args.a[0], b.h, f) && weight(&args.b[0], b.wd, f, d, kN / S::kCtas);
     } else if (kKind == kBack) {
-        ok = activation(&args.a[0], b.dy, d) && make_map<T>(&args.b[0], b.wd, f, d, count, kDepth);
+        ok = ok && activation(&args.a[0], b.dy, d) && weight(&args.b[0], b.wd, f, d, kDepth);
     } else {
-        ok = activation(&args.a[0], b.dgate, f) && activation(&args.a[1], b.dup, f) && make_map<T>(&args.b[0], b.wg, d, f, count, kDepth) &&
-             make_map<T>(&args.b[1], b.wu, d, f, count, kDepth);
+        ok = ok && activation(&args.a[0], b.dgate, f) && activation(&args.a[1], b.dup, f) && weight(&args.b[0], b.wg, d, f, kDepth) &&
+             weight(&args.b[1], b.wu, d, f, kDepth);
     }
     if (!ok) return set_error(SPMV_ERR_CUDA, "the feed-forward block's matrices could not be described to the copy engine");
     if (kKind != kWeights)
         tiles = ceil_div(product_columns<kKind>(b, 0), S::kCols) * (rows / S::kTileRows + (count < rows ? count : rows) + 1);
-    const size_t smem = S::smem(static_cast<int>(count));
-    SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    k_ffn<T, kKind, kN, kLoaded><<<static_cast<unsigned>(tiles < kSms ? tiles : kSms), kThreads, smem, s>>>(args, true);
-    SPMV_TRY_CUDA(cudaGetLastError());
+    const size_t smem = S::smem(static_cast<int>(count), args.stages);
+    const int64_t workers = kSms / S::kCtas;
+    SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    SPMV_TRY_CUDA(launch_rows(k_ffn<T, kKind, kN, kLoaded, kPair>, (tiles < workers ? tiles : workers) * S::kCtas, kThreads, S::kCtas, smem, s, args));
     return SPMV_OK;
 }
 
+template <typename T, int kKind>
+int launch_shape(const Block &b, cudaStream_t s) {
+    const int64_t rows = b.seg.rows, mean = ceil_div(rows, b.seg.count);  // rows of a segment, taking them as equally long
+    const int64_t columns = product_columns<kKind>(b, 0);
+    if constexpr (kKind == kWeights) {
+        const int64_t tiles = (2 * ceil_div(b.f, 256) * ceil_div(b.d, 256) + ceil_div(b.d, 256) * ceil_div(b.f, 256)) * b.seg.count;
+        if (tiles >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, s);
+        return launch<T, kKind, 64, 128, false>(b, s);
+    } else {
+        if (mean <= 16) return launch<T, kKind, 64, 16, false>(b, s);
+        const int64_t wide = ceil_div(columns, kKind == kGated ? 128 : 256);
+        if (mean >= 192 && ceil_div(rows, 256) * wide >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, s);
+        if (ceil_div(rows, 128) * wide >= kSms) return launch<T, kKind, 256, 128, false>(b, s);
+        return launch<T, kKind, 64, 128, false>(b, s);
+    }
+}
 template <typename T>
 int launch_kind(int kind, const Block &b, cudaStream_t s) {
-    // rows of a segment that a tile has at least, taking segments as equally long
-    const int64_t rows = ceil_div(b.seg.rows, b.seg.count);
-    const bool few = rows <= 16;
-    const auto small = [&](int64_t columns) { return (b.seg.rows / kRows + 1) * columns < kSms; };
     switch (kind) {
-        case kGated: return few ? launch<T, kGated, 64, 16>(b, s) : small(ceil_div(b.f, 128)) ? launch<T, kGated, 64, 128>(b, s) : launch<T, kGated, 256, 128>(b, s);
-        case kDown: return few ? launch<T, kDown, 64, 16>(b, s) : small(ceil_div(b.d, 256)) ? launch<T, kDown, 64, 128>(b, s) : launch<T, kDown, 256, 128>(b, s);
-        case kBack: return few ? launch<T, kBack, 64, 16>(b, s) : small(ceil_div(b.f, 256)) ? launch<T, kBack, 64, 128>(b, s) : launch<T, kBack, 256, 128>(b, s);
-        case kInput: return few ? launch<T, kInput, 64, 16>(b, s) : small(ceil_div(b.d, 256)) ? launch<T, kInput, 64, 128>(b, s) : launch<T, kInput, 256, 128>(b, s);
-        default: {
-            const int64_t tiles = ceil_div(b.f, kRows) * ceil_div(b.d, 256) * b.seg.count;
-            return tiles * 3 < kSms ? launch<T, kWeights, 64, 128>(b, s) : launch<T, kWeights, 256, 128>(b, s);
-        }
+        case kGated: return launch_shape<T, kGated>(b, s);
+        case kDown: return launch_shape<T, kDown>(b, s);
+        case kBack: return launch_shape<T, kBack>(b, s);
+        case kInput: return launch_shape<T, kInput>(b, s);
+        default: return launch_shape<T, kWeights>(b, s);
     }
 }
 
