@@ -90,6 +90,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;
 constexpr int64_t kSortShare = 4096;  // tokens a CTA sorts, at least
+constexpr int kHeld = 8;              // times 32: of a warp's tokens in registers
 
 struct SortShape {
     int ctas;    // a cluster
@@ -114,11 +115,13 @@ struct SortArgs {
     int passes, bits;
     const int32_t *ids;
     int32_t *key[2], *src[2];  // the last pass writes the first of each
-    int32_t *count;            // tokens that are entries
+    int32_t *count;            // tokens that are entries; chunks in whose end a row stays open (0, for k_embed_sum)
 };
 struct ZeroArgs {  // rows x row_bytes at a distance of ld bytes
     char *p;
     int64_t rows, row_bytes, ld;
+    const char *ahead;  // and then to L2: this many lines from here on
+    int64_t ahead_lines;
 };
 
 __device__ __forceinline__ void zero_bytes(char *p, int64_t n, int64_t worker, int64_t workers) {
@@ -147,8 +150,8 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
         } else {
             for (int64_t r = worker / 32; r < z.rows; r += workers / 32) zero_bytes(z.p + r * z.ld, z.row_bytes, lane, 32);
         }
-        dev::allow_dependents();
-        return;
+        for (int64_t i = worker; i < z.ahead_lines; i += workers) asm volatile("prefetch.global.L2 [%0];" ::"l"(z.ahead + i * 128));
+            return;
     }
     const int bins = 1 << a.bits, rank = blockIdx.x;
     int32_t *wcount = shared;                         // [warps][bins]: counts, then next places
@@ -166,22 +169,40 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
         const int64_t run = (end - begin + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32;
         const int64_t r0 = begin + warp * run, r1 = min(end, r0 + run);
         int32_t *mine = wcount + warp * bins;
-        // (from L2: other SMs of the cluster wrote it in the pass before)
-        const auto key_at = [&](int64_t i) { return __ldcg(key_in + i); };
-        const auto digit = [&](int32_t key) { return (key >> shift) & (bins - 1); };
-
+        // kHeld times 32 keys of the warp's run and where their tokens are, all loads at once (from L2: other SMs of
+        // the cluster wrote them in the pass before)
+        int32_t key[kHeld], src[kHeld], found[kHeld];
+        const auto load = [&](int64_t i0) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int64_t at = i0 + i * 32 + lane;
+                key[i] = at < r1 ? __ldcg(key_in + at) : -1;
+                src[i] = src_in && at < r1 ? __ldcg(src_in + at) : static_cast<int32_t>(at);
+            }
+        };
+        // a key's digit, the entries of the same digit in lower lanes and how many have it; -1: no entry
+        const auto match = [&](int32_t k) {
+            const int dig = is_entry(k, a.vocab) ? (k >> shift) & (bins - 1) : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, dig);
+            return dig < 0 ? -1 : dig | __popc(same & ((1u << lane) - 1)) << 10 | __popc(same) << 16;
+        };
+        load(r0);
         for (int i = tid; i < kSortWarps * bins; i += kSortThreads) wcount[i] = 0;
         __syncthreads();
-        for (int64_t i0 = r0; i0 < r1; i0 += 32) {
-            const int32_t key = i0 + lane < r1 ? key_at(i0 + lane) : -1;
-            const int dig = is_entry(key, a.vocab) ? digit(key) : -1;
-            const uint32_t same = __match_any_sync(0xffffffffu, dig);
-            if (dig >= 0 && (same & ((1u << lane) - 1)) == 0) mine[dig] += __popc(same);
-            __syncwarp();
+        for (int64_t i0 = r0; i0 < r1; i0 += 32 * kHeld) {
+            if (i0 != r0) load(i0);
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) found[i] = match(key[i]);
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                if (found[i] >= 0 && (found[i] >> 10 & 63) == 0) mine[found[i] & 1023] += found[i] >> 16;
+                __syncwarp();
+            }
         }
         __syncthreads();
         for (int b = tid; b < bins; b += kSortThreads) {  // (at most one a thread)
             int32_t at = 0;
+#pragma unroll 8
             for (int w = 0; w < kSortWarps; ++w) {
                 const int32_t c = wcount[w * bins + b];
                 wcount[w * bins + b] = at;
@@ -212,52 +233,64 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
         if (lane == 31) warp_part[warp] = incl;
         __syncthreads();
         int32_t at = incl - total, all = 0;
+#pragma unroll 8
         for (int w = 0; w < kSortWarps; ++w) {
             at += w < warp ? warp_part[w] : 0;
             all += warp_part[w];
         }
         if (tid < bins) place0[tid] = at + before;
         __syncthreads();
-        for (int64_t i0 = r0; i0 < r1; i0 += 32) {
-            const int64_t i = i0 + lane;
-            const int32_t key = i < r1 ? key_at(i) : -1;
-            const int dig = is_entry(key, a.vocab) ? digit(key) : -1;
-            const uint32_t same = __match_any_sync(0xffffffffu, dig);
-            const int earlier = __popc(same & ((1u << lane) - 1));
-            const int32_t to = dig >= 0 ? place0[dig] + mine[dig] + earlier : 0;
-            __syncwarp();
-            if (dig >= 0 && earlier == 0) mine[dig] += __popc(same);
-            __syncwarp();
-            if (dig >= 0) {
-                key_out[to] = key;
-                src_out[to] = src_in ? __ldcg(src_in + i) : static_cast<int32_t>(i);
+        for (int64_t i0 = r0; i0 < r1; i0 += 32 * kHeld) {
+            if (run > 32 * kHeld) {
+                load(i0);
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) found[i] = match(key[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int dig = found[i] & 1023, earlier = found[i] >> 10 & 63;
+                const int32_t to = found[i] >= 0 ? place0[dig] + mine[dig] + earlier : -1;
+                __syncwarp();
+                if (found[i] >= 0 && earlier == 0) mine[dig] += found[i] >> 16;
+                __syncwarp();
+                if (to >= 0) {
+                    key_out[to] = key[i];
+                    src_out[to] = src[i];
+                }
             }
         }
         n = all;
         cluster_sync(ctas);  // the places are written, the counts read
     }
-    if (rank == 0 && tid == 0) *a.count = static_cast<int32_t>(n);
+    if (rank == 0 && tid == 0) {
+        a.count[0] = static_cast<int32_t>(n);
+        a.count[1] = 0;
+    }
     dev::allow_dependents();
 }
 
 // ----------------------------------------------------------------------------
 // sums over each row's tokens
 // ----------------------------------------------------------------------------
-constexpr int64_t kMaxChunks = 4096;
-// entries that one warp sums
-int64_t chunk_entries(int64_t tokens) {
-    int64_t c = 32;
-    while (ceil_div(tokens, c) > kMaxChunks) c *= 2;
+// Entries that one warp sums: as few as leave no more than `warps` of them for the pieces of a row that go to warps
+// of their own (a chunk's entries follow one another, so fewer are faster where they fill the GPU), 8 to 64,
+// and more where the carries of 8192 chunks would not do.
+int64_t chunk_entries(int64_t tokens, int64_t d) {
+    int64_t c = 8;
+    while (c < 64 && ceil_div(tokens, c) * ceil_div(d, 256) > 5000) c *= 2;
+    while (ceil_div(tokens, c) > 8192) c *= 2;
     return c;
 }
-constexpr int kJoinChunks = 8;    // per CTA of k_embed_join
-constexpr int kJoinCols = 4 * 32;  // of a row, per CTA
+constexpr int kJoinCols = 4 * 32;  // of a row, per item of k_embed_join
+constexpr int kJoinAlone = 16;     // carries that one warp adds up
 
 struct SumArgs {
     int64_t d, chunk, parts;
     float scale;
     int accumulate;
-    const int32_t *key, *src, *count;
+    const int32_t *key, *src;
+    int32_t *count, *open;  // open: the chunks in whose end a row begun in them stays open
+    uint8_t *through;       // [chunks]: a row comes from the chunk in front and goes on behind
     float *carry;  // [chunks][2][ldc]: sum up to the end of a row begun in front of the chunk; from the start of a row open at its end
     int64_t ldc;
 };
@@ -280,11 +313,10 @@ __device__ __forceinline__ void store_values(O *p, const float *f) {
 }
 
 // A warp sums kU x 32 units of kN values of the rows of one chunk of sorted entries, kR rows' loads in
-// flight, in 32 bits, in the tokens' order.
-template <typename T, typename O, int kN, int kU>
-__global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T *__restrict__ dx, int64_t lddx, O *out, int64_t ldo) {
+// flight (and, where they are added to, the gradient's), in 32 bits, in the tokens' order.
+template <typename T, typename O, int kN, int kU, int kR, bool kAdd>
+__global__ void __launch_bounds__(kThreads, 4) k_embed_sum(SumArgs a, const T *__restrict__ dx, int64_t lddx, O *out, int64_t ldo) {
     using U = typename Unit<kN * static_cast<int>(sizeof(T))>::type;
-    constexpr int kR = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     dev::grid_wait();
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp, c = item / a.parts;
@@ -292,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T *__re
     if (lo >= total) return;
     const int64_t col0 = ((item - c * a.parts) * (32 * kU) + lane) * kN;  // unit i's values: from col0 + i * 32 * kN
     float acc[kU][kN] = {};
-    const auto flush = [&](int32_t row, float *carry) {
+    const auto flush = [&](int32_t row, float *carry, const float (*old)[kN]) {
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
             const int64_t col = col0 + i * 32 * kN;
@@ -301,12 +333,10 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T *__re
 #pragma unroll
                     for (int j = 0; j < kN; ++j) carry[col + j] = acc[i][j];
                 } else {
-                    O *p = out + static_cast<int64_t>(row) * ldo + col;
-                    float f[kN] = {};
-                    if (a.accumulate) load_values<O, kN>(p, f);
+                    float f[kN];
 #pragma unroll
-                    for (int j = 0; j < kN; ++j) f[j] = a.accumulate ? fmaf(acc[i][j], a.scale, f[j]) : acc[i][j] * a.scale;
-                    store_values<O, kN>(p, f);
+                    for (int j = 0; j < kN; ++j) f[j] = kAdd ? fmaf(acc[i][j], a.scale, old[i][j]) : acc[i][j] * a.scale;
+                    store_values<O, kN>(out + static_cast<int64_t>(row) * ldo + col, f);
                 }
             }
 #pragma unroll
@@ -321,14 +351,22 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T *__re
         const int32_t behind = g + n < total ? a.key[g + n] : -1;
         for (int q0 = 0; q0 < n; q0 += kR) {
             U v[kR][kU];
+            float old[kAdd ? kR : 1][kU][kN];
 #pragma unroll
             for (int q = 0; q < kR; ++q) {
                 const int64_t t = __shfl_sync(0xffffffffu, src, q0 + q);
+                const int32_t row = __shfl_sync(0xffffffffu, key, q0 + q), later = __shfl_sync(0xffffffffu, key, (q0 + q + 1) & 31);
                 if (q0 + q < n) {
+                    const bool ends = (q0 + q + 1 < n ? later : behind) != row;
 #pragma unroll
-                    for (int i = 0; i < kU; ++i)
-                        if (col0 + i * 32 * kN < a.d)
-                            v[q][i] = __ldcs(reinterpret_cast<const U *>(dx + t * lddx + col0 + i * 32 * kN));
+                    for (int i = 0; i < kU; ++i) {
+                        const int64_t col = col0 + i * 32 * kN;
+                        if (col < a.d) {
+                            v[q][i] = __ldcs(reinterpret_cast<const U *>(dx + t * lddx + col));
+                            if constexpr (kAdd)
+                                if (ends) load_values<O, kN>(out + static_cast<int64_t>(row) * ldo + col, old[q][i]);
+                        }
+                    }
                 }
             }
 #pragma unroll
@@ -345,10 +383,17 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T *__re
                             for (int j = 0; j < kN; ++j) acc[i][j] += f[j];
                         }
                     if ((q0 + q + 1 < n ? later : behind) != row) {
-                        flush(row, carried ? carry : nullptr);
+                        flush(row, carried ? carry : nullptr, old[kAdd ? q : 0]);
                         carried = false;
                     } else if (q0 + q + 1 == n && g + n == hi) {  // the row goes on in the next chunk
-                        flush(row, carried ? carry : carry + a.ldc);
+                        flush(row, carried ? carry : carry + a.ldc, old[0]);
+                        if (item == c * a.parts && lane == 0) {
+                            if (!carried) a.open[atomicAdd(a.count + 1, 1)] = static_cast<int32_t>(c);
+                            a.through[c] = carried;
+                        }
+                    }
+                    if (q0 + q + 1 == n && g + n == hi && behind != row) {
+                        if (item == c * a.parts && lane == 0) a.through[c] = 0;
                     }
                 }
             }
@@ -358,47 +403,51 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(SumArgs a, const T *__re
 }
 
 // The rows that reach over several chunks: the sum of the open end of the first chunk and what the next
-// chunks have of the row, each warp of a CTA an eighth of those, in a fixed order.
+// chunks have of the row, in a fixed order: one after the other by one warp where they are few, else each warp
+// of the CTA an eighth of them.  An item is kJoinCols columns of one of the rows that k_embed_sum listed.
 template <typename O>
 __global__ void __launch_bounds__(kThreads) k_embed_join(SumArgs a, O *out, int64_t ldo) {
     __shared__ float4 part[kWarps][32];
+    __shared__ int many[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     dev::grid_wait();
-    const int64_t total = *a.count, c0 = static_cast<int64_t>(blockIdx.x) * kJoinChunks;
-    const int64_t mine = c0 + (lane & (kJoinChunks - 1)), lo = mine * a.chunk, hi = lo + a.chunk;
-    bool opens = false;  // a row begins in this chunk and goes on behind it
-    if (hi < total) {
-        const int32_t last = a.key[hi - 1];
-        opens = a.key[hi] == last && !(lo > 0 && a.key[lo] == last && a.key[lo - 1] == last);
-    }
-    uint32_t open = __ballot_sync(0xffffffffu, opens) & ((1u << kJoinChunks) - 1);
-    const int64_t col = static_cast<int64_t>(blockIdx.y) * kJoinCols + lane * 4;
-    for (; open; open &= open - 1) {
-        const int64_t c = c0 + __ffs(open) - 1;
-        const int32_t row = a.key[(c + 1) * a.chunk - 1];
-        int64_t end = c + 1;  // the row's last chunk
+    const int64_t total = a.count[0], opened = a.count[1], items = (a.d + kJoinCols - 1) / kJoinCols * opened;
+    struct Run {
+        int64_t c, n, col;  // first chunk, carries, column
+        int32_t row;
+    };
+    const auto find = [&](int64_t item) {
+        Run r;
+        const int64_t piece = item / opened;  // (a long row's pieces go to CTAs far from one another)
+        r.c = a.open[item - piece * opened];
+        r.col = piece * kJoinCols + lane * 4;
+        r.row = a.key[(r.c + 1) * a.chunk - 1];
+        int64_t end = r.c + 1;  // the row's last chunk: the first behind r.c through which it does not go
         for (;;) {
-            const int64_t behind = (end + lane + 1) * a.chunk;
-            const bool through = behind < total && a.key[behind - 1] == row && a.key[behind] == row;
-            const uint32_t stops = ~__ballot_sync(0xffffffffu, through);
-            if (stops) {
-                end += __ffs(stops) - 1;
+            const bool through = (end + lane + 1) * a.chunk < total && a.through[end + lane];
+            const bool through2 = (end + lane + 33) * a.chunk < total && a.through[end + lane + 32];
+            const uint32_t stops = ~__ballot_sync(0xffffffffu, through), stops2 = ~__ballot_sync(0xffffffffu, through2);
+            if (stops | stops2) {
+                end += stops ? __ffs(stops) - 1 : 31 + __ffs(stops2);
                 break;
             }
-            end += 32;
+            end += 64;
         }
-        // carries of the row: its start in chunk c, then the heads of chunks c + 1 .. end
-        const int64_t n = end - c + 1;
+        r.n = end - r.c + 1;
+        return r;
+    };
+    // carries q0, q0 + every, ...: the row's start in its first chunk, then the heads of the next ones
+    const auto add = [&](const Run &r, int64_t q0, int64_t every) {
         float4 sum = make_float4(0, 0, 0, 0);
-        if (col < a.d) {
-            constexpr int kLoads = 8;
-            for (int64_t q0 = warp; q0 < n; q0 += kWarps * kLoads) {
+        constexpr int kLoads = 16;
+        if (r.col < a.d)
+            for (; q0 < r.n; q0 += every * kLoads) {
                 float4 v[kLoads];
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
-                    const int64_t q = q0 + i * kWarps;
+                    const int64_t q = q0 + i * every;
                     v[i] = make_float4(0, 0, 0, 0);
-                    if (q < n) v[i] = *reinterpret_cast<const float4 *>(a.carry + (2 * (c + q) + (q == 0 ? 1 : 0)) * a.ldc + col);
+                    if (q < r.n) v[i] = *reinterpret_cast<const float4 *>(a.carry + (2 * (r.c + q) + (q == 0 ? 1 : 0)) * a.ldc + r.col);
                 }
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
@@ -408,21 +457,41 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(SumArgs a, O *out, int6
                     sum.w += v[i].w;
                 }
             }
-        }
-        part[warp][lane] = sum;
-        __syncthreads();
-        if (warp == 0) {
-            float f[4] = {0, 0, 0, 0};
-            for (int w = 0; w < kWarps; ++w) {
-                f[0] += part[w][lane].x;
-                f[1] += part[w][lane].y;
-                f[2] += part[w][lane].z;
-                f[3] += part[w][lane].w;
-            }
-            O *p = out + static_cast<int64_t>(row) * ldo + col;
+        return sum;
+    };
+    const auto write = [&](const Run &r, const float4 &sum) {
+        const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+        O *p = out + static_cast<int64_t>(r.row) * ldo + r.col;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (col + j < a.d) p[j] = from_f32<O>(a.accumulate ? fmaf(f[j], a.scale, to_f32(p[j])) : f[j] * a.scale);
+        for (int j = 0; j < 4; ++j)
+            if (r.col + j < a.d) p[j] = from_f32<O>(a.accumulate ? fmaf(f[j], a.scale, to_f32(p[j])) : f[j] * a.scale);
+    };
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kWarps; i0 < items; i0 += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int64_t item = i0 + warp;
+        bool long_one = false;
+        if (item < items) {
+            const Run r = find(item);
+            long_one = r.n > kJoinAlone;
+            if (!long_one) write(r, add(r, 0, 1));
+        }
+        if (lane == 0) many[warp] = long_one;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) {
+            if (!many[w]) continue;
+            const Run r = find(i0 + w);
+            part[warp][lane] = add(r, warp, kWarps);
+            __syncthreads();
+            if (warp == 0) {
+                float4 sum = part[0][lane];
+                for (int k = 1; k < kWarps; ++k) {
+                    sum.x += part[k][lane].x;
+                    sum.y += part[k][lane].y;
+                    sum.z += part[k][lane].z;
+                    sum.w += part[k][lane].w;
+                }
+                write(r, sum);
+            }
+            __syncthreads();
         }
         __syncthreads();
     }
@@ -439,29 +508,36 @@ cudaError_t launch_sums(int values, const SumArgs &a, int64_t chunks, const void
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto go = [&](auto n_values, auto per_lane) {
+    auto go = [&](auto n_values, auto per_lane, auto in_flight, auto add) {
         constexpr int kN = decltype(n_values)::value, kU = decltype(per_lane)::value;
         SumArgs b = a;
         b.parts = ceil_div(a.d, 32 * kU * kN);
         cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(chunks * b.parts, kWarps)));
-        return cudaLaunchKernelEx(&cfg, k_embed_sum<T, O, kN, kU>, b, static_cast<const T *>(dx), lddx, static_cast<O *>(out), ldo);
+        return cudaLaunchKernelEx(&cfg, k_embed_sum<T, O, kN, kU, decltype(in_flight)::value, decltype(add)::value>, b,
+                                  static_cast<const T *>(dx), lddx, static_cast<O *>(out), ldo);
     };
     constexpr std::integral_constant<int, 1> one;
     constexpr std::integral_constant<int, 2> two;
     constexpr std::integral_constant<int, 4> four;
     constexpr std::integral_constant<int, 8> eight;
+    // rows in flight
+    auto either = [&](auto n_values, auto per_lane) {
+        if (!a.accumulate) return go(n_values, per_lane, four, std::false_type{});
+        return go(n_values, per_lane, four, std::true_type{});
+    };
     cudaError_t e;
-    if (values == 1) e = go(one, four);
-    else if (values == 2) e = go(two, four);
-    else if (values == 4) e = go(four, two);
-    else if constexpr (sizeof(T) == 2) e = go(eight, two);
+    if (values == 1) e = either(one, four);
+    else if (values == 2) e = either(two, four);
+    else if (values == 4) e = either(four, two);
+    else if constexpr (sizeof(T) == 2) e = either(eight, one);
     else e = cudaErrorInvalidValue;
     if (e != cudaSuccess || chunks < 2) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(chunks, kJoinChunks)), static_cast<unsigned>(ceil_div(a.d, kJoinCols)));
+    const int64_t items = ceil_div(chunks * ceil_div(a.d, kJoinCols), kWarps);
+    cfg.gridDim = dim3(static_cast<unsigned>(items < 4 * kSms ? items : 4 * kSms));
     return cudaLaunchKernelEx(&cfg, k_embed_join<O>, a, static_cast<O *>(out), ldo);
 }
 
-constexpr int64_t kMaxEmbedWidth = 65535 * kJoinCols;  // a grid's second dimension
+constexpr int64_t kMaxEmbedWidth = int64_t(1) << 23;
 
 int check_embed(int64_t tokens, int64_t vocab, int64_t d) {
     if (tokens < 0 || tokens >= int64_t(1) << 31) return refuse("tokens must lie in [0, 2^31)");
@@ -473,7 +549,7 @@ int check_embed(int64_t tokens, int64_t vocab, int64_t d) {
 
 // The parts of the gradient's workspace, each at a multiple of 16 bytes.
 struct EmbedSpace {
-    int64_t key[2], src[2], count, carry, bytes;
+    int64_t key[2], src[2], count, open, through, carry, bytes;
     int64_t chunks, ldc;
 };
 EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t d) {
@@ -489,8 +565,10 @@ EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t d) {
     w.src[0] = take(tokens * 4);
     w.key[1] = one ? 0 : take(tokens * 4);
     w.src[1] = one ? 0 : take(tokens * 4);
-    w.count = take(4);
-    w.chunks = ceil_div(tokens, chunk_entries(tokens));
+    w.count = take(8);
+    w.chunks = ceil_div(tokens, chunk_entries(tokens, d));
+    w.open = take(w.chunks * 4);
+    w.through = take(w.chunks);
     w.ldc = ceil_div(d, 4) * 4;
     w.carry = take(w.chunks > 1 ? w.chunks * 2 * w.ldc * 4 : 0);
     w.bytes = at;
@@ -558,14 +636,19 @@ extern "C" SPMV_API int spmv_embed_rows_grad(int64_t tokens, int64_t vocab, int6
         sort.key[i] = reinterpret_cast<int32_t *>(base + w.key[i]);
         sort.src[i] = reinterpret_cast<int32_t *>(base + w.src[i]);
     }
-    const ZeroArgs zero{static_cast<char *>(dtable), vocab, d * vo, lddtable * vo};
-    // CTAs that write zeros: two fit an SM; at least 64 KB each
-    int64_t fill = 0;
-    if (!accumulate) {
-        fill = ceil_div(vocab * d * vo, 64 * 1024);
-        if (fill > 2 * kSms - shape.ctas) fill = 2 * kSms - shape.ctas;
-        fill = ceil_div(fill, shape.ctas) * shape.ctas;
+    ZeroArgs zero{static_cast<char *>(dtable), accumulate ? 0 : vocab, d * vo, lddtable * vo, static_cast<const char *>(dx), 0};
+    // The sort alone takes about 15 us, in which 96 MB can be written and read: as much of dx as that leaves room for
+    // waits in L2 for the sums.
+    const int64_t zeros = zero.rows * zero.row_bytes, dx_bytes = static_cast<int64_t>(span_bytes(tokens, d, lddx, vb));
+    if (zeros < 96000000) {
+        zero.ahead = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(dx) & ~uintptr_t(127));
+        const int64_t room = 96000000 - zeros;
+        zero.ahead_lines = (dx_bytes < room ? dx_bytes : room) / 128;
     }
+    // CTAs that do that: two fit an SM; at least 64 KB each
+    int64_t fill = ceil_div(zeros + zero.ahead_lines * 128, 64 * 1024);
+    if (fill > 2 * kSms - shape.ctas) fill = 2 * kSms - shape.ctas;
+    fill = ceil_div(fill, shape.ctas) * shape.ctas;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (shape.smem > 48 * 1024)
         SPMV_TRY_CUDA(cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shape.smem)));
@@ -574,8 +657,8 @@ extern "C" SPMV_API int spmv_embed_rows_grad(int64_t tokens, int64_t vocab, int6
     // values of a lane's unit: what the alignment of both matrices' rows allows
     const int in = unit_bytes(vb, d, {{dx, lddx}}) / vb, to = unit_bytes(vo, d, {{dtable, lddtable}});
     const int values = to == 16 ? in : (in < to / vo ? in : to / vo);
-    const SumArgs sum{d, chunk_entries(tokens), 1, static_cast<float>(scale), accumulate, sort.key[0], sort.src[0], sort.count,
-                      reinterpret_cast<float *>(base + w.carry), w.ldc};
+    const SumArgs sum{d, chunk_entries(tokens, d), 1, static_cast<float>(scale), accumulate, sort.key[0], sort.src[0], sort.count,
+                      reinterpret_cast<int32_t *>(base + w.open), reinterpret_cast<uint8_t *>(base + w.through), reinterpret_cast<float *>(base + w.carry), w.ldc};
     cudaError_t e;
     if (dtype == SPMV_F32) e = launch_sums<float, float>(values, sum, w.chunks, dx, lddx, dtable, lddtable, s);
     else if (dtype == SPMV_F16 && out_dtype == SPMV_F16) e = launch_sums<__half, __half>(values, sum, w.chunks, dx, lddx, dtable, lddtable, s);
