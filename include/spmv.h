@@ -734,14 +734,16 @@ typedef enum { SPMV_ACT_SILU = 0, SPMV_ACT_GELU_TANH = 1, SPMV_ACT_RELU = 2 } sp
  *            e * wd_expert + i * ldwd, in values (16-byte aligned rows run fastest).
  *   gate, up rows x f (leading dimension ldg), what spmv_feed_forward_grad needs of the forward call, or both
  *            NULL.
- * Sums are in 32 bits; h, gate, up and y are each rounded once to the type.  No product of a value that no
+ * Sums are in 32 bits; h, gate, up and y are each rounded once to the type (h of segments of up to 16 rows on
+ * average, whose weights take longer than their products, is kept with what its rounding left out).  No product of a value that no
  * row or matrix holds enters a sum: NaN and infinities of a row stay in that row.
  *   1 <= d, f <= 2^20; 1 <= experts <= 4096.
  * The workspace starts at a multiple of 16 bytes and is free for other use when the call's kernels have run.
  * spmv_feed_forward_workspace gives its bytes (gradient 0: spmv_feed_forward's, else
  * spmv_feed_forward_grad's), or a negative status.
  */
-SPMV_API int64_t spmv_feed_forward_workspace(int64_t rows, int64_t d, int64_t f, int dtype, int gradient);
+SPMV_API int64_t spmv_feed_forward_workspace(int64_t rows, int64_t d, int64_t f, int32_t experts, int dtype,
+                                             int gradient);
 SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, int32_t experts, const int32_t *offsets,
                                const void *x, int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw,
                                int64_t w_expert, const void *w_down, int64_t ldwd, int64_t wd_expert, int activation,

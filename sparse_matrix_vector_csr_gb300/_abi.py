@@ -161,7 +161,7 @@ def _load():
     lib.spmv_embed_workspace.restype = i64
     lib.spmv_embed_rows_grad.argtypes = [i64, i64, i64, vp, vp, i64, c_int, f64, c_int, vp, i64, c_int, vp, i64, vp]
     lib.spmv_embed_rows_grad.restype = c_int
-    lib.spmv_feed_forward_workspace.argtypes = [i64, i64, i64, c_int, c_int]
+    lib.spmv_feed_forward_workspace.argtypes = [i64, i64, i64, i32, c_int, c_int]
     lib.spmv_feed_forward_workspace.restype = i64
     block = [i64, i64, i64, i32, vp, vp, i64, vp, vp, i64, i64, vp, i64, i64, c_int, vp, vp, i64]
     lib.spmv_feed_forward.argtypes = block + [vp, i64, c_int, vp, i64, vp]
@@ -498,9 +498,10 @@ def spmv_embed_rows_grad(tokens, vocab, d, ids, dx, lddx, dtype, scale, accumula
                                     _ptr(workspace), int(workspace_bytes), _stream(stream)))
 
 
-def spmv_feed_forward_workspace(rows, d, f, dtype, gradient=False) -> int:
+def spmv_feed_forward_workspace(rows, d, f, experts, dtype, gradient=False) -> int:
     """Bytes of workspace that spmv_feed_forward or spmv_feed_forward_grad needs."""
-    return int(_check(lib.spmv_feed_forward_workspace(int(rows), int(d), int(f), int(dtype), int(gradient))))
+    return int(_check(lib.spmv_feed_forward_workspace(int(rows), int(d), int(f), int(experts), int(dtype),
+                                                       int(gradient))))
 
 
 def spmv_feed_forward(rows, d, f, experts, offsets, x, ldx, w_gate, w_up, ldw, w_expert, w_down, ldwd, wd_expert,

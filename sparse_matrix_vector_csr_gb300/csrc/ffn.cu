@@ -38,13 +38,17 @@ int check_outputs(std::initializer_list<Array> outputs, std::initializer_list<Ar
     }
     return SPMV_OK;
 }
-int check_segments(int64_t rows, int32_t experts, const int32_t *offsets) {
-    (void)rows;
-    if (experts < 1 || experts > kMaxSegments) return refuse("experts must lie in [1, " + std::to_string(kMaxSegments) + "]");
+int check_experts(int32_t experts) {
+    return experts < 1 || experts > kMaxSegments ? refuse("experts must lie in [1, " + std::to_string(kMaxSegments) + "]") : SPMV_OK;
+}
+// h is held in two parts
+bool two_parts(int64_t rows, int32_t experts, int dtype) { return dtype != SPMV_F32 && rows <= int64_t(kShortRows) * experts; }
+int check_segments(int32_t experts, const int32_t *offsets) {
+    SPMV_TRY(check_experts(experts));
     if (!offsets) return experts == 1 ? SPMV_OK : refuse("offsets is NULL, which means one segment of all rows, with experts not 1");
     return check_array(offsets, "offsets", 4);
 }
-using Launch = int (*)(int, const Block &, int, cudaStream_t);
+using Launch = int (*)(int, const Block &, int, bool, cudaStream_t);
 Matrix matrix(const void *p, int64_t ld, int64_t expert = 0) { return Matrix{const_cast<void *>(p), ld, expert}; }
 
 }  // namespace
@@ -54,9 +58,11 @@ Matrix matrix(const void *p, int64_t ld, int64_t expert = 0) { return Matrix{con
 using namespace spmv;
 using namespace spmv::ffn;
 
-extern "C" SPMV_API int64_t spmv_feed_forward_workspace(int64_t rows, int64_t d, int64_t f, int dtype, int gradient) {
+extern "C" SPMV_API int64_t spmv_feed_forward_workspace(int64_t rows, int64_t d, int64_t f, int32_t experts, int dtype,
+                                                        int gradient) {
     SPMV_TRY(check_sizes(rows, d, f, dtype));
-    return rows * padded(f) * row_value_bytes(dtype) * (gradient ? 3 : 1);
+    SPMV_TRY(check_experts(experts));
+    return rows * padded(f) * row_value_bytes(dtype) * (gradient ? 3 : two_parts(rows, experts, dtype) ? 2 : 1);
 }
 
 extern "C" SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, int32_t experts, const int32_t *offsets,
@@ -67,9 +73,9 @@ extern "C" SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, in
     SPMV_TRY(check_sizes(rows, d, f, dtype));
     if (activation < SPMV_ACT_SILU || activation > SPMV_ACT_RELU) return refuse("activation is not one of spmv_activation");
     if (!gate != !up) return refuse("gate and up are kept both or not at all");
-    SPMV_TRY(check_segments(rows, experts, offsets));
+    SPMV_TRY(check_segments(experts, offsets));
     if (rows == 0) return SPMV_OK;
-    const int64_t need = spmv_feed_forward_workspace(rows, d, f, dtype, 0);
+    const int64_t need = spmv_feed_forward_workspace(rows, d, f, experts, dtype, 0);
     if (workspace_bytes < need) return refuse("the workspace has fewer bytes than spmv_feed_forward_workspace says");
     SPMV_TRY(check_matrix(x, "x", rows, d, ldx, dtype));
     SPMV_TRY(check_weights(w_gate, "w_gate", experts, f, d, ldw, w_expert, dtype));
@@ -100,10 +106,12 @@ extern "C" SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, in
     b.gate = matrix(gate, ldg);
     b.up = matrix(up, ldg);
     b.h = matrix(workspace, padded(f));
+    if (two_parts(rows, experts, dtype)) b.h2 = matrix(static_cast<char *>(workspace) + need / 2, padded(f));
     b.y = matrix(y, ldy);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const Launch run = tc_supported(b, dtype) ? launch_tc : launch_simt;
-    for (int kind : {kGated, kDown}) SPMV_TRY(run(kind, b, dtype, s));
+    SPMV_TRY(run(kGated, b, dtype, false, s));
+    SPMV_TRY(run(kDown, b, dtype, true, s));
     return SPMV_OK;
 }
 
@@ -115,8 +123,8 @@ extern "C" SPMV_API int spmv_feed_forward_grad(int64_t rows, int64_t d, int64_t 
                                                int dtype, void *workspace, int64_t workspace_bytes, void *stream) {
     SPMV_TRY(check_sizes(rows, d, f, dtype));
     if (activation < SPMV_ACT_SILU || activation > SPMV_ACT_RELU) return refuse("activation is not one of spmv_activation");
-    SPMV_TRY(check_segments(rows, experts, offsets));
-    const int64_t need = spmv_feed_forward_workspace(rows, d, f, dtype, 1);
+    SPMV_TRY(check_segments(experts, offsets));
+    const int64_t need = spmv_feed_forward_workspace(rows, d, f, experts, dtype, 1);
     if (workspace_bytes < need) return refuse("the workspace has fewer bytes than spmv_feed_forward_workspace says");
     SPMV_TRY(check_matrix(x, "x", rows, d, ldx, dtype));
     SPMV_TRY(check_weights(w_gate, "w_gate", experts, f, d, ldw, w_expert, dtype));
@@ -162,8 +170,8 @@ extern "C" SPMV_API int spmv_feed_forward_grad(int64_t rows, int64_t d, int64_t 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // (no rows: the weights' gradients are 0, by the products that need no map of the rows)
     const Launch run = rows && tc_supported(b, dtype) ? launch_tc : launch_simt;
-    if (rows && (dx || weights)) SPMV_TRY(run(kBack, b, dtype, s));
-    if (rows && dx) SPMV_TRY(run(kInput, b, dtype, s));
-    if (weights) SPMV_TRY(run(kWeights, b, dtype, s));
+    if (rows && (dx || weights)) SPMV_TRY(run(kBack, b, dtype, false, s));
+    if (rows && dx) SPMV_TRY(run(kInput, b, dtype, true, s));
+    if (weights) SPMV_TRY(run(kWeights, b, dtype, rows > 0, s));
     return SPMV_OK;
 }

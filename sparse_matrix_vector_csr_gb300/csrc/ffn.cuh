@@ -33,6 +33,8 @@ __host__ __device__ constexpr bool a_transposed(int kind) { return kind == kWeig
 __host__ __device__ constexpr bool b_transposed(int kind) { return kind >= kBack; }
 
 constexpr int kMaxSegments = 4096;
+// segments this short on average wait for their weights, not for products
+constexpr int kShortRows = 16;
 
 // rows in segments; offsets == nullptr: one segment of all rows.  Whatever offsets holds, spans lie in [0, rows).
 struct Segments {
@@ -69,6 +71,7 @@ struct Block {
     int act;
     Matrix x, wg, wu, wd;        // rows x d; experts x f x d; experts x d x f
     Matrix gate, up, h;          // rows x f (gate.p and up.p may be null forward)
+    Matrix h2;                   // rows x f: what h's rounding left out (tensor cores, short segments)
     Matrix y;                    // rows x d
     Matrix dy, dgate, dup, dx;   // rows x d; rows x f; rows x d
     Matrix dwg, dwu, dwd;        // as wg, wu, wd (any may be null)
@@ -185,13 +188,14 @@ __host__ __device__ inline int64_t weight_rows(const Block &b, int which) { retu
 // ----------------------------------------------------------------------------
 // implementations
 // ----------------------------------------------------------------------------
+// `follows`: behind a kernel of the same call, on whose results it depends.
 // ffn_simt.cu: any type and address
-int launch_simt(int kind, const Block &b, int dtype, cudaStream_t s);
+int launch_simt(int kind, const Block &b, int dtype, bool follows, cudaStream_t s);
 // ffn_tc.cu: 16-bit values in rows that start at multiples of 16 bytes
 bool tc_supported(const Block &b, int dtype);
-int launch_tc(int kind, const Block &b, int dtype, cudaStream_t s);
-int launch_tc_f16(int kind, const Block &b, cudaStream_t s);
-int launch_tc_bf16(int kind, const Block &b, cudaStream_t s);
+int launch_tc(int kind, const Block &b, int dtype, bool follows, cudaStream_t s);
+int launch_tc_f16(int kind, const Block &b, bool follows, cudaStream_t s);
+int launch_tc_bf16(int kind, const Block &b, bool follows, cudaStream_t s);
 
 }  // namespace ffn
 }  // namespace spmv

@@ -255,7 +255,7 @@ int launch_kind(int kind, const Block &b, cudaStream_t s) {
 
 }  // namespace
 
-int launch_simt(int kind, const Block &b, int dtype, cudaStream_t s) {
+int launch_simt(int kind, const Block &b, int dtype, bool, cudaStream_t s) {
     if (dtype == SPMV_F32) return launch_kind<float>(kind, b, s);
     if (dtype == SPMV_F16) return launch_kind<__half>(kind, b, s);
     return launch_kind<__nv_bfloat16>(kind, b, s);

@@ -2,6 +2,8 @@
 // engine, and the flag of waits that ran out.
 #include "ffn_tc.cuh"
 
+#include <atomic>
+
 namespace spmv {
 namespace ffn {
 namespace {
@@ -31,8 +33,17 @@ Encode encoder() {
 }
 
 int *failure_flag() {
+    // an address of the library's own, the same for as long as a device's context lives (looked up at each call it
+    // takes a microsecond)
+    static std::atomic<int *> known[64];
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return nullptr;
+    int *at = device < 64 ? known[device].load(std::memory_order_relaxed) : nullptr;
+    if (at) return at;
     void *p = nullptr;
-    return cudaGetSymbolAddress(&p, gave_up_flag) == cudaSuccess ? static_cast<int *>(p) : nullptr;
+    if (cudaGetSymbolAddress(&p, gave_up_flag) != cudaSuccess) return nullptr;
+    if (device < 64) known[device].store(static_cast<int *>(p), std::memory_order_relaxed);
+    return static_cast<int *>(p);
 }
 
 }  // namespace tc
@@ -40,15 +51,15 @@ int *failure_flag() {
 bool tc_supported(const Block &b, int dtype) {
     if (dtype == SPMV_F32 || !tc::encoder()) return false;
     const int64_t n = b.seg.count;
-    for (const Matrix *m : {&b.x, &b.gate, &b.up, &b.h, &b.y, &b.dy, &b.dgate, &b.dup, &b.dx})
+    for (const Matrix *m : {&b.x, &b.gate, &b.up, &b.h, &b.h2, &b.y, &b.dy, &b.dgate, &b.dup, &b.dx})
         if (!describable(*m, 1)) return false;
     for (const Matrix *m : {&b.wg, &b.wu, &b.wd, &b.dwg, &b.dwu, &b.dwd})
         if (!describable(*m, n)) return false;
     return true;
 }
 
-int launch_tc(int kind, const Block &b, int dtype, cudaStream_t s) {
-    return dtype == SPMV_F16 ? launch_tc_f16(kind, b, s) : launch_tc_bf16(kind, b, s);
+int launch_tc(int kind, const Block &b, int dtype, bool follows, cudaStream_t s) {
+    return dtype == SPMV_F16 ? launch_tc_f16(kind, b, follows, s) : launch_tc_bf16(kind, b, follows, s);
 }
 
 }  // namespace ffn

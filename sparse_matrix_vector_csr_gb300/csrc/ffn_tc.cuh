@@ -31,6 +31,7 @@ constexpr int kRowBytes = 128;
 constexpr int kGroupRows = 2048;  // of the row tiles that take turns before the next column tile, so that both stay in L2
 constexpr int kSharedBytes = 227 * 1024;
 constexpr int kMaxStages = 16;
+constexpr int kFewRows = kShortRows;  // of a tile where segments are short
 constexpr long long kWaitCycles = 4000000000LL;  // about two seconds
 
 struct Args {
@@ -39,6 +40,7 @@ struct Args {
     int products;      // kWeights: how many of the three, and
     int which[3];      // which
     int stages;        // of the ring
+    bool follows;      // launched behind a kernel of the same call that may still run
     int *failed;
 };
 
@@ -392,12 +394,13 @@ __device__ __forceinline__ void clear_rows(uint32_t a, uint32_t b, int left) {
 // 325 ns a stage, and copies of 8 KB a stage had to wait): narrow tiles take turns with four.
 template <int kKind, int kN, int kLoaded, bool kPair>
 struct Shape {
+    static constexpr bool kSplit = kKind == kDown && kLoaded == kFewRows;  // h in two parts, one behind the other in A's tile
     static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kCols = kKind == kGated ? kN / 2 : kN;
     static constexpr int kMine = kKind == kWeights ? kRows : kLoaded;  // rows of D that a CTA has
     static constexpr int kTileRows = kMine * kCtas;
     static constexpr int kAccs = 256 / kN;
-    static constexpr int kABytes = kMine * kRowBytes, kBBytes = kN / kCtas * kRowBytes;
+    static constexpr int kABytes = (kSplit ? 2 : 1) * kMine * kRowBytes, kBBytes = kN / kCtas * kRowBytes;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kSlack = kRows * kRowBytes - kABytes;  // behind the ring: what the last stage's product reads
     static constexpr int kWriterBytes = kKind == kBack ? 5 * kPatchBytes : kPatchBytes;
@@ -463,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
     __syncthreads();
     if constexpr (kPair) cluster_sync(2);
     fence_after();
+    dev::allow_dependents();
     const uint32_t tmem = tmem_at;
     const Tiles<kKind, S::kTileRows, S::kCols> tiles(args, prefix);
     const auto stages_of = [&](const Tile &t) { return static_cast<int>((t.depth + kDepth - 1) / kDepth) * (kKind == kInput ? 2 : 1); };
@@ -471,44 +475,74 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
         if (one_lane()) {
             int s = 0, round = 0;
             bool ok = true;
+            // stage q of the tile: B's part, A's part
+            const auto copy_b = [&](const Tile &t, int q, int once, uint32_t bar) {
+                const uint32_t b = ring_b + s * S::kBBytes;
+                const int pass = q >= once, k = (pass ? q - once : q) * kDepth;
+                // this CTA's part: half of the columns (kGated: gate or up)
+                const int col = static_cast<int>(t.col) + (kKind == kGated ? 0 : rank * (kN / S::kCtas));
+                if constexpr (kAcrossA) {
+#pragma unroll
+                    for (int j = 0; j < kN / S::kCtas / 64; ++j)
+                        copy2<kPair>(b + j * (kDepth * kRowBytes), &args.b[t.which], col + j * 64, static_cast<int>(t.first) + k, bar);
+                } else if constexpr (kKind == kGated && kPair) {
+                    copy3<kPair>(b, &args.b[rank], k, col, t.e, bar);
+                } else if constexpr (kKind == kGated) {
+                    copy3<kPair>(b, &args.b[0], k, col, t.e, bar);
+                    copy3<kPair>(b + kN / 2 * kRowBytes, &args.b[1], k, col, t.e, bar);
+                } else if constexpr (kAcrossB) {
+#pragma unroll
+                    for (int j = 0; j < kN / S::kCtas / 64; ++j)
+                        copy3<kPair>(b + j * (kDepth * kRowBytes), &args.b[pass], col + j * 64, k, t.e, bar);
+                } else {
+                    copy3<kPair>(b, &args.b[0], k, col, t.e, bar);
+                }
+            };
+            const auto copy_a = [&](const Tile &t, int q, int once, uint32_t bar) {
+                const uint32_t a = ring_a + s * S::kABytes;
+                const int pass = q >= once, k = (pass ? q - once : q) * kDepth, row = static_cast<int>(t.row) + rank * S::kMine;
+                if constexpr (kAcrossA) {
+#pragma unroll
+                    for (int j = 0; j < S::kMine / 64; ++j)
+                        copy2<kPair>(a + j * (kDepth * kRowBytes), &args.a[t.which], row + j * 64, static_cast<int>(t.first) + k, bar);
+                } else {
+                    copy2<kPair>(a, &args.a[pass], k, row, bar);
+                    if constexpr (S::kSplit) copy2<kPair>(a + S::kMine * kRowBytes, &args.a[1], k, row, bar);
+                }
+            };
+            // Behind a kernel that may still run: its results are A (kWeights: B too).  B's stages of the first tile
+            // come before them.
+            int ahead = 0;
+            if (args.follows) {
+                if (kKind != kWeights && first < tiles.total) {
+                    const Tile t = tiles[first];
+                    const int n = stages_of(t);
+                    for (; s < n && s < stages; ++s) {
+                        const uint32_t bar = rank == 0 ? full(s) : bar_first(full(s));
+                        if (rank == 0) bar_expect(full(s), S::kCtas * S::kStageBytes);
+                        copy_b(t, s, kKind == kInput ? n / 2 : n, bar);
+                    }
+                    ahead = s;
+                    s = 0;
+                }
+                dev::grid_wait();
+            }
             for (int64_t i = first; ok && i < tiles.total; i += step) {
                 const Tile t = tiles[i];
                 const int n = stages_of(t), once = kKind == kInput ? n / 2 : n;
-                const int row = static_cast<int>(t.row) + rank * S::kMine;
-                // this CTA's part of B: half of the columns (kGated: gate or up)
-                const int col = static_cast<int>(t.col) + (kKind == kGated ? 0 : rank * (kN / S::kCtas));
                 for (int q = 0; q < n; ++q) {
                     if (!(ok = bar_wait(empty(s), (round & 1) ^ 1, gave_up, failed))) break;
                     // a pair's copies are counted by its first CTA, but for a segment's last rows (kWeights), in which each
                     // CTA has something to clear first
                     const bool own = !kPair || (kKind == kWeights && t.depth - static_cast<int64_t>(q) * kDepth < kDepth);
                     const uint32_t bar = own || rank == 0 ? full(s) : bar_first(full(s));
-                    if (own || rank == 0) bar_expect(full(s), own ? S::kStageBytes : 2 * S::kStageBytes);
-                    const int pass = q >= once, k = (pass ? q - once : q) * kDepth;
-                    const uint32_t a = ring_a + s * S::kABytes, b = ring_b + s * S::kBBytes;
-                    if constexpr (kAcrossA) {
-                        const int k0 = static_cast<int>(t.first) + k;
-#pragma unroll
-                        for (int j = 0; j < S::kMine / 64; ++j)
-                            copy2<kPair>(a + j * (kDepth * kRowBytes), &args.a[t.which], row + j * 64, k0, bar);
-#pragma unroll
-                        for (int j = 0; j < kN / S::kCtas / 64; ++j)
-                            copy2<kPair>(b + j * (kDepth * kRowBytes), &args.b[t.which], col + j * 64, k0, bar);
+                    if (ahead > 0) {
+                        --ahead;
                     } else {
-                        copy2<kPair>(a, &args.a[pass], k, row, bar);
-                        if constexpr (kKind == kGated && kPair) {
-                            copy3<kPair>(b, &args.b[rank], k, col, t.e, bar);
-                        } else if constexpr (kKind == kGated) {
-                            copy3<kPair>(b, &args.b[0], k, col, t.e, bar);
-                            copy3<kPair>(b + kN / 2 * kRowBytes, &args.b[1], k, col, t.e, bar);
-                        } else if constexpr (kAcrossB) {
-#pragma unroll
-                            for (int j = 0; j < kN / S::kCtas / 64; ++j)
-                                copy3<kPair>(b + j * (kDepth * kRowBytes), &args.b[pass], col + j * 64, k, t.e, bar);
-                        } else {
-                            copy3<kPair>(b, &args.b[0], k, col, t.e, bar);
-                        }
+                        if (own || rank == 0) bar_expect(full(s), own ? S::kStageBytes : 2 * S::kStageBytes);
+                        copy_b(t, q, once, bar);
                     }
+                    copy_a(t, q, once, bar);
                     if (++s == stages) {
                         s = 0;
                         ++round;
@@ -671,6 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 } else {
                     take(c, v);
+                    if constexpr (S::kSplit) {  // the sums of h's second parts, 16 lanes on
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] += __shfl_down_sync(0xffffffffu, v[j], kFewRows);
+                    }
                 }
                 const int64_t left = columns - c;
                 if constexpr (kKind == kGated) {
@@ -690,9 +728,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                     if (!zero) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = activate<false>(v[j], b.act).value * w[j];
-                        // rounded to the type: the next product takes it so (one rounding of each term of y's sums)
+                        // rounded to the type: the next product takes it so (one rounding of each term of y's sums); of short
+                        // segments, whose products wait for the weights, it takes what the rounding left out, too
                         patch_row<T>(mine, v);
                         patch_out<T>(mine, at(b.h, c), b.h.ld, rows, left);
+                        if constexpr (kLoaded == kFewRows) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float rest = v[j] - to_f32(from_f32<T>(v[j]));
+                                v[j] = fabsf(rest) < INFINITY ? rest : 0.0f;  // (nothing of an infinity, or of a value beyond the type's)
+                            }
+                            patch_row<T>(mine, v);
+                            patch_out<T>(mine, at(b.h2, c), b.h2.ld, rows, left);
+                        }
                     }
                 } else if constexpr (kKind == kBack) {
                     const uint32_t gate = mine + kPatchBytes * (1 + (c / (32 * kHalves) & 1) * 2), up = gate + kPatchBytes;
@@ -772,12 +820,13 @@ bool make_map(CUtensorMap *map, const Matrix &m, int64_t n, int64_t rows, int64_
 }
 
 template <typename T, int kKind, int kN, int kLoaded, bool kPair>
-int launch(const Block &b, cudaStream_t s) {
+int launch(const Block &b, bool follows, cudaStream_t s) {
     using S = Shape<kKind, kN, kLoaded, kPair>;
     Args args;
     args.block = b;
     args.failed = failure_flag();
     args.products = 0;
+    args.follows = follows;
     const int64_t rows = b.seg.rows, d = b.d, f = b.f, count = b.seg.count;
     args.stages = S::stages(static_cast<int>(count));
     const auto activation = [&](CUtensorMap *map, const Matrix &m, int64_t n) {
@@ -797,7 +846,7 @@ int launch(const Block &b, cudaStream_t s) {
     } else if (kKind == kGated) {
         ok = ok && activation(&args.a[0], b.x, d) && weight(&args.b[0], b.wg, d, f, kN / 2) && weight(&args.b[1], b.wu, d, f, kN / 2);
     } else if (kKind == kDown) {
-        ok = ok && activation(&args.a[0], b.h, f) && weight(&args.b[0], b.wd, f, d, kN / S::kCtas);
+        ok = ok && activation(&args.a[0], b.h, f) && (!S::kSplit || activation(&args.a[1], b.h2, f)) && weight(&args.b[0], b.wd, f, d, kN / S::kCtas);
     } else if (kKind == kBack) {
         ok = ok && activation(&args.a[0], b.dy, d) && weight(&args.b[0], b.wd, f, d, kDepth);
     } else {
@@ -810,34 +859,52 @@ int launch(const Block &b, cudaStream_t s) {
     const size_t smem = S::smem(static_cast<int>(count), args.stages);
     const int64_t workers = kSms / S::kCtas;
     SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    SPMV_TRY_CUDA(launch_rows(k_ffn<T, kKind, kN, kLoaded, kPair>, (tiles < workers ? tiles : workers) * S::kCtas, kThreads, S::kCtas, smem, s, args));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((tiles < workers ? tiles : workers) * S::kCtas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    if (kPair) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = 2;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (follows) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    cfg.attrs = attr;
+    SPMV_TRY_CUDA(cudaLaunchKernelEx(&cfg, k_ffn<T, kKind, kN, kLoaded, kPair>, args));
     return SPMV_OK;
 }
 
 template <typename T, int kKind>
-int launch_shape(const Block &b, cudaStream_t s) {
+int launch_shape(const Block &b, bool follows, cudaStream_t s) {
     const int64_t rows = b.seg.rows, mean = ceil_div(rows, b.seg.count);  // rows of a segment, taking them as equally long
     const int64_t columns = product_columns<kKind>(b, 0);
     if constexpr (kKind == kWeights) {
         const int64_t tiles = (2 * ceil_div(b.f, 256) * ceil_div(b.d, 256) + ceil_div(b.d, 256) * ceil_div(b.f, 256)) * b.seg.count;
-        if (tiles >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, s);
-        return launch<T, kKind, 64, 128, false>(b, s);
+        if (tiles >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, follows, s);
+        return launch<T, kKind, 64, 128, false>(b, follows, s);
     } else {
-        if (mean <= 16) return launch<T, kKind, 64, 16, false>(b, s);
+        if (mean <= kFewRows) return launch<T, kKind, 64, kFewRows, false>(b, follows, s);
         const int64_t wide = ceil_div(columns, kKind == kGated ? 128 : 256);
-        if (mean >= 192 && ceil_div(rows, 256) * wide >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, s);
-        if (ceil_div(rows, 128) * wide >= kSms) return launch<T, kKind, 256, 128, false>(b, s);
-        return launch<T, kKind, 64, 128, false>(b, s);
+        if (mean >= 192 && ceil_div(rows, 256) * wide >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, follows, s);
+        if (ceil_div(rows, 128) * wide >= kSms) return launch<T, kKind, 256, 128, false>(b, follows, s);
+        return launch<T, kKind, 64, 128, false>(b, follows, s);
     }
 }
 template <typename T>
-int launch_kind(int kind, const Block &b, cudaStream_t s) {
+int launch_kind(int kind, const Block &b, bool follows, cudaStream_t s) {
     switch (kind) {
-        case kGated: return launch_shape<T, kGated>(b, s);
-        case kDown: return launch_shape<T, kDown>(b, s);
-        case kBack: return launch_shape<T, kBack>(b, s);
-        case kInput: return launch_shape<T, kInput>(b, s);
-        default: return launch_shape<T, kWeights>(b, s);
+        case kGated: return launch_shape<T, kGated>(b, follows, s);
+        case kDown: return launch_shape<T, kDown>(b, follows, s);
+        case kBack: return launch_shape<T, kBack>(b, follows, s);
+        case kInput: return launch_shape<T, kInput>(b, follows, s);
+        default: return launch_shape<T, kWeights>(b, follows, s);
     }
 }
 

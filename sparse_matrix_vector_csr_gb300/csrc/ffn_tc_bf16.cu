@@ -3,6 +3,6 @@
 
 namespace spmv {
 namespace ffn {
-int launch_tc_bf16(int kind, const Block &b, cudaStream_t s) { return tc::launch_kind<__nv_bfloat16>(kind, b, s); }
+int launch_tc_bf16(int kind, const Block &b, bool follows, cudaStream_t s) { return tc::launch_kind<__nv_bfloat16>(kind, b, follows, s); }
 }  // namespace ffn
 }  // namespace spmv

@@ -369,7 +369,7 @@ def _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, stream, offset
     if keep:
         res.gate, res.up = _empty((2, rows, wide), dtype=dtype, device=device)[:, :, :f].unbind(0)
     res.y, ldy = _out(out, "out", x, rows, d)
-    work = _check(lib.spmv_feed_forward_workspace(rows, d, f, code, 0))
+    work = _check(lib.spmv_feed_forward_workspace(rows, d, f, experts or 1, code, 0))
     space = _empty((work,), dtype=torch.uint8, device=device)
     call = (rows, d, f, experts or 1, None if offsets is None else offsets.data_ptr(), x.data_ptr() or None, ldx,
             w_gate.data_ptr(), w_up.data_ptr(), ldw, apart, w_down.data_ptr(), ldd, apart_d, act,
@@ -398,7 +398,7 @@ class FeedForward:
         lddy = _matrix(dy, "dy", rows, d, x.dtype)[1]
         dx, lddx = _out(out, "out", x, rows, d)
         dws = [_empty(w.shape, dtype=x.dtype, device=x.device) if weights else None for w in (w_gate, w_up, w_down)]
-        work = _check(lib.spmv_feed_forward_workspace(rows, d, f, code, 1))
+        work = _check(lib.spmv_feed_forward_workspace(rows, d, f, call[3], code, 1))
         space = _empty((work,), dtype=torch.uint8, device=x.device)
         _check(lib.spmv_feed_forward_grad(*call, dy.data_ptr() or None, lddy, dx.data_ptr() or None, lddx,
                                           *[None if w is None else w.data_ptr() for w in dws], code,
