@@ -105,7 +105,7 @@ extern "C" SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, in
     b.wd = matrix(w_down, ldwd, wd_expert);
     b.gate = matrix(gate, ldg);
     b.up = matrix(up, ldg);
-    b.h = matrix(workspace, padded(f));
+    b.h = matrix(workspace, padded(f), rows * padded(f));
     if (two_parts(rows, experts, dtype)) b.h2 = matrix(static_cast<char *>(workspace) + need / 2, padded(f));
     b.y = matrix(y, ldy);
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -30,7 +30,7 @@ constexpr int kDepth = 64;        // of a stage: 128 bytes, the width of the swi
 constexpr int kRowBytes = 128;
 constexpr int kGroupRows = 2048;  // of the row tiles that take turns before the next column tile, so that both stay in L2
 constexpr int kSharedBytes = 227 * 1024;
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 32;
 constexpr int kFewRows = kShortRows;  // of a tile where segments are short
 constexpr long long kWaitCycles = 4000000000LL;  // about two seconds
 
@@ -388,20 +388,23 @@ __device__ __forceinline__ void clear_rows(uint32_t a, uint32_t b, int left) {
 // the kernel
 // ----------------------------------------------------------------------------
 // kN columns of the accumulator (kGated: half of them gate's, then as many of up); kLoaded rows of A's tile are
-// copied where segments are short (the accumulator's other lanes then hold sums of whatever lies behind
+// copied where segments are short (8 or 16; the accumulator's other lanes then hold sums of whatever lies behind
 // them in the ring, which nothing reads).  Products that follow on in one accumulator wait for one
 // another, about 150 cycles whatever their size (measured; 4 x 16 of k into one accumulator of 64 columns
 // 325 ns a stage, and copies of 8 KB a stage had to wait): narrow tiles take turns with four.
 template <int kKind, int kN, int kLoaded, bool kPair>
 struct Shape {
-    static constexpr bool kSplit = kKind == kDown && kLoaded == kFewRows;  // h in two parts, one behind the other in A's tile
+    static constexpr bool kTwoParts = kKind == kDown && kLoaded <= kFewRows;  // of h, one behind the other in A's tile
     static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kCols = kKind == kGated ? kN / 2 : kN;
     static constexpr int kMine = kKind == kWeights ? kRows : kLoaded;  // rows of D that a CTA has
     static constexpr int kTileRows = kMine * kCtas;
-    static constexpr int kAccs = 256 / kN;
-    static constexpr int kABytes = (kSplit ? 2 : 1) * kMine * kRowBytes, kBBytes = kN / kCtas * kRowBytes;
-    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kAccs = kN == 256 ? 1 : 4;
+    static constexpr int kABytes = (kTwoParts ? 2 : 1) * kMine * kRowBytes, kBBytes = kN / kCtas * kRowBytes;
+    // 64s of k of a stage: where their products are short, what a stage costs besides (two waits and a signal, about
+    // 160 ns) is shared by several
+    static constexpr int kBlocks = kKind == kWeights || kN == 256 ? 1 : kLoaded == kRows ? 2 : 4;
+    static constexpr int kBlockBytes = kABytes + kBBytes, kStageBytes = kBlocks * kBlockBytes;
     static constexpr int kSlack = kRows * kRowBytes - kABytes;  // behind the ring: what the last stage's product reads
     static constexpr int kWriterBytes = kKind == kBack ? 5 * kPatchBytes : kPatchBytes;
     static constexpr int kFixed = 1024 + kSlack + kWriters * kWriterBytes + (3 * kMaxStages + 5) * 8;
@@ -422,8 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
     __shared__ int gave_up_at;
     const int stages = args.stages;
     const uint32_t ring_b = (smem_addr(raw) + 1023) & ~1023u;       // B's stages, then A's: each a multiple of 1024 bytes
-    const uint32_t ring_a = ring_b + stages * S::kBBytes;
-    const uint32_t patches = ring_a + stages * S::kABytes + S::kSlack;
+    const uint32_t ring_a = ring_b + stages * S::kBlocks * S::kBBytes;
+    const uint32_t patches = ring_a + stages * S::kBlocks * S::kABytes + S::kSlack;
     const uint32_t bars = patches + kWriters * S::kWriterBytes;
     const auto full = [&](int s) { return bars + 8 * s; };
     const auto empty = [&](int s) { return bars + 8 * (kMaxStages + s); };
@@ -469,15 +472,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
     dev::allow_dependents();
     const uint32_t tmem = tmem_at;
     const Tiles<kKind, S::kTileRows, S::kCols> tiles(args, prefix);
-    const auto stages_of = [&](const Tile &t) { return static_cast<int>((t.depth + kDepth - 1) / kDepth) * (kKind == kInput ? 2 : 1); };
+    const auto blocks_of = [&](const Tile &t) { return static_cast<int>((t.depth + kDepth - 1) / kDepth) * (kKind == kInput ? 2 : 1); };
 
     if (warp == kWriters) {
         if (one_lane()) {
             int s = 0, round = 0;
             bool ok = true;
-            // stage q of the tile: B's part, A's part
-            const auto copy_b = [&](const Tile &t, int q, int once, uint32_t bar) {
-                const uint32_t b = ring_b + s * S::kBBytes;
+            // block q of the tile to place `at` of the ring: B's part, A's part
+            const auto copy_b = [&](const Tile &t, int at, int q, int once, uint32_t bar) {
+                const uint32_t b = ring_b + at * S::kBBytes;
                 const int pass = q >= once, k = (pass ? q - once : q) * kDepth;
                 // this CTA's part: half of the columns (kGated: gate or up)
                 const int col = static_cast<int>(t.col) + (kKind == kGated ? 0 : rank * (kN / S::kCtas));
@@ -498,16 +501,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                     copy3<kPair>(b, &args.b[0], k, col, t.e, bar);
                 }
             };
-            const auto copy_a = [&](const Tile &t, int q, int once, uint32_t bar) {
-                const uint32_t a = ring_a + s * S::kABytes;
+            const auto copy_a = [&](const Tile &t, int at, int q, int once, uint32_t bar) {
+                const uint32_t a = ring_a + at * S::kABytes;
                 const int pass = q >= once, k = (pass ? q - once : q) * kDepth, row = static_cast<int>(t.row) + rank * S::kMine;
                 if constexpr (kAcrossA) {
 #pragma unroll
                     for (int j = 0; j < S::kMine / 64; ++j)
                         copy2<kPair>(a + j * (kDepth * kRowBytes), &args.a[t.which], row + j * 64, static_cast<int>(t.first) + k, bar);
                 } else {
-                    copy2<kPair>(a, &args.a[pass], k, row, bar);
-                    if constexpr (S::kSplit) copy2<kPair>(a + S::kMine * kRowBytes, &args.a[1], k, row, bar);
+                    if constexpr (S::kTwoParts) copy3<kPair>(a, &args.a[0], k, row, 0, bar);
+                    else copy2<kPair>(a, &args.a[pass], k, row, bar);
                 }
             };
             // Behind a kernel that may still run: its results are A (kWeights: B too).  B's stages of the first tile
@@ -516,33 +519,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
             if (args.follows) {
                 if (kKind != kWeights && first < tiles.total) {
                     const Tile t = tiles[first];
-                    const int n = stages_of(t);
-                    for (; s < n && s < stages; ++s) {
-                        const uint32_t bar = rank == 0 ? full(s) : bar_first(full(s));
-                        if (rank == 0) bar_expect(full(s), S::kCtas * S::kStageBytes);
-                        copy_b(t, s, kKind == kInput ? n / 2 : n, bar);
+                    const int n = blocks_of(t);
+                    for (; ahead < stages && ahead * S::kBlocks < n; ++ahead) {
+                        const int q0 = ahead * S::kBlocks, blocks = min(S::kBlocks, n - q0);
+                        const uint32_t bar = rank == 0 ? full(ahead) : bar_first(full(ahead));
+                        if (rank == 0) bar_expect(full(ahead), S::kCtas * blocks * S::kBlockBytes);
+                        for (int j = 0; j < blocks; ++j) copy_b(t, q0 + j, q0 + j, kKind == kInput ? n / 2 : n, bar);
                     }
-                    ahead = s;
-                    s = 0;
                 }
                 dev::grid_wait();
             }
             for (int64_t i = first; ok && i < tiles.total; i += step) {
                 const Tile t = tiles[i];
-                const int n = stages_of(t), once = kKind == kInput ? n / 2 : n;
-                for (int q = 0; q < n; ++q) {
+                const int n = blocks_of(t), once = kKind == kInput ? n / 2 : n;
+                for (int q0 = 0; q0 < n; q0 += S::kBlocks) {
                     if (!(ok = bar_wait(empty(s), (round & 1) ^ 1, gave_up, failed))) break;
+                    const int blocks = min(S::kBlocks, n - q0);
                     // a pair's copies are counted by its first CTA, but for a segment's last rows (kWeights), in which each
                     // CTA has something to clear first
-                    const bool own = !kPair || (kKind == kWeights && t.depth - static_cast<int64_t>(q) * kDepth < kDepth);
+                    const bool own = !kPair || (kKind == kWeights && t.depth - static_cast<int64_t>(q0) * kDepth < kDepth);
                     const uint32_t bar = own || rank == 0 ? full(s) : bar_first(full(s));
                     if (ahead > 0) {
                         --ahead;
                     } else {
-                        if (own || rank == 0) bar_expect(full(s), own ? S::kStageBytes : 2 * S::kStageBytes);
-                        copy_b(t, q, once, bar);
+                        if (own || rank == 0) bar_expect(full(s), (own ? 1 : 2) * blocks * S::kBlockBytes);
+                        for (int j = 0; j < blocks; ++j) copy_b(t, s * S::kBlocks + j, q0 + j, once, bar);
                     }
-                    copy_a(t, q, once, bar);
+                    for (int j = 0; j < blocks; ++j) copy_a(t, s * S::kBlocks + j, q0 + j, once, bar);
                     if (++s == stages) {
                         s = 0;
                         ++round;
@@ -572,27 +575,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                 ++round;
             }
         };
-        // by one lane: stage s of a tile, `steps` 16s of k
-        const auto products = [&](int q, int n, int steps) {
+        // by one lane: stage s of a tile, its blocks from q0 on, the last block `steps` 16s of k
+        const auto products = [&](int q0, int n, int steps) {
             fence_after();
             const uint32_t d = tmem + (done & 1) * (kN * S::kAccs);
-            uint64_t da = operand<kAcrossA>(ring_a + s * S::kABytes), db = operand<kAcrossB>(ring_b + s * S::kBBytes);
+            const int blocks = min(S::kBlocks, n - q0);
 #pragma unroll
-            for (int k = 0; k < kDepth / 16; ++k) {
-                if (k < steps) multiply<kPair>(d + k % S::kAccs * kN, da, db, shape, q > 0 || k >= S::kAccs);
-                da += kStep<kAcrossA>;
-                db += kStep<kAcrossB>;
+            for (int j = 0; j < S::kBlocks; ++j) {
+                if (j >= blocks) break;
+                const int at = s * S::kBlocks + j;
+                uint64_t da = operand<kAcrossA>(ring_a + at * S::kABytes), db = operand<kAcrossB>(ring_b + at * S::kBBytes);
+#pragma unroll
+                for (int k = 0; k < kDepth / 16; ++k) {
+                    if (k < steps) multiply<kPair>(d + k % S::kAccs * kN, da, db, shape, q0 + j > 0 || k >= S::kAccs);
+                    da += kStep<kAcrossA>;
+                    db += kStep<kAcrossB>;
+                }
             }
             signal_done<kPair>(empty(s));
-            if (q == n - 1) signal_done<kPair>(acc_full(done & 1));
+            if (q0 + blocks == n) signal_done<kPair>(acc_full(done & 1));
         };
         if constexpr (kKind != kWeights) {
             if (rank == 0 && one_lane())
                 for (int64_t i = first; ok && i < tiles.total; i += step) {
-                    const int n = stages_of(tiles[i]);
+                    const int n = blocks_of(tiles[i]);
                     if (n == 0) continue;
                     if (!(ok = bar_wait(acc_empty(done & 1), ((done >> 1) & 1) ^ 1, gave_up, failed))) break;
-                    for (int q = 0; q < n; ++q) {
+                    for (int q = 0; q < n; q += S::kBlocks) {
                         if (!(ok = bar_wait(full(s), round & 1, gave_up, failed))) break;
                         products(q, n, kDepth / 16);
                         next();
@@ -604,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
         } else {
             for (int64_t i = first; ok && i < tiles.total; i += step) {
                 const Tile t = tiles[i];
-                const int n = stages_of(t), left = static_cast<int>(t.depth % kDepth);
+                const int n = blocks_of(t), left = static_cast<int>(t.depth % kDepth);
                 if (n == 0) continue;
                 // one lane has the stages in which nothing is to be cleared, the warp the last one where something is
                 const int alone = left ? n - 1 : n;
@@ -657,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
         const int quarter = warp & 3, half = warp >> 2;
         for (int64_t i = first; i < tiles.total; i += step) {
             const Tile t = tiles[i];
-            const bool zero = stages_of(t) == 0;
+            const bool zero = blocks_of(t) == 0;
             const int which = done & 1;
             const int64_t row = t.row + rank * S::kMine + quarter * 32;
             const int64_t columns = product_columns<kKind>(b, t.which) - t.col;  // from the tile's first on
@@ -705,9 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 } else {
                     take(c, v);
-                    if constexpr (S::kSplit) {  // the sums of h's second parts, 16 lanes on
+                    if constexpr (S::kTwoParts) {  // the sums of h's second parts, kLoaded lanes on
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] += __shfl_down_sync(0xffffffffu, v[j], kFewRows);
+                        for (int j = 0; j < 32; ++j) v[j] += __shfl_down_sync(0xffffffffu, v[j], kLoaded);
                     }
                 }
                 const int64_t left = columns - c;
@@ -732,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                         // segments, whose products wait for the weights, it takes what the rounding left out, too
                         patch_row<T>(mine, v);
                         patch_out<T>(mine, at(b.h, c), b.h.ld, rows, left);
-                        if constexpr (kLoaded == kFewRows) {
+                        if constexpr (kLoaded <= kFewRows) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 const float rest = v[j] - to_f32(from_f32<T>(v[j]));
@@ -806,14 +815,15 @@ using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void
 Encode encoder();  // nullptr where the driver has none
 int *failure_flag();
 
-// `count` matrices (0: one, as a map of two dimensions) of `rows` rows of `n` values; boxes of 64 values x box_rows
+// `count` matrices (0: one, as a map of two dimensions) of `rows` rows of `n` values; boxes of 64 values x box_rows (of
+// box_count matrices)
 template <typename T>
-bool make_map(CUtensorMap *map, const Matrix &m, int64_t n, int64_t rows, int64_t count, int box_rows) {
+bool make_map(CUtensorMap *map, const Matrix &m, int64_t n, int64_t rows, int64_t count, int box_rows, int box_count = 1) {
     const cuuint64_t sizes[3] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count ? count : 1)};
     // (one matrix: its distance to the next is not used, but has to be a valid one)
     const int64_t apart = count > 1 ? m.expert : ceil_div((rows - 1) * m.ld + n, 8) * 8;
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(m.ld) * sizeof(T), static_cast<cuuint64_t>(apart) * sizeof(T)};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_count)}, step[3] = {1, 1, 1};
     return encoder()(map, std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                      count ? 3 : 2, m.p, sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -846,7 +856,8 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
     } else if (kKind == kGated) {
         ok = ok && activation(&args.a[0], b.x, d) && weight(&args.b[0], b.wg, d, f, kN / 2) && weight(&args.b[1], b.wu, d, f, kN / 2);
     } else if (kKind == kDown) {
-        ok = ok && activation(&args.a[0], b.h, f) && (!S::kSplit || activation(&args.a[1], b.h2, f)) && weight(&args.b[0], b.wd, f, d, kN / S::kCtas);
+        // (both parts of h as two matrices)
+        ok = ok && (S::kTwoParts ? make_map<T>(&args.a[0], b.h, f, rows, 2, S::kMine, 2) : activation(&args.a[0], b.h, f)) && weight(&args.b[0], b.wd, f, d, kN / S::kCtas);
     } else if (kKind == kBack) {
         ok = ok && activation(&args.a[0], b.dy, d) && weight(&args.b[0], b.wd, f, d, kDepth);
     } else {
@@ -890,7 +901,15 @@ int launch_shape(const Block &b, bool follows, cudaStream_t s) {
         if (tiles >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, follows, s);
         return launch<T, kKind, 64, 128, false>(b, follows, s);
     } else {
-        if (mean <= kFewRows) return launch<T, kKind, 64, kFewRows, false>(b, follows, s);
+        if constexpr (kKind == kDown) {
+            // tiles of 32 columns where those of 64 would leave SMs without one
+            const bool narrow = ceil_div(rows, mean) * ceil_div(columns, 64) < kSms;
+            if (mean <= 8) return narrow ? launch<T, kKind, 32, 8, false>(b, follows, s) : launch<T, kKind, 64, 8, false>(b, follows, s);
+            if (mean <= kFewRows) return narrow ? launch<T, kKind, 32, kFewRows, false>(b, follows, s) : launch<T, kKind, 64, kFewRows, false>(b, follows, s);
+        } else {
+            if (kKind == kGated && mean <= 8) return launch<T, kKind, 64, 8, false>(b, follows, s);
+            if (mean <= kFewRows) return launch<T, kKind, 64, kFewRows, false>(b, follows, s);
+        }
         const int64_t wide = ceil_div(columns, kKind == kGated ? 128 : 256);
         if (mean >= 192 && ceil_div(rows, 256) * wide >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, follows, s);
         if (ceil_div(rows, 128) * wide >= kSms) return launch<T, kKind, 256, 128, false>(b, follows, s);
