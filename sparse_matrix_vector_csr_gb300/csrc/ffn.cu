@@ -48,6 +48,41 @@ int check_segments(int32_t experts, const int32_t *offsets) {
     if (!offsets) return experts == 1 ? SPMV_OK : refuse("offsets is NULL, which means one segment of all rows, with experts not 1");
     return check_array(offsets, "offsets", 4);
 }
+// Parts of each segment's rows in the weights' gradients: enough tiles for the GPU where the matrices are small, of at
+// least 512 rows on average (a backward pass of 65536 rows, d = f = 64: float 7434 -> 343 us, bf16 258 -> 60; 256: 301 -> 128).
+int weight_splits(int64_t rows, int64_t d, int64_t f, int32_t experts) {
+    const int64_t tiles = 3 * ceil_div(d, 128) * ceil_div(f, 128) * experts, mean = rows / experts;
+    int splits = 1;
+    while (splits < 64 && tiles * splits < 2 * kSms && mean / (2 * splits) >= 512) splits *= 2;
+    return splits;
+}
+int64_t rows_bytes(int64_t rows, int64_t f, int dtype) { return rows * padded(f) * row_value_bytes(dtype); }
+
+// The parts' sums, in the order of the rows, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) k_join_weights(Block b) {
+    const int64_t n = b.d * b.f, all = 3 * b.seg.count * n;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t matrix = i / n;  // which product, then segment
+        const int which = static_cast<int>(matrix / b.seg.count), e = static_cast<int>(matrix % b.seg.count);
+        T *out = static_cast<T *>((which == 0 ? b.dwg : which == 1 ? b.dwu : b.dwd).p);
+        if (!out) continue;
+        const float *p = b.part_sums(which, e, 0) + (i - matrix * n);
+        float sum = p[0];
+#pragma unroll 8
+        for (int k = 1; k < b.splits; ++k) sum += p[k * n];
+        out[e * n + (i - matrix * n)] = from_f32<T>(sum);
+    }
+}
+int launch_join(const Block &b, int dtype, cudaStream_t s) {
+    const int64_t ctas = ceil_div(3 * b.seg.count * b.d * b.f, 256);
+    const dim3 grid(static_cast<unsigned>(ctas < 8 * kSms ? ctas : 8 * kSms));
+    if (dtype == SPMV_F32) k_join_weights<float><<<grid, 256, 0, s>>>(b);
+    else if (dtype == SPMV_F16) k_join_weights<__half><<<grid, 256, 0, s>>>(b);
+    else k_join_weights<__nv_bfloat16><<<grid, 256, 0, s>>>(b);
+    SPMV_TRY_CUDA(cudaGetLastError());
+    return SPMV_OK;
+}
 using Launch = int (*)(int, const Block &, int, bool, cudaStream_t);
 Matrix matrix(const void *p, int64_t ld, int64_t expert = 0) { return Matrix{const_cast<void *>(p), ld, expert}; }
 
@@ -62,7 +97,10 @@ extern "C" SPMV_API int64_t spmv_feed_forward_workspace(int64_t rows, int64_t d,
                                                         int gradient) {
     SPMV_TRY(check_sizes(rows, d, f, dtype));
     SPMV_TRY(check_experts(experts));
-    return rows * padded(f) * row_value_bytes(dtype) * (gradient ? 3 : two_parts(rows, experts, dtype) ? 2 : 1);
+    const int64_t each = rows_bytes(rows, f, dtype);
+    if (!gradient) return each * (two_parts(rows, experts, dtype) ? 2 : 1);
+    const int splits = weight_splits(rows, d, f, experts);
+    return 3 * each + (splits > 1 ? splits * 3 * experts * d * f * static_cast<int64_t>(sizeof(float)) : 0);
 }
 
 extern "C" SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, int32_t experts, const int32_t *offsets,
@@ -159,9 +197,12 @@ extern "C" SPMV_API int spmv_feed_forward_grad(int64_t rows, int64_t d, int64_t 
     b.up = matrix(up, ldg);
     b.dy = matrix(dy, lddy);
     char *space = static_cast<char *>(workspace);
+    const int64_t each = rows_bytes(rows, f, dtype);
     b.dgate = matrix(space, padded(f));
-    b.dup = matrix(space + need / 3, padded(f));
-    b.h = matrix(space + need / 3 * 2, padded(f));
+    b.dup = matrix(space + each, padded(f));
+    b.h = matrix(space + 2 * each, padded(f));
+    b.splits = weight_splits(rows, d, f, experts);
+    b.partial = reinterpret_cast<float *>(space + 3 * each);
     b.dx = matrix(dx, lddx);
     b.dwg = matrix(dw_gate, d, f * d);
     b.dwu = matrix(dw_up, d, f * d);
@@ -173,5 +214,6 @@ extern "C" SPMV_API int spmv_feed_forward_grad(int64_t rows, int64_t d, int64_t 
     if (rows && (dx || weights)) SPMV_TRY(run(kBack, b, dtype, false, s));
     if (rows && dx) SPMV_TRY(run(kInput, b, dtype, true, s));
     if (weights) SPMV_TRY(run(kWeights, b, dtype, rows > 0, s));
+    if (weights && b.splits > 1) SPMV_TRY(launch_join(b, dtype, s));
     return SPMV_OK;
 }

@@ -75,6 +75,21 @@ struct Block {
     Matrix y;                    // rows x d
     Matrix dy, dgate, dup, dx;   // rows x d; rows x f; rows x d
     Matrix dwg, dwu, dwd;        // as wg, wu, wd (any may be null)
+    // kWeights of few tiles and many rows: each segment's rows in `splits` parts, whose sums go to `partial`
+    // (which product, segment, part, then its matrix) and are joined by k_join_weights
+    int splits;
+    float *partial;
+    // segment e's rows of part `p`: multiples of 64 but for the last
+    __device__ __forceinline__ Segments::Span part(int e, int p) const {
+        Segments::Span s = seg.span(e);
+        const int64_t each = ((s.end - s.begin + splits - 1) / splits + 63) / 64 * 64;
+        s.begin = s.begin + p * each < s.end ? s.begin + p * each : s.end;
+        if (s.begin + each < s.end) s.end = s.begin + each;
+        return s;
+    }
+    __device__ __forceinline__ float *part_sums(int which, int e, int p) const {
+        return partial + ((static_cast<int64_t>(which) * seg.count + e) * splits + p) * d * f;
+    }
 };
 
 // ----------------------------------------------------------------------------
@@ -135,9 +150,9 @@ __device__ __forceinline__ void get(const T *p, float *v, int64_t left, bool who
 
 // kG values of D from column `col` of row `row` on (kGated: `v` is x Wg^T, `w` is x Wu^T); `whole`: rows of
 // every matrix written or read start at multiples of the pieces' size.  kWeights: `which` of the three
-// products, `e` its segment, `row` and `col` in the segment's matrix.
+// products, `e` its segment, `p` the part of its rows, `row` and `col` in the segment's matrix.
 template <typename T, int kKind, int kG>
-__device__ __forceinline__ void finish(const Block &b, int which, int e, int64_t row, int64_t col, float *v, float *w,
+__device__ __forceinline__ void finish(const Block &b, int which, int e, int p, int64_t row, int64_t col, float *v, float *w,
                                        bool whole) {
     const auto at = [&](const Matrix &m) { return static_cast<T *>(m.p) + row * m.ld + col; };
     if constexpr (kKind == kGated) {
@@ -173,7 +188,8 @@ __device__ __forceinline__ void finish(const Block &b, int which, int e, int64_t
     } else {
         const Matrix &m = which == 0 ? b.dwg : which == 1 ? b.dwu : b.dwd;
         const int64_t n = which == 2 ? b.f : b.d;
-        put<T, kG>(static_cast<T *>(m.p) + e * m.expert + row * m.ld + col, v, n - col, whole);
+        if (b.splits > 1) put<float, kG>(b.part_sums(which, e, p) + row * n + col, v, n - col, n % 4 == 0);
+        else put<T, kG>(static_cast<T *>(m.p) + e * m.expert + row * m.ld + col, v, n - col, whole);
     }
 }
 template <int kKind>

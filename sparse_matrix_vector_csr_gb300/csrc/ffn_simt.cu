@@ -102,15 +102,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_ffn_simt(Block b, unsigned quad
     constexpr int kCols = kKind == kGated ? kTile / 2 : kTile;  // gate's and up's beside each other
     const int which = kKind == kWeights ? blockIdx.z : 0;
     Place place;
-    int64_t col0, m_left, depth;
+    int64_t col0, m_left, depth, k0 = 0;
+    int part = 0;
     if constexpr (kKind == kWeights) {
         const int64_t n_cols = product_columns<kKind>(b, which), n_rows = weight_rows(b, which);
         const int64_t tiles_n = (n_cols + kTile - 1) / kTile;
-        place = Place{static_cast<int>(blockIdx.y), blockIdx.x / tiles_n * kTile, n_rows};
+        place = Place{static_cast<int>(blockIdx.y / b.splits), blockIdx.x / tiles_n * kTile, n_rows};
+        part = static_cast<int>(blockIdx.y % b.splits);
         col0 = (blockIdx.x % tiles_n) * kTile;
         if (place.row >= n_rows || !(which == 0 ? b.dwg : which == 1 ? b.dwu : b.dwd).p) return;
-        const Segments::Span s = b.seg.span(place.e);
+        const Segments::Span s = b.part(place.e, part);
         depth = s.end - s.begin;
+        k0 = s.begin;
     } else {
         if (!find_tile(b.seg, place)) return;
         col0 = static_cast<int64_t>(blockIdx.y) * kCols;
@@ -152,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_ffn_simt(Block b, unsigned quad
             pa = start(pass == 0 ? b.dgate : b.dup, place.row, 0, lda);
             pb = weight(pass == 0 ? b.wg : b.wu, 0, col0, ldb);
         } else {
-            const int64_t k0 = b.seg.span(place.e).begin;
             pa = start(which == 0 ? b.dgate : which == 1 ? b.dup : b.dy, k0, place.row, lda);
             pb = start(which == 2 ? b.h : b.x, k0, col0, ldb);
         }
@@ -202,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_ffn_simt(Block b, unsigned quad
         float v[4] = {acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y};
         float w[4] = {acc[r][2].x, acc[r][2].y, acc[r][3].x, acc[r][3].y};
         if constexpr (kKind == kGated) {
-            if (tx * 4 < n_left) finish<T, kKind, 4>(b, which, place.e, row, col0 + tx * 4, v, w, quads_out);
+            if (tx * 4 < n_left) finish<T, kKind, 4>(b, which, place.e, part, row, col0 + tx * 4, v, w, quads_out);
         } else {
             float spare[4];
-            if (tx * 4 < n_left) finish<T, kKind, 4>(b, which, place.e, row, col0 + tx * 4, v, spare, quads_out);
-            if (64 + tx * 4 < n_left) finish<T, kKind, 4>(b, which, place.e, row, col0 + 64 + tx * 4, w, spare, quads_out);
+            if (tx * 4 < n_left) finish<T, kKind, 4>(b, which, place.e, part, row, col0 + tx * 4, v, spare, quads_out);
+            if (64 + tx * 4 < n_left) finish<T, kKind, 4>(b, which, place.e, part, row, col0 + 64 + tx * 4, w, spare, quads_out);
         }
     }
 }
@@ -230,7 +232,7 @@ int launch(const Block &b, cudaStream_t s) {
     int64_t gx, gy, gz = 1;
     if (kKind == kWeights) {
         gx = ceil_div(b.d, kTile) * ceil_div(b.f, kTile);
-        gy = b.seg.count;
+        gy = static_cast<int64_t>(b.seg.count) * b.splits;
         gz = 3;
     } else {
         gx = b.seg.rows / kTile + (b.seg.count < b.seg.rows ? b.seg.count : b.seg.rows) + 1;

@@ -205,7 +205,7 @@ __device__ __forceinline__ void read_done() { asm volatile("tcgen05.wait::ld.syn
 // tiles
 // ----------------------------------------------------------------------------
 struct Tile {
-    int e, which;
+    int e, which, part;
     int64_t row, end;   // of D: first row and where its rows end
     int64_t col;
     int64_t first, depth;  // kWeights: the segment's rows; else depth is k's extent (0: D is 0)
@@ -223,7 +223,7 @@ struct Tiles {
             total = 0;
             for (int i = 0; i < a.products; ++i) total += of(a.which[i]);
             columns = total;  // of one segment
-            total *= b.seg.count;
+            total *= static_cast<int64_t>(b.seg.count) * b.splits;
         } else {
             columns = (product_columns<kKind>(b, 0) + kCols - 1) / kCols;
             total = columns * prefix[b.seg.count + (kKind == kBack ? 0 : 1)];
@@ -234,11 +234,13 @@ struct Tiles {
     }
     __device__ __forceinline__ Tile operator[](int64_t t) const {
         Tile r;
-        r.which = 0;
+        r.which = r.part = 0;
         r.first = 0;
         if constexpr (kKind == kWeights) {
-            r.e = static_cast<int>(t / columns);
-            int64_t i = t - r.e * columns;
+            const int64_t parts = t / columns;
+            int64_t i = t - parts * columns;
+            r.e = static_cast<int>(parts / b.splits);
+            r.part = static_cast<int>(parts % b.splits);
             for (int p = 0;; ++p) {
                 r.which = args.which[p];
                 const int64_t n = of(r.which);
@@ -249,7 +251,7 @@ struct Tiles {
             const int64_t m = (r.end + kTileRows - 1) / kTileRows;
             r.row = i % m * kTileRows;
             r.col = i / m * kCols;
-            const Segments::Span s = b.seg.span(r.e);
+            const Segments::Span s = b.part(r.e, r.part);
             r.first = s.begin;
             r.depth = s.end - s.begin;
         } else {
@@ -782,6 +784,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                     patch_out<T>(mine, at(b.h, c), b.h.ld, rows, left);
                 } else {
                     const Matrix &m = kKind == kDown ? b.y : kKind == kInput ? b.dx : t.which == 0 ? b.dwg : t.which == 1 ? b.dwu : b.dwd;
+                    if constexpr (kKind == kWeights) {
+                        if (b.splits > 1) {
+                            const int64_t n = product_columns<kKind>(b, t.which);
+                            if (lane < rows) put<float, 32>(b.part_sums(t.which, t.e, t.part) + (row + lane) * n + t.col + c, v, left, n % 4 == 0);
+                            continue;
+                        }
+                    }
                     patch_row<T>(mine, v);
                     patch_out<T>(mine, at(m, c) + (kKind == kWeights ? t.e * m.expert : 0), m.ld, rows, left);
                 }
@@ -851,7 +860,7 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
             if (!out[i]->p) continue;
             args.which[args.products++] = i;
             ok = ok && activation(&args.a[i], *in[i], weight_rows(b, i)) && activation(&args.b[i], i == 2 ? b.h : b.x, i == 2 ? f : d);
-            tiles += ceil_div(weight_rows(b, i), S::kTileRows) * ceil_div(product_columns<kKind>(b, i), kN) * count;
+            tiles += ceil_div(weight_rows(b, i), S::kTileRows) * ceil_div(product_columns<kKind>(b, i), kN) * count * b.splits;
         }
     } else if (kKind == kGated) {
         ok = ok && activation(&args.a[0], b.x, d) && weight(&args.b[0], b.wg, d, f, kN / 2) && weight(&args.b[1], b.wu, d, f, kN / 2);
@@ -897,7 +906,7 @@ int launch_shape(const Block &b, bool follows, cudaStream_t s) {
     const int64_t rows = b.seg.rows, mean = ceil_div(rows, b.seg.count);  // rows of a segment, taking them as equally long
     const int64_t columns = product_columns<kKind>(b, 0);
     if constexpr (kKind == kWeights) {
-        const int64_t tiles = (2 * ceil_div(b.f, 256) * ceil_div(b.d, 256) + ceil_div(b.d, 256) * ceil_div(b.f, 256)) * b.seg.count;
+        const int64_t tiles = (2 * ceil_div(b.f, 256) * ceil_div(b.d, 256) + ceil_div(b.d, 256) * ceil_div(b.f, 256)) * b.seg.count * b.splits;
         if (tiles >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, follows, s);
         return launch<T, kKind, 64, 128, false>(b, follows, s);
     } else {

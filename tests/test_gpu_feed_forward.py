@@ -165,6 +165,57 @@ def test_experts_without_rows_and_all_in_one(spmv, dtype):
                 assert not any(t[e].any() for t in grads[1:])
 
 
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows,d,f", [(1024, 64, 64), (2500, 40, 136), (5000, 37, 53), (4133, 8, 8), (1100, 264, 72)])
+def test_many_rows_of_small_matrices(spmv, dtype, rows, d, f):
+    """the weights' gradients in several parts of the rows"""
+    g = gen(rows)
+    x, dy = torch.randn(rows, d, generator=g).to(dtype).cuda(), torch.randn(rows, d, generator=g).to(dtype).cuda()
+    ws = weights(None, d, f, dtype, g)
+    check(spmv, x, ws, "silu", dy, [(0, rows)], lambda keep: spmv.feed_forward(x, *ws, keep=keep))
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("align,d,f", [(1, 64, 40), (16, 72, 128), (1, 21, 30)])
+def test_experts_of_many_rows(spmv, dtype, align, d, f):
+    """parts of segments of different lengths, one of them empty, one of a few rows"""
+    g = gen(align + d)
+    ids = torch.tensor([0] * 3000 + [2] * 1500 + [3] * 7, dtype=torch.int32)[torch.randperm(4507, generator=g)][:, None].cuda()
+    plan = spmv.RoutePlan(ids, 4, align=align)
+    xs, dys = (plan.dispatch(torch.randn(4507, d, generator=g).to(dtype).cuda()) for _ in range(2))
+    offsets = plan.offsets.tolist()
+    xs[offsets[-1]:], dys[offsets[-1]:] = math.nan, math.nan
+    ws = weights(4, d, f, dtype, g)
+    _, grads = check(spmv, xs, ws, "silu", dys, list(zip(offsets, offsets[1:])), lambda keep: plan.feed_forward(xs, *ws, keep=keep))
+    assert not any(w[1].any() for w in grads[1:])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_wide_tiles(spmv, dtype):
+    """sizes at which pairs of CTAs share a tile, in the forward and every backward product, ragged at every border; against
+    products in 64 bits on the GPU"""
+    g = gen(11)
+    plan, xs, dys, spans = routed(spmv, 1500, 2, 3, 1, 1032, dtype, g)
+    ws = weights(3, 1032, 4104, dtype, g)
+    ff = plan.feed_forward(xs, *ws, keep=True)
+    grads = ff.grad(dys)
+    for e, (a, b) in enumerate(spans):
+        leaves = [t.double().requires_grad_() for t in (xs[a:b], *(w[e] for w in ws))]
+        gate, up = leaves[0] @ leaves[1].t(), leaves[0] @ leaves[2].t()
+        y = (torch.nn.functional.silu(gate) * up) @ leaves[3].t()
+        want = [gate, up, y, *torch.autograd.grad(y, leaves, dys[a:b].double())]
+        got = [ff.gate[a:b], ff.up[a:b], ff.y[a:b], grads[0][a:b], *(w[e] for w in grads[1:])]
+        for i, (p, q) in enumerate(zip(got, want)):
+            # roundings, each within H of a value: of the result; of h (y); of gate, up and their gradients (the others)
+            assert float((p.double() - q).norm() / q.norm()) <= H[dtype] * (1, 1, 2, 4, 4, 4, 4)[i], i
+            assert float((p.double() - q).abs().max()) <= H[dtype] * 8 * float(q.abs().max()), i
+
+
+def test_status(spmv):
+    """no wait of any call before has run out"""
+    spmv.spmv_feed_forward_status()
+
+
 def test_many_experts(spmv):
     g = gen(4)
     ids = torch.randint(0, 4096, (300, 2), generator=g, dtype=torch.int32).cuda()
