@@ -24,7 +24,9 @@ namespace ffn {
 namespace tc {
 
 constexpr int kWriters = 8;       // warps that write D; behind them one that copies and one that multiplies
-constexpr int kThreads = (kWriters + 2) * 32;
+// (kWeights: one more, that clears what is not the segment's)
+constexpr int threads_of(int kind) { return (kWriters + (kind == kWeights ? 3 : 2)) * 32; }
+constexpr int kThreads = threads_of(kGated);
 constexpr int kRows = 128;        // of a tile of D: the accumulator's lanes
 constexpr int kDepth = 64;        // of a stage: 128 bytes, the width of the swizzle
 constexpr int kRowBytes = 128;
@@ -409,7 +411,7 @@ struct Shape {
     static constexpr int kBlockBytes = kABytes + kBBytes, kStageBytes = kBlocks * kBlockBytes;
     static constexpr int kSlack = kRows * kRowBytes - kABytes;  // behind the ring: what the last stage's product reads
     static constexpr int kWriterBytes = kKind == kBack ? 5 * kPatchBytes : kPatchBytes;
-    static constexpr int kFixed = 1024 + kSlack + kWriters * kWriterBytes + (3 * kMaxStages + 5) * 8;
+    static constexpr int kFixed = 1024 + kSlack + kWriters * kWriterBytes + (4 * kMaxStages + 5) * 8;
     static constexpr int kColumns = 2 * kN * kAccs;  // of tensor memory: two buffers
     static int stages(int segments) {
         const int n = (kSharedBytes - 256 - kFixed - (segments + 2) * 4) / kStageBytes;
@@ -419,7 +421,7 @@ struct Shape {
 };
 
 template <typename T, int kKind, int kN, int kLoaded, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Args args) {
+__global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_constant__ Args args) {
     using S = Shape<kKind, kN, kLoaded, kPair>;
     constexpr bool kAcrossA = a_transposed(kKind), kAcrossB = b_transposed(kKind);
     extern __shared__ uint8_t raw[];
@@ -432,11 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
     const uint32_t bars = patches + kWriters * S::kWriterBytes;
     const auto full = [&](int s) { return bars + 8 * s; };
     const auto empty = [&](int s) { return bars + 8 * (kMaxStages + s); };
-    const auto other_full = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };  // the second CTA's stage
-    const auto acc_full = [&](int i) { return bars + 8 * (3 * kMaxStages + i); };
-    const auto acc_empty = [&](int i) { return bars + 8 * (3 * kMaxStages + 2 + i); };
-    const uint32_t drained = bars + 8 * (3 * kMaxStages + 4);
-    int32_t *prefix = reinterpret_cast<int32_t *>(raw + (bars + 8 * (3 * kMaxStages + 5) - smem_addr(raw)));
+    // a segment's last rows (kWeights), which every CTA has to clear something in first: here, and cleared in every CTA
+    const auto rest_full = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };
+    const auto cleared = [&](int s) { return bars + 8 * (3 * kMaxStages + s); };
+    const auto acc_full = [&](int i) { return bars + 8 * (4 * kMaxStages + i); };
+    const auto acc_empty = [&](int i) { return bars + 8 * (4 * kMaxStages + 2 + i); };
+    const uint32_t drained = bars + 8 * (4 * kMaxStages + 4);
+    int32_t *prefix = reinterpret_cast<int32_t *>(raw + (bars + 8 * (4 * kMaxStages + 5) - smem_addr(raw)));
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (seen to be the warp's)
     const int rank = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // in the pair
     const int64_t first = blockIdx.x / S::kCtas, step = gridDim.x / S::kCtas;
@@ -448,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
         for (int s = 0; s < stages; ++s) {
             bar_init(full(s), 1);
             bar_init(empty(s), 1);
-            bar_init(other_full(s), 1);
+            bar_init(rest_full(s), 1);
+            bar_init(cleared(s), S::kCtas);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(acc_full(i), 1);
@@ -479,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
     if (warp == kWriters) {
         if (one_lane()) {
             int s = 0, round = 0;
+            uint32_t full_fills = 0, rest_fills = 0, rest_last = 0;  // a bit a stage: parity of its fills of either kind, kind of the last
             bool ok = true;
             // block q of the tile to place `at` of the ring: B's part, A's part
             const auto copy_b = [&](const Tile &t, int at, int q, int once, uint32_t bar) {
@@ -537,14 +543,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                 for (int q0 = 0; q0 < n; q0 += S::kBlocks) {
                     if (!(ok = bar_wait(empty(s), (round & 1) ^ 1, gave_up, failed))) break;
                     const int blocks = min(S::kBlocks, n - q0);
-                    // a pair's copies are counted by its first CTA, but for a segment's last rows (kWeights), in which each
-                    // CTA has something to clear first
-                    const bool own = !kPair || (kKind == kWeights && t.depth - static_cast<int64_t>(q0) * kDepth < kDepth);
-                    const uint32_t bar = own || rank == 0 ? full(s) : bar_first(full(s));
+                    // a pair's copies are counted by its first CTA, but for a segment's last rows, by each CTA
+                    const bool rest = kKind == kWeights && t.depth - static_cast<int64_t>(q0) * kDepth < kDepth;
+                    const bool own = !kPair || rest;
+                    const uint32_t here = rest ? rest_full(s) : full(s), bar = own || rank == 0 ? here : bar_first(here);
+                    (rest ? rest_fills : full_fills) ^= 1u << s;
+                    rest_last = rest ? rest_last | 1u << s : rest_last & ~(1u << s);
                     if (ahead > 0) {
                         --ahead;
                     } else {
-                        if (own || rank == 0) bar_expect(full(s), (own ? 1 : 2) * blocks * S::kBlockBytes);
+                        if (own || rank == 0) bar_expect(here, (own ? 1 : 2) * blocks * S::kBlockBytes);
                         for (int j = 0; j < blocks; ++j) copy_b(t, s * S::kBlocks + j, q0 + j, once, bar);
                     }
                     for (int j = 0; j < blocks; ++j) copy_a(t, s * S::kBlocks + j, q0 + j, once, bar);
@@ -559,24 +567,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
                 const int last = j < s ? round : round - 1;  // the round in which the stage was filled last
                 if (last < 0) continue;
                 if (ok) ok = bar_wait(empty(j), last & 1, gave_up, failed);
-                if (!ok && rank == 0) {
+                const bool rest = rest_last >> j & 1;
+                if (!ok && (rest || rank == 0)) {
                     const long long t0 = clock64();
-                    while (!bar_try(full(j), last & 1) && clock64() - t0 < kWaitCycles) {}
+                    while (!bar_try(rest ? rest_full(j) : full(j), (~(rest ? rest_fills : full_fills)) >> j & 1) && clock64() - t0 < kWaitCycles) {}
                 }
             }
         }
         __syncwarp();
     } else if (warp == kWriters + 1) {
         constexpr uint32_t shape = product_shape<T, kKind, kN, kPair>();
-        int s = 0, round = 0, done = 0;
-        uint32_t own_parity = 0;  // of the stages' barriers in the second CTA, and of other_full: used for a segment's last rows only
+        int s = 0, done = 0;
+        uint32_t full_parity = 0, cleared_parity = 0;  // a bit a stage
         bool ok = true;
-        const auto next = [&] {
-            if (++s == stages) {
-                s = 0;
-                ++round;
-            }
-        };
         // by one lane: stage s of a tile, its blocks from q0 on, the last block `steps` 16s of k
         const auto products = [&](int q0, int n, int steps) {
             fence_after();
@@ -597,69 +600,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_ffn(const __grid_constant__ Arg
             signal_done<kPair>(empty(s));
             if (q0 + blocks == n) signal_done<kPair>(acc_full(done & 1));
         };
-        if constexpr (kKind != kWeights) {
-            if (rank == 0 && one_lane())
-                for (int64_t i = first; ok && i < tiles.total; i += step) {
-                    const int n = blocks_of(tiles[i]);
-                    if (n == 0) continue;
-                    if (!(ok = bar_wait(acc_empty(done & 1), ((done >> 1) & 1) ^ 1, gave_up, failed))) break;
-                    for (int q = 0; q < n; q += S::kBlocks) {
-                        if (!(ok = bar_wait(full(s), round & 1, gave_up, failed))) break;
-                        products(q, n, kDepth / 16);
-                        next();
-                    }
-                    ++done;
-                }
-            __syncwarp();
-            ok = __all_sync(0xffffffffu, ok);
-        } else {
+        if (rank == 0 && one_lane())
             for (int64_t i = first; ok && i < tiles.total; i += step) {
                 const Tile t = tiles[i];
-                const int n = blocks_of(t), left = static_cast<int>(t.depth % kDepth);
+                const int n = blocks_of(t), left = kKind == kWeights ? static_cast<int>(t.depth % kDepth) : 0;
                 if (n == 0) continue;
-                // one lane has the stages in which nothing is to be cleared, the warp the last one where something is
-                const int alone = left ? n - 1 : n;
-                if (rank == 0) {
-                    if (one_lane()) {
-                        const int s0 = s, round0 = round;
-                        ok = bar_wait(acc_empty(done & 1), ((done >> 1) & 1) ^ 1, gave_up, failed);
-                        for (int q = 0; ok && q < alone; ++q) {
-                            if (!(ok = bar_wait(full(s), round & 1, gave_up, failed))) break;
-                            products(q, n, kDepth / 16);
-                            next();
-                        }
-                        s = s0;
-                        round = round0;
+                if (!(ok = bar_wait(acc_empty(done & 1), ((done >> 1) & 1) ^ 1, gave_up, failed))) break;
+                for (int q = 0; q < n; q += S::kBlocks) {
+                    int steps = kDepth / 16;
+                    if (left && q == n - 1) {
+                        if (!(ok = bar_wait(cleared(s), cleared_parity >> s & 1, gave_up, failed))) break;
+                        if (kPair) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                        cleared_parity ^= 1u << s;
+                        steps = (left + 15) / 16;
+                    } else {
+                        if (!(ok = bar_wait(full(s), full_parity >> s & 1, gave_up, failed))) break;
+                        full_parity ^= 1u << s;
                     }
-                    __syncwarp();
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                }
-                round += (s + alone) / stages;
-                s = (s + alone) % stages;
-                if (left) {  // rows of other segments, up to a whole 16 of k
-                    if (!(ok = warp_wait<false>(full(s), rank == 0 ? round & 1 : own_parity >> s & 1, gave_up, failed))) break;
-                    clear_rows<kN / S::kCtas>(ring_a + s * S::kABytes, ring_b + s * S::kBBytes, left);
-                    if (kPair && rank == 1) {
-                        if (lane == 0) bar_arrive_first<true>(other_full(s));
-                        __syncwarp();
-                    } else if (kPair) {
-                        if (!(ok = warp_wait<false>(other_full(s), own_parity >> s & 1, gave_up, failed))) break;
-                        asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                    }
-                    own_parity ^= 1u << s;
-                    if (rank == 0 && one_lane()) products(n - 1, n, (left + 15) / 16);
-                    __syncwarp();
-                    next();
+                    products(q, n, steps);
+                    if (++s == stages) s = 0;
                 }
                 ++done;
             }
-        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok && rank == 0 && one_lane()) {  // given up: the products in flight end before their memory is given back
             signal_done<kPair>(drained);
             const long long t0 = clock64();
             while (!bar_try(drained, 0) && clock64() - t0 < kWaitCycles) {}
         }
         __syncwarp();
+    } else if (kKind == kWeights && warp == kWriters + 2) {
+        // rows of other segments in a tile's last stage, up to a whole 16 of k, as soon as they are there
+        int s = 0;
+        uint32_t parity = 0;  // a bit a stage
+        for (int64_t i = first; i < tiles.total; i += step) {
+            const Tile t = tiles[i];
+            const int left = static_cast<int>(t.depth % kDepth);
+            if (left == 0) {
+                s = (s + blocks_of(t)) % stages;
+                continue;
+            }
+            s = (s + blocks_of(t) - 1) % stages;
+            if (!warp_wait<false>(rest_full(s), parity >> s & 1, gave_up, failed)) break;
+            parity ^= 1u << s;
+            clear_rows<kN / S::kCtas>(ring_a + s * S::kABytes, ring_b + s * S::kBBytes, left);
+            if (lane == 0) {
+                if (kPair && rank == 1) bar_arrive_first<true>(cleared(s));
+                else bar_arrive(cleared(s));
+            }
+            __syncwarp();
+            s = (s + 1) % stages;
+        }
     } else {
         int done = 0;
         const Block &b = args.block;
@@ -881,7 +873,7 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
     SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((tiles < workers ? tiles : workers) * S::kCtas));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(kKind));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
