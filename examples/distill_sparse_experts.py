@@ -4,12 +4,14 @@ A student (embedding, router, experts, output matrix) learns a random teacher's 
 vocabulary of which only the k largest logits of each row, and their log-sum, are kept.  One step:
 
     teacher:  topk_rows             its logits -> k columns and values a row, log-sum
-    student:  topk_rows             router logits -> experts and weights a token
+    student:  embed_rows            tokens -> rows of the embedding
+              topk_rows             router logits -> experts and weights a token
               RoutePlan, dispatch   tokens sorted by expert
               (the experts' dense products, by torch)
               combine               experts' rows back to tokens, weighted
               distill_loss_grad     loss, and its gradient in place of the logits
               combine_grad, dispatch_grad, TopRows.grad   back to the experts, the tokens, the router
+              embed_rows_grad       back to the embedding
 
     python examples/distill_sparse_experts.py [--steps 60]
 """
@@ -46,7 +48,8 @@ class Student:
 
     def step(self, token, target, lr):
         w = self.weights
-        x = w["embed"][token]
+        token = token.to(torch.int32)
+        x = spmv.embed_rows(w["embed"], token)
         top = spmv.topk_rows(x @ w["router"], self.k, weights="selected")
         plan = spmv.RoutePlan(top.ids, self.experts, align=self.align)
         offsets = plan.offsets.tolist()
@@ -62,7 +65,7 @@ class Student:
         dlogits = top.grad(dweights)
         dx = dh + plan.dispatch_grad(dxs) + dlogits @ w["router"].t()
         grads = {"out": h.t() @ dz, "router": x.t() @ dlogits, "up": torch.zeros_like(w["up"]),
-                 "embed": torch.zeros_like(w["embed"]).index_add_(0, token, dx)}
+                 "embed": spmv.embed_rows_grad(dx, token, len(w["embed"]))}
         for e in range(self.experts):
             a, b = offsets[e], offsets[e + 1]
             grads["up"][e] = xs[a:b].t() @ dys[a:b]

@@ -213,67 +213,63 @@ struct Tile {
     int64_t first, depth;  // kWeights: the segment's rows; else depth is k's extent (0: D is 0)
 };
 
-// Tiles of kTileRows x kCols columns; row tiles of the segments counted in `prefix` (its last entry: all).
+// Tiles of kTileRows x kCols columns; row tiles of the segments counted in `prefix` (its last entry: all).  Fewer than
+// 2^31, so that a tile's place takes divisions of 32 bits: it is worked out between two tiles' copies, and the ring has
+// to cover what that takes (weights' gradients of 64 experts, 6144 tiles: 597 us, with divisions of 64 bits 615).
 template <int kKind, int kTileRows, int kCols>
 struct Tiles {
     const Block &b;
     const Args &args;
     const int32_t *prefix;
-    int64_t columns, total;
+    uint32_t columns, total;
+    int e = 0;  // the segment of the last tile asked for: those asked for next lie in it or behind
     __device__ __forceinline__ Tiles(const Args &a, const int32_t *p) : b(a.block), args(a), prefix(p) {
         if constexpr (kKind == kWeights) {
-            total = 0;
-            for (int i = 0; i < a.products; ++i) total += of(a.which[i]);
-            columns = total;  // of one segment
-            total *= static_cast<int64_t>(b.seg.count) * b.splits;
+            columns = 0;  // of one part of a segment
+            for (int i = 0; i < a.products; ++i) columns += of(a.which[i]);
+            total = columns * static_cast<uint32_t>(b.seg.count * b.splits);
         } else {
-            columns = (product_columns<kKind>(b, 0) + kCols - 1) / kCols;
-            total = columns * prefix[b.seg.count + (kKind == kBack ? 0 : 1)];
+            columns = static_cast<uint32_t>((product_columns<kKind>(b, 0) + kCols - 1) / kCols);
+            total = columns * static_cast<uint32_t>(prefix[b.seg.count + (kKind == kBack ? 0 : 1)]);
         }
     }
-    __device__ __forceinline__ int64_t of(int which) const {
-        return (weight_rows(b, which) + kTileRows - 1) / kTileRows * ((product_columns<kKind>(b, which) + kCols - 1) / kCols);
+    __device__ __forceinline__ uint32_t of(int which) const {
+        return static_cast<uint32_t>((weight_rows(b, which) + kTileRows - 1) / kTileRows * ((product_columns<kKind>(b, which) + kCols - 1) / kCols));
     }
-    __device__ __forceinline__ Tile operator[](int64_t t) const {
+    __device__ __forceinline__ Tile operator[](uint32_t t) {
         Tile r;
         r.which = r.part = 0;
         r.first = 0;
         if constexpr (kKind == kWeights) {
-            const int64_t parts = t / columns;
-            int64_t i = t - parts * columns;
-            r.e = static_cast<int>(parts / b.splits);
-            r.part = static_cast<int>(parts % b.splits);
+            const uint32_t parts = t / columns, splits = static_cast<uint32_t>(b.splits);
+            uint32_t i = t - parts * columns;
+            r.e = static_cast<int>(parts / splits);
+            r.part = static_cast<int>(parts - r.e * splits);
             for (int p = 0;; ++p) {
                 r.which = args.which[p];
-                const int64_t n = of(r.which);
+                const uint32_t n = of(r.which);
                 if (i < n) break;
                 i -= n;
             }
             r.end = weight_rows(b, r.which);
-            const int64_t m = (r.end + kTileRows - 1) / kTileRows;
-            r.row = i % m * kTileRows;
-            r.col = i / m * kCols;
+            const uint32_t m = static_cast<uint32_t>((r.end + kTileRows - 1) / kTileRows), col = i / m;
+            r.row = static_cast<int64_t>(i - col * m) * kTileRows;
+            r.col = static_cast<int64_t>(col) * kCols;
             const Segments::Span s = b.part(r.e, r.part);
             r.first = s.begin;
             r.depth = s.end - s.begin;
         } else {
-            int lo = 0, hi = b.seg.count + 1;  // prefix[lo] * columns <= t < prefix[hi] * columns
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (prefix[mid] * columns <= t) lo = mid;
-                else hi = mid;
-            }
-            r.e = lo;
-            const int64_t i = t - prefix[lo] * columns;
-            const int m = prefix[lo + 1] - prefix[lo];
-            constexpr int kGroup = kGroupRows / kTileRows;
-            const int64_t g = i / (kGroup * columns), j = i - g * kGroup * columns;
-            const int64_t in_group = min(static_cast<int64_t>(m) - g * kGroup, static_cast<int64_t>(kGroup));
-            const Segments::Span s = b.seg.span(lo);
-            r.row = s.begin + (g * kGroup + j % in_group) * kTileRows;
+            while (static_cast<uint32_t>(prefix[e + 1]) * columns <= t) ++e;
+            r.e = e;
+            constexpr uint32_t kGroup = kGroupRows / kTileRows;
+            const uint32_t i = t - static_cast<uint32_t>(prefix[e]) * columns, m = static_cast<uint32_t>(prefix[e + 1] - prefix[e]);
+            const uint32_t g = i / (kGroup * columns), j = i - g * kGroup * columns;
+            const uint32_t in_group = min(m - g * kGroup, kGroup), col = j / in_group;
+            const Segments::Span s = b.seg.span(e);
+            r.row = s.begin + static_cast<int64_t>(g * kGroup + j - col * in_group) * kTileRows;
             r.end = s.end;
-            r.col = j / in_group * kCols;
-            r.depth = lo == b.seg.count ? 0 : kKind == kGated || kKind == kBack ? b.d : b.f;
+            r.col = static_cast<int64_t>(col) * kCols;
+            r.depth = e == b.seg.count ? 0 : kKind == kGated || kKind == kBack ? b.d : b.f;
         }
         return r;
     }
@@ -443,7 +439,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
     int32_t *prefix = reinterpret_cast<int32_t *>(raw + (bars + 8 * (4 * kMaxStages + 5) - smem_addr(raw)));
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (seen to be the warp's)
     const int rank = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // in the pair
-    const int64_t first = blockIdx.x / S::kCtas, step = gridDim.x / S::kCtas;
+    const uint32_t first = blockIdx.x / S::kCtas, step = gridDim.x / S::kCtas;
     volatile int *gave_up = &gave_up_at;
     int *failed = args.failed;
 
@@ -478,7 +474,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
     fence_after();
     dev::allow_dependents();
     const uint32_t tmem = tmem_at;
-    const Tiles<kKind, S::kTileRows, S::kCols> tiles(args, prefix);
+    Tiles<kKind, S::kTileRows, S::kCols> tiles(args, prefix);
     const auto blocks_of = [&](const Tile &t) { return static_cast<int>((t.depth + kDepth - 1) / kDepth) * (kKind == kInput ? 2 : 1); };
 
     if (warp == kWriters) {
@@ -537,7 +533,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                 }
                 dev::grid_wait();
             }
-            for (int64_t i = first; ok && i < tiles.total; i += step) {
+            for (uint32_t i = first; ok && i < tiles.total; i += step) {
                 const Tile t = tiles[i];
                 const int n = blocks_of(t), once = kKind == kInput ? n / 2 : n;
                 for (int q0 = 0; q0 < n; q0 += S::kBlocks) {
@@ -601,7 +597,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
             if (q0 + blocks == n) signal_done<kPair>(acc_full(done & 1));
         };
         if (rank == 0 && one_lane())
-            for (int64_t i = first; ok && i < tiles.total; i += step) {
+            for (uint32_t i = first; ok && i < tiles.total; i += step) {
                 const Tile t = tiles[i];
                 const int n = blocks_of(t), left = kKind == kWeights ? static_cast<int>(t.depth % kDepth) : 0;
                 if (n == 0) continue;
@@ -634,7 +630,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
         // rows of other segments in a tile's last stage, up to a whole 16 of k, as soon as they are there
         int s = 0;
         uint32_t parity = 0;  // a bit a stage
-        for (int64_t i = first; i < tiles.total; i += step) {
+        for (uint32_t i = first; i < tiles.total; i += step) {
             const Tile t = tiles[i];
             const int left = static_cast<int>(t.depth % kDepth);
             if (left == 0) {
@@ -658,7 +654,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
         const uint32_t mine = patches + warp * S::kWriterBytes;
         constexpr int kHalves = S::kCols > 32 ? 2 : 1;  // the two warps of a quarter of the lanes take columns in turn
         const int quarter = warp & 3, half = warp >> 2;
-        for (int64_t i = first; i < tiles.total; i += step) {
+        for (uint32_t i = first; i < tiles.total; i += step) {
             const Tile t = tiles[i];
             const bool zero = blocks_of(t) == 0;
             const int which = done & 1;
@@ -868,6 +864,7 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
     if (!ok) return set_error(SPMV_ERR_CUDA, "the feed-forward block's matrices could not be described to the copy engine");
     if (kKind != kWeights)
         tiles = ceil_div(product_columns<kKind>(b, 0), S::kCols) * (rows / S::kTileRows + (count < rows ? count : rows) + 1);
+    if (tiles >= int64_t(1) << 31) return set_error(SPMV_ERR_TOO_LARGE, "the feed-forward block has too many tiles");
     const size_t smem = S::smem(static_cast<int>(count), args.stages);
     const int64_t workers = kSms / S::kCtas;
     SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));

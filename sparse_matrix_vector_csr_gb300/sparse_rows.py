@@ -349,56 +349,71 @@ def _weights(t, name, experts, rows, cols, dtype):
     return ld, apart
 
 
-def _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, stream, offsets, experts, rows):
-    if stream is not None:
-        with _on(stream, x, w_gate, w_up, w_down, out, offsets):
-            return _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, None, offsets, experts, rows)
-    code, ldx = _matrix(x, "x", rows)
+def _block(x, w_gate, w_up, w_down, offsets, experts, gate, up, act):
+    """(row type, what spmv_feed_forward and its gradient begin with) for these tensors."""
+    code, ldx = _matrix(x, "x")
     rows, d = x.shape
-    if w_gate.dim() != (2 if experts is None else 3):
-        raise ValueError("w_gate must be a matrix" if experts is None else "w_gate must be experts x f x d")
-    f, dtype, device = w_gate.shape[-2], x.dtype, x.device
+    f, dtype = w_gate.shape[-2], x.dtype
     ldw, apart = _weights(w_gate, "w_gate", experts, f, d, dtype)
     if _weights(w_up, "w_up", experts, f, d, dtype) != (ldw, apart):
         raise ValueError("w_up must have the strides of w_gate")
     ldd, apart_d = _weights(w_down, "w_down", experts, d, f, dtype)
-    act = ACTIVATIONS[activation]
+    if gate is None:
+        kept = (None, None, f)
+    else:
+        ldg = _matrix(gate, "gate", rows, f, dtype)[1]
+        if _matrix(up, "up", rows, f, dtype)[1] != ldg:
+            raise ValueError("up must have the row stride of gate")
+        kept = (gate.data_ptr() or None, up.data_ptr() or None, ldg)
+    return code, (rows, d, f, experts or 1, None if offsets is None else offsets.data_ptr(), x.data_ptr() or None, ldx,
+                  w_gate.data_ptr(), w_up.data_ptr(), ldw, apart, w_down.data_ptr(), ldd, apart_d, act, *kept)
+
+
+def _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, stream, offsets, experts, rows):
+    if stream is not None:
+        with _on(stream, x, w_gate, w_up, w_down, out, offsets):
+            return _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, None, offsets, experts, rows)
+    if x.dim() != 2 or (rows is not None and x.shape[0] != rows):
+        raise ValueError("x must be a matrix" + (f" of {rows} rows" if rows is not None else ""))
+    if w_gate.dim() != (2 if experts is None else 3):
+        raise ValueError("w_gate must be a matrix" if experts is None else "w_gate must be experts x f x d")
+    act, device, f = ACTIVATIONS[activation], x.device, w_gate.shape[-2]
     res = FeedForward()
     res.gate = res.up = None
-    wide = (f + 7) // 8 * 8  # rows that the tensor cores can be fed from
-    if keep:
-        res.gate, res.up = _empty((2, rows, wide), dtype=dtype, device=device)[:, :, :f].unbind(0)
+    if keep:  # rows that the tensor cores can be fed from
+        wide = (f + 7) // 8 * 8
+        res.gate, res.up = _empty((2, x.shape[0], wide), dtype=x.dtype, device=device)[:, :, :f].unbind(0)
+    code, call = _block(x, w_gate, w_up, w_down, offsets, experts, res.gate, res.up, act)
+    rows, d = x.shape
     res.y, ldy = _out(out, "out", x, rows, d)
-    work = _check(lib.spmv_feed_forward_workspace(rows, d, f, experts or 1, code, 0))
+    work = _check(lib.spmv_feed_forward_workspace(rows, d, f, call[3], code, 0))
     space = _empty((work,), dtype=torch.uint8, device=device)
-    call = (rows, d, f, experts or 1, None if offsets is None else offsets.data_ptr(), x.data_ptr() or None, ldx,
-            w_gate.data_ptr(), w_up.data_ptr(), ldw, apart, w_down.data_ptr(), ldd, apart_d, act,
-            res.gate.data_ptr() if keep else None, res.up.data_ptr() if keep else None, wide)
-    _check(lib.spmv_feed_forward(*call, res.y.data_ptr(), ldy, code, space.data_ptr() or None, work, _current(x)))
-    res._call, res._held = (call, code) if keep else None, (x, w_gate, w_up, w_down, offsets, res.gate, res.up)
+    _check(lib.spmv_feed_forward(*call, res.y.data_ptr() or None, ldy, code, space.data_ptr() or None, work, _current(x)))
+    res._args = (x, w_gate, w_up, w_down, offsets, experts, res.gate, res.up, act) if keep else None
     return res
 
 
 class FeedForward:
     """``y``, and with keep the ``gate`` and ``up`` rows that the gradient needs."""
 
-    __slots__ = ("y", "gate", "up", "_call", "_held")
+    __slots__ = ("y", "gate", "up", "_args")
 
     def grad(self, dy, weights=True, out=None, stream=None):
         """(dx, dw_gate, dw_up, dw_down) for dy, the loss's gradient in y; the last three None without
-        ``weights``.  Neither the call's inputs nor gate and up may have been changed in place."""
-        if self._call is None:
+        ``weights``.  They are those of the call as it was made, whatever tensors the attributes have by then;
+        neither its inputs nor gate and up may have been changed in place."""
+        if self._args is None:
             raise ValueError("feed_forward was called without keep")
         if stream is not None:
-            with _on(stream, *self._held, dy, out):
+            with _on(stream, *[t for t in self._args if isinstance(t, torch.Tensor)], dy, out):
                 return self.grad(dy, weights, out)
-        call, code = self._call
-        rows, d, f = call[:3]
-        x, w_gate, w_up, w_down = self._held[:4]
+        code, call = _block(*self._args)
+        x = self._args[0]
+        rows, d, f, experts = call[:4]
         lddy = _matrix(dy, "dy", rows, d, x.dtype)[1]
         dx, lddx = _out(out, "out", x, rows, d)
-        dws = [_empty(w.shape, dtype=x.dtype, device=x.device) if weights else None for w in (w_gate, w_up, w_down)]
-        work = _check(lib.spmv_feed_forward_workspace(rows, d, f, call[3], code, 1))
+        dws = [_empty(w.shape, dtype=x.dtype, device=x.device) if weights else None for w in self._args[1:4]]
+        work = _check(lib.spmv_feed_forward_workspace(rows, d, f, experts, code, 1))
         space = _empty((work,), dtype=torch.uint8, device=x.device)
         _check(lib.spmv_feed_forward_grad(*call, dy.data_ptr() or None, lddy, dx.data_ptr() or None, lddx,
                                           *[None if w is None else w.data_ptr() for w in dws], code,

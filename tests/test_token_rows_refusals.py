@@ -140,3 +140,29 @@ def test_experts_feed_forward_arguments(rows):
                 lambda: plan.feed_forward(xs, fused[:, :12].expand(4, 12, 8), fused[:, 12:], wd[:1].expand(4, 8, 12))):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("change", ["none", "deepcopy", "pickle", "assigned"])
+def test_a_block_passes_the_tensors_it_has(rows, change):
+    """the gradient's call gets the addresses of the tensors that the result holds, copied or not; other tensors
+    in the public attributes change nothing"""
+    import copy
+    import pickle
+
+    plan = rows.RoutePlan(torch.zeros(6, 2, dtype=torch.int32), 4, align=2)
+    xs, w, wd = torch.zeros(plan.rows, 8), [torch.zeros(4, 12, 8) for _ in range(2)], torch.zeros(4, 8, 12)
+    res = kept = plan.feed_forward(xs, *w, wd, keep=True)
+    if change == "deepcopy":
+        res = copy.deepcopy(res)
+    elif change == "pickle":
+        res = pickle.loads(pickle.dumps(res))
+    elif change == "assigned":
+        res.gate, plan.offsets = torch.ones_like(res.gate), torch.ones_like(plan.offsets)
+    rows.lib.calls.clear()
+    res.grad(xs)
+    (name, args), = rows.lib.calls
+    x, wg, wu, wdown, offsets, _, gate, up, _ = res._args
+    assert name == "spmv_feed_forward_grad"
+    assert [args[i] for i in (4, 5, 7, 8, 11, 15, 16)] == [t.data_ptr() for t in (offsets, x, wg, wu, wdown, gate, up)]
+    assert (x.data_ptr() == xs.data_ptr()) == (change in ("none", "assigned")) and args[15] != (res.gate if change == "assigned" else x).data_ptr()
+    del kept
