@@ -737,7 +737,7 @@ typedef enum { SPMV_ACT_SILU = 0, SPMV_ACT_GELU_TANH = 1, SPMV_ACT_RELU = 2 } sp
  * Sums are in 32 bits; h, gate, up and y are each rounded once to the type (h of segments of up to 16 rows on
  * average, whose weights take longer than their products, is kept with what its rounding left out).  No product of a value that no
  * row or matrix holds enters a sum: NaN and infinities of a row stay in that row.
- *   1 <= d, f <= 2^20; 1 <= experts <= 4096.
+ *   rows <= 2^31 - 4096; 1 <= d, f <= 2^20; 1 <= experts <= 4096.
  * The workspace starts at a multiple of 16 bytes and is free for other use when the call's kernels have run.
  * spmv_feed_forward_workspace gives its bytes (gradient 0: spmv_feed_forward's, else
  * spmv_feed_forward_grad's), or a negative status.

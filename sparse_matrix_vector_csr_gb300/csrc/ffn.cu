@@ -10,7 +10,8 @@ constexpr int64_t kMaxWidth = int64_t(1) << 20;
 int64_t padded(int64_t f) { return ceil_div(f, 8) * 8; }
 
 int check_sizes(int64_t rows, int64_t d, int64_t f, int dtype) {
-    if (rows < 0 || rows >= int64_t(1) << 31) return refuse("rows must lie in [0, 2^31)");
+    // (a tile's first row and the rows of its copies are 32-bit coordinates)
+    if (rows < 0 || rows > (int64_t(1) << 31) - 4096) return refuse("rows must lie in [0, 2^31 - 4096]");
     if (d < 1 || d > kMaxWidth || f < 1 || f > kMaxWidth) return refuse("d and f must lie in [1, 2^20]");
     if (!row_dtype_ok(dtype)) return refuse("dtype must be SPMV_F32, SPMV_F16 or SPMV_BF16");
     return SPMV_OK;

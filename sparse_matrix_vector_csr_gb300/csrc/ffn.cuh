@@ -212,6 +212,9 @@ bool tc_supported(const Block &b, int dtype);
 int launch_tc(int kind, const Block &b, int dtype, bool follows, cudaStream_t s);
 int launch_tc_f16(int kind, const Block &b, bool follows, cudaStream_t s);
 int launch_tc_bf16(int kind, const Block &b, bool follows, cudaStream_t s);
+// whether a wait of their kernels has run out since the last question
+cudaError_t tc_flag_f16(int *value);
+cudaError_t tc_flag_bf16(int *value);
 
 }  // namespace ffn
 }  // namespace spmv

@@ -1,14 +1,10 @@
 // What the tensor-core products share: when they can be used, the driver's description of matrices to the copy
-// engine, and the flag of waits that ran out.
+// engine, and the report of waits that ran out.
 #include "ffn_tc.cuh"
-
-#include <atomic>
 
 namespace spmv {
 namespace ffn {
 namespace {
-
-__device__ int gave_up_flag;
 
 // rows (and matrices) that start at multiples of 16 bytes
 bool describable(const Matrix &m, int64_t count) {
@@ -30,20 +26,6 @@ Encode encoder() {
         return found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(p) : nullptr;
     }();
     return fn;
-}
-
-int *failure_flag() {
-    // an address of the library's own, the same for as long as a device's context lives (looked up at each call it
-    // takes a microsecond)
-    static std::atomic<int *> known[64];
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return nullptr;
-    int *at = device < 64 ? known[device].load(std::memory_order_relaxed) : nullptr;
-    if (at) return at;
-    void *p = nullptr;
-    if (cudaGetSymbolAddress(&p, gave_up_flag) != cudaSuccess) return nullptr;
-    if (device < 64) known[device].store(static_cast<int *>(p), std::memory_order_relaxed);
-    return static_cast<int *>(p);
 }
 
 }  // namespace tc
@@ -69,10 +51,9 @@ using namespace spmv;
 
 extern "C" SPMV_API int spmv_feed_forward_status(void *stream) {
     SPMV_TRY_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
-    int *flag = ffn::tc::failure_flag(), value = 0;
-    if (!flag) return set_error(SPMV_ERR_CUDA, "the flag of the feed-forward block's waits was not found");
-    SPMV_TRY_CUDA(cudaMemcpy(&value, flag, sizeof(int), cudaMemcpyDeviceToHost));
-    if (!value) return SPMV_OK;
-    SPMV_TRY_CUDA(cudaMemset(flag, 0, sizeof(int)));
+    int first = 0, second = 0;
+    SPMV_TRY_CUDA(ffn::tc_flag_bf16(&first));
+    SPMV_TRY_CUDA(ffn::tc_flag_f16(&second));
+    if (!first && !second) return SPMV_OK;
     return set_error(SPMV_ERR_TIMEOUT, "a kernel of the feed-forward block gave up a wait: the results of the calls since the last report are invalid");
 }

@@ -43,8 +43,10 @@ struct Args {
     int which[3];      // which
     int stages;        // of the ring
     bool follows;      // launched behind a kernel of the same call that may still run
-    int *failed;
 };
+
+// a wait of one of this file's kernels ran out (each file that includes this has its own)
+static __device__ int gave_up_flag;
 
 // ----------------------------------------------------------------------------
 // barriers, copies, products
@@ -91,7 +93,7 @@ __device__ __forceinline__ bool one_lane() {
 // false after kWaitCycles, or when another warp has given up (the clock and the flag are looked at now and then only:
 // a wait's end is seen at once)
 template <bool kNap>
-static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up, int *failed) {
+static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     const long long t0 = clock64();
     for (;;) {
 #pragma unroll 1
@@ -102,19 +104,19 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
         if (*gave_up) return false;
         if (clock64() - t0 > kWaitCycles) {
             *gave_up = 1;
-            atomicExch(failed, 1);
+            atomicExch(&gave_up_flag, 1);
             return false;
         }
     }
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, int *failed) {
-    return bar_try(bar, parity) || bar_wait_slow<false>(bar, parity, gave_up, failed);
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    return bar_try(bar, parity) || bar_wait_slow<false>(bar, parity, gave_up);
 }
 // the same for a whole warp, by one of its lanes; kNap: one that does not mind to see it a little later
 template <bool kNap>
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, int *failed) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     bool ok = true;
-    if (one_lane()) ok = bar_try(bar, parity) || bar_wait_slow<kNap>(bar, parity, gave_up, failed);
+    if (one_lane()) ok = bar_try(bar, parity) || bar_wait_slow<kNap>(bar, parity, gave_up);
     return __all_sync(0xffffffffu, ok);
 }
 // one box of a tensor map to shared memory, counted on a barrier of this CTA or (kPair) of either of the pair; the
@@ -389,9 +391,11 @@ __device__ __forceinline__ void clear_rows(uint32_t a, uint32_t b, int left) {
 // ----------------------------------------------------------------------------
 // kN columns of the accumulator (kGated: half of them gate's, then as many of up); kLoaded rows of A's tile are
 // copied where segments are short (8 or 16; the accumulator's other lanes then hold sums of whatever lies behind
-// them in the ring, which nothing reads).  Products that follow on in one accumulator wait for one
-// another, about 150 cycles whatever their size (measured; 4 x 16 of k into one accumulator of 64 columns
-// 325 ns a stage, and copies of 8 KB a stage had to wait): narrow tiles take turns with four.
+// them in the ring, which nothing reads).  What a stage costs besides its products (two waits and a signal, about
+// 160 ns) is shared by several 64s of k where those are short, and tiles of 64 columns take turns with four
+// accumulators, so that a product need not wait for the one in front (100 rows, d = f = 2048, forward and back: 94.9 us;
+// with one accumulator 110.3, with one 64 of k a stage 99.7; 4 rows, d = 4096, f = 12288, forward: 65.7 us, with four
+// accumulators 67.3, with one 64 of k a stage 91.2).
 template <int kKind, int kN, int kLoaded, bool kPair>
 struct Shape {
     static constexpr bool kTwoParts = kKind == kDown && kLoaded <= kFewRows;  // of h, one behind the other in A's tile
@@ -399,11 +403,9 @@ struct Shape {
     static constexpr int kCols = kKind == kGated ? kN / 2 : kN;
     static constexpr int kMine = kKind == kWeights ? kRows : kLoaded;  // rows of D that a CTA has
     static constexpr int kTileRows = kMine * kCtas;
-    static constexpr int kAccs = kN == 256 ? 1 : 4;
+    static constexpr int kAccs = kN == 256 || kLoaded <= kFewRows ? 1 : 4;
     static constexpr int kABytes = (kTwoParts ? 2 : 1) * kMine * kRowBytes, kBBytes = kN / kCtas * kRowBytes;
-    // 64s of k of a stage: where their products are short, what a stage costs besides (two waits and a signal, about
-    // 160 ns) is shared by several
-    static constexpr int kBlocks = kKind == kWeights || kN == 256 ? 1 : kLoaded == kRows ? 2 : 4;
+    static constexpr int kBlocks = kKind == kWeights || kN == 256 ? 1 : kLoaded == kRows ? 2 : 4;  // 64s of k of a stage
     static constexpr int kBlockBytes = kABytes + kBBytes, kStageBytes = kBlocks * kBlockBytes;
     static constexpr int kSlack = kRows * kRowBytes - kABytes;  // behind the ring: what the last stage's product reads
     static constexpr int kWriterBytes = kKind == kBack ? 5 * kPatchBytes : kPatchBytes;
@@ -441,7 +443,6 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
     const int rank = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // in the pair
     const uint32_t first = blockIdx.x / S::kCtas, step = gridDim.x / S::kCtas;
     volatile int *gave_up = &gave_up_at;
-    int *failed = args.failed;
 
     if (threadIdx.x == 0) {
         gave_up_at = 0;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                 const Tile t = tiles[i];
                 const int n = blocks_of(t), once = kKind == kInput ? n / 2 : n;
                 for (int q0 = 0; q0 < n; q0 += S::kBlocks) {
-                    if (!(ok = bar_wait(empty(s), (round & 1) ^ 1, gave_up, failed))) break;
+                    if (!(ok = bar_wait(empty(s), (round & 1) ^ 1, gave_up))) break;
                     const int blocks = min(S::kBlocks, n - q0);
                     // a pair's copies are counted by its first CTA, but for a segment's last rows, by each CTA
                     const bool rest = kKind == kWeights && t.depth - static_cast<int64_t>(q0) * kDepth < kDepth;
@@ -559,13 +560,13 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                 }
             }
             // the ring is empty again (given up: at least every copy has landed)
+            long long t0 = ok ? 0 : clock64();
             for (int j = 0; j < stages; ++j) {
                 const int last = j < s ? round : round - 1;  // the round in which the stage was filled last
                 if (last < 0) continue;
-                if (ok) ok = bar_wait(empty(j), last & 1, gave_up, failed);
+                if (ok && !(ok = bar_wait(empty(j), last & 1, gave_up))) t0 = clock64();
                 const bool rest = rest_last >> j & 1;
                 if (!ok && (rest || rank == 0)) {
-                    const long long t0 = clock64();
                     while (!bar_try(rest ? rest_full(j) : full(j), (~(rest ? rest_fills : full_fills)) >> j & 1) && clock64() - t0 < kWaitCycles) {}
                 }
             }
@@ -601,16 +602,16 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                 const Tile t = tiles[i];
                 const int n = blocks_of(t), left = kKind == kWeights ? static_cast<int>(t.depth % kDepth) : 0;
                 if (n == 0) continue;
-                if (!(ok = bar_wait(acc_empty(done & 1), ((done >> 1) & 1) ^ 1, gave_up, failed))) break;
+                if (!(ok = bar_wait(acc_empty(done & 1), ((done >> 1) & 1) ^ 1, gave_up))) break;
                 for (int q = 0; q < n; q += S::kBlocks) {
                     int steps = kDepth / 16;
                     if (left && q == n - 1) {
-                        if (!(ok = bar_wait(cleared(s), cleared_parity >> s & 1, gave_up, failed))) break;
+                        if (!(ok = bar_wait(cleared(s), cleared_parity >> s & 1, gave_up))) break;
                         if (kPair) asm volatile("fence.acq_rel.cluster;" ::: "memory");
                         cleared_parity ^= 1u << s;
                         steps = (left + 15) / 16;
                     } else {
-                        if (!(ok = bar_wait(full(s), full_parity >> s & 1, gave_up, failed))) break;
+                        if (!(ok = bar_wait(full(s), full_parity >> s & 1, gave_up))) break;
                         full_parity ^= 1u << s;
                     }
                     products(q, n, steps);
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                 continue;
             }
             s = (s + blocks_of(t) - 1) % stages;
-            if (!warp_wait<false>(rest_full(s), parity >> s & 1, gave_up, failed)) break;
+            if (!warp_wait<false>(rest_full(s), parity >> s & 1, gave_up)) break;
             parity ^= 1u << s;
             clear_rows<kN / S::kCtas>(ring_a + s * S::kABytes, ring_b + s * S::kBBytes, left);
             if (lane == 0) {
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
             if constexpr (kKind == kBack)
                 if (rows > 0 && half * 32 < width) ask(half * 32);
             if (!zero) {
-                if (!warp_wait<true>(acc_full(which), (done >> 1) & 1, gave_up, failed)) break;
+                if (!warp_wait<true>(acc_full(which), (done >> 1) & 1, gave_up)) break;
                 fence_after();
                 ++done;
             }
@@ -810,7 +811,14 @@ using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void
                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 Encode encoder();  // nullptr where the driver has none
-int *failure_flag();
+
+// reads and clears the flag
+inline cudaError_t take_flag(int *value) {
+    cudaError_t e = cudaMemcpyFromSymbol(value, gave_up_flag, sizeof(int));
+    const int none = 0;
+    if (e == cudaSuccess && *value) e = cudaMemcpyToSymbol(gave_up_flag, &none, sizeof(int));
+    return e;
+}
 
 // `count` matrices (0: one, as a map of two dimensions) of `rows` rows of `n` values; boxes of 64 values x box_rows (of
 // box_count matrices)
@@ -831,7 +839,6 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
     using S = Shape<kKind, kN, kLoaded, kPair>;
     Args args;
     args.block = b;
-    args.failed = failure_flag();
     args.products = 0;
     args.follows = follows;
     const int64_t rows = b.seg.rows, d = b.d, f = b.f, count = b.seg.count;
@@ -840,7 +847,7 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
         return make_map<T>(map, m, n, rows, 0, kKind == kWeights ? kDepth : S::kMine);
     };
     const auto weight = [&](CUtensorMap *map, const Matrix &m, int64_t n, int64_t m_rows, int box) { return make_map<T>(map, m, n, m_rows, count, box); };
-    bool ok = args.failed != nullptr;
+    bool ok = true;
     int64_t tiles = 0;
     if (kKind == kWeights) {
         const Matrix *out[3] = {&b.dwg, &b.dwu, &b.dwd}, *in[3] = {&b.dgate, &b.dup, &b.dy};

@@ -4,5 +4,6 @@
 namespace spmv {
 namespace ffn {
 int launch_tc_bf16(int kind, const Block &b, bool follows, cudaStream_t s) { return tc::launch_kind<__nv_bfloat16>(kind, b, follows, s); }
+cudaError_t tc_flag_bf16(int *value) { return tc::take_flag(value); }
 }  // namespace ffn
 }  // namespace spmv
