@@ -166,8 +166,10 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
         int32_t *key_out = a.key[(a.passes - 1 - p) & 1], *src_out = a.src[(a.passes - 1 - p) & 1];
         const int shift = p * a.bits;
         const int64_t share = (n + ctas - 1) / ctas, begin = min(n, rank * share), end = min(n, begin + share);
-        const int64_t run = (end - begin + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32;
-        const int64_t r0 = begin + warp * run, r1 = min(end, r0 + run);
+        // as few warps as hold their tokens in registers: their counts have to be cleared and added up
+        const int n_warps = static_cast<int>(min((share + 32 * kHeld - 1) / (32 * kHeld), int64_t(kSortWarps)));
+        const int64_t run = (end - begin + 32 * n_warps - 1) / (32 * n_warps) * 32;
+        const int64_t r0 = begin + warp * run, r1 = warp < n_warps ? min(end, r0 + run) : r0;
         int32_t *mine = wcount + warp * bins;
         // kHeld times 32 keys of the warp's run and where their tokens are, all loads at once (from L2: other SMs of
         // the cluster wrote them in the pass before)
@@ -180,19 +182,26 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
                 src[i] = src_in && at < r1 ? __ldcg(src_in + at) : static_cast<int32_t>(at);
             }
         };
-        // a key's digit, the entries of the same digit in lower lanes and how many have it; -1: no entry
+        // a key's digit, the entries of the same digit in lower lanes and how many have it; -1: no entry.  (By a vote a bit:
+        // 65536 tokens of 300 rows 22.7 us; by __match_any_sync 23.8.)
         const auto match = [&](int32_t k) {
-            const int dig = is_entry(k, a.vocab) ? (k >> shift) & (bins - 1) : -1;
-            const uint32_t same = __match_any_sync(0xffffffffu, dig);
-            return dig < 0 ? -1 : dig | __popc(same & ((1u << lane) - 1)) << 10 | __popc(same) << 16;
+            const bool entry = is_entry(k, a.vocab);
+            const int dig = (k >> shift) & (bins - 1);
+            uint32_t same = __ballot_sync(0xffffffffu, entry);
+#pragma unroll
+            for (int b = 0; b < kDigitBits; ++b) {
+                const uint32_t ones = __ballot_sync(0xffffffffu, dig >> b & 1);
+                same &= dig >> b & 1 ? ones : ~ones;
+            }
+            return entry ? dig | __popc(same & ((1u << lane) - 1)) << 10 | __popc(same) << 16 : -1;
         };
         load(r0);
-        for (int i = tid; i < kSortWarps * bins; i += kSortThreads) wcount[i] = 0;
+        for (int i = tid; i < n_warps * bins; i += kSortThreads) wcount[i] = 0;
         __syncthreads();
         for (int64_t i0 = r0; i0 < r1; i0 += 32 * kHeld) {
             if (i0 != r0) load(i0);
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) found[i] = match(key[i]);
+            for (int i = 0; i < kHeld; ++i) found[i] = i0 + i * 32 < r1 ? match(key[i]) : -1;
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
                 if (found[i] >= 0 && (found[i] >> 10 & 63) == 0) mine[found[i] & 1023] += found[i] >> 16;
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
         for (int b = tid; b < bins; b += kSortThreads) {  // (at most one a thread)
             int32_t at = 0;
 #pragma unroll 8
-            for (int w = 0; w < kSortWarps; ++w) {
+            for (int w = 0; w < n_warps; ++w) {
                 const int32_t c = wcount[w * bins + b];
                 wcount[w * bins + b] = at;
                 at += c;
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
             if (run > 32 * kHeld) {
                 load(i0);
 #pragma unroll
-                for (int i = 0; i < kHeld; ++i) found[i] = match(key[i]);
+                for (int i = 0; i < kHeld; ++i) found[i] = i0 + i * 32 < r1 ? match(key[i]) : -1;
             }
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
@@ -315,7 +324,7 @@ __device__ __forceinline__ void store_values(O *p, const float *f) {
 // A warp sums kU x 32 units of kN values of the rows of one chunk of sorted entries, kR rows' loads in
 // flight (and, where they are added to, the gradient's), in 32 bits, in the tokens' order.
 template <typename T, typename O, int kN, int kU, int kR, bool kAdd>
-__global__ void __launch_bounds__(kThreads, 4) k_embed_sum(SumArgs a, const T *__restrict__ dx, int64_t lddx, O *out, int64_t ldo) {
+__global__ void __launch_bounds__(kThreads, kAdd ? 2 : 4) k_embed_sum(SumArgs a, const T *__restrict__ dx, int64_t lddx, O *out, int64_t ldo) {
     using U = typename Unit<kN * static_cast<int>(sizeof(T))>::type;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     dev::grid_wait();
