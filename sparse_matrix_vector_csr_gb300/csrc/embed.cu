@@ -89,7 +89,7 @@ void launch_embed(int unit, int64_t tokens, int64_t vocab, int64_t d, float scal
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;
-constexpr int64_t kSortShare = 4096;  // tokens a CTA sorts, at least
+constexpr int64_t kSortShare = 1024;  // tokens a CTA sorts, at least, while the cluster has room
 constexpr int kHeld = 8;              // times 32: of a warp's tokens in registers
 
 struct SortShape {
@@ -114,7 +114,7 @@ struct SortArgs {
     int64_t tokens, vocab;
     int passes, bits;
     const int32_t *ids;
-    int32_t *key[2], *src[2];  // the last pass writes the first of each
+    int2 *sorted[2];           // row and token; the last pass writes the first
     int32_t *count;            // tokens that are entries; chunks in whose end a row stays open (0, for k_embed_sum)
 };
 struct ZeroArgs {  // rows x row_bytes at a distance of ld bytes
@@ -161,9 +161,8 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
     int64_t n = a.tokens;
     if (ctas > 1) cluster_sync(ctas);  // every CTA is there before its shared memory is written
     for (int p = 0; p < a.passes; ++p) {
-        const int32_t *key_in = p == 0 ? a.ids : a.key[(a.passes - p) & 1];
-        const int32_t *src_in = p == 0 ? nullptr : a.src[(a.passes - p) & 1];
-        int32_t *key_out = a.key[(a.passes - 1 - p) & 1], *src_out = a.src[(a.passes - 1 - p) & 1];
+        const int2 *in = p == 0 ? nullptr : a.sorted[(a.passes - p) & 1];
+        int2 *out = a.sorted[(a.passes - 1 - p) & 1];
         const int shift = p * a.bits;
         const int64_t share = (n + ctas - 1) / ctas, begin = min(n, rank * share), end = min(n, begin + share);
         // as few warps as hold their tokens in registers: their counts have to be cleared and added up
@@ -178,8 +177,15 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
                 const int64_t at = i0 + i * 32 + lane;
-                key[i] = at < r1 ? __ldcg(key_in + at) : -1;
-                src[i] = src_in && at < r1 ? __ldcg(src_in + at) : static_cast<int32_t>(at);
+                key[i] = -1;
+                src[i] = static_cast<int32_t>(at);
+                if (at < r1 && in) {
+                    const int2 v = __ldcg(in + at);
+                    key[i] = v.x;
+                    src[i] = v.y;
+                } else if (at < r1) {
+                    key[i] = a.ids[at];
+                }
             }
         };
         // a key's digit, the entries of the same digit in lower lanes and how many have it; -1: no entry.  (By a vote a bit:
@@ -241,12 +247,9 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
         }
         if (lane == 31) warp_part[warp] = incl;
         __syncthreads();
-        int32_t at = incl - total, all = 0;
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) {
-            at += w < warp ? warp_part[w] : 0;
-            all += warp_part[w];
-        }
+        const int32_t of_warp = warp_part[lane];
+        const int32_t at = incl - total + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0);
+        const int32_t all = __reduce_add_sync(0xffffffffu, of_warp);
         if (tid < bins) place0[tid] = at + before;
         __syncthreads();
         for (int64_t i0 = r0; i0 < r1; i0 += 32 * kHeld) {
@@ -262,10 +265,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
                 __syncwarp();
                 if (found[i] >= 0 && earlier == 0) mine[dig] += found[i] >> 16;
                 __syncwarp();
-                if (to >= 0) {
-                    key_out[to] = key[i];
-                    src_out[to] = src[i];
-                }
+                if (to >= 0) out[to] = make_int2(key[i], src[i]);  // (stores to places of their own: one of 8 bytes, not two)
             }
         }
         n = all;
@@ -297,7 +297,7 @@ struct SumArgs {
     int64_t d, chunk, parts;
     float scale;
     int accumulate;
-    const int32_t *key, *src;
+    const int2 *sorted;
     int32_t *count, *open;  // open: the chunks in whose end a row begun in them stays open
     uint8_t *through;       // [chunks]: a row comes from the chunk in front and goes on behind
     float *carry;  // [chunks][2][ldc]: sum up to the end of a row begun in front of the chunk; from the start of a row open at its end
@@ -353,11 +353,11 @@ __global__ void __launch_bounds__(kThreads, kAdd ? 2 : 4) k_embed_sum(SumArgs a,
         }
     };
     float *carry = a.carry + 2 * c * a.ldc;
-    bool carried = lo > 0 && a.key[lo - 1] == a.key[lo];
+    bool carried = lo > 0 && a.sorted[lo - 1].x == a.sorted[lo].x;
     for (int64_t g = lo; g < hi; g += 32) {
         const int n = static_cast<int>(min(hi - g, int64_t(32)));
-        const int32_t key = lane < n ? a.key[g + lane] : -1, src = lane < n ? a.src[g + lane] : 0;
-        const int32_t behind = g + n < total ? a.key[g + n] : -1;
+        const int2 mine = lane < n ? a.sorted[g + lane] : make_int2(-1, 0);
+        const int32_t key = mine.x, src = mine.y, behind = g + n < total ? a.sorted[g + n].x : -1;
         for (int q0 = 0; q0 < n; q0 += kR) {
             U v[kR][kU];
             float old[kAdd ? kR : 1][kU][kN];
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(SumArgs a, O *out, int6
         const int64_t piece = item / opened;  // (a long row's pieces go to CTAs far from one another)
         r.c = a.open[item - piece * opened];
         r.col = piece * kJoinCols + lane * 4;
-        r.row = a.key[(r.c + 1) * a.chunk - 1];
+        r.row = a.sorted[(r.c + 1) * a.chunk - 1].x;
         int64_t end = r.c + 1;  // the row's last chunk: the first behind r.c through which it does not go
         for (;;) {
             const bool through = (end + lane + 1) * a.chunk < total && a.through[end + lane];
@@ -558,7 +558,7 @@ int check_embed(int64_t tokens, int64_t vocab, int64_t d) {
 
 // The parts of the gradient's workspace, each at a multiple of 16 bytes.
 struct EmbedSpace {
-    int64_t key[2], src[2], count, open, through, carry, bytes;
+    int64_t sorted[2], count, open, through, carry, bytes;
     int64_t chunks, ldc;
 };
 EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t d) {
@@ -570,10 +570,8 @@ EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t d) {
         return here;
     };
     const bool one = sort_shape(tokens, vocab).passes == 1;
-    w.key[0] = take(tokens * 4);
-    w.src[0] = take(tokens * 4);
-    w.key[1] = one ? 0 : take(tokens * 4);
-    w.src[1] = one ? 0 : take(tokens * 4);
+    w.sorted[0] = take(tokens * 8);
+    w.sorted[1] = one ? 0 : take(tokens * 8);
     w.count = take(8);
     w.chunks = ceil_div(tokens, chunk_entries(tokens, d));
     w.open = take(w.chunks * 4);
@@ -640,10 +638,9 @@ extern "C" SPMV_API int spmv_embed_rows_grad(int64_t tokens, int64_t vocab, int6
 
     char *base = static_cast<char *>(workspace);
     const SortShape shape = sort_shape(tokens, vocab);
-    SortArgs sort{tokens, vocab, shape.passes, shape.bits, ids, {}, {}, reinterpret_cast<int32_t *>(base + w.count)};
+    SortArgs sort{tokens, vocab, shape.passes, shape.bits, ids, {}, reinterpret_cast<int32_t *>(base + w.count)};
     for (int i = 0; i < 2; ++i) {
-        sort.key[i] = reinterpret_cast<int32_t *>(base + w.key[i]);
-        sort.src[i] = reinterpret_cast<int32_t *>(base + w.src[i]);
+        sort.sorted[i] = reinterpret_cast<int2 *>(base + w.sorted[i]);
     }
     ZeroArgs zero{static_cast<char *>(dtable), accumulate ? 0 : vocab, d * vo, lddtable * vo, static_cast<const char *>(dx), 0};
     // The sort alone takes about 15 us, in which 96 MB can be written and read: as much of dx as that leaves room for
@@ -666,7 +663,7 @@ extern "C" SPMV_API int spmv_embed_rows_grad(int64_t tokens, int64_t vocab, int6
     // values of a lane's unit: what the alignment of both matrices' rows allows
     const int in = unit_bytes(vb, d, {{dx, lddx}}) / vb, to = unit_bytes(vo, d, {{dtable, lddtable}});
     const int values = to == 16 ? in : (in < to / vo ? in : to / vo);
-    const SumArgs sum{d, chunk_entries(tokens, d), 1, static_cast<float>(scale), accumulate, sort.key[0], sort.src[0], sort.count,
+    const SumArgs sum{d, chunk_entries(tokens, d), 1, static_cast<float>(scale), accumulate, sort.sorted[0], sort.count,
                       reinterpret_cast<int32_t *>(base + w.open), reinterpret_cast<uint8_t *>(base + w.through), reinterpret_cast<float *>(base + w.carry), w.ldc};
     cudaError_t e;
     if (dtype == SPMV_F32) e = launch_sums<float, float>(values, sum, w.chunks, dx, lddx, dtable, lddtable, s);
