@@ -164,7 +164,7 @@ class RoutePlan:
     Every call takes the tensors that these attributes have by then."""
 
     __slots__ = ("tokens", "k", "experts", "align", "rows", "offsets", "slots", "sources", "_known_slots",
-                 "_known_sources")
+                 "_known_sources", "_known_offsets")
 
     def __init__(self, ids, experts, align=1, stream=None):
         if stream is not None:
@@ -177,7 +177,7 @@ class RoutePlan:
         self.experts, self.align = experts, align = int(experts), int(align)
         self.rows, work = _plan_sizes(tokens, k, experts, align)
         device = ids.device
-        self.offsets = _empty((experts + 1,), dtype=_I32, device=device)
+        self.offsets = self._known_offsets = _empty((experts + 1,), dtype=_I32, device=device)
         self.slots = self._known_slots = slots = _empty((tokens, k), dtype=_I32, device=device)
         self.sources = self._known_sources = sources = _empty((self.rows,), dtype=_I32, device=device)
         space = _empty((work,), dtype=torch.uint8, device=device) if work else None
@@ -248,7 +248,10 @@ class RoutePlan:
         """Each expert's gated feed-forward block over its segment of xs (rows x d): see
         :func:`feed_forward`, with weights of one more leading dimension (experts).  Rows behind the
         last segment become 0."""
-        offsets = _plain(self.offsets, "offsets", (self.experts + 1,), _I32) and self.offsets
+        offsets = self.offsets
+        if offsets is not self._known_offsets:
+            _plain(offsets, "offsets", (self.experts + 1,), _I32)
+            self._known_offsets = offsets
         return _feed_forward(xs, w_gate, w_up, w_down, activation, keep, out, stream, offsets, self.experts, self.rows)
 
 
@@ -337,16 +340,22 @@ def _weights(t, name, experts, rows, cols, dtype):
     shape = (rows, cols) if experts is None else (experts, rows, cols)
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
-    if cols > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have unit column stride")
-    ld = t.stride(-2) if rows > 1 else cols
+    ld = strides[-2] if rows > 1 else cols
     if ld < cols:
         raise ValueError(f"{name} has overlapping rows")
     one = (rows - 1) * ld + cols
-    apart = t.stride(0) if experts is not None and experts > 1 else one
+    apart = strides[0] if experts is not None and experts > 1 else one
     if apart < one:
         raise ValueError(f"{name} has overlapping or interleaved experts")
     return ld, apart
+
+
+@functools.lru_cache(maxsize=4096)
+def _block_workspace(rows, d, f, experts, code, gradient):
+    return _check(lib.spmv_feed_forward_workspace(rows, d, f, experts, code, gradient))
 
 
 def _block(x, w_gate, w_up, w_down, offsets, experts, gate, up, act):
@@ -355,8 +364,9 @@ def _block(x, w_gate, w_up, w_down, offsets, experts, gate, up, act):
     rows, d = x.shape
     f, dtype = w_gate.shape[-2], x.dtype
     ldw, apart = _weights(w_gate, "w_gate", experts, f, d, dtype)
-    if _weights(w_up, "w_up", experts, f, d, dtype) != (ldw, apart):
-        raise ValueError("w_up must have the strides of w_gate")
+    if w_up.stride() != w_gate.stride() or w_up.shape != w_gate.shape or w_up.dtype != dtype:
+        if _weights(w_up, "w_up", experts, f, d, dtype) != (ldw, apart):
+            raise ValueError("w_up must have the strides of w_gate")
     ldd, apart_d = _weights(w_down, "w_down", experts, d, f, dtype)
     if gate is None:
         kept = (None, None, f)
@@ -386,7 +396,7 @@ def _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, stream, offset
     code, call = _block(x, w_gate, w_up, w_down, offsets, experts, res.gate, res.up, act)
     rows, d = x.shape
     res.y, ldy = _out(out, "out", x, rows, d)
-    work = _check(lib.spmv_feed_forward_workspace(rows, d, f, call[3], code, 0))
+    work = _block_workspace(rows, d, f, call[3], code, 0)
     space = _empty((work,), dtype=torch.uint8, device=device)
     _check(lib.spmv_feed_forward(*call, res.y.data_ptr() or None, ldy, code, space.data_ptr() or None, work, _current(x)))
     res._args = (x, w_gate, w_up, w_down, offsets, experts, res.gate, res.up, act) if keep else None
@@ -413,7 +423,7 @@ class FeedForward:
         lddy = _matrix(dy, "dy", rows, d, x.dtype)[1]
         dx, lddx = _out(out, "out", x, rows, d)
         dws = [_empty(w.shape, dtype=x.dtype, device=x.device) if weights else None for w in self._args[1:4]]
-        work = _check(lib.spmv_feed_forward_workspace(rows, d, f, experts, code, 1))
+        work = _block_workspace(rows, d, f, experts, code, 1)
         space = _empty((work,), dtype=torch.uint8, device=x.device)
         _check(lib.spmv_feed_forward_grad(*call, dy.data_ptr() or None, lddy, dx.data_ptr() or None, lddx,
                                           *[None if w is None else w.data_ptr() for w in dws], code,
