@@ -734,8 +734,9 @@ typedef enum { SPMV_ACT_SILU = 0, SPMV_ACT_GELU_TANH = 1, SPMV_ACT_RELU = 2 } sp
  *            e * wd_expert + i * ldwd, in values (16-byte aligned rows run fastest).
  *   gate, up rows x f (leading dimension ldg), what spmv_feed_forward_grad needs of the forward call, or both
  *            NULL.
- * Sums are in 32 bits; h, gate, up and y are each rounded once to the type (h of segments of up to 16 rows on
- * average, whose weights take longer than their products, is kept with what its rounding left out).  No product of a value that no
+ * Sums are in 32 bits; h, gate, up and y are each rounded once to the type (h of up to 16
+ * rows, or of segments of up to 8 on average, whose weights take longer than their products, is kept
+ * with what its rounding left out).  No product of a value that no
  * row or matrix holds enters a sum: NaN and infinities of a row stay in that row.
  *   rows <= 2^31 - 4096; 1 <= d, f <= 2^20; 1 <= experts <= 4096.
  * The workspace starts at a multiple of 16 bytes and is free for other use when the call's kernels have run.

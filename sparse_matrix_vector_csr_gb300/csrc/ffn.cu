@@ -43,7 +43,7 @@ int check_experts(int32_t experts) {
     return experts < 1 || experts > kMaxSegments ? refuse("experts must lie in [1, " + std::to_string(kMaxSegments) + "]") : SPMV_OK;
 }
 // h is held in two parts
-bool two_parts(int64_t rows, int32_t experts, int dtype) { return dtype != SPMV_F32 && rows <= int64_t(kShortRows) * experts; }
+bool two_parts(int64_t rows, int32_t experts, int dtype) { return dtype != SPMV_F32 && short_rows(rows, experts) != 0; }
 int check_segments(int32_t experts, const int32_t *offsets) {
     SPMV_TRY(check_experts(experts));
     if (!offsets) return experts == 1 ? SPMV_OK : refuse("offsets is NULL, which means one segment of all rows, with experts not 1");

@@ -1,7 +1,10 @@
 // The products of the feed-forward block by the ordinary units: float, and 16-bit values at any address.
 // A CTA of 256 threads has 128 x 128 values of D, 8 x 8 a thread, in 32 bits; pieces of A and B of 16
 // along k go through shared memory, k first, two of each so that one is filled while the other is
-// multiplied.  Bound by the arithmetic of the ordinary units (two multiply-adds an instruction).
+// multiplied.  Bound by the ordinary units' arithmetic (two multiply-adds an instruction) and the reads of shared memory that
+// feed it, an equal share of cycles: 4096 rows, d = 2048, f = 4096, float: 43.6 TFLOP/s forward, 44.5 back.  Pieces of 8 along k:
+// 34.9; A's values twice in shared memory, to be a pair's operand as they are: 34.4; 128 x 256 values, 8 x 16 a thread, one
+// CTA an SM: 41.3.
 #include "ffn.cuh"
 
 namespace spmv {

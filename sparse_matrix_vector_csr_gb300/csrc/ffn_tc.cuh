@@ -897,27 +897,35 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
     return SPMV_OK;
 }
 
+// Which tiles (d = f = 2048 unless said; us, forward and then back without weights, of all the call's products):
+//   short segments    8 or 16 rows x 64 columns (16 dense rows 17.7 22.1; tiles of 128 x 64 24.9 34.5, of 128 x 256 28.2 43.9)
+//   pairs of CTAs     segments of 112 rows on average, enough tiles for 48 pairs (16 experts of 64 rows 84.0 93.3, of 128 87.6 98.7;
+//                     2048 dense rows 40.6 50.0)
+//   128 x 256         enough tiles for 96 SMs (the same three: 74.3 78.7; 93.3 115.6; 43.0 53.5)
+//   128 x 64          the rest (512 dense rows 25.6 27.6; 128 x 256 30.0 49.1, pairs 27.8 43.6)
 template <typename T, int kKind>
 int launch_shape(const Block &b, bool follows, cudaStream_t s) {
-    const int64_t rows = b.seg.rows, mean = ceil_div(rows, b.seg.count);  // rows of a segment, taking them as equally long
+    const int64_t rows = b.seg.rows, count = b.seg.count, used = count < rows ? count : rows;
+    const auto row_tiles = [&](int64_t n) { return ceil_div(rows, n) > used ? ceil_div(rows, n) : used; };
     const int64_t columns = product_columns<kKind>(b, 0);
     if constexpr (kKind == kWeights) {
-        const int64_t tiles = (2 * ceil_div(b.f, 256) * ceil_div(b.d, 256) + ceil_div(b.d, 256) * ceil_div(b.f, 256)) * b.seg.count * b.splits;
-        if (tiles >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, follows, s);
+        const int64_t tiles = (2 * ceil_div(b.f, 256) * ceil_div(b.d, 256) + ceil_div(b.d, 256) * ceil_div(b.f, 256)) * count * b.splits;
+        if (tiles >= 48) return launch<T, kKind, 256, 128, true>(b, follows, s);
         return launch<T, kKind, 64, 128, false>(b, follows, s);
     } else {
+        const int few = short_rows(rows, count);
         if constexpr (kKind == kDown) {
             // tiles of 32 columns where those of 64 would leave SMs without one
-            const bool narrow = ceil_div(rows, mean) * ceil_div(columns, 64) < kSms;
-            if (mean <= 8) return narrow ? launch<T, kKind, 32, 8, false>(b, follows, s) : launch<T, kKind, 64, 8, false>(b, follows, s);
-            if (mean <= kFewRows) return narrow ? launch<T, kKind, 32, kFewRows, false>(b, follows, s) : launch<T, kKind, 64, kFewRows, false>(b, follows, s);
+            const bool narrow = used * ceil_div(columns, 64) < kSms;
+            if (few == 8) return narrow ? launch<T, kKind, 32, 8, false>(b, follows, s) : launch<T, kKind, 64, 8, false>(b, follows, s);
+            if (few) return narrow ? launch<T, kKind, 32, kFewRows, false>(b, follows, s) : launch<T, kKind, 64, kFewRows, false>(b, follows, s);
         } else {
-            if (kKind == kGated && mean <= 8) return launch<T, kKind, 64, 8, false>(b, follows, s);
-            if (mean <= kFewRows) return launch<T, kKind, 64, kFewRows, false>(b, follows, s);
+            if (kKind == kGated && few == 8) return launch<T, kKind, 64, 8, false>(b, follows, s);
+            if (few) return launch<T, kKind, 64, kFewRows, false>(b, follows, s);
         }
         const int64_t wide = ceil_div(columns, kKind == kGated ? 128 : 256);
-        if (mean >= 192 && ceil_div(rows, 256) * wide >= kSms / 2) return launch<T, kKind, 256, 128, true>(b, follows, s);
-        if (ceil_div(rows, 128) * wide >= kSms) return launch<T, kKind, 256, 128, false>(b, follows, s);
+        if (rows >= 112 * count && row_tiles(256) * wide >= 48) return launch<T, kKind, 256, 128, true>(b, follows, s);
+        if (row_tiles(128) * wide >= 96) return launch<T, kKind, 256, 128, false>(b, follows, s);
         return launch<T, kKind, 64, 128, false>(b, follows, s);
     }
 }
