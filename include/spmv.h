@@ -729,7 +729,9 @@ typedef enum { SPMV_ACT_SILU = 0, SPMV_ACT_GELU_TANH = 1, SPMV_ACT_RELU = 2 } sp
  * of f.
  *   offsets  int32[experts + 1] as spmv_route_plan gives them: expert e has the rows [offsets[e],
  *            offsets[e + 1]).  Rows from offsets[experts] on have no expert: their x is not looked at
- *            and their y, gate and up become 0.  NULL with experts 1: one block for all rows.
+ *            and their y, gate and up become 0.  NULL with experts 1: one block for all rows.  Offsets that no
+ *            plan gives are cut to [0, rows]: rows in front of offsets[0] are left as they are, and rows of two
+ *            segments have no one result.
  *   w_gate, w_up   row i of expert e's matrix starts at e * w_expert + i * ldw (the same for both), w_down's at
  *            e * wd_expert + i * ldwd, in values (16-byte aligned rows run fastest).
  *   gate, up rows x f (leading dimension ldg), what spmv_feed_forward_grad needs of the forward call, or both

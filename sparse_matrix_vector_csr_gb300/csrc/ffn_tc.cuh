@@ -261,7 +261,7 @@ struct Tiles {
             r.first = s.begin;
             r.depth = s.end - s.begin;
         } else {
-            while (static_cast<uint32_t>(prefix[e + 1]) * columns <= t) ++e;
+            while (e < b.seg.count && static_cast<uint32_t>(prefix[e + 1]) * columns <= t) ++e;
             r.e = e;
             constexpr uint32_t kGroup = kGroupRows / kTileRows;
             const uint32_t i = t - static_cast<uint32_t>(prefix[e]) * columns, m = static_cast<uint32_t>(prefix[e + 1] - prefix[e]);

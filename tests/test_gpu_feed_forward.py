@@ -211,6 +211,26 @@ def test_wide_tiles(spmv, dtype):
             assert float((p.double() - q).abs().max()) <= H[dtype] * 8 * float(q.abs().max()), i
 
 
+@pytest.mark.parametrize("dtype,d,f", [(torch.bfloat16, 64, 72), (torch.float32, 30, 21)])
+def test_offsets_of_no_plan(spmv, dtype, d, f):
+    """offsets that no plan gives (out of range, falling): spans are cut to the rows, nothing beside the rows is
+    written.  (Rows in two spans have no one result.)"""
+    g = gen(12)
+    rows, experts = 150, 4
+    xs, dys = (torch.randn(rows, d, generator=g).to(dtype).cuda() for _ in range(2))
+    ws = weights(experts, d, f, dtype, g)
+    plan = spmv.RoutePlan(torch.zeros(rows, 1, dtype=torch.int32, device="cuda"), experts)
+    for values in ([0, 40, 30, 2 ** 31 - 1, -5], [-3, -2, -1, 0, 10 ** 9], [149, 149, 149, 149, 149], [2 ** 31 - 1] * 5):
+        plan.offsets = torch.tensor(values, dtype=torch.int32).cuda()
+        around = [torch.full((rows + 20, d), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+        res = plan.feed_forward(xs, *ws, keep=True, out=around[0][10:-10])
+        res.grad(dys, out=around[1][10:-10])
+        for t in around:
+            assert t[:10].eq(7).all() and t[-10:].eq(7).all() and torch.isfinite(t).all()
+    assert res.y.eq(7).all()  # (the last: every row lies in front of the first segment, and is left as it was)
+    spmv.spmv_feed_forward_status()
+
+
 def test_status(spmv):
     """no wait of any call before has run out"""
     spmv.spmv_feed_forward_status()
