@@ -408,7 +408,9 @@ struct Shape {
     static constexpr int kBlocks = kKind == kWeights || kN == 256 ? 1 : kLoaded == kRows ? 2 : 4;  // 64s of k of a stage
     static constexpr int kBlockBytes = kABytes + kBBytes, kStageBytes = kBlocks * kBlockBytes;
     static constexpr int kSlack = kRows * kRowBytes - kABytes;  // behind the ring: what the last stage's product reads
-    static constexpr int kWriterBytes = kKind == kBack ? 5 * kPatchBytes : kPatchBytes;
+    // (kBack: gate and up, in whose place their gradients and then h go out; a second pair to ask for the next columns earlier
+    // costs two of the ring's six stages: 8192 rows, d = f = 4096: 206 us, so 180)
+    static constexpr int kWriterBytes = (kKind == kBack ? 2 : 1) * kPatchBytes;
     static constexpr int kFixed = 1024 + kSlack + kWriters * kWriterBytes + (4 * kMaxStages + 5) * 8;
     static constexpr int kColumns = 2 * kN * kAccs;  // of tensor memory: two buffers
     static int stages(int segments) {
@@ -666,14 +668,13 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                                  : static_cast<int>(max(min(t.end - row, static_cast<int64_t>(min(32, S::kMine))), int64_t(0)));
             const int width = static_cast<int>(min(columns, static_cast<int64_t>(S::kCols)));
             const auto at = [&](const Matrix &m, int c) { return static_cast<T *>(m.p) + row * m.ld + t.col + c; };
-            const auto ask = [&](int c) {  // kBack: gate and up of 32 columns, into one of two places
-                const uint32_t to = mine + kPatchBytes * (1 + (c / (32 * kHalves) & 1) * 2);
-                patch_in<T>(to, at(b.gate, c), b.gate.ld, rows, columns - c);
-                patch_in<T>(to + kPatchBytes, at(b.up, c), b.up.ld, rows, columns - c);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            };
+            const auto ask_gate = [&](int c) { patch_in<T>(mine, at(b.gate, c), b.gate.ld, rows, columns - c); };  // kBack
+            const auto ask_up = [&](int c) { patch_in<T>(mine + kPatchBytes, at(b.up, c), b.up.ld, rows, columns - c); };
             if constexpr (kKind == kBack)
-                if (rows > 0 && half * 32 < width) ask(half * 32);
+                if (rows > 0 && half * 32 < width) {
+                    ask_gate(half * 32);
+                    ask_up(half * 32);
+                }
             if (!zero) {
                 if (!warp_wait<true>(acc_full(which), (done >> 1) & 1, gave_up)) break;
                 fence_after();
@@ -743,13 +744,9 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                         }
                     }
                 } else if constexpr (kKind == kBack) {
-                    const uint32_t gate = mine + kPatchBytes * (1 + (c / (32 * kHalves) & 1) * 2), up = gate + kPatchBytes;
-                    if (c + 32 * kHalves < width) {
-                        ask(c + 32 * kHalves);
-                        asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    } else {
-                        asm volatile("cp.async.wait_group 0;" ::: "memory");
-                    }
+                    const uint32_t gate = mine, up = mine + kPatchBytes;
+                    uint4 h_row[4];
+                    asm volatile("cp.async.wait_all;" ::: "memory");
                     __syncwarp();
                     // each result rounded once, to the type that the next products take
 #pragma unroll
@@ -766,11 +763,16 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                         }
                         patch_store(patch_piece(gate, lane, p), pack<T>(g));
                         patch_store(patch_piece(up, lane, p), pack<T>(u));
-                        patch_store(patch_piece(mine, lane, p), pack<T>(h));
+                        h_row[p] = pack<T>(h);
                     }
-                    patch_out<T>(gate, at(b.dgate, c), b.dgate.ld, rows, left);
+                    const bool more = c + 32 * kHalves < width;
                     patch_out<T>(up, at(b.dup, c), b.dup.ld, rows, left);
-                    patch_out<T>(mine, at(b.h, c), b.h.ld, rows, left);
+                    if (more) ask_up(c + 32 * kHalves);
+                    patch_out<T>(gate, at(b.dgate, c), b.dgate.ld, rows, left);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) patch_store(patch_piece(gate, lane, p), h_row[p]);
+                    patch_out<T>(gate, at(b.h, c), b.h.ld, rows, left);
+                    if (more) ask_gate(c + 32 * kHalves);
                 } else {
                     const Matrix &m = kKind == kDown ? b.y : kKind == kInput ? b.dx : t.which == 0 ? b.dwg : t.which == 1 ? b.dwu : b.dwd;
                     if constexpr (kKind == kWeights) {
