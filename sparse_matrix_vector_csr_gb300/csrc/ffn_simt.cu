@@ -1,10 +1,12 @@
 // The products of the feed-forward block by the ordinary units: float, and 16-bit values at any address.
-// A CTA of 256 threads has 128 x 128 values of D, 8 x 8 a thread, in 32 bits; pieces of A and B of 16
-// along k go through shared memory, k first, two of each so that one is filled while the other is
-// multiplied.  Bound by the ordinary units' arithmetic (two multiply-adds an instruction) and the reads of shared memory that
-// feed it, an equal share of cycles: 4096 rows, d = 2048, f = 4096, float: 43.6 TFLOP/s forward, 44.5 back.  Pieces of 8 along k:
-// 34.9; A's values twice in shared memory, to be a pair's operand as they are: 34.4; 128 x 256 values, 8 x 16 a thread, one
-// CTA an SM: 41.3.
+// A CTA of 256 threads has 128 x 128 values of D, 8 x 8 a thread (32 x 128 where segments are short), in 32 bits; pieces of A
+// and B of 16 along k go through shared memory, k first, two of each so that one is filled while the other is
+// multiplied.  Sums of 256 of k join totals in shared memory, so that their rounding does not grow with k (28 rows, d = 3781,
+// f = 9793: 5e-7 from 64 bits, 3e-6 before), and where the tiles would leave SMs without one, up to eight CTAs share a tile's k (2
+// rows, d = 3089, f = 8394: 1468 us forward, 341 with that and tiles of 32 rows).  Bound by the ordinary units' arithmetic (two
+// multiply-adds an instruction) and the reads of shared memory that feed it, an equal share of cycles: 4096 rows, d = 2048, f =
+// 4096, float: 38.7 TFLOP/s forward, 35.9 back (43.6 and 44.5 without the totals).  Tried without them: pieces of 8 along k 34.9
+// forward; A's values twice in shared memory, to be a pair's operand as they are, 34.4; 128 x 256 values, 8 x 16 a thread, 41.3.
 #include "ffn.cuh"
 
 namespace spmv {
@@ -12,43 +14,48 @@ namespace ffn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;
+constexpr int kTile = 128;  // columns of D; rows: 16 kR (128 or 32)
 constexpr int kDepth = 16;
-constexpr int kPitch = kTile + 4;  // floats of a row in shared memory
+constexpr int kFold = 16;   // pieces of k (256 of k) that are summed before the sum joins a total
 
-// Thread t's eight values of a piece (kTile x kDepth) of an operand whose (0, 0) is at p.
-// Along k: four of rows t / 4 and t / 4 + 64; along m or n: four of k = t / 32 and t / 32 + 8.
-template <typename T, bool kAcross>
+// fours of a piece (kRows x kDepth) that a thread has
+template <int kRows>
+constexpr int kFours = (kRows * kDepth / 4 + kThreads - 1) / kThreads;
+// A thread's values of a piece of an operand whose (0, 0) is at p: along k, four threads a row; along m or n, kRows / 4 a
+// row.  Along k the two halves of the rows may be of two matrices (p2: the second half's).
+template <typename T, bool kAcross, int kRows>
 __device__ __forceinline__ void fetch(const T *p, const T *p2, int64_t ld, int64_t mn_left, int64_t mn_left2, int64_t k_left, bool quads,
-                                      float (&v)[8]) {
-    const int t = threadIdx.x;
+                                      float (&v)[4 * kFours<kRows>]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kFours<kRows>; ++i) {
         float *out = v + 4 * i;
-        const int mn = kAcross ? (t & 31) * 4 : t / 4 + 64 * i, k = kAcross ? t / 32 + 8 * i : (t & 3) * 4;
-        // along k the two halves of the rows may be of two matrices (p2: the second half's)
-        const T *q = kAcross ? p + k * ld + mn : (i == 0 ? p : p2) + (t / 4) * ld + k;
-        const int64_t rows = kAcross ? k_left - k : (i == 0 ? mn_left - mn : mn_left2 - (mn - 64));
+        const int q = threadIdx.x + kThreads * i;
+        const int mn = kAcross ? q % (kRows / 4) * 4 : q / 4, k = kAcross ? q / (kRows / 4) : (q & 3) * 4;
+        const bool second = !kAcross && mn >= kRows / 2;
+        const int in_half = second ? mn - kRows / 2 : mn;
+        const T *at = kAcross ? p + k * ld + mn : (second ? p2 : p) + in_half * ld + k;
+        const int64_t rows = q * 4 >= kRows * kDepth ? 0 : kAcross ? k_left - k : (second ? mn_left2 : mn_left) - in_half;
         const int64_t run = kAcross ? mn_left - mn : k_left - k;  // values that follow on
         if (rows > 0 && run >= 4 && quads) {
             using U = typename Unit<4 * sizeof(T)>::type;
-            unit_to_f32<T>(*reinterpret_cast<const U *>(q), out);
+            unit_to_f32<T>(*reinterpret_cast<const U *>(at), out);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) out[j] = rows > 0 && j < run ? to_f32(q[j]) : 0.0f;
+            for (int j = 0; j < 4; ++j) out[j] = rows > 0 && j < run ? to_f32(at[j]) : 0.0f;
         }
     }
 }
-template <bool kAcross>
-__device__ __forceinline__ void stage(float (*s)[kPitch], const float (&v)[8]) {
-    const int t = threadIdx.x;
+template <bool kAcross, int kRows>
+__device__ __forceinline__ void stage(float (*s)[kRows + 4], const float (&v)[4 * kFours<kRows>]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kFours<kRows>; ++i) {
+        const int q = threadIdx.x + kThreads * i;
+        if (q * 4 >= kRows * kDepth) continue;
         if (kAcross) {
-            *reinterpret_cast<float4 *>(&s[t / 32 + 8 * i][(t & 31) * 4]) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            *reinterpret_cast<float4 *>(&s[q / (kRows / 4)][q % (kRows / 4) * 4]) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[(t & 3) * 4 + j][t / 4 + 64 * i] = v[4 * i + j];
+            for (int j = 0; j < 4; ++j) s[(q & 3) * 4 + j][q / 4] = v[4 * i + j];
         }
     }
 }
@@ -58,6 +65,7 @@ struct Place {
     int e;
     int64_t row, end;  // its first row, the segment's end
 };
+template <int kRows>
 __device__ bool find_tile(const Segments &seg, Place &place) {
     __shared__ int32_t part[kThreads / 32];
     __shared__ Place found;
@@ -65,7 +73,7 @@ __device__ bool find_tile(const Segments &seg, Place &place) {
     const int per = (seg.count + 1 + kThreads - 1) / kThreads;
     const auto tiles = [&](int e) {
         const Segments::Span s = seg.span(e);
-        return static_cast<int32_t>((s.end - s.begin + kTile - 1) / kTile);
+        return static_cast<int32_t>((s.end - s.begin + kRows - 1) / kRows);
     };
     int32_t mine = 0;
     for (int i = 0; i < per; ++i)
@@ -87,7 +95,7 @@ __device__ bool find_tile(const Segments &seg, Place &place) {
             const int e = t * per + i, n = e <= seg.count ? tiles(e) : 0;
             if (want >= at && want < at + n) {
                 const Segments::Span s = seg.span(e);
-                found = Place{e, s.begin + static_cast<int64_t>(want - at) * kTile, s.end};
+                found = Place{e, s.begin + static_cast<int64_t>(want - at) * kRows, s.end};
             }
             at += n;
         }
@@ -97,10 +105,15 @@ __device__ bool find_tile(const Segments &seg, Place &place) {
 }
 
 // D's tile of the CTA.  grid: x tiles of rows (kWeights: of the segment's matrix), y tiles of columns
-// (kWeights: segments), z (kWeights) which of the three products.
-template <typename T, int kKind>
+// (kWeights: segments and their parts), z which of the three products (kWeights), or which part of k: a cluster of up to
+// eight CTAs has the parts of one tile, whose sums each of them joins for its share of the rows, in the parts' order.
+template <typename T, int kKind, int kR>
 __global__ void __launch_bounds__(kThreads, 2) k_ffn_simt(Block b, unsigned quads_in, bool quads_out) {
-    __shared__ __align__(16) float sa[2][kDepth][kPitch], sb[2][kDepth][kPitch];
+    constexpr int kRows = 16 * kR;
+    __shared__ __align__(16) float sa[2][kDepth][kRows + 4], sb[2][kDepth][kTile + 4];
+    extern __shared__ __align__(16) uint8_t more[];
+    float4 *totals = reinterpret_cast<float4 *>(more) + threadIdx.x;  // [2 kR], kThreads apart
+    const int parts = kKind == kWeights ? 1 : static_cast<int>(gridDim.z), rank = kKind == kWeights ? 0 : static_cast<int>(blockIdx.z);
     constexpr bool kAcrossA = a_transposed(kKind), kAcrossB = b_transposed(kKind);
     constexpr int kCols = kKind == kGated ? kTile / 2 : kTile;  // gate's and up's beside each other
     const int which = kKind == kWeights ? blockIdx.z : 0;
@@ -118,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_ffn_simt(Block b, unsigned quad
         depth = s.end - s.begin;
         k0 = s.begin;
     } else {
-        if (!find_tile(b.seg, place)) return;
+        if (!find_tile<kRows>(b.seg, place)) return;
         col0 = static_cast<int64_t>(blockIdx.y) * kCols;
         depth = kKind == kGated || kKind == kBack ? b.d : b.f;
         if (place.e == b.seg.count) {
@@ -129,7 +142,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_ffn_simt(Block b, unsigned quad
     m_left = place.end - place.row;
     const int64_t n_left = product_columns<kKind>(b, which) - col0;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float2 acc[8][4] = {};
+    float2 acc[kR][4] = {};
+    bool folded = false;
 
     for (int pass = 0; pass < (kKind == kInput ? 2 : 1); ++pass) {
         // A's and B's first value of the tile
@@ -161,47 +175,97 @@ __global__ void __launch_bounds__(kThreads, 2) k_ffn_simt(Block b, unsigned quad
             pa = start(which == 0 ? b.dgate : which == 1 ? b.dup : b.dy, k0, place.row, lda);
             pb = start(which == 2 ? b.h : b.x, k0, col0, ldb);
         }
+        // this CTA's part of k, a multiple of the pieces' depth
+        const int64_t each = ((depth + parts - 1) / parts + kDepth - 1) / kDepth * kDepth, k_first = rank * each;
+        const int64_t mine = depth - k_first < each ? depth - k_first : each;
+        if (mine <= 0) break;  // (of every pass)
+        pa += kAcrossA ? k_first * lda : k_first;
+        pb += kAcrossB ? k_first * ldb : k_first;
+        if (!kAcrossB && pb2) pb2 += k_first;
         const bool qa = quads_in & 1, qb = quads_in & 2;
         const int64_t step_a = kAcrossA ? kDepth * lda : kDepth, step_b = kAcrossB ? kDepth * ldb : kDepth;
         const int64_t n2 = kKind == kGated ? n_left : n_left - 64;
-        const int64_t steps = (depth + kDepth - 1) / kDepth;
-        float va[8], vb[8];
+        const int64_t steps = (mine + kDepth - 1) / kDepth;
+        float va[4 * kFours<kRows>], vb[4 * kFours<kTile>];
         const auto load = [&](int64_t i) {
-            const int64_t k_left = depth - i * kDepth;
-            fetch<T, kAcrossA>(pa + i * step_a, pa + i * step_a + 64 * lda, lda, m_left, m_left - 64, k_left, qa, va);
-            fetch<T, kAcrossB>(pb + i * step_b, pb2 + i * step_b, ldb, n_left, n2, k_left, qb, vb);
+            const int64_t k_left = mine - i * kDepth;
+            fetch<T, kAcrossA, kRows>(pa + i * step_a, pa + i * step_a + kRows / 2 * lda, lda, m_left, m_left - kRows / 2, k_left, qa, va);
+            fetch<T, kAcrossB, kTile>(pb + i * step_b, pb2 + i * step_b, ldb, n_left, n2, k_left, qb, vb);
         };
         load(0);
         __syncthreads();  // (the pass before may still read)
-        stage<kAcrossA>(sa[0], va);
-        stage<kAcrossB>(sb[0], vb);
+        stage<kAcrossA, kRows>(sa[0], va);
+        stage<kAcrossB, kTile>(sb[0], vb);
         __syncthreads();
         for (int64_t i = 0; i < steps; ++i) {
             const int now = i & 1;
             if (i + 1 < steps) load(i + 1);
 #pragma unroll
             for (int k = 0; k < kDepth; ++k) {
-                float a[8];
+                float a[kR];
                 float2 c[4];
-                *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(&sa[now][k][ty * 4]);
-                *reinterpret_cast<float4 *>(a + 4) = *reinterpret_cast<const float4 *>(&sa[now][k][64 + ty * 4]);
+                if constexpr (kR == 8) {
+                    *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(&sa[now][k][ty * 4]);
+                    *reinterpret_cast<float4 *>(a + 4) = *reinterpret_cast<const float4 *>(&sa[now][k][64 + ty * 4]);
+                } else {
+                    *reinterpret_cast<float2 *>(a) = *reinterpret_cast<const float2 *>(&sa[now][k][ty * 2]);
+                }
                 *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(&sb[now][k][tx * 4]);
                 *reinterpret_cast<float4 *>(c + 2) = *reinterpret_cast<const float4 *>(&sb[now][k][64 + tx * 4]);
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
+                for (int r = 0; r < kR; ++r)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[r][j] = fma2(both(a[r]), c[j], acc[r][j]);
             }
             if (i + 1 < steps) {
-                stage<kAcrossA>(sa[now ^ 1], va);
-                stage<kAcrossB>(sb[now ^ 1], vb);
+                stage<kAcrossA, kRows>(sa[now ^ 1], va);
+                stage<kAcrossB, kTile>(sb[now ^ 1], vb);
+            }
+            // long sums in parts, so that their rounding does not grow with k
+            if ((i & (kFold - 1)) == kFold - 1 && i + 1 < steps) {
+#pragma unroll
+                for (int q = 0; q < 2 * kR; ++q) {
+                    float4 sum = folded ? totals[q * kThreads] : make_float4(0, 0, 0, 0);
+                    float2 *two = &acc[q / 2][q % 2 * 2];
+                    totals[q * kThreads] = make_float4(sum.x + two[0].x, sum.y + two[0].y, sum.z + two[1].x, sum.w + two[1].y);
+                    two[0] = two[1] = make_float2(0, 0);
+                }
+                folded = true;
             }
             __syncthreads();
         }
     }
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const int m = (r < 4 ? 0 : 60) + ty * 4 + r;
+    for (int q = 0; q < 2 * kR; ++q) {
+        float2 *two = &acc[q / 2][q % 2 * 2];
+        if (folded) {
+            const float4 sum = totals[q * kThreads];
+            two[0] = add2(two[0], make_float2(sum.x, sum.y));
+            two[1] = add2(two[1], make_float2(sum.z, sum.w));
+        }
+        if (parts > 1) totals[q * kThreads] = make_float4(two[0].x, two[0].y, two[1].x, two[1].y);
+    }
+    if (parts > 1) cluster_sync(parts);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int m = kR == 8 ? (r < 4 ? 0 : 60) + ty * 4 + r : ty * kR + r;
+        if (parts > 1) {  // the parts' sums of every parts-th row
+            if (r % parts != rank) continue;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float4 sum = make_float4(0, 0, 0, 0);
+                for (int p = 0; p < parts; ++p) {
+                    float4 v;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                                 : "r"(peer_addr(totals + (2 * r + q) * kThreads, p))
+                                 : "memory");
+                    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+                }
+                acc[r][2 * q] = make_float2(sum.x, sum.y);
+                acc[r][2 * q + 1] = make_float2(sum.z, sum.w);
+            }
+        }
         if (m >= m_left) continue;
         const int64_t row = place.row + m;
         float v[4] = {acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y};
@@ -214,10 +278,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_ffn_simt(Block b, unsigned quad
             if (64 + tx * 4 < n_left) finish<T, kKind, 4>(b, which, place.e, part, row, col0 + 64 + tx * 4, w, spare, quads_out);
         }
     }
+    if (parts > 1) cluster_sync(parts);  // the other CTAs have read this one's sums
 }
 
-template <typename T, int kKind>
-int launch(const Block &b, cudaStream_t s) {
+template <typename T, int kKind, int kR>
+int launch(const Block &b, int parts, cudaStream_t s) {
+    constexpr int kRows = 16 * kR;
     // every row (and every segment's matrix) of these starts at a multiple of four values
     const auto quads = [&](std::initializer_list<const Matrix *> ms) {
         for (const Matrix *m : ms)
@@ -232,29 +298,56 @@ int launch(const Block &b, cudaStream_t s) {
     else if (kKind == kBack) qa = quads({&b.dy}), qb = quads({&b.wd}), qo = quads({&b.gate, &b.up, &b.dgate, &b.dup, &b.h});
     else if (kKind == kInput) qa = quads({&b.dgate, &b.dup}), qb = quads({&b.wg, &b.wu}), qo = quads({&b.dx});
     else qa = quads({&b.dgate, &b.dup, &b.dy}), qb = quads({&b.x, &b.h}), qo = quads({&b.dwg, &b.dwu, &b.dwd});
-    int64_t gx, gy, gz = 1;
+    int64_t gx, gy, gz = parts;
     if (kKind == kWeights) {
         gx = ceil_div(b.d, kTile) * ceil_div(b.f, kTile);
         gy = static_cast<int64_t>(b.seg.count) * b.splits;
         gz = 3;
     } else {
-        gx = b.seg.rows / kTile + (b.seg.count < b.seg.rows ? b.seg.count : b.seg.rows) + 1;
+        gx = b.seg.rows / kRows + (b.seg.count < b.seg.rows ? b.seg.count : b.seg.rows) + 1;
         gy = ceil_div(product_columns<kKind>(b, 0), kKind == kGated ? kTile / 2 : kTile);
     }
     if (gx >= int64_t(1) << 31 || gy > 65535) return set_error(SPMV_ERR_TOO_LARGE, "the feed-forward block has too many tiles");
-    k_ffn_simt<T, kKind><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), static_cast<unsigned>(gz)), kThreads, 0, s>>>(
-        b, (qa ? 1u : 0u) | (qb ? 2u : 0u), qo);
-    SPMV_TRY_CUDA(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), static_cast<unsigned>(gz));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 2 * kR * kThreads * sizeof(float4);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = static_cast<unsigned>(parts);
+    cfg.attrs = attr;
+    cfg.numAttrs = parts > 1 ? 1 : 0;
+    SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn_simt<T, kKind, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes)));
+    SPMV_TRY_CUDA(cudaLaunchKernelEx(&cfg, k_ffn_simt<T, kKind, kR>, b, (qa ? 1u : 0u) | (qb ? 2u : 0u), qo));
     return SPMV_OK;
+}
+// Tiles of 32 rows for segments of up to that (taken as up to twice their mean, where there are several), and k in parts where
+// the tiles would leave SMs without one.
+template <typename T, int kKind>
+int launch_shape(const Block &b, cudaStream_t s) {
+    if constexpr (kKind == kWeights) {
+        return launch<T, kKind, 8>(b, 1, s);
+    } else {
+        const int64_t rows = b.seg.rows, count = b.seg.count, used = count < rows ? count : rows;
+        const bool few = (count == 1 ? rows : 2 * ceil_div(rows, count)) <= 32;
+        const int64_t high = few ? 32 : 128, row_tiles = ceil_div(rows, high) > used ? ceil_div(rows, high) : used;
+        const int64_t tiles = row_tiles * ceil_div(product_columns<kKind>(b, 0), kKind == kGated ? kTile / 2 : kTile);
+        const int64_t depth = kKind == kGated || kKind == kBack ? b.d : b.f;
+        int parts = 1;
+        while (parts < kMaxCluster && tiles * parts < 2 * kSms && depth / (2 * parts) >= 4 * kDepth) parts *= 2;
+        return few ? launch<T, kKind, 2>(b, parts, s) : launch<T, kKind, 8>(b, parts, s);
+    }
 }
 template <typename T>
 int launch_kind(int kind, const Block &b, cudaStream_t s) {
     switch (kind) {
-        case kGated: return launch<T, kGated>(b, s);
-        case kDown: return launch<T, kDown>(b, s);
-        case kBack: return launch<T, kBack>(b, s);
-        case kInput: return launch<T, kInput>(b, s);
-        default: return launch<T, kWeights>(b, s);
+        case kGated: return launch_shape<T, kGated>(b, s);
+        case kDown: return launch_shape<T, kDown>(b, s);
+        case kBack: return launch_shape<T, kBack>(b, s);
+        case kInput: return launch_shape<T, kInput>(b, s);
+        default: return launch_shape<T, kWeights>(b, s);
     }
 }
 
