@@ -50,7 +50,7 @@ int check_segments(int32_t experts, const int32_t *offsets) {
     return check_array(offsets, "offsets", 4);
 }
 // Parts of each segment's rows in the weights' gradients: enough tiles for the GPU where the matrices are small, of at
-// least 512 rows on average (a backward pass of 65536 rows, d = f = 64: float 7434 -> 343 us, bf16 258 -> 60; 256: 301 -> 128).
+// least 512 rows on average (a backward pass of 65536 rows, d = f = 64: float 7434 -> 343 us, bf16 258 -> 60; 256: bf16 301 -> 128).
 int weight_splits(int64_t rows, int64_t d, int64_t f, int32_t experts) {
     const int64_t tiles = 3 * ceil_div(d, 128) * ceil_div(f, 128) * experts, mean = rows / experts;
     int splits = 1;
