@@ -708,7 +708,11 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                     take(c, v);
                     if constexpr (S::kTwoParts) {  // the sums of h's second parts, kLoaded lanes on
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] += __shfl_down_sync(0xffffffffu, v[j], kLoaded);
+                        for (int j = 0; j < 32; ++j) {
+                            const float rest = __shfl_down_sync(0xffffffffu, v[j], kLoaded);
+                            // (a weight that is no number times a second part, which may be 0, is not what it is times h)
+                            if (fabsf(v[j]) < INFINITY) v[j] += rest;
+                        }
                     }
                 }
                 const int64_t left = columns - c;
