@@ -849,6 +849,10 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
     args.follows = follows;
     const int64_t rows = b.seg.rows, d = b.d, f = b.f, count = b.seg.count;
     args.stages = S::stages(static_cast<int>(count));
+    const size_t smem = S::smem(static_cast<int>(count), args.stages);
+    // (in front of the maps: they are made for the context that is current to this host thread, and this makes the
+    // device's that where no call has yet)
+    SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
     const auto activation = [&](CUtensorMap *map, const Matrix &m, int64_t n) {
         return make_map<T>(map, m, n, rows, 0, kKind == kWeights ? kDepth : S::kMine);
     };
@@ -878,9 +882,7 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
     if (kKind != kWeights)
         tiles = ceil_div(product_columns<kKind>(b, 0), S::kCols) * (rows / S::kTileRows + (count < rows ? count : rows) + 1);
     if (tiles >= int64_t(1) << 31) return set_error(SPMV_ERR_TOO_LARGE, "the feed-forward block has too many tiles");
-    const size_t smem = S::smem(static_cast<int>(count), args.stages);
     const int64_t workers = kSms / S::kCtas;
-    SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((tiles < workers ? tiles : workers) * S::kCtas));
     cfg.blockDim = dim3(threads_of(kKind));

@@ -1,6 +1,7 @@
 """The feed-forward block where its kernels change shape and where values leave their range, against its 64-bit
 statement (oracle/token_rows.py).  The helpers and how their tolerances are derived: test_gpu_feed_forward.py."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -51,3 +52,38 @@ def test_infinite_weights(spmv, dtype, rows, experts):
         assert np.array_equal(y[a:b][sure][:, hit], want[sure][:, hit], equal_nan=True), (e, y[a:b][:, hit], want[:, hit])
     rest = [c for c in range(d) if c not in hit]
     assert np.array_equal(y[:, rest], f64(clean.y)[:, rest])
+
+
+@pytest.mark.parametrize("dtype", ALL)
+def test_first_call_of_a_host_thread(spmv, dtype):
+    """a host thread that has made no CUDA call yet: the library's is the first"""
+    from sparse_matrix_vector_csr_gb300._abi import _check, lib
+
+    g, code = gen(2), {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}[dtype]
+    x, dy = torch.randn(40, 64, generator=g).to(dtype).cuda(), torch.randn(40, 64, generator=g).to(dtype).cuda()
+    ws = weights(None, 64, 72, dtype, g)
+    want = spmv.feed_forward(x, *ws, keep=True)
+    want_dx = want.grad(dy)[0]
+    y, dx = torch.zeros_like(x), torch.zeros_like(x)
+    sizes = [spmv.spmv_feed_forward_workspace(40, 64, 72, 1, code, gradient) for gradient in (0, 1)]
+    spaces = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    call = (40, 64, 72, 1, None, x.data_ptr(), 64, ws[0].data_ptr(), ws[1].data_ptr(), 64, 0, ws[2].data_ptr(), 72, 0, 0)
+    forward = (*call, None, None, 72, y.data_ptr(), 64, code, spaces[0].data_ptr(), sizes[0], None)
+    back = (*call, want.gate.data_ptr(), want.up.data_ptr(), want.gate.stride(0), dy.data_ptr(), 64, dx.data_ptr(), 64, None, None, None, code,
+            spaces[1].data_ptr(), sizes[1], None)
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(entry, args):
+        try:
+            _check(entry(*args))
+        except spmv.SpmvError as e:
+            failed.append(str(e))
+
+    for entry, args in ((lib.spmv_feed_forward, forward), (lib.spmv_feed_forward_grad, back)):
+        t = threading.Thread(target=work, args=(entry, args))
+        t.start()
+        t.join()
+    assert not failed, failed
+    torch.cuda.synchronize()
+    assert torch.equal(y, want.y) and torch.equal(dx, want_dx)
