@@ -31,7 +31,7 @@ constexpr int kRows = 128;        // of a tile of D: the accumulator's lanes
 constexpr int kDepth = 64;        // of a stage: 128 bytes, the width of the swizzle
 constexpr int kRowBytes = 128;
 constexpr int kGroupRows = 2048;  // of the row tiles that take turns before the next column tile, so that both stay in L2
-constexpr int kSharedBytes = 227 * 1024;
+constexpr int kSharedBytes = 227 * 1024 - 256;  // dynamic; the rest for the variables of fixed size
 constexpr int kMaxStages = 32;
 constexpr int kFewRows = kShortRows;  // of a tile where segments are short
 constexpr long long kWaitCycles = 4000000000LL;  // about two seconds
@@ -414,7 +414,7 @@ struct Shape {
     static constexpr int kFixed = 1024 + kSlack + kWriters * kWriterBytes + (4 * kMaxStages + 5) * 8;
     static constexpr int kColumns = 2 * kN * kAccs;  // of tensor memory: two buffers
     static int stages(int segments) {
-        const int n = (kSharedBytes - 256 - kFixed - (segments + 2) * 4) / kStageBytes;
+        const int n = (kSharedBytes - kFixed - (segments + 2) * 4) / kStageBytes;
         return n > kMaxStages ? kMaxStages : n;
     }
     static size_t smem(int segments, int stages) { return kFixed + stages * kStageBytes + (segments + 2) * 4; }
@@ -851,8 +851,8 @@ int launch(const Block &b, bool follows, cudaStream_t s) {
     args.stages = S::stages(static_cast<int>(count));
     const size_t smem = S::smem(static_cast<int>(count), args.stages);
     // (in front of the maps: they are made for the context that is current to this host thread, and this makes the
-    // device's that where no call has yet)
-    SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    // device's that where no call has yet; always the same limit: another thread's call may set it between this and the launch)
+    SPMV_TRY_CUDA(cudaFuncSetAttribute(k_ffn<T, kKind, kN, kLoaded, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes));
     const auto activation = [&](CUtensorMap *map, const Matrix &m, int64_t n) {
         return make_map<T>(map, m, n, rows, 0, kKind == kWeights ? kDepth : S::kMine);
     };

@@ -87,3 +87,41 @@ def test_first_call_of_a_host_thread(spmv, dtype):
     assert not failed, failed
     torch.cuda.synchronize()
     assert torch.equal(y, want.y) and torch.equal(dx, want_dx)
+
+
+def test_calls_of_two_threads(spmv):
+    """blocks of few and of many experts, which share kernels and need different amounts of shared memory, from two
+    host threads at once (a call's arguments made beforehand: the threads meet inside the library)"""
+    g = gen(1)
+    sets = []
+    for experts, rows in ((2, 6), (4096, 300)):
+        plan, x, _, _ = routed(spmv, rows, 1, experts, 1, 64, torch.bfloat16, g, dropped=0.0)
+        ws, y, stream = weights(experts, 64, 72, torch.bfloat16, g), torch.zeros_like(x), torch.cuda.Stream()
+        n = spmv.spmv_feed_forward_workspace(rows, 64, 72, experts, 3)
+        space = torch.empty(n, dtype=torch.uint8, device="cuda")
+        args = (rows, 64, 72, experts, plan.offsets.data_ptr(), x.data_ptr(), 64, ws[0].data_ptr(), ws[1].data_ptr(), 64, 64 * 72,
+                ws[2].data_ptr(), 72, 64 * 72, 0, None, None, 72, y.data_ptr(), 64, 3, space.data_ptr(), n, stream.cuda_stream)
+        sets.append((args, plan.feed_forward(x, *ws).y, y, stream, (plan, x, ws, space)))
+    torch.cuda.synchronize()
+    from sparse_matrix_vector_csr_gb300._abi import _check, lib
+
+    refused = []
+
+    def work(i):
+        args, _, _, stream, _ = sets[i]
+        for n in range(4000):
+            try:
+                _check(lib.spmv_feed_forward(*args))
+            except spmv.SpmvError as e:
+                refused.append((i, n, str(e)))
+            if n % 200 == 0:
+                stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, refused
+    assert all(torch.equal(want, y) for _, want, y, _, _ in sets)
