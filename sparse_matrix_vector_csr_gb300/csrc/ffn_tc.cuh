@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                     }
                     if (!zero) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = activate<false>(v[j], b.act).value * w[j];
+                        for (int j = 0; j < 32; ++j) v[j] = activate<T, false>(v[j], b.act).value * w[j];
                         // rounded to the type: the next product takes it so (one rounding of each term of y's sums); of short
                         // segments, whose products wait for the weights, it takes what the rounding left out, too
                         patch_row<T>(mine, v);
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(threads_of(kKind), 1) k_ffn(const __grid_const
                         unpack<T>(patch_load(patch_piece(up, lane, p)), u);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const Activated a = activate<true>(g[j], b.act);
+                            const Activated a = activate<T, true>(g[j], b.act);
                             g[j] = v[8 * p + j] * u[j] * a.slope;
                             h[j] = a.value * u[j];
                             u[j] = v[8 * p + j] * a.value;

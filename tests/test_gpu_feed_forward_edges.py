@@ -125,3 +125,51 @@ def test_calls_of_two_threads(spmv):
     torch.cuda.synchronize()
     assert not refused, refused
     assert all(torch.equal(want, y) for _, want, y, _, _ in sets)
+
+
+def activations(spmv, gates, act, dtype):
+    """(act, act') of the gates as the block computes them: x is a unit row, up is 1, w_down the identity and dy 1, so that y and the
+    gradients in the first columns of w_up and w_gate are single products with 1"""
+    n = len(gates)
+    x = torch.zeros(1, n, dtype=dtype, device="cuda")
+    x[0, 0] = 1.0
+    wg, wu = (torch.zeros(n, n, dtype=dtype, device="cuda") for _ in range(2))
+    wg[:, 0], wu[:, 0] = gates.to(dtype).cuda(), 1.0
+    res = spmv.feed_forward(x, wg, wu, torch.eye(n, dtype=dtype, device="cuda"), activation=act, keep=True)
+    _, dwg, dwu, _ = res.grad(torch.ones_like(x))
+    assert torch.equal(res.gate[0].cpu(), gates.to(dtype))
+    return f64(res.y[0]), f64(dwu[:, 0]), f64(dwg[:, 0])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_float_activations(spmv, act):
+    """act and act' of float rows to 32 bits relative to their value, over the whole range of the exponential.
+
+    With E = 2^-23 and v the exponent (x, or gelu's 2 z): the exponential and the quotient, which is at least 1/2, are within 2 E (two
+    units in the last place), 1 + e and the product add E / 2 each, so s and 1 - s are within 5 E and x s within 5.5 E.  gelu's 2 z is
+    within 3 E of its value (two constants, four operations), which the exponential turns into 3 E |v|.  An exponential below
+    2^-126 is within two of the smallest steps, 2^-148.
+    """
+    gates = torch.cat([torch.linspace(-110, 110, 441), torch.linspace(-12, 12, 389), torch.tensor([-1e-30, 0.0, 1e-30, 1e18, -1e18])])
+    x = f64(gates)
+    if act == "silu":
+        v, dv = x, np.ones_like(x)
+    else:
+        v = 2 * np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3)
+        dv = 2 * np.sqrt(2 / np.pi) * (1 + 3 * 0.044715 * x * x)
+    E, lost = 2.0 ** -23, 2.0 ** -148
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        e = np.exp(-np.abs(v))
+        s, c = np.where(v < 0, e, 1) / (1 + e), np.where(v < 0, 1, e) / (1 + e)  # s and 1 - s, without a difference
+        value, part = x * s, np.where(c * s == 0, 0.0, x * s * c * dv)
+    slope = s + part
+    off = 3 * E * np.abs(v) if act == "gelu_tanh" else 0 * v
+    off = np.minimum(off, 1.0)  # (beyond it s is 0 or 1 and its error the smallest step's)
+    y, by_up, by_gate = activations(spmv, gates, act, torch.float32)
+    bound = (5.5 * E + off) * np.abs(value) + 2 * lost * (1 + np.abs(x))
+    within_ = lambda got, want, b: np.argwhere(~(np.abs(got - want) <= b))[:5].ravel().tolist()  # noqa: E731
+    assert not within_(y, value, bound), [(x[i], y[i], value[i]) for i in within_(y, value, bound)]
+    assert np.array_equal(by_up, y)
+    # s, x s (1 - s) and their sum; 5 E + E / 2 each, gelu's slope of 2 z 3 E, and roundings
+    bound = (15 * E + 2 * off) * (s + np.abs(part)) + 4 * lost * (1 + np.abs(x)) * (1 + np.minimum(np.abs(dv), 1e3))
+    assert not within_(by_gate, slope, bound), [(x[i], by_gate[i], slope[i]) for i in within_(by_gate, slope, bound)]
