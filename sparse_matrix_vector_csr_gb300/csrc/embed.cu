@@ -169,8 +169,9 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(SortArgs a, ZeroArg
         int2 *out = a.sorted[(a.passes - 1 - p) & 1];
         const int shift = p * a.bits;
         const int64_t share = (n + ctas - 1) / ctas, begin = min(n, rank * share), end = min(n, begin + share);
-        // as few warps as hold their tokens in registers: their counts have to be cleared and added up
-        const int n_warps = static_cast<int>(min((share + 32 * kHeld - 1) / (32 * kHeld), int64_t(kSortWarps)));
+        // as few warps as hold their tokens in registers: their counts have to be cleared and added up (one where no
+        // token is left)
+        const int n_warps = static_cast<int>(min(max((share + 32 * kHeld - 1) / (32 * kHeld), int64_t(1)), int64_t(kSortWarps)));
         const int64_t run = (end - begin + 32 * n_warps - 1) / (32 * n_warps) * 32;
         const int64_t r0 = begin + warp * run, r1 = warp < n_warps ? min(end, r0 + run) : r0;
         int32_t *mine = wcount + warp * bins;
