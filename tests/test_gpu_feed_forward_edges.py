@@ -173,3 +173,142 @@ def test_float_activations(spmv, act):
     # s, x s (1 - s) and their sum; 5 E + E / 2 each, gelu's slope of 2 z 3 E, and roundings
     bound = (15 * E + 2 * off) * (s + np.abs(part)) + 4 * lost * (1 + np.abs(x)) * (1 + np.minimum(np.abs(dv), 1e3))
     assert not within_(by_gate, slope, bound), [(x[i], by_gate[i], slope[i]) for i in within_(by_gate, slope, bound)]
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows", [8, 9, 12, 16, 17])
+@pytest.mark.parametrize("d,f", [(72, 200), (136, 1032), (9800, 40)])
+def test_few_dense_rows(spmv, dtype, rows, d, f):
+    """tiles of 8 and of 16 rows, w_down's of 32 columns and (d = 9800) of 64, and the first size beyond them"""
+    g = gen(rows + d)
+    x, dy = torch.randn(rows, d, generator=g).to(dtype).cuda(), torch.randn(rows, d, generator=g).to(dtype).cuda()
+    ws = weights(None, d, f, dtype, g)
+    check(spmv, x, ws, "silu", dy, [(0, rows)], lambda keep: spmv.feed_forward(x, *ws, keep=keep))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows", [1, 8, 9, 16])
+@pytest.mark.parametrize("d,f", [(72, 200), (9800, 40)])
+def test_few_rows_keep_what_rounding_leaves(spmv, dtype, rows, d, f):
+    """y of up to 16 rows with a bound that leaves no room for h's rounding: what that leaves out is rounded (H of it) and kept"""
+    g = gen(rows + f)
+    x, ws, half = torch.randn(rows, d, generator=g).to(dtype).cuda(), weights(None, d, f, dtype, g), H[dtype]
+    w = [f64(t) for t in ws]
+    y, sums = ref.feed_forward(f64(x), *w, "relu", unit=U, half=0.0, tiny=0.0)["y"]
+    h = np.maximum(f64(x) @ w[0].T, 0) * (f64(x) @ w[1].T)
+    kept = sums + (half * half * np.abs(h) + 2 * TINY[dtype]) @ np.abs(w[2]).T
+    within(spmv.feed_forward(x, *ws, activation="relu").y, y, kept + half * (np.abs(y) + kept) + TINY[dtype], "y")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("entries,experts,hot", [(200, 64, 0), (448, 64, 0), (500, 64, 150), (250, 64, 70), (30, 5, 0)])
+@pytest.mark.parametrize("d,f", [(256, 72), (88, 264)])
+def test_short_segments(spmv, dtype, entries, experts, hot, d, f):
+    """segments of a few rows, in tiles of 8 (mean 4) and of 16 (mean 7 and 8); with one expert far beyond the mean"""
+    g = gen(entries + d)
+    ids = torch.randint(0, experts, (entries,), generator=g, dtype=torch.int32)
+    ids[:hot] = 3
+    plan = spmv.RoutePlan(ids[torch.randperm(entries, generator=g)][:, None].cuda(), experts)
+    xs, dys = (plan.dispatch(torch.randn(entries, d, generator=g).to(dtype).cuda()) for _ in range(2))
+    offsets = plan.offsets.tolist()
+    ws = weights(experts, d, f, dtype, g)
+    check(spmv, xs, ws, "gelu_tanh", dys, list(zip(offsets, offsets[1:])),
+          lambda keep: plan.feed_forward(xs, *ws, activation="gelu_tanh", keep=keep))
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("entries,experts,d,f", [(3400, 48, 264, 280), (1500, 24, 1032, 1000), (3400, 48, 280, 512)])
+def test_many_middling_segments(spmv, dtype, entries, experts, d, f):
+    """tiles of 128 x 256 (gate and up: 2 x 128) by one CTA each: segments of about 70 rows, enough of them for 96 SMs"""
+    g = gen(entries + d)
+    plan, xs, dys, spans = routed(spmv, entries, 1, experts, 1, d, dtype, g)
+    ws = weights(experts, d, f, dtype, g)
+    check(spmv, xs, ws, "silu", dys, spans, lambda keep: plan.feed_forward(xs, *ws, keep=keep))
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows,d,f", [(8200, 256, 256), (4200, 264, 280)])
+def test_wide_weights_in_parts(spmv, dtype, rows, d, f):
+    """the weights' gradients by pairs of CTAs and in parts of the rows at once"""
+    g = gen(rows)
+    x, dy = torch.randn(rows, d, generator=g).to(dtype).cuda(), torch.randn(rows, d, generator=g).to(dtype).cuda()
+    ws = weights(None, d, f, dtype, g)
+    check(spmv, x, ws, "relu", dy, [(0, rows)], lambda keep: spmv.feed_forward(x, *ws, activation="relu", keep=keep))
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows,d,f", [(2, 2117, 2205), (16, 2117, 2205), (28, 1029, 2205), (32, 2117, 1061), (33, 1029, 1061),
+                                      (1300, 301, 3561), (1300, 3561, 301)])
+def test_long_sums_by_the_ordinary_units(spmv, dtype, rows, d, f):
+    """odd sizes: tiles of 32 and of 128 rows, each tile's k shared by a cluster and (1300 rows) not, sums of more than 256 of k"""
+    g = gen(rows + d)
+    x, dy = torch.randn(rows, d, generator=g).to(dtype).cuda(), torch.randn(rows, d, generator=g).to(dtype).cuda()
+    ws = weights(None, d, f, dtype, g)
+    check(spmv, x, ws, "silu", dy, [(0, rows)], lambda keep: spmv.feed_forward(x, *ws, keep=keep))
+
+
+@pytest.mark.parametrize("rows,d,f", [(2, 2117, 2205), (28, 2117, 2205), (1300, 301, 3561)])
+def test_float_sums_do_not_grow_with_k(spmv, rows, d, f):
+    """Sums of float products in parts of 256: n terms of the size t have a total whose rounding is at most 2^-23 times
+    256 + n / 256 + 8 additions of sums of up to n t (and not n); against products in 64 bits."""
+    g = gen(f)
+    x = torch.rand(rows, d, generator=g).cuda() + 0.5  # (no cancelling: the rounding of the partial sums adds up)
+    ws = [(torch.rand(w.shape, generator=g) + 0.5).cuda() / w.shape[-1] for w in weights(None, d, f, torch.float32, g)]
+    res = spmv.feed_forward(x, *ws, activation="relu", keep=True)
+    gate = x.double() @ ws[0].double().t()
+    y = (res.gate.double() * res.up.double()) @ ws[2].double().t()
+    for got, want, n in ((res.gate, gate, d), (res.y, y, f)):
+        assert float(((got.double() - want).abs() / want).max()) <= 2.0 ** -23 * (256 + n / 256 + 8), n
+
+
+def guarded(shape, dtype, shift=0, pad=0):
+    """(a matrix of zeros, the NaN around it: all of the buffer)"""
+    view = placed(torch.zeros(shape, dtype=dtype), shift, pad)
+    return view, view._base if view._base is not None else view
+
+
+def untouched(view, buf):
+    inside = torch.zeros_like(buf, dtype=torch.bool)
+    torch.as_strided(inside, view.shape, view.stride(), view.storage_offset()).fill_(True)
+    return bool((~inside).any()) and bool(torch.isnan(buf[~inside]).all())
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("shift,pad", [(0, 8), (8, 16), (4, 4), (1, 3)])
+@pytest.mark.parametrize("rows,d,f,experts", [(5, 72, 200, 0), (12, 72, 200, 0), (140, 72, 200, 0), (140, 50, 24, 0), (3000, 1000, 520, 0),
+                                              (300, 104, 72, 64), (3400, 264, 280, 48), (4200, 264, 280, 0)])
+def test_nothing_beside_the_results(spmv, dtype, shift, pad, rows, d, f, experts):
+    """every array that the block writes, gate and up, both workspaces and the weights' gradients among them, with NaN between its
+    rows and around it: what was there stays, and the results are those of the plain call"""
+    g = gen(rows + pad)
+    lead = experts or None
+    if experts:
+        plan, x, dy, _ = routed(spmv, rows, 1, experts, 1, d, dtype, g)
+        x, dy = placed(x.cpu(), shift, pad), placed(dy.cpu(), shift, pad)
+        want = plan.feed_forward(x, *(ws := weights(lead, d, f, dtype, g, shift, pad)), keep=True)
+    else:
+        x, dy = (placed(torch.randn(rows, d, generator=g).to(dtype), shift, pad) for _ in range(2))
+        want = spmv.feed_forward(x, *(ws := weights(lead, d, f, dtype, g, shift, pad)), keep=True)
+    rows = len(x)
+    want_grad = want.grad(dy)
+    code = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}[dtype]
+    (y, y_all), (dx, dx_all) = (guarded((rows, d), dtype, shift, pad) for _ in range(2))
+    (gate, gate_all), (up, up_all) = (guarded((rows, f), dtype, shift, pad) for _ in range(2))
+    dws = [guarded(w.shape, dtype, 8) for w in ws]  # (contiguous, in front of a row's worth of values)
+    spaces = []
+    for gradient in (0, 1):
+        n = spmv.spmv_feed_forward_workspace(rows, d, f, experts or 1, code, gradient)
+        spaces.append((n, torch.full((n + 512,), 0x5a, dtype=torch.uint8, device="cuda")))
+    apart = [w.stride(0) if experts else 0 for w in ws]
+    call = (rows, d, f, experts or 1, plan.offsets if experts else None, x, x.stride(0), ws[0], ws[1], ws[0].stride(-2), apart[0], ws[2],
+            ws[2].stride(-2), apart[2], "silu", gate, up, gate.stride(0))
+    spmv.spmv_feed_forward(*call, y, y.stride(0), code, spaces[0][1][256:], spaces[0][0])
+    spmv.spmv_feed_forward_grad(*call, dy, dy.stride(0), dx, dx.stride(0), *[v for v, _ in dws], code, spaces[1][1][256:], spaces[1][0])
+    for name, view, buf in (("y", y, y_all), ("dx", dx, dx_all), ("gate", gate, gate_all), ("up", up, up_all),
+                            *((f"dw{i}", *pair) for i, pair in enumerate(dws))):
+        assert untouched(view, buf), name
+    for n, space in spaces:
+        assert space[:256].eq(0x5a).all() and space[256 + n:].eq(0x5a).all()
+    for name, got, ref_ in (("gate", gate, want.gate), ("up", up, want.up), ("y", y, want.y), ("dx", dx, want_grad[0]),
+                            *((f"dw{i}", v, w) for i, ((v, _), w) in enumerate(zip(dws, want_grad[1:])))):
+        assert torch.equal(got, ref_), name
