@@ -706,8 +706,8 @@ SPMV_API int spmv_embed_rows(int64_t tokens, int64_t vocab, int64_t d, const int
 
 /*
  * The gradient of spmv_embed_rows in the table: dtable[v] = scale * sum of dx[t] over the tokens with
- * ids[t] = v, in the tokens' order, in 32 bits, rounded once; 0 for a row without tokens.  With `accumulate`
- * not 0 it is added to what dtable holds (one rounding of the sum), and rows without tokens are not
+ * ids[t] = v, in a fixed order (same call, same bits), in 32 bits, rounded once; 0 for a row without tokens.  With
+ * `accumulate` not 0 it is added to what dtable holds (one rounding of the sum), and rows without tokens are not
  * touched.  dx is of type `dtype`, dtable (vocab x d) of type `out_dtype`: the same, or SPMV_F32.
  * The workspace (spmv_embed_workspace gives its bytes, or a negative status) starts at a multiple
  * of 16 bytes and is free for other use when the call's kernels have run.
@@ -738,7 +738,8 @@ typedef enum { SPMV_ACT_SILU = 0, SPMV_ACT_GELU_TANH = 1, SPMV_ACT_RELU = 2 } sp
  *            NULL.
  * Sums are in 32 bits; h, gate, up and y are each rounded once to the type (h of up to 16
  * rows, or of segments of up to 8 on average, whose weights take longer than their products, is kept
- * with what its rounding left out).  No product of a value that no
+ * with what its rounding left out).  A value beyond the type's range becomes an infinity, h too: in SPMV_F16
+ * an |act(gate) * up| above 65504 leaves no number in its row of y.  No product of a value that no
  * row or matrix holds enters a sum: NaN and infinities of a row stay in that row.
  *   rows <= 2^31 - 4096; 1 <= d, f <= 2^20; 1 <= experts <= 4096.
  * The workspace starts at a multiple of 16 bytes and is free for other use when the call's kernels have run.
@@ -760,7 +761,8 @@ SPMV_API int spmv_feed_forward(int64_t rows, int64_t d, int64_t f, int32_t exper
  *   dw_gate, dw_up (experts x f x d), dw_down (experts x d x f), contiguous: the gradients in the weights, sums
  *            over each expert's rows, 0 for an expert without rows; each may be NULL.
  * Rows without an expert enter nothing, whatever x and dy hold there.  Sums are in 32 bits; the gradients in
- * gate and up, and h, are rounded once to the type for the products that follow.
+ * gate and up, and h, are rounded once to the type for the products that follow (SPMV_F16: an infinity beyond
+ * 65504, as gate and up themselves).
  */
 SPMV_API int spmv_feed_forward_grad(int64_t rows, int64_t d, int64_t f, int32_t experts, const int32_t *offsets,
                                     const void *x, int64_t ldx, const void *w_gate, const void *w_up, int64_t ldw,

@@ -435,7 +435,9 @@ def feed_forward(x, w_gate, w_up, w_down, activation="silu", keep=False, out=Non
     """The gated feed-forward block y = (act(x w_gate^T) * (x w_up^T)) w_down^T of the rows of x
     (rows x d), with w_gate and w_up f x d (of the same strides) and w_down d x f, all of x's type.
     ``activation``: "silu", "gelu_tanh" or "relu".  ``keep``: also what :meth:`FeedForward.grad`
-    needs.  :meth:`RoutePlan.feed_forward` is the same for experts."""
+    needs.  :meth:`RoutePlan.feed_forward` is the same for experts.  What lies between the products is rounded to
+    x's type: in float16 act(gate) * up above 65504 is an infinity.  ``spmv_feed_forward_status`` waits for the stream and
+    raises where a kernel gave up a wait of its own (results are invalid then)."""
     return _feed_forward(x, w_gate, w_up, w_down, activation, keep, out, stream, None, None, None)
 
 

@@ -312,3 +312,41 @@ def test_nothing_beside_the_results(spmv, dtype, shift, pad, rows, d, f, experts
     for name, got, ref_ in (("gate", gate, want.gate), ("up", up, want.up), ("y", y, want.y), ("dx", dx, want_grad[0]),
                             *((f"dw{i}", v, w) for i, ((v, _), w) in enumerate(zip(dws, want_grad[1:])))):
         assert torch.equal(got, ref_), name
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("rows", [2, 20])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+def test_large_gates_of_other_types(spmv, dtype, rows, act):
+    """gates up to the end of the type's range, or of the exponential's: act tends to x or to 0, no NaN"""
+    scale = [0.0, 1.0, 20.0, 90.0, 1e4, 6e4, -20.0, -90.0] if dtype == torch.float16 else [0.0, 1.0, 20.0, 90.0, 1e4, 1e15, 1e18, -1e18]
+    x = torch.tensor([1.0, -1.0]).repeat(rows // 2)[:, None].repeat(1, 8).to(dtype).cuda()
+    wg, wu = torch.zeros(8, 8, dtype=dtype), torch.zeros(8, 8, dtype=dtype)
+    wg[:, 0], wu[:, 0] = torch.tensor(scale).to(dtype), 1.0
+    ws = (wg.cuda(), wu.cuda(), torch.eye(8, dtype=dtype, device="cuda"))
+    dy = torch.ones_like(x)
+    res = spmv.feed_forward(x, *ws, activation=act, keep=True)
+    dx, dwg, dwu, dwd = res.grad(dy)
+    kw = dict(unit=U, half=H[dtype], tiny=TINY[dtype])
+    w = [f64(t) for t in ws]
+    fwd = ref.feed_forward(f64(x), *w, act, **kw)
+    back = ref.feed_forward_grad(f64(x), *w, act, f64(res.gate), f64(res.up), f64(dy), **kw)
+    for got, (want, bound) in ((res.gate, fwd["gate"]), (res.up, fwd["up"]), (res.y, fwd["y"]), (dx, back["dx"]), (dwg, back["dw_gate"]),
+                               (dwu, back["dw_up"]), (dwd, back["dw_down"])):
+        beyond = np.abs(want) - bound > torch.finfo(dtype).max  # (a sum of gradients beyond the type's range is an infinity)
+        got = f64(got)
+        assert np.array_equal(got[beyond], np.copysign(np.inf, want[beyond]))
+        assert (np.abs(got - want) <= bound)[~beyond].all()
+
+
+@pytest.mark.parametrize("rows", [4, 12, 40])
+def test_values_beyond_float16(spmv, rows):
+    """h is a value of the type: beyond 65504 it is an infinity, in y an infinity or (beside a 0 of w_down) NaN, in its row only"""
+    x = torch.ones(rows, 16, dtype=torch.float16, device="cuda")
+    x[::2] = 0.125
+    wg, wu, wd = (torch.zeros(16, 16, dtype=torch.float16, device="cuda") for _ in range(3))
+    wg[0, 0] = wu[0, 0] = 300.0
+    wd[3, 0] = 0.5
+    y = spmv.feed_forward(x, wg, wu, wd).y
+    assert torch.isinf(y[1::2, 3]).all() and torch.isnan(y[1::2, 4]).all()
+    assert torch.equal(y[::2, 3], torch.full_like(y[::2, 3], 37.5 * 37.5 / 2)) and not y[::2, 4].any()
